@@ -1,0 +1,78 @@
+// mnb_paged_attention: argument checks and the choice of a kernel.
+#include <cmath>
+
+#include "attention.h"
+
+using namespace mnb;
+
+extern "C" {
+
+size_t mnb_attention_workspace_size(int64_t batch, int64_t T, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                                    int64_t max_q, int64_t max_kv, mnb_dtype dtype) {
+    (void)batch; (void)T; (void)q_heads; (void)kv_heads; (void)head_dim; (void)max_q; (void)max_kv; (void)dtype;
+    return 0;
+}
+
+mnb_status mnb_paged_attention(const mnb_attention_args* a, const mnb_kv_cache* c) {
+    if (!a || !dec::valid_cache(c)) return MNB_ERR_INVALID_ARG;
+    const int64_t i31 = int64_t(1) << 31;
+    if (a->T < 0 || a->T >= i31 || a->q_heads < 1 || a->q_heads > 65535 || a->q_heads % c->kv_heads != 0 || a->max_q < 1 ||
+        a->max_q >= (i31 >> 1) || a->max_kv < 0 || a->max_kv >= (i31 >> 1) || a->window < 0 || a->window >= i31 ||
+        (a->causal != 0 && a->causal != 1) || !std::isfinite(a->scale) || c->head_dim % 8 != 0 || c->head_dim > 256)
+        return MNB_ERR_INVALID_ARG;
+    const int64_t vec = 16 / dec::dt_bytes(c->dtype);
+    const int64_t st[4] = {a->q_token_stride, a->q_head_stride, a->o_token_stride, a->o_head_stride};
+    for (int64_t x : st)
+        if (x < 0 || x % vec != 0 || x >= (int64_t(1) << 38)) return MNB_ERR_INVALID_ARG;
+    if (a->T == 0) return MNB_OK;
+    if (!a->q || !a->o || !a->q_start || !dec::aligned_to(a->q, 16) || !dec::aligned_to(a->o, 16) ||
+        !dec::aligned_to(a->lse, 4) || !dec::aligned_to(a->q_start, 4))
+        return MNB_ERR_INVALID_ARG;
+    const size_t need = mnb_attention_workspace_size(c->batch, a->T, a->q_heads, c->kv_heads, c->head_dim, a->max_q, a->max_kv, c->dtype);
+    if (need && (!a->workspace || a->workspace_bytes < need)) return MNB_ERR_NO_MEM;
+    if (a->workspace && !dec::aligned_to(a->workspace, 256)) return MNB_ERR_INVALID_ARG;
+
+    attn::AttnParams p{};
+    p.status = device_status_word();
+    if (!p.status) return dec::status_of(cudaErrorUnknown);
+    p.q = a->q;
+    p.o = a->o;
+    p.lse = a->lse;
+    p.k = c->k_pages;
+    p.v = c->v_pages;
+    p.tables = c->tables;
+    p.kv_lens = c->kv_lens;
+    p.q_start = a->q_start;
+    p.T = a->T;
+    p.table_stride = c->table_stride;
+    p.q_ts = a->q_token_stride;
+    p.q_hs = a->q_head_stride;
+    p.o_ts = a->o_token_stride;
+    p.o_hs = a->o_head_stride;
+    p.page_stride = c->page_stride;
+    p.token_stride = c->token_stride;
+    p.head_stride = c->head_stride;
+    p.batch = (int)c->batch;
+    p.q_heads = (int)a->q_heads;
+    p.kv_heads = c->kv_heads;
+    p.group = (int)(a->q_heads / c->kv_heads);
+    p.D = c->head_dim;
+    while ((1 << p.page_shift) < c->page_size) ++p.page_shift;
+    p.num_pages = (int)c->num_pages;
+    p.max_q = (int)a->max_q;
+    p.max_kv = (int)a->max_kv;
+    p.window = (int)a->window;
+    p.causal = a->causal;
+    p.scale = a->scale;
+    p.scale_log2 = a->scale * attn::kLog2e;
+    p.workspace = a->workspace;
+    p.dtype = c->dtype;
+    wait_limits(&p.wait_limit, &p.wait_hint_ns);
+    if (inject_launch_failure()) return MNB_ERR_CUDA;
+    ProfileScope prof("mnb_paged_attention", (cudaStream_t)a->stream);
+    const cudaError_t e = attn::launch_generic(p, (cudaStream_t)a->stream);
+    if (e == cudaSuccess) prof.done("attn_generic");
+    return dec::status_of(e);
+}
+
+}  // extern "C"

@@ -1,0 +1,45 @@
+// Attention of new tokens over a paged cache: what its kernels share.
+#pragma once
+
+#include "decoder.h"
+
+namespace mnb {
+namespace attn {
+
+struct AttnParams {
+    const void* q;
+    void* o;
+    float* lse;
+    const void* k;
+    const void* v;
+    const int32_t* tables;
+    const int32_t* kv_lens;
+    const int32_t* q_start;
+    int64_t T, table_stride;
+    int64_t q_ts, q_hs, o_ts, o_hs;                  // elements
+    int64_t page_stride, token_stride, head_stride;  // elements
+    int batch, q_heads, kv_heads, group;             // group = q_heads / kv_heads
+    int D, page_shift, num_pages;
+    int max_q, max_kv;
+    int window, causal;                              // window 0: none
+    float scale, scale_log2;                         // scale, scale * log2(e)
+    int* status;
+    void* workspace;
+    uint32_t wait_limit, wait_hint_ns;
+    int dtype;
+};
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// Keys [lo, hi) that some row of the new tokens [i0, i1) of a sequence sees
+// (n new tokens, len keys); hi <= lo: none.
+__host__ __device__ inline void visible_range(const AttnParams& p, int n, int len, int i0, int i1, int* lo, int* hi) {
+    const int first = len - n + i0, last = len - n + i1 - 1;  // positions of the first and last row
+    *hi = p.causal ? (last + 1 < len ? last + 1 : len) : len;
+    *lo = p.window > 0 && first - p.window + 1 > 0 ? first - p.window + 1 : 0;
+}
+
+cudaError_t launch_generic(const AttnParams& p, cudaStream_t s);
+
+}  // namespace attn
+}  // namespace mnb

@@ -1,0 +1,128 @@
+// Paged attention on CUDA cores: any type (f32 above all), any head_dim that
+// is a multiple of 8 up to 256.
+//
+// One CTA of 8 warps per (token, query head).  Each warp walks every eighth
+// block of 32 keys with an online softmax: a lane scores one key (its whole
+// row against the query in shared memory), the warp takes the block's maximum
+// and sum with shuffles, then the lanes turn to the depths and add p_j V[j].
+// The 8 partial (m, l, O) are joined at the end in a fixed order.
+#include <cmath>
+
+#include "attention.h"
+
+namespace mnb {
+namespace attn {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kMaxD = 256;
+constexpr int kPer = kMaxD / 32;  // depths a lane owns
+
+template <int DT>
+__device__ __forceinline__ float at(const void* p, int64_t i) {
+    if constexpr (DT == kF32) return static_cast<const float*>(p)[i];
+    else if constexpr (DT == kF16) return __half2float(static_cast<const __half*>(p)[i]);
+    else return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kWarps * 32) attn_generic_kernel(const AttnParams p) {
+    __shared__ float qs[kMaxD];
+    __shared__ float os[kWarps][kMaxD];
+    __shared__ float ms[kWarps], ls[kWarps];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t t = blockIdx.x / (unsigned)p.q_heads;
+    const int h = (int)(blockIdx.x % (unsigned)p.q_heads), hk = h / p.group;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (t >= p.q_start[p.batch]) return;
+    const int b = dec::sequence_of(p.q_start, p.batch, t);
+    const int n = p.q_start[b + 1] - p.q_start[b], len = p.kv_lens[b];
+    if (n > p.max_q || len > p.max_kv || len < 0) {
+        if (threadIdx.x == 0) set_status(p.status, MNB_ERR_INVALID_ARG);
+        return;
+    }
+    const int i = (int)(t - p.q_start[b]);
+    int lo, hi;
+    visible_range(p, n, len, i, i + 1, &lo, &hi);
+    for (int d = threadIdx.x; d < p.D; d += kWarps * 32) qs[d] = at<DT>(p.q, t * p.q_ts + h * p.q_hs + d) * p.scale;
+    __syncthreads();
+
+    float m = -INFINITY, l = 0.f, o[kPer] = {};
+    const int ps = 1 << p.page_shift;
+    for (int j0 = lo + warp * 32; j0 < hi; j0 += kWarps * 32) {
+        const int j = j0 + lane;
+        int64_t row = -1;
+        float s = -INFINITY;
+        if (j < hi) {
+            const int col = j >> p.page_shift;
+            const int page = col < p.table_stride ? p.tables[(int64_t)b * p.table_stride + col] : -1;
+            s = 0.f;
+            if ((unsigned)page < (unsigned)p.num_pages) {
+                row = page * p.page_stride + (j & (ps - 1)) * p.token_stride + hk * p.head_stride;
+                for (int d = 0; d < p.D; ++d) s = fmaf(qs[d], at<DT>(p.k, row + d), s);
+            } else {
+                set_status(p.status, MNB_ERR_INVALID_ARG);
+            }
+        }
+        float top = s;
+#pragma unroll
+        for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, x));
+        const float mn = fmaxf(m, top);
+        const float base = mn == -INFINITY ? 0.f : mn;  // every score of the block may be -inf
+        const float scale = expf(m - base), e = expf(s - base);
+        float sum = e;
+#pragma unroll
+        for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(~0u, sum, x);
+        l = l * scale + sum;
+        m = mn;
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) o[c] *= scale;
+        const int cnt = min(32, hi - j0);
+        for (int k = 0; k < cnt; ++k) {
+            const int64_t r = __shfl_sync(~0u, row, k);
+            const float w = __shfl_sync(~0u, e, k);
+            if (r < 0) continue;
+#pragma unroll
+            for (int c = 0; c < kPer; ++c) {
+                const int d = c * 32 + lane;
+                if (d < p.D) o[c] = fmaf(w, at<DT>(p.v, r + d), o[c]);
+            }
+        }
+    }
+    if (lane == 0) {
+        ms[warp] = m;
+        ls[warp] = l;
+    }
+#pragma unroll
+    for (int c = 0; c < kPer; ++c)
+        if (c * 32 + lane < p.D) os[warp][c * 32 + lane] = o[c];
+    __syncthreads();
+    float top = -INFINITY;
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ms[w]);
+    const float base = top == -INFINITY ? 0.f : top;
+    float total = 0.f;
+    for (int w = 0; w < kWarps; ++w) total += ls[w] * expf(ms[w] - base);
+    for (int d = threadIdx.x; d < p.D; d += kWarps * 32) {
+        float a = 0.f;
+        for (int w = 0; w < kWarps; ++w) a = fmaf(os[w][d], expf(ms[w] - base), a);
+        store_f32(p.o, t * p.o_ts + h * p.o_hs + d, hi > lo ? a / total : 0.f, DT);
+    }
+    if (threadIdx.x == 0 && p.lse) p.lse[t * p.q_heads + h] = hi > lo ? top + logf(total) : -INFINITY;
+}
+
+}  // namespace
+
+cudaError_t launch_generic(const AttnParams& p, cudaStream_t s) {
+    const int64_t blocks = p.T * p.q_heads;
+    if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    const dim3 grid((unsigned)blocks), block(kWarps * 32);
+    switch (p.dtype) {
+        case kF32: return dec::launch_pdl(attn_generic_kernel<kF32>, grid, block, 0, s, 1, p);
+        case kF16: return dec::launch_pdl(attn_generic_kernel<kF16>, grid, block, 0, s, 1, p);
+        default: return dec::launch_pdl(attn_generic_kernel<kBF16>, grid, block, 0, s, 1, p);
+    }
+}
+
+}  // namespace attn
+}  // namespace mnb

@@ -381,6 +381,244 @@ MNB_API mnb_status mnb_matmul_fp_ex(const void* x, const void* packed, const voi
                             void* y, int64_t M, int64_t N, int64_t K, mnb_wformat format,
                             mnb_dtype act_dtype, mnb_dtype out_dtype, mnb_stream_t stream, int flags);
 
+/* ---- between the weight products: positions, cache, attention -----------
+ * What a decoder layer runs between its QKV product and its output product:
+ * rotary positions, a paged cache of keys and values, attention of the new
+ * tokens over it, and the management of the cache's pages.  The operator names
+ * and the cos / sin table inputs are those of ONNX Runtime's
+ * com.microsoft::RotaryEmbedding contrib operator; no page of the reference
+ * has a kernel for them.
+ *
+ * These calls use programmatic dependent launch on their own: each kernel
+ * waits for the preceding kernel on the stream before it touches memory, so
+ * nothing is required of the caller.  Sizes that live on the device (lengths,
+ * page numbers, positions) are checked by the kernels: an invalid one sets
+ * MNB_ERR_INVALID_ARG in the device status word, and the access is skipped. */
+
+/* The paged cache of one layer, as rotary and attention see it.
+ *   k_pages, v_pages  device, 16-byte aligned, num_pages pages of page_size
+ *                     tokens x kv_heads heads x head_dim values of dtype.
+ *                     Value (page, token, head, i) sits at page * page_stride +
+ *                     token * token_stride + head * head_stride + i (elements;
+ *                     the same strides for both, each a multiple of 16 bytes):
+ *                     pages of [heads][tokens][dim] and [tokens][heads][dim]
+ *                     are both such layouts.
+ *   tables            device int32 [batch, table_stride]: page of tokens
+ *                     i * page_size .. of a sequence
+ *   kv_lens           device int32 [batch]: tokens held by each sequence, the
+ *                     new ones of this step included
+ *   page_size         a power of two, 8 .. 1024
+ * Entries of tables at or past ceil(kv_len / page_size) are not read, and
+ * cached rows past kv_len never reach a result, whatever they hold. */
+typedef struct mnb_kv_cache {
+    void* k_pages;
+    void* v_pages;
+    const int32_t* tables;
+    const int32_t* kv_lens;
+    int64_t batch, table_stride, num_pages;
+    int64_t page_stride, token_stride, head_stride;
+    int page_size, kv_heads, head_dim;
+    mnb_dtype dtype;
+} mnb_kv_cache;
+
+/* How a rotary table stretches to contexts longer than the trained ones.  With
+ * f_i = base^(-2i / rot_dim), s = factor, L = trained_len:
+ *   NONE      f_i
+ *   LINEAR    f_i / s
+ *   NTK       (base * s^(rot_dim / (rot_dim - 2)))^(-2i / rot_dim), rot_dim > 2
+ *   BY_PARTS  g f_i + (1 - g) f_i / s with g = clamp((L f_i / 2 pi - low) / (high - low), 0, 1):
+ *             depths that turn more than `high` times over L keep their
+ *             frequency, those below `low` turns are interpolated (the
+ *             by-parts interpolation of the YaRN paper; low 1, high 32 there) */
+typedef enum mnb_rope_scaling {
+    MNB_ROPE_NONE = 0,
+    MNB_ROPE_LINEAR = 1,
+    MNB_ROPE_NTK = 2,
+    MNB_ROPE_BY_PARTS = 3
+} mnb_rope_scaling;
+
+/* Fill cos_table and sin_table (device f32 [n_pos, rot_dim / 2], 4-byte
+ * aligned) with attn_factor * cos and attn_factor * sin of position * f_i,
+ * evaluated in f64 and rounded once.  rot_dim even; factor > 0; trained_len,
+ * low and high (low < high) are read by BY_PARTS only. */
+MNB_API mnb_status mnb_rotary_table(float* cos_table, float* sin_table, int64_t n_pos, int64_t rot_dim, double base,
+                            mnb_rope_scaling scaling, double factor, double trained_len, double low, double high,
+                            double attn_factor, mnb_stream_t stream);
+
+/* Flags of the rotary calls.  Without INTERLEAVED, depth i pairs with
+ * i + rot_dim / 2; with it, 2i with 2i + 1.  INVERSE turns the other way: the
+ * transpose of the rotation, that is its gradient with respect to x. */
+#define MNB_ROTARY_INTERLEAVED 1
+#define MNB_ROTARY_INVERSE 2
+
+/* Y[t, h, :] = X[t, h, :] with its first rot_dim depths turned by the table
+ * row of positions[t]:  (a, b) -> (a c - b s, b c + a s); depths from rot_dim
+ * on are copied.  The products are formed and added in f32, the result is
+ * rounded once to dtype.
+ *   x, y       device [T, H, D] of dtype with the given token and head strides
+ *              (elements, >= 0), aligned to the element; y == x with equal
+ *              strides turns in place, any other overlap is undefined
+ *   positions  device int32 [T]; a value outside [0, n_pos) sets the status
+ *              word and leaves the token's rows of y unwritten
+ *   cos_table, sin_table  device f32 [n_pos, rot_dim / 2]
+ * 16-byte accesses where every base, stride and half allows them, narrower
+ * ones otherwise.  T == 0 is a no-op. */
+MNB_API mnb_status mnb_rotary(const void* x, void* y, const int32_t* positions, const float* cos_table,
+                      const float* sin_table, int64_t T, int64_t H, int64_t D, int64_t rot_dim, int64_t n_pos,
+                      int64_t x_token_stride, int64_t x_head_stride, int64_t y_token_stride, int64_t y_head_stride,
+                      mnb_dtype dtype, int flags, mnb_stream_t stream);
+
+/* Rotary positions of a step's queries and keys with the append of its keys
+ * and values to the cache, in one launch.
+ *   q, q_out   device [T, q_heads, D]: turned queries (q_out == q in place);
+ *              q == NULL appends only
+ *   k, v       device [T, kv_heads, D]: k is turned, v copied, into row
+ *              pos % page_size of page tables[b][pos / page_size]
+ *   q_start    device int32 [batch + 1], ascending from 0: sequence b owns
+ *              tokens q_start[b] .. q_start[b + 1] - 1 of the call, the last
+ *              ones of its kv_lens[b].  Tokens from q_start[batch] on (padding
+ *              of a captured graph) are left alone.
+ *   positions  device int32 [T] or NULL: positions for the table; NULL takes
+ *              the token's place in its sequence
+ * A token whose place, position or page is out of range sets the status word
+ * and is skipped.  Pages that two appending sequences share are the caller's
+ * to separate first (mnb_cache_resize does). */
+typedef struct mnb_rotary_args {
+    const void* q;
+    void* q_out;
+    const void* k;
+    const void* v;
+    const float* cos_table;
+    const float* sin_table;
+    const int32_t* q_start;
+    const int32_t* positions;
+    int64_t T, q_heads, rot_dim, n_pos;
+    int64_t q_token_stride, q_head_stride, q_out_token_stride, q_out_head_stride;
+    int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+    int flags; /* MNB_ROTARY_* */
+    mnb_stream_t stream;
+} mnb_rotary_args;
+
+MNB_API mnb_status mnb_rotary_append(const mnb_rotary_args* args, const mnb_kv_cache* cache);
+
+/* Attention of the new tokens of a step over the paged cache.  Token i (of n)
+ * of sequence b stands at pos = kv_lens[b] - n + i and sees the keys
+ * j <= pos (causal; every j < kv_lens[b] otherwise) with j > pos - window
+ * (window 0: no lower limit).  Query head h reads key head
+ * h / (q_heads / kv_heads):
+ *     O[t, h, :] = sum_j p_j V[j, :] / sum_j p_j,   p_j = exp(scale * Q[t, h, :] . K[j, :])
+ *     lse[t, h]  = ln sum_j p_j
+ * A row that sees no key (kv_len 0, or pos < 0) is O = 0, lse = -inf.  Scores,
+ * maxima, sums and O are held in f32; the bf16 / f16 kernels round p_j to that
+ * type for the product with V, as its operand.
+ *   q, o       device [T, q_heads, head_dim] of the cache's dtype, 16-byte
+ *              aligned, strides in elements, multiples of 16 bytes
+ *   lse        device f32 [T, q_heads] or NULL
+ *   q_start    device int32 [batch + 1], as for mnb_rotary_append; o and lse
+ *              of tokens from q_start[batch] on are left alone
+ *   max_q, max_kv  upper bounds of the sequences' new tokens and of kv_lens;
+ *              they size the launch.  A sequence that exceeds one sets the
+ *              status word (its rows are unspecified).
+ *   head_dim   a multiple of 8, at most 256; q_heads a multiple of kv_heads;
+ *              scale finite
+ *   workspace  device, 256-byte aligned, mnb_attention_workspace_size() bytes
+ *              of the same sizes, for the partial results of a split context;
+ *              its contents need no preparation
+ * A page number outside [0, num_pages) sets the status word; its keys count as
+ * zeros.  NaN or infinities in visible values of the cache reach every row of
+ * their sequence that the same tile of keys covers. */
+typedef struct mnb_attention_args {
+    const void* q;
+    void* o;
+    float* lse;
+    const int32_t* q_start;
+    int64_t T, q_heads, max_q, max_kv, window;
+    int64_t q_token_stride, q_head_stride, o_token_stride, o_head_stride;
+    float scale;
+    int causal; /* 0 or 1 */
+    void* workspace;
+    size_t workspace_bytes;
+    mnb_stream_t stream;
+} mnb_attention_args;
+
+MNB_API mnb_status mnb_paged_attention(const mnb_attention_args* args, const mnb_kv_cache* cache);
+
+/* Workspace bytes of mnb_paged_attention for a call of these sizes (0 if they
+ * are invalid or none is needed). */
+MNB_API size_t mnb_attention_workspace_size(int64_t batch, int64_t T, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                                    int64_t max_q, int64_t max_kv, mnb_dtype dtype);
+
+/* Pages as bytes: num_planes planes (for instance the keys and the values of
+ * every layer) of num_pages pages each; page p of plane l starts at base +
+ * l * plane_stride + p * page_stride (bytes; base, strides and page_bytes
+ * multiples of 16, page_stride >= page_bytes). */
+typedef struct mnb_page_planes {
+    void* base;
+    int64_t num_planes, plane_stride, page_stride, page_bytes, num_pages;
+} mnb_page_planes;
+
+/* Which sequence holds which page.  All device int32, 4-byte aligned.
+ *   refs    [num_pages]: sequences that hold the page; 0: the page is free
+ *   tables  [num_seqs, table_stride]: pages of each sequence in order; entries
+ *           past its last page are -1 after a call that writes the row
+ *   lens    [num_seqs]: tokens of each sequence; it holds
+ *           ceil(len / page_size) pages
+ * Every call is one parallel step: it reads the state before it, and its
+ * result does not depend on any order of execution.  A call whose list is
+ * invalid (an index out of range, a destination named twice, a length that
+ * needs more than table_stride pages) sets MNB_ERR_INVALID_ARG in the device
+ * status word and changes nothing. */
+typedef struct mnb_cache_state {
+    int32_t* refs;
+    int32_t* tables;
+    int32_t* lens;
+    int64_t num_pages, num_seqs, table_stride;
+    int page_size; /* tokens per page, > 0 */
+} mnb_cache_state;
+
+/* Workspace bytes of the mnb_cache_* calls (256-byte aligned device memory;
+ * its contents need no preparation), or 0 if the sizes are invalid
+ * (num_pages below 2^30, num_seqs * (table_stride + 1) and table_stride *
+ * page_size below 2^31, num_seqs at most 262144). */
+MNB_API size_t mnb_cache_workspace_size(int64_t num_pages, int64_t num_seqs, int64_t table_stride);
+
+/* Copy page src[i] to page dst[i] in every plane, i < n (device int32 lists).
+ * No page may be both a source and a destination, and destinations are
+ * distinct.  A pair with an index outside [0, num_pages) is skipped and sets
+ * the status word. */
+MNB_API mnb_status mnb_pages_copy(const mnb_page_planes* planes, const int32_t* src, const int32_t* dst, int64_t n,
+                          mnb_stream_t stream);
+
+/* Sequence dst[i] becomes a fork of sequence src[i], i < n <= num_seqs, as of
+ * before the call (a parallel assignment: beams may swap).  Its former pages
+ * are released, and it shares the source's pages, the partly filled last one
+ * too; nothing is copied until one of them grows (mnb_cache_resize). */
+MNB_API mnb_status mnb_cache_fork(const mnb_cache_state* state, const int32_t* src, const int32_t* dst, int64_t n,
+                          void* workspace, size_t workspace_bytes, mnb_stream_t stream);
+
+/* Sequence seqs[i] gets length new_lens[i], i < n <= num_seqs.
+ *   shorter: pages past the new end are released (0 frees the sequence)
+ *   longer:  pages are taken from the free ones, lowest number first, in the
+ *            order of the list; a sequence whose partly filled last page is
+ *            shared first gets a copy of its own of that page, over all planes
+ * Pages released by the call are free from the next call on.  If the free
+ * pages do not suffice, MNB_ERR_NO_MEM is set in the device status word and
+ * nothing changes.  planes may be NULL when no partly filled page is shared
+ * (such a page then sets MNB_ERR_INVALID_ARG, and nothing changes). */
+MNB_API mnb_status mnb_cache_resize(const mnb_cache_state* state, const mnb_page_planes* planes, const int32_t* seqs,
+                            const int32_t* new_lens, int64_t n, void* workspace, size_t workspace_bytes,
+                            mnb_stream_t stream);
+
+/* Press the held pages together: with L held pages, those numbered L and up
+ * move, in ascending order, to the free numbers below L, in ascending order.
+ *   refs_out, tables_out  state->refs and ->tables with the pages renamed
+ *            (they may be the same arrays; entries past a sequence's pages are
+ *            copied as they are)
+ *   counts   device int32 [2]: L, and the pages moved */
+MNB_API mnb_status mnb_cache_compact(const mnb_cache_state* state, const mnb_page_planes* planes, int32_t* refs_out,
+                             int32_t* tables_out, int32_t* counts, void* workspace, size_t workspace_bytes,
+                             mnb_stream_t stream);
+
 /* ---- diagnostics ------------------------------------------------------- */
 
 /* Environment overrides, read at each call (none changes a result beyond
