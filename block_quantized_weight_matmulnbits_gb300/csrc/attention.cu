@@ -9,8 +9,12 @@ extern "C" {
 
 size_t mnb_attention_workspace_size(int64_t batch, int64_t T, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
                                     int64_t max_q, int64_t max_kv, mnb_dtype dtype) {
-    (void)batch; (void)T; (void)q_heads; (void)kv_heads; (void)head_dim; (void)max_q; (void)max_kv; (void)dtype;
-    return 0;
+    const int64_t i31 = int64_t(1) << 31;
+    if (batch < 1 || T < 0 || q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0 || head_dim < 8 || head_dim % 8 != 0 ||
+        head_dim > 256 || max_q < 1 || max_kv < 0 || batch >= i31 || T >= i31 || max_q >= i31 || max_kv >= i31)
+        return 0;
+    if (dtype != MNB_F16 && dtype != MNB_BF16) return 0;
+    return (attn::mma_workspace_bytes((int)head_dim) + 255) & ~size_t(255);
 }
 
 mnb_status mnb_paged_attention(const mnb_attention_args* a, const mnb_kv_cache* c) {
@@ -70,8 +74,9 @@ mnb_status mnb_paged_attention(const mnb_attention_args* a, const mnb_kv_cache* 
     wait_limits(&p.wait_limit, &p.wait_hint_ns);
     if (inject_launch_failure()) return MNB_ERR_CUDA;
     ProfileScope prof("mnb_paged_attention", (cudaStream_t)a->stream);
-    const cudaError_t e = attn::launch_generic(p, (cudaStream_t)a->stream);
-    if (e == cudaSuccess) prof.done("attn_generic");
+    const bool f32 = c->dtype == MNB_F32;
+    const cudaError_t e = f32 ? attn::launch_generic(p, (cudaStream_t)a->stream) : attn::launch_mma(p, (cudaStream_t)a->stream);
+    if (e == cudaSuccess) prof.done(f32 ? "attn_generic" : "attn_mma");
     return dec::status_of(e);
 }
 

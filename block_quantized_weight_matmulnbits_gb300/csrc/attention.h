@@ -39,6 +39,10 @@ __host__ __device__ inline void visible_range(const AttnParams& p, int n, int le
     *lo = p.window > 0 && first - p.window + 1 > 0 ? first - p.window + 1 : 0;
 }
 
+// Few rows a key head, bf16 / f16 (attn_mma.cuh); its workspace.
+cudaError_t launch_mma(const AttnParams& p, cudaStream_t s);
+size_t mma_workspace_bytes(int D);
+// Any type, CUDA cores (attn_generic.cu).
 cudaError_t launch_generic(const AttnParams& p, cudaStream_t s);
 
 }  // namespace attn

@@ -117,11 +117,7 @@ cudaError_t launch_generic(const AttnParams& p, cudaStream_t s) {
     const int64_t blocks = p.T * p.q_heads;
     if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     const dim3 grid((unsigned)blocks), block(kWarps * 32);
-    switch (p.dtype) {
-        case kF32: return dec::launch_pdl(attn_generic_kernel<kF32>, grid, block, 0, s, 1, p);
-        case kF16: return dec::launch_pdl(attn_generic_kernel<kF16>, grid, block, 0, s, 1, p);
-        default: return dec::launch_pdl(attn_generic_kernel<kBF16>, grid, block, 0, s, 1, p);
-    }
+    return dec::launch_pdl(attn_generic_kernel<kF32>, grid, block, 0, s, 1, p);
 }
 
 }  // namespace attn

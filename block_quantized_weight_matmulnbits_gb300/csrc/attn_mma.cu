@@ -1,0 +1,53 @@
+// Host side of the few-row attention kernel: grid, workspace and launches.
+#include "attn_mma.cuh"
+
+namespace mnb {
+namespace attn {
+namespace {
+
+// The grid of the first kernel is fixed (two CTAs on each of 152 SMs, one
+// for head_dim above 128), so the workspace does not depend on the device.
+constexpr int ctas_of(int dp) { return dp == 256 ? 152 : 304; }
+
+template <int DT, int DP>
+cudaError_t launch_as(const AttnParams& p, cudaStream_t s) {
+    using S = mma::Shape<DP>;
+    SplitParams sp{};
+    sp.ctas = ctas_of(DP);
+    sp.whole_tiles = 16;
+    sp.min_tiles = 4;
+    sp.part_o = static_cast<float*>(p.workspace);
+    sp.part_ml = reinterpret_cast<float2*>(sp.part_o + (size_t)sp.ctas * 2 * mma::kRows * DP);
+    auto kern = mma::attn_mma_kernel<DT, DP>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e != cudaSuccess) return e;
+    e = dec::launch_pdl(kern, dim3(sp.ctas), dim3(mma::kThreads), S::kSmem, s, 1, p, sp);
+    if (e != cudaSuccess) return e;
+    // No unit is cut when the bounds already say that each is short and has a CTA.
+    const int64_t units = (int64_t)p.kv_heads * (p.T * p.group / mma::kRows + p.batch);
+    const int64_t keys = p.window > 0 && (int64_t)p.window + p.max_q < p.max_kv ? (int64_t)p.window + p.max_q : p.max_kv;
+    if (units <= sp.ctas && keys / mma::kKeys + 2 <= sp.whole_tiles) return cudaSuccess;
+    auto join = attn_join_kernel<DT, DP, mma::kRows, mma::kKeys>;
+    return dec::launch_pdl(join, dim3(sp.ctas, mma::kRows / 4), dim3(128), 0, s, 1, p, sp);
+}
+
+template <int DT>
+cudaError_t launch_dt(const AttnParams& p, cudaStream_t s) {
+    if (p.D <= 64) return launch_as<DT, 64>(p, s);
+    if (p.D <= 128) return launch_as<DT, 128>(p, s);
+    return launch_as<DT, 256>(p, s);
+}
+
+}  // namespace
+
+size_t mma_workspace_bytes(int D) {
+    const int dp = D <= 64 ? 64 : D <= 128 ? 128 : 256;
+    return (size_t)ctas_of(dp) * 2 * mma::kRows * (dp + 2) * 4;
+}
+
+cudaError_t launch_mma(const AttnParams& p, cudaStream_t s) {
+    return p.dtype == kF16 ? launch_dt<kF16>(p, s) : launch_dt<kBF16>(p, s);
+}
+
+}  // namespace attn
+}  // namespace mnb

@@ -1,0 +1,356 @@
+// Paged attention for few rows (decode, and any head_dim up to 256) in bf16 /
+// f16: warp-level MMA with the context divided evenly over the GPU.
+//
+// One query row of a key head does 4 D flops for the 4 D bytes of a key and
+// its value, and a group of up to 16 heads shares them, so the bound is the
+// bytes of the cache and everything here serves to keep its loads in flight.
+//   - A row tile is the 16 rows of one m16n8k16 MMA: new tokens x the query
+//     heads of one key head, so a cached value is read once for the group.
+//   - Each of a CTA's 4 warps walks its own 16 keys of every 64-key tile with
+//     its own ring of cp.async stages, its own online softmax and its own O
+//     accumulator: no barrier inside the walk.  The four (m, l, O) are joined
+//     through shared memory when the CTA leaves a unit.
+//   - 2 CTAs per SM with 3 stages of 8 KB a warp (D = 128) hold 128 KB of loads
+//     in flight per SM while a third of the ring is computed on.
+//   - Page numbers are read one stage ahead of the loads that need them.
+// The maximum a row is scaled by follows the true one only when it falls more
+// than 8 (log2) behind, so O is rarely rescaled; p then stays below 2^8, exact
+// in the f32 sums and rounded once to the MMA's type for the product with V.
+#pragma once
+
+#include "attn_split.cuh"
+
+namespace mnb {
+namespace attn {
+namespace mma {
+
+constexpr int kWarps = 4, kThreads = kWarps * 32;
+constexpr int kRows = 16, kKeys = kWarps * 16;
+
+template <int DP> struct Shape {
+    static constexpr int kStages = DP == 64 ? 6 : 3;
+    static constexpr int kCtasPerSm = DP == 256 ? 1 : 2;
+    static constexpr int kHalf = 16 * DP * 2;              // K or V of a stage, bytes
+    static constexpr int kStage = 2 * kHalf;
+    static constexpr int kRing = kStages * kStage;         // of one warp
+    static constexpr int kSmem = kWarps * kRing + kRows * DP * 2 + kWarps * kRows * 8;
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+template <int DT>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (DT == kBF16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <int DT>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+    uint32_t d;
+    if constexpr (DT == kBF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 16-byte chunk c of row r in a [rows][DP] 16-bit tile: the chunk index is
+// xored with the row so that eight rows' equal chunks lie in eight banks groups.
+template <int DP>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) { return (uint32_t)(r * DP * 2 + ((c ^ (r & 7)) << 4)); }
+
+template <int DT, int DP>
+__global__ void __launch_bounds__(kThreads, Shape<DP>::kCtasPerSm) attn_mma_kernel(const AttnParams p, const SplitParams sp) {
+    using S = Shape<DP>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint8_t* qs = smem + kWarps * S::kRing;
+    float2* ml_s = reinterpret_cast<float2*>(qs + kRows * DP * 2);
+    float* o_s = reinterpret_cast<float*>(smem);  // [warp][row][DP], once the rings are drained
+    static_assert(kWarps * kRows * DP * 4 <= kWarps * S::kRing, "the partial results fit in the rings");
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    griddep_wait();
+    griddep_launch_dependents();
+    const Division dv = divide<kRows, kKeys, kThreads>(p, sp, blockIdx.x == 0);
+    const int64_t x0 = dv.begin(blockIdx.x), x1 = dv.begin((int64_t)blockIdx.x + 1);
+    if (x0 >= x1) return;
+    Place pl = locate<kRows, kKeys, kThreads>(p, dv, x0);
+
+    const uint32_t ring = smem_u32(smem) + warp * S::kRing, qa = smem_u32(qs);
+    const uint16_t* kp = static_cast<const uint16_t*>(p.k);
+    const uint16_t* vp = static_cast<const uint16_t*>(p.v);
+    const int ps_mask = (1 << p.page_shift) - 1;
+    constexpr int kChunks = DP / 8;              // 16-byte chunks of a row
+    constexpr int kLanes = kChunks < 32 ? kChunks : 32;
+    constexpr int kRpi = 32 / kLanes;            // rows a warp-wide copy covers
+    const int lrow = lane / kLanes, lchunk = lane % kLanes;
+    const bool col_ok = lchunk * 8 < p.D;
+
+    for (int64_t x = x0;;) {
+        const int rt = pl.unit / p.kv_heads, hk = pl.unit - rt * p.kv_heads;
+        const int t0 = pl.tile;
+        const int64_t left = x1 - x;
+        const int t1 = dv.whole ? pl.s.tiles : (int)(left < pl.s.tiles - t0 ? t0 + left : pl.s.tiles);
+        const int rows = pl.s.n * p.group - rt * kRows < kRows ? pl.s.n * p.group - rt * kRows : kRows;
+        const int64_t tok0 = p.q_start[pl.b];
+        const int i0 = rt * kRows / p.group, i1 = (rt * kRows + rows - 1) / p.group + 1;
+        int lo, hi;  // keys that a row of the tile sees
+        visible_range(p, pl.s.n, pl.s.len, i0, i1, &lo, &hi);
+        const int32_t* table = p.tables + (int64_t)pl.b * p.table_stride;
+        const int key_w = pl.s.lo + warp * 16;
+        const int64_t head_off = (int64_t)hk * p.head_stride;
+
+        // page numbers of the 16 keys from key0 on: rows 0-7 in lane 0, 8-15 in lane 1 (and so on)
+        auto pages_at = [&](int t) -> int {
+            const int key = key_w + t * kKeys + (lane & 1) * 8;
+            if (t >= t1 || key >= hi || key + 8 <= lo) return -1;
+            const int col = key >> p.page_shift;
+            int page = col < p.table_stride ? __ldg(table + col) : -1;
+            if ((unsigned)page >= (unsigned)p.num_pages) {
+                set_status(p.status, MNB_ERR_INVALID_ARG);
+                page = -1;
+            }
+            return page;
+        };
+        auto load = [&](int t, int pages) {
+            const int key0 = key_w + t * kKeys;
+            if (t < t1 && key0 < hi && key0 + 16 > lo) {
+                const int pa = __shfl_sync(~0u, pages, 0), pb = __shfl_sync(~0u, pages, 1);
+                const int64_t offa = pa * p.page_stride + head_off + (key0 & ps_mask) * p.token_stride + lchunk * 8;
+                const int64_t offb = pb * p.page_stride + head_off + ((key0 + 8) & ps_mask) * p.token_stride + lchunk * 8;
+                const uint32_t dst = ring + ((t - t0) % S::kStages) * S::kStage;
+#pragma unroll
+                for (int i = 0; i < 16 / kRpi; ++i) {
+                    const int r = i * kRpi + lrow;
+                    const bool b = r >= 8;
+                    const bool ok = (b ? pb : pa) >= 0 && key0 + r < hi && col_ok;
+                    const int64_t off = ok ? (b ? offb : offa) + (r & 7) * p.token_stride : 0;
+                    const uint32_t to = dst + chunk_at<DP>(r, lchunk);
+                    cp16(to, kp + off, ok);
+                    cp16(to + S::kHalf, vp + off, ok);
+                }
+            }
+            cp_commit();
+        };
+
+        int pg = pages_at(t0);
+#pragma unroll
+        for (int s = 0; s < S::kStages - 1; ++s) {
+            const int nx = pages_at(t0 + s + 1);
+            load(t0 + s, pg);
+            pg = nx;
+        }
+        // the unit's rows of Q (past the last row or depth: zero)
+        for (int c = tid; c < kRows * kChunks; c += kThreads) {
+            const int r = c / kChunks, ch = c % kChunks;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (r < rows && ch * 8 < p.D) {
+                const int g = rt * kRows + r;
+                const int64_t t = tok0 + g / p.group;
+                const int h = hk * p.group + g % p.group;
+                v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + t * p.q_ts + h * p.q_hs + ch * 8);
+            }
+            *reinterpret_cast<uint4*>(qs + chunk_at<DP>(r, ch)) = v;
+        }
+        __syncthreads();
+        const int mi = lane >> 3;
+        const uint32_t q_lane = (mi & 1) * 8 + (lane & 7);
+        constexpr int KK = DP / 16;
+        constexpr bool kQRegs = DP <= 128;
+        uint32_t qf[kQRegs ? KK : 1][4];
+        if constexpr (kQRegs) {
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk) ldsm4(qf[kk], qa + chunk_at<DP>(q_lane, kk * 2 + (mi >> 1)));
+        }
+        // visible keys of this thread's rows, lane / 4 and lane / 4 + 8
+        int row_lo[2], row_hi[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int g = rt * kRows + (lane >> 2) + 8 * j;
+            visible_range(p, pl.s.n, pl.s.len, g / p.group, g / p.group + 1, &row_lo[j], &row_hi[j]);
+        }
+        // every row sees all keys of [full_lo, full_hi)
+        int full_lo, full_hi, dummy;
+        visible_range(p, pl.s.n, pl.s.len, i0, i0 + 1, &dummy, &full_hi);
+        visible_range(p, pl.s.n, pl.s.len, i1 - 1, i1, &full_lo, &dummy);
+
+        float o[DP / 8][4] = {};
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        for (int t = t0; t < t1; ++t) {
+            const int nx = pages_at(t + S::kStages);
+            load(t + S::kStages - 1, pg);
+            pg = nx;
+            cp_wait<S::kStages - 1>();
+            __syncwarp();
+            const int key0 = key_w + t * kKeys;
+            if (key0 < hi && key0 + 16 > lo) {
+                const uint32_t ka = ring + ((t - t0) % S::kStages) * S::kStage, va = ka + S::kHalf;
+                float s[2][4] = {};
+                const uint32_t k_row = (mi >> 1) * 8 + (lane & 7);
+#pragma unroll
+                for (int kk = 0; kk < KK; ++kk) {
+                    uint32_t b[4];
+                    ldsm4(b, ka + chunk_at<DP>(k_row, kk * 2 + (mi & 1)));
+                    if constexpr (kQRegs) {
+                        mma16816<DT>(s[0], qf[kk], b[0], b[1]);
+                        mma16816<DT>(s[1], qf[kk], b[2], b[3]);
+                    } else {
+                        uint32_t a[4];
+                        ldsm4(a, qa + chunk_at<DP>(q_lane, kk * 2 + (mi >> 1)));
+                        mma16816<DT>(s[0], a, b[0], b[1]);
+                        mma16816<DT>(s[1], a, b[2], b[3]);
+                    }
+                }
+                const bool edge = key0 < full_lo || key0 + 16 > full_hi;
+                float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float v = s[n][e] * p.scale_log2;
+                        const int j = e >> 1;
+                        if (edge) {
+                            const int key = key0 + n * 8 + (lane & 3) * 2 + (e & 1);
+                            if (key < row_lo[j] || key >= row_hi[j]) v = -INFINITY;
+                        }
+                        s[n][e] = v;
+                        top[j] = fmaxf(top[j], v);
+                    }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    top[j] = fmaxf(top[j], __shfl_xor_sync(~0u, top[j], 1));
+                    top[j] = fmaxf(top[j], __shfl_xor_sync(~0u, top[j], 2));
+                }
+                if (__any_sync(~0u, top[0] > m[0] + 8.f || top[1] > m[1] + 8.f)) {
+                    float f[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float mn = fmaxf(m[j], top[j]);
+                        f[j] = mn == -INFINITY ? 1.f : ex2(m[j] - mn);
+                        m[j] = mn;
+                        l[j] *= f[j];
+                    }
+#pragma unroll
+                    for (int n = 0; n < DP / 8; ++n) {
+                        o[n][0] *= f[0];
+                        o[n][1] *= f[0];
+                        o[n][2] *= f[1];
+                        o[n][3] *= f[1];
+                    }
+                }
+                const float base[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+                float e[2][4];
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        e[n][c] = ex2(s[n][c] - base[c >> 1]);
+                        l[c >> 1] += e[n][c];
+                    }
+                const uint32_t pa[4] = {pack16<DT>(e[0][0], e[0][1]), pack16<DT>(e[0][2], e[0][3]),
+                                        pack16<DT>(e[1][0], e[1][1]), pack16<DT>(e[1][2], e[1][3])};
+                const uint32_t v_row = (mi & 1) * 8 + (lane & 7);
+#pragma unroll
+                for (int n = 0; n < DP / 16; ++n) {
+                    uint32_t b[4];
+                    ldsm4t(b, va + chunk_at<DP>(v_row, n * 2 + (mi >> 1)));
+                    mma16816<DT>(o[2 * n], pa, b[0], b[1]);
+                    mma16816<DT>(o[2 * n + 1], pa, b[2], b[3]);
+                }
+            }
+            __syncwarp();  // the stage is free for the next load
+        }
+        cp_wait<0>();
+        __syncthreads();  // every warp is done with its ring: it becomes the exchange buffer
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            l[j] += __shfl_xor_sync(~0u, l[j], 1);
+            l[j] += __shfl_xor_sync(~0u, l[j], 2);
+            const int r = (lane >> 2) + 8 * j;
+            if ((lane & 3) == 0) ml_s[warp * kRows + r] = make_float2(m[j], l[j]);
+            float* row = o_s + (warp * kRows + r) * DP + (lane & 3) * 2;
+#pragma unroll
+            for (int n = 0; n < DP / 8; ++n) *reinterpret_cast<float2*>(row + ((n ^ (r & 7)) * 8)) = make_float2(o[n][2 * j], o[n][2 * j + 1]);
+        }
+        __syncthreads();
+        const bool done = dv.whole || (t0 == 0 && t1 == pl.s.tiles);
+        {
+            const int r = tid >> 3, q8 = tid & 7;  // 8 threads a row, groups of 8 columns each
+            float top = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml_s[w * kRows + r].x);
+            const float base = top == -INFINITY ? 0.f : top;
+            float wt[kWarps], sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float2 v = ml_s[w * kRows + r];
+                wt[w] = ex2(v.x - base);
+                sum = fmaf(v.y, wt[w], sum);
+            }
+            if (r < rows) {
+                const int g = rt * kRows + r;
+                const int64_t tk = tok0 + g / p.group;
+                const int h = hk * p.group + g % p.group;
+                const int slot = x == x0 ? 0 : 1;
+                const int64_t at = ((int64_t)blockIdx.x * 2 + slot) * kRows + r;
+                const float inv = sum > 0.f ? 1.f / sum : 0.f;
+                for (int c = q8; c < DP / 8; c += 8) {
+                    float a[8] = {};
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) {
+                        const float4* src = reinterpret_cast<const float4*>(o_s + (w * kRows + r) * DP + ((c ^ (r & 7)) * 8));
+                        const float4 u = src[0], v = src[1];
+                        a[0] = fmaf(u.x, wt[w], a[0]); a[1] = fmaf(u.y, wt[w], a[1]);
+                        a[2] = fmaf(u.z, wt[w], a[2]); a[3] = fmaf(u.w, wt[w], a[3]);
+                        a[4] = fmaf(v.x, wt[w], a[4]); a[5] = fmaf(v.y, wt[w], a[5]);
+                        a[6] = fmaf(v.z, wt[w], a[6]); a[7] = fmaf(v.w, wt[w], a[7]);
+                    }
+                    if (done) {
+                        if (c * 8 < p.D) {
+                            uint4 out;
+                            out.x = pack16<DT>(a[0] * inv, a[1] * inv);
+                            out.y = pack16<DT>(a[2] * inv, a[3] * inv);
+                            out.z = pack16<DT>(a[4] * inv, a[5] * inv);
+                            out.w = pack16<DT>(a[6] * inv, a[7] * inv);
+                            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + tk * p.o_ts + h * p.o_hs + c * 8) = out;
+                        }
+                    } else {
+                        float4* dst = reinterpret_cast<float4*>(sp.part_o + at * DP + c * 8);
+                        dst[0] = make_float4(a[0], a[1], a[2], a[3]);
+                        dst[1] = make_float4(a[4], a[5], a[6], a[7]);
+                    }
+                }
+                if (q8 == 0) {
+                    if (!done) sp.part_ml[at] = make_float2(top, sum);
+                    else if (p.lse) p.lse[tk * p.q_heads + h] = sum > 0.f ? (base + log2f(sum)) * kLn2 : -INFINITY;
+                }
+            }
+        }
+        x += dv.whole ? 1 : t1 - t0;
+        if (x >= x1) break;
+        __syncthreads();  // the exchange buffer becomes the rings again
+        next_unit<kRows, kKeys>(p, dv, pl);
+    }
+}
+
+}  // namespace mma
+}  // namespace attn
+}  // namespace mnb
