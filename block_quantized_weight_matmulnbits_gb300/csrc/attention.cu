@@ -14,7 +14,13 @@ size_t mnb_attention_workspace_size(int64_t batch, int64_t T, int64_t q_heads, i
         head_dim > 256 || max_q < 1 || max_kv < 0 || batch >= i31 || T >= i31 || max_q >= i31 || max_kv >= i31)
         return 0;
     if (dtype != MNB_F16 && dtype != MNB_BF16) return 0;
-    return (attn::mma_workspace_bytes((int)head_dim) + 255) & ~size_t(255);
+    // the few-row kernel also takes what the many-row one declines
+    size_t n = attn::mma_workspace_bytes((int)head_dim);
+    if (attn::tc_serves(q_heads, kv_heads, head_dim, max_q, dtype)) {
+        const size_t t = attn::tc_workspace_bytes(batch, T, q_heads, kv_heads, head_dim, max_kv);
+        n = t > n ? t : n;
+    }
+    return (n + 255) & ~size_t(255);
 }
 
 mnb_status mnb_paged_attention(const mnb_attention_args* a, const mnb_kv_cache* c) {
@@ -69,14 +75,29 @@ mnb_status mnb_paged_attention(const mnb_attention_args* a, const mnb_kv_cache* 
     p.causal = a->causal;
     p.scale = a->scale;
     p.scale_log2 = a->scale * attn::kLog2e;
+    // a masked score is -inf before it is scaled; 2^-100 leaves every finite score at 0
+    if (std::fabs(p.scale_log2) < 0x1p-100f) p.scale_log2 = 0x1p-100f;
     p.workspace = a->workspace;
     p.dtype = c->dtype;
     wait_limits(&p.wait_limit, &p.wait_hint_ns);
     if (inject_launch_failure()) return MNB_ERR_CUDA;
     ProfileScope prof("mnb_paged_attention", (cudaStream_t)a->stream);
-    const bool f32 = c->dtype == MNB_F32;
-    const cudaError_t e = f32 ? attn::launch_generic(p, (cudaStream_t)a->stream) : attn::launch_mma(p, (cudaStream_t)a->stream);
-    if (e == cudaSuccess) prof.done(f32 ? "attn_generic" : "attn_mma");
+    const cudaStream_t s = (cudaStream_t)a->stream;
+    const char* family = "attn_generic";
+    cudaError_t e = cudaErrorNotSupported;
+    if (c->dtype == MNB_F32) {
+        e = attn::launch_generic(p, s);
+    } else {
+        if (attn::tc_serves(p.q_heads, p.kv_heads, p.D, p.max_q, p.dtype)) {
+            family = "attn_tc";
+            e = attn::launch_tc(p, s);
+        }
+        if (e == cudaErrorNotSupported) {
+            family = "attn_mma";
+            e = attn::launch_mma(p, s);
+        }
+    }
+    if (e == cudaSuccess) prof.done(family);
     return dec::status_of(e);
 }
 

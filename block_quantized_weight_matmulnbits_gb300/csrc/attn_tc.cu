@@ -1,0 +1,119 @@
+// Host side of the many-row attention kernel: tensor maps, the cut of few
+// units into ranges of keys, workspace and launches.
+#include <cstring>
+
+#include "attn_tc.cuh"
+
+namespace mnb {
+namespace attn {
+namespace {
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+    static EncodeTiledFn fn = [] {
+        void* ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            return (EncodeTiledFn) nullptr;
+        }
+        return reinterpret_cast<EncodeTiledFn>(ptr);
+    }();
+    return fn;
+}
+
+struct Plan {
+    int tokens, splits;
+    int64_t units;
+};
+
+// Units and splits from the bounds of a call.  A wave of 152 CTAs takes as
+// long as its key tiles plus about four tiles' worth of prologue and epilogue;
+// the cut with the least waves * (tiles + 4) is taken, and one with as many
+// tiles again must save a tenth to be worth its partial results.
+Plan make_plan(int64_t batch, int64_t T, int64_t q_heads, int64_t kv_heads, int64_t max_kv) {
+    Plan pl;
+    const int64_t group = q_heads / kv_heads;
+    pl.tokens = (int)(tca::kRows / group);
+    pl.units = (T / (2 * pl.tokens) + (batch < T ? batch : T)) * kv_heads;
+    pl.splits = 1;
+    const int64_t tiles = (max_kv + tca::kKeys - 1) / tca::kKeys;
+    double best = 0;
+    for (int64_t s = 1; s <= 64 && s <= tiles; ++s) {
+        const int64_t waves = (pl.units * s + 151) / 152;
+        double cost = (double)waves * (double)((tiles + s - 1) / s + 4);
+        if (s > 1) cost = cost * 1.02 + (double)(pl.units * s) / 152.0;
+        if (s == 1 || cost < best) {
+            best = cost;
+            pl.splits = (int)s;
+        }
+    }
+    return pl;
+}
+
+template <int DT, int DP>
+cudaError_t launch_as(const AttnParams& p, const Plan& pl, cudaStream_t s) {
+    using S = tca::Shape<DP>;
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return cudaErrorNotSupported;
+    const CUtensorMapDataType dt = DT == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    CUtensorMap maps[3];
+    std::memset(maps, 0, sizeof(maps));
+    {
+        const cuuint64_t dims[4] = {(cuuint64_t)p.D, (cuuint64_t)p.group, (cuuint64_t)p.kv_heads, (cuuint64_t)p.T};
+        const cuuint64_t st[3] = {(cuuint64_t)p.q_hs * 2, (cuuint64_t)p.q_hs * 2 * (cuuint64_t)p.group, (cuuint64_t)p.q_ts * 2};
+        const cuuint32_t box[4] = {64, (cuuint32_t)p.group, 1, (cuuint32_t)pl.tokens};
+        if (enc(&maps[0], dt, 4, const_cast<void*>(p.q), dims, st, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorNotSupported;
+    }
+    const int page = 1 << p.page_shift, rows = page < tca::kKeys ? page : tca::kKeys;
+    for (int i = 0; i < 2; ++i) {
+        const cuuint64_t dims[4] = {(cuuint64_t)p.D, (cuuint64_t)page, (cuuint64_t)p.kv_heads, (cuuint64_t)p.num_pages};
+        const cuuint64_t st[3] = {(cuuint64_t)p.token_stride * 2, (cuuint64_t)p.head_stride * 2, (cuuint64_t)p.page_stride * 2};
+        const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1};
+        if (enc(&maps[1 + i], dt, 4, const_cast<void*>(i ? p.v : p.k), dims, st, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorNotSupported;
+    }
+    tca::TcParams tp{};
+    tp.tokens = pl.tokens;
+    tp.units = (int)pl.units;
+    tp.splits = pl.splits;
+    tp.box_rows = rows;
+    tp.part_o = static_cast<float*>(p.workspace);
+    tp.part_ml = reinterpret_cast<float2*>(tp.part_o + (size_t)pl.units * pl.splits * 256 * DP);
+    auto kern = tca::attn_tc_kernel<DT, DP>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e != cudaSuccess) return e;
+    e = dec::launch_pdl(kern, dim3((unsigned)(pl.units * pl.splits)), dim3(tca::kThreads), S::kSmem, s, 1, p, tp, maps[0], maps[1], maps[2]);
+    if (e != cudaSuccess || pl.splits == 1) return e;
+    return dec::launch_pdl(tca::attn_tc_join_kernel<DT, DP>, dim3((unsigned)(pl.units * 32)), dim3(256), 0, s, 1, p, tp);
+}
+
+}  // namespace
+
+bool tc_serves(int64_t q_heads, int64_t kv_heads, int64_t D, int64_t max_q, int dtype) {
+    const int64_t group = q_heads / kv_heads;
+    return dtype != kF32 && D <= 128 && group <= tca::kRows && max_q * group > 16;
+}
+
+size_t tc_workspace_bytes(int64_t batch, int64_t T, int64_t q_heads, int64_t kv_heads, int64_t D, int64_t max_kv) {
+    const Plan pl = make_plan(batch, T, q_heads, kv_heads, max_kv);
+    return pl.splits == 1 ? 0 : (size_t)pl.units * pl.splits * 256 * ((D <= 64 ? 64 : 128) + 2) * 4;
+}
+
+cudaError_t launch_tc(const AttnParams& p, cudaStream_t s) {
+    const Plan pl = make_plan(p.batch, p.T, p.q_heads, p.kv_heads, p.max_kv);
+    if (pl.units * pl.splits * 32 > 0x7FFFFFFF) return cudaErrorNotSupported;
+    if (p.dtype == kF16) return p.D <= 64 ? launch_as<kF16, 64>(p, pl, s) : launch_as<kF16, 128>(p, pl, s);
+    return p.D <= 64 ? launch_as<kBF16, 64>(p, pl, s) : launch_as<kBF16, 128>(p, pl, s);
+}
+
+}  // namespace attn
+}  // namespace mnb
