@@ -23,9 +23,10 @@
 // before is complete by then, because S was committed after it.
 //   warps 0-3    softmax and epilogue of row tile A
 //   warps 4-7    the same for B
-//   warp 8       TMEM, all MMAs; zeroes V rows past the visible keys, whose
-//                pages may hold anything (0 * NaN is NaN)
-//   warp 9       TMA (warps 10 and 11 complete the warpgroup)
+//   warp 8       TMEM; one thread issues all MMAs
+//   warp 9       TMA
+//   warp 10      zeroes V rows past the visible keys, whose pages may hold
+//                anything (0 * NaN is NaN); warp 11 completes the warpgroup
 // Few units (a short chunk over a long context) are cut into ranges of key
 // tiles; attn_tc_join adds their (m, l, O) in order.
 #pragma once
@@ -38,7 +39,7 @@ namespace attn {
 namespace tca {
 
 constexpr int kRows = 128, kKeys = 128;
-constexpr int kSoftWarps = 8, kMmaWarp = 8, kTmaWarp = 9, kThreads = 384;
+constexpr int kSoftWarps = 8, kMmaWarp = 8, kTmaWarp = 9, kZeroWarp = 10, kThreads = 384;
 // Registers: 384 threads start with 168 each (64512); the third warpgroup (MMA, TMA, two idle warps) gives
 // 88 of each of its threads back, the softmax warpgroups take 40 more: 256 * 208 + 128 * 80 = 63488.
 constexpr int kSoftRegs = 208, kCtlRegs = 80;
@@ -92,6 +93,20 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+// Bounded wait on an mbarrier phase: false when it ran out, or when another
+// role of the CTA gave up.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort, const AttnParams& p) {
+    if (mbar_try_wait(bar, parity)) return true;
+    for (uint32_t i = 1; i < p.wait_limit; ++i) {
+        const bool ok = p.wait_hint_ns == kWaitPoll ? mbar_test_wait(bar, parity)
+                        : p.wait_hint_ns         ? mbar_try_wait_sleep(bar, parity, p.wait_hint_ns)
+                                                 : mbar_try_wait(bar, parity);
+        if (ok) return true;
+        if (*abort) return false;
+    }
+    set_status(p.status, MNB_ERR_TIMEOUT);
+    return false;
 }
 template <int DT>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
@@ -193,10 +208,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
     uint64_t* s_full = q_full + 2;       // [2]
     uint64_t* p_ready = s_full + 2;      // [2] one arrival per softmax warp
     uint64_t* o_full = p_ready + 2;      // [2]
-    uint64_t* done = o_full + 2;
+    uint64_t* v_edge = o_full + 2;
+    uint64_t* v_zeroed = v_edge + 1;
+    uint64_t* done = v_zeroed + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
     int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
-    static_assert((2 * R + 9) * 8 + 8 <= 256, "barriers fit");
+    static_assert((2 * R + 11) * 8 + 8 <= 256, "barriers fit");
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
@@ -210,6 +227,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
             mbar_init(&p_ready[x], 4);
             mbar_init(&o_full[x], 1);
         }
+        mbar_init(v_edge, 1);
+        mbar_init(v_zeroed, 1);
         mbar_init(done, 1);
         *abort_flag = 0;
         fence_barrier_init();
@@ -226,10 +245,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
     tc::fence_after();
     const uint32_t tmem = *tmem_slot;  // S_A | S_B | O_A | O_B, 128 columns each
     volatile int* abort_v = abort_flag;
-    const uint32_t wl = p.wait_limit, wh = p.wait_hint_ns;
     const Range rg = unit_range(p, tp, u, split);
     const int steps = rg.na > rg.nb ? rg.na : rg.nb;
 
+    const int box_log = __ffs(tp.box_rows) - 1;
+    // rows [z0, z1) of key tile j hold visible keys or lie in a box that was loaded for one
+    auto zero_range = [&](int j, int* z0, int* z1) {
+        const int kb = (rg.first + j) * kKeys;
+        *z0 = rg.lo > kb ? ((rg.lo - kb) >> box_log) << box_log : 0;
+        *z1 = rg.hi - kb < kKeys ? rg.hi - kb : kKeys;
+        return *z0 > 0 || *z1 < kKeys;
+    };
     if (warp >= kSoftWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtlRegs));
         if (warp == kTmaWarp) {
@@ -237,44 +263,54 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
             if (steps > 0) {
                 const uint32_t q_bytes = (uint32_t)(tp.tokens * p.group * 128 * S::kHalves);
                 const int tok = p.q_start[u.b] + u.pair * 2 * tp.tokens;
-                auto load_q = [&](int x) {
-                    if (lane == 0) {
+                if (lane == 0) {
+                    for (int x = 0; x < 2; ++x) {
+                        if ((x ? rg.nb : rg.na) == 0) continue;
                         mbar_arrive_expect_tx(&q_full[x], q_bytes);
                         for (int h = 0; h < S::kHalves; ++h)
                             tma_load_4d(smem_u32(qs + x * S::kTile + h * kHalfBytes), &qmap, h * 64, 0, u.hk, tok + x * tp.tokens, &q_full[x]);
                     }
-                };
-                if (rg.na) load_q(0);
-                if (rg.nb) load_q(1);
-                const int32_t* table = p.tables + (int64_t)u.b * p.table_stride;
-                const int boxes = kKeys / tp.box_rows;
-                bool ok = true;
-                for (int i = 0; i < 2 * steps && ok; ++i) {  // K_0, V_0, K_1, V_1, ...
-                    const int slot = i % R;
-                    const uint32_t ph = (uint32_t)((i / R) & 1);
-                    ok = tc::wait_bounded(&kv_empty[slot], ph ^ 1u, p.status, wl, wh);
-                    if (!ok || *abort_v) break;
-                    const int kb = (rg.first + (i >> 1)) * kKeys;
-                    const int lo = rg.lo > kb ? (rg.lo - kb) / tp.box_rows : 0;
-                    const int hi = rg.hi - kb < kKeys ? (rg.hi - kb + tp.box_rows - 1) / tp.box_rows : boxes;
-                    if (lane == 0) mbar_arrive_expect_tx(&kv_full[slot], (uint32_t)((hi - lo) * tp.box_rows * 128 * S::kHalves));
-                    __syncwarp();
-                    const CUtensorMap* map = (i & 1) ? &vmap : &kmap;
-                    for (int e = lane; e < (hi - lo) * S::kHalves; e += 32) {
-                        const int box = lo + e / S::kHalves, h = e % S::kHalves;
-                        const int key = kb + box * tp.box_rows, col = key >> p.page_shift;
-                        int page = col < p.table_stride ? __ldg(table + col) : -1;
-                        if ((unsigned)page >= (unsigned)p.num_pages) {
-                            set_status(p.status, MNB_ERR_INVALID_ARG);
-                            page = p.num_pages;  // past the last page: the box is filled with zeros
-                        }
-                        tma_load_4d(smem_u32(ring + slot * S::kTile + h * kHalfBytes + box * tp.box_rows * 128), map, h * 64,
-                                    key & ((1 << p.page_shift) - 1), u.hk, page, &kv_full[slot]);
-                    }
-                    issued = i + 1;
                 }
-                if (!ok) *abort_v = 1;
-                if (*abort_v) {
+                const int32_t* table = p.tables + (int64_t)u.b * p.table_stride;
+                const int boxes = kKeys >> box_log;
+                // a lane's box of the tile (at most 16 boxes): its page is read a tile ahead
+                const int box = lane / S::kHalves, half = lane % S::kHalves;
+                const int ps_mask = (1 << p.page_shift) - 1;
+                auto page_of = [&](int j) -> int {
+                    const int key = (rg.first + j) * kKeys + (box << box_log), col = key >> p.page_shift;
+                    if (j >= steps || box >= boxes || key >= rg.hi || key + tp.box_rows <= rg.lo) return -1;
+                    return col < p.table_stride ? __ldg(table + col) : -1;
+                };
+                bool ok = true;
+                int page = page_of(0);
+                for (int j = 0; j < steps && ok; ++j) {
+                    const int next = page_of(j + 1);
+                    const int kb = (rg.first + j) * kKeys;
+                    const int lo = rg.lo > kb ? (rg.lo - kb) >> box_log : 0;
+                    const int hi = rg.hi - kb < kKeys ? (rg.hi - kb + tp.box_rows - 1) >> box_log : boxes;
+                    const bool mine = box >= lo && box < hi;
+                    if (mine && (unsigned)page >= (unsigned)p.num_pages) {
+                        set_status(p.status, MNB_ERR_INVALID_ARG);
+                        page = p.num_pages;  // past the last page: the box is filled with zeros
+                    }
+                    const uint32_t bytes = (uint32_t)(((hi - lo) << box_log) * 128 * S::kHalves);
+                    const uint32_t dst = smem_u32(ring) + (uint32_t)(half * kHalfBytes + (box << box_log) * 128);
+                    const int row = (kb + (box << box_log)) & ps_mask;
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {  // K, then V
+                        const int i = 2 * j + kv, slot = i % R;
+                        ok = ok && wait_for(&kv_empty[slot], (uint32_t)((i / R) & 1) ^ 1u, abort_v, p);
+                        ok = __all_sync(~0u, ok);
+                        if (!ok) break;
+                        if (lane == 0) mbar_arrive_expect_tx(&kv_full[slot], bytes);
+                        __syncwarp();
+                        if (mine) tma_load_4d(dst + (uint32_t)(slot * S::kTile), kv ? &vmap : &kmap, half * 64, row, u.hk, page, &kv_full[slot]);
+                        issued = i + 1;
+                    }
+                    page = next;
+                }
+                if (!ok) {
+                    *abort_v = 1;
                     __syncwarp();
                     if (rg.na) tc::drain_wait(&q_full[0], 0);
                     if (rg.nb) tc::drain_wait(&q_full[1], 0);
@@ -283,92 +319,95 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
                 }
             }
         } else if (warp == kMmaWarp) {
-            const uint32_t id_s = tc::idesc_f16(DT == kBF16, kRows, kKeys);
-            const uint32_t id_o = tc::idesc_f16(DT == kBF16, kRows, DP) | (1u << 16);  // B is MN-major
-            bool ok = true;
-            auto wait = [&](uint64_t* bar, uint32_t ph) {
-                if (ok) ok = tc::wait_bounded(bar, ph, p.status, wl, wh) && !*abort_v;
-                return ok;
-            };
-            auto issue_s = [&](int x, int i) {  // S_x = Q_x . K of ring entry i
-                if (lane == 0) {
-                    const uint64_t a = tc::sdesc_sw128(smem_u32(qs + x * S::kTile));
-                    const uint64_t b = tc::sdesc_sw128(smem_u32(ring + (i % R) * S::kTile));
-    #pragma unroll
+            if (lane == 0 && steps > 0) {
+                const uint32_t id_s = tc::idesc_f16(DT == kBF16, kRows, kKeys);
+                const uint32_t id_o = tc::idesc_f16(DT == kBF16, kRows, DP) | (1u << 16);  // B is MN-major
+                const uint64_t q_desc = tc::sdesc_sw128(smem_u32(qs)), k_desc = tc::sdesc_sw128(smem_u32(ring));
+                const uint64_t v_desc = sdesc_mn_sw128(smem_u32(ring));
+                bool ok = true;
+                auto wait = [&](uint64_t* bar, uint32_t ph) {
+                    ok = ok && wait_for(bar, ph, abort_v, p);
+                    return ok;
+                };
+                auto issue_s = [&](int x, int slot) {  // S_x = Q_x . K
+                    const uint64_t a = q_desc + (uint64_t)(x * (S::kTile >> 4)), b = k_desc + (uint64_t)(slot * (S::kTile >> 4));
+#pragma unroll
                     for (int kk = 0; kk < DP / 16; ++kk) {
                         const uint64_t off = (uint64_t)(((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4);
                         mma_ss(tmem + (uint32_t)(x * 128), a + off, b + off, id_s, kk > 0 ? 1u : 0u);
                     }
-                }
-            };
-            auto issue_o = [&](int x, int i, int step) {  // O_x += P_x . V of ring entry i
-                if (lane == 0) {
-                    const uint64_t b = sdesc_mn_sw128(smem_u32(ring + (i % R) * S::kTile));
-    #pragma unroll
+                };
+                auto issue_o = [&](int x, int slot, int step) {  // O_x += P_x . V
+                    const uint64_t b = v_desc + (uint64_t)(slot * (S::kTile >> 4));
+#pragma unroll
                     for (int kk = 0; kk < kKeys / 16; ++kk)
-                        tc::mma_ta(tmem + 256u + (uint32_t)(x * 128), tmem + (uint32_t)(x * 128 + kk * 8), b + (uint64_t)(kk * (2048 >> 4)), id_o,
-                                   (step > 0 || kk > 0) ? 1u : 0u);
-                }
-            };
-            auto commit = [&](uint64_t* bar) {
-                if (lane == 0) tc::commit(bar);
-            };
-            if (steps > 0) {
+                        tc::mma_ta(tmem + 256u + (uint32_t)(x * 128), tmem + (uint32_t)(x * 128 + kk * 8), b + (uint64_t)(kk * (2048 >> 4)),
+                                   id_o, (step > 0 || kk > 0) ? 1u : 0u);
+                };
                 wait(&kv_full[0], 0);
                 for (int x = 0; x < 2 && ok; ++x) {
                     if ((x ? rg.nb : rg.na) == 0 || !wait(&q_full[x], 0)) continue;
                     tc::fence_after();
                     issue_s(x, 0);
-                    commit(&s_full[x]);
+                    tc::commit(&s_full[x]);
                 }
-                if (ok) commit(&kv_empty[0]);
+                if (ok) tc::commit(&kv_empty[0]);
+                uint32_t edges = 0;
                 for (int j = 0; j < steps && ok; ++j) {
-                    const int iv = 2 * j + 1, ik = 2 * j + 2;
-                    if (!wait(&kv_full[iv % R], (uint32_t)((iv / R) & 1))) break;
-                    // V rows that no row of the unit sees: their products with p = 0 must be 0
-                    const int kb = (rg.first + j) * kKeys;
-                    const int z0 = rg.lo > kb ? (rg.lo - kb) / tp.box_rows * tp.box_rows : 0;
-                    const int z1 = rg.hi - kb < kKeys ? rg.hi - kb : kKeys;
-                    if (z0 > 0 || z1 < kKeys) {
-                        uint8_t* v = ring + (iv % R) * S::kTile;
-                        for (int c = lane; c < kKeys * 8; c += 32) {
-                            const int r = c >> 3;
-                            if (r < z0 || r >= z1) {
-    #pragma unroll
-                                for (int h = 0; h < S::kHalves; ++h)
-                                    *reinterpret_cast<uint4*>(v + h * kHalfBytes + c * 16) = make_uint4(0, 0, 0, 0);
-                            }
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
+                    const int iv = 2 * j + 1, ik = iv + 1;
+                    const int sv = iv % R, sk = ik % R;
+                    int z0, z1;
+                    if (!wait(&kv_full[sv], (uint32_t)((iv / R) & 1))) break;
+                    if (zero_range(j, &z0, &z1)) {  // warp 10 clears the V rows that no row of the unit sees
+                        mbar_arrive(v_edge);
+                        if (!wait(v_zeroed, edges++ & 1)) break;
                     }
-                    if (j + 1 < steps && !wait(&kv_full[ik % R], (uint32_t)((ik / R) & 1))) break;
-                    for (int x = 0; x < 2 && ok; ++x) {
+                    if (j + 1 < steps && !wait(&kv_full[sk], (uint32_t)((ik / R) & 1))) break;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
                         const int nx = x ? rg.nb : rg.na;
                         if (j >= nx || !wait(&p_ready[x], (uint32_t)(j & 1))) continue;
                         tc::fence_after();
-                        issue_o(x, iv, j);
+                        issue_o(x, sv, j);
                         if (j + 1 < nx) {
-                            issue_s(x, ik);
-                            commit(&s_full[x]);
+                            issue_s(x, sk);
+                            tc::commit(&s_full[x]);
                         } else {
-                            commit(&o_full[x]);
+                            tc::commit(&o_full[x]);
                         }
                     }
                     if (!ok) break;
-                    commit(&kv_empty[iv % R]);
-                    if (j + 1 < steps) commit(&kv_empty[ik % R]);
-                    __syncwarp();
+                    tc::commit(&kv_empty[sv]);
+                    if (j + 1 < steps) tc::commit(&kv_empty[sk]);
                 }
                 if (!ok) {
                     *abort_v = 1;
-                    __syncwarp();
-                    if (lane == 0) {
-                        tc::commit(done);
-                        tc::drain_wait(done, 0);
-                    }
-                    __syncwarp();
+                    tc::commit(done);
+                    tc::drain_wait(done, 0);
                 }
+            }
+        } else if (warp == kZeroWarp) {
+            // Rows of V past the visible keys: their pages may hold anything, and 0 * NaN is NaN.
+            // The MMA thread asks for it once the tile has arrived.
+            uint32_t edges = 0;
+            for (int j = 0; j < steps; ++j) {
+                int z0, z1;
+                if (!zero_range(j, &z0, &z1)) continue;
+                const int iv = 2 * j + 1;
+                const bool ok = wait_for(v_edge, edges++ & 1, abort_v, p);
+                if (!__all_sync(~0u, ok)) break;
+                uint8_t* v = ring + (iv % R) * S::kTile;
+                for (int c = lane; c < kKeys * 8; c += 32) {
+                    const int r = c >> 3;
+                    if (r < z0 || r >= z1) {
+#pragma unroll
+                        for (int h = 0; h < S::kHalves; ++h)
+                            *reinterpret_cast<uint4*>(v + h * kHalfBytes + c * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(v_zeroed);
             }
         }
     } else {
@@ -392,8 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
         uint64_t l2a = pack2(0.f, 0.f), l2b = l2a;
         bool ok = true;
         for (int j = 0; j < nx; ++j) {
-            ok = tc::wait_bounded(&s_full[x], (uint32_t)(j & 1), p.status, wl, wh) && !*abort_v;
-            ok = __all_sync(~0u, ok);
+            ok = __all_sync(~0u, wait_for(&s_full[x], (uint32_t)(j & 1), abort_v, p));
             if (!ok) break;
             tc::fence_after();
             uint32_t s[4][32];
@@ -453,16 +491,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
             const uint64_t sc2 = pack2(p.scale_log2, p.scale_log2), nb2 = pack2(nb, nb);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                uint32_t pk[16];
+                // 32 columns at a time, one kind of operation after the other: independent
+                // instructions lie next to each other, so their latencies overlap
+                float e[32];
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
-                    const float2 e = unpack2(ffma2(pack2u(s[c][2 * k], s[c][2 * k + 1]), sc2, nb2));
-                    const float a = ex2(e.x), b = ex2(e.y);
-                    if (k & 1) l2a = fadd2(l2a, pack2(a, b));
-                    else l2b = fadd2(l2b, pack2(a, b));
-                    pk[k] = pack16<DT>(a, b);
+                    const float2 a = unpack2(ffma2(pack2u(s[c][2 * k], s[c][2 * k + 1]), sc2, nb2));
+                    e[2 * k] = a.x;
+                    e[2 * k + 1] = a.y;
                 }
+#pragma unroll
+                for (int k = 0; k < 32; ++k) e[k] = ex2(e[k]);
+                uint32_t pk[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) pk[k] = pack16<DT>(e[2 * k], e[2 * k + 1]);
                 tc::st_32x32b_x16(ts + (uint32_t)(c * 16), pk);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    if (k & 1) l2a = fadd2(l2a, pack2(e[2 * k], e[2 * k + 1]));
+                    else l2b = fadd2(l2b, pack2(e[2 * k], e[2 * k + 1]));
+                }
             }
             tc::wait_st();
             tc::fence_before();
@@ -471,8 +519,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
         }
         const float2 la = unpack2(l2a), lb = unpack2(l2b);
         const float l = (la.x + la.y) + (lb.x + lb.y);
-        bool fine = ok && !*abort_v;
-        if (fine && nx > 0) fine = tc::wait_bounded(&o_full[x], 0, p.status, wl, wh);
+        bool fine = ok;
+        if (fine && nx > 0) fine = wait_for(&o_full[x], 0, abort_v, p);
         fine = __all_sync(~0u, fine);
         if (!fine) *abort_v = 1;
         tc::fence_after();
