@@ -88,7 +88,7 @@ cudaError_t launch_as(const AttnParams& p, const Plan& pl, cudaStream_t s) {
     tp.box_rows = rows;
     tp.part_o = static_cast<float*>(p.workspace);
     tp.part_ml = reinterpret_cast<float2*>(tp.part_o + (size_t)pl.units * pl.splits * 256 * DP);
-    auto kern = tca::attn_tc_kernel<DT, DP>;
+    auto kern = p.scale_log2 < 0.f ? tca::attn_tc_kernel<DT, DP, true> : tca::attn_tc_kernel<DT, DP, false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess) return e;
     e = dec::launch_pdl(kern, dim3((unsigned)(pl.units * pl.splits)), dim3(tca::kThreads), S::kSmem, s, 1, p, tp, maps[0], maps[1], maps[2]);

@@ -23,8 +23,11 @@
 // before is complete by then, because S was committed after it.
 //   warps 0-3    softmax and epilogue of row tile A
 //   warps 4-7    the same for B
-//   warp 8       TMEM; one thread issues all MMAs
-//   warp 9       TMA
+//   warp 8       one thread issues all MMAs
+//   warp 9       TMA, and the schedule: it takes over blocks of the grid that
+//                have not started (cluster launch control) and tells the others
+//                what is next, so a unit's first loads and products overlap the
+//                epilogue of the one before and nothing is set up twice
 //   warp 10      zeroes V rows past the visible keys, whose pages may hold
 //                anything (0 * NaN is NaN); warp 11 completes the warpgroup
 // Few units (a short chunk over a long context) are cut into ranges of key
@@ -40,16 +43,17 @@ namespace tca {
 
 constexpr int kRows = 128, kKeys = 128;
 constexpr int kSoftWarps = 8, kMmaWarp = 8, kTmaWarp = 9, kZeroWarp = 10, kThreads = 384;
-// Registers: 384 threads start with 168 each (64512); the third warpgroup (MMA, TMA, two idle warps) gives
+// Registers: 384 threads start with 168 each (64512); the third warpgroup (MMA, TMA, zeroing) gives
 // 88 of each of its threads back, the softmax warpgroups take 40 more: 256 * 208 + 128 * 80 = 63488.
 constexpr int kSoftRegs = 208, kCtlRegs = 80;
+constexpr int kBarBytes = 512;         // jobs and barriers
 constexpr int kHalfBytes = 128 * 128;  // 128 rows of 64 values: one swizzled half of a Q, K or V tile
 
 template <int DP> struct Shape {
     static constexpr int kHalves = DP / 64;
     static constexpr int kTile = kHalves * kHalfBytes;
     static constexpr int kRing = DP == 128 ? 5 : 8;
-    static constexpr int kSmem = 1024 + 2 * kTile + kRing * kTile + 256;
+    static constexpr int kSmem = 1024 + 2 * kTile + kRing * kTile + kBarBytes;
 };
 
 struct TcParams {
@@ -76,6 +80,14 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint3
         : "memory");
 }
 
+// One thread of the (converged) warp.  Code under this predicate keeps warp-
+// uniform operands in uniform registers, where tcgen05.mma takes them from.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(ok));
+    return ok != 0;
+}
+
 // MN-major, 128-byte swizzle: 64 values of the M / N dimension by 8 of K are a
 // 1024-byte atom; atoms follow each other along K every 1024 bytes (stride
 // byte offset), blocks of 64 along N every kHalfBytes (leading byte offset).
@@ -94,19 +106,37 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// Bounded wait on an mbarrier phase: false when it ran out, or when another
-// role of the CTA gave up.
+// Bounded waits on an mbarrier phase: false when one ran out (the role then
+// records it and gives up), or when another role of the CTA gave up.  Kept to a
+// few instructions: the roles share the instruction cache with the unrolled
+// softmax, and the MMA thread's time is mostly instruction fetches.
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort, const AttnParams& p) {
-    if (mbar_try_wait(bar, parity)) return true;
-    for (uint32_t i = 1; i < p.wait_limit; ++i) {
-        const bool ok = p.wait_hint_ns == kWaitPoll ? mbar_test_wait(bar, parity)
-                        : p.wait_hint_ns         ? mbar_try_wait_sleep(bar, parity, p.wait_hint_ns)
-                                                 : mbar_try_wait(bar, parity);
-        if (ok) return true;
+    for (uint32_t i = 0; i < p.wait_limit; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
         if (*abort) return false;
     }
-    set_status(p.status, MNB_ERR_TIMEOUT);
     return false;
+}
+// Polling: a thread that try_wait has put to sleep was seen to wake about 300
+// cycles after the arrival.
+__device__ __forceinline__ bool spin_for(uint64_t* bar, uint32_t parity, uint32_t limit) {
+    for (uint32_t i = 0; i < limit; ++i)
+        if (mbar_test_wait(bar, parity)) return true;
+    return false;
+}
+__device__ __forceinline__ void give_up(volatile int* abort, const AttnParams& p) {
+    if (!*abort) set_status(p.status, MNB_ERR_TIMEOUT);
+    *abort = 1;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+    float d;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 template <int DT>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
@@ -116,10 +146,26 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
     return d;
 }
 
+// Largest (MIN: smallest) of 32 scores.
+template <bool MIN>
+__device__ __forceinline__ float extreme32(const uint32_t (&v)[32]) {
+    float a = __uint_as_float(v[0]), b = __uint_as_float(v[1]);
+#pragma unroll
+    for (int k = 2; k < 32; k += 4) {
+        const float w = __uint_as_float(v[k]), x = __uint_as_float(v[k + 1]);
+        a = MIN ? min3(a, w, x) : max3(a, w, x);
+        if (k + 3 < 32) {
+            const float y = __uint_as_float(v[k + 2]), z = __uint_as_float(v[k + 3]);
+            b = MIN ? min3(b, y, z) : max3(b, y, z);
+        }
+    }
+    return MIN ? fminf(a, b) : fmaxf(a, b);
+}
+
 // Unit `idx`: sequence, row-tile pair and key head.  The pairs of a sequence
 // come last first, so that the longest ranges start first.  By one whole warp.
 struct Unit {
-    int b, n, len, pair, hk;
+    int b, n, len, pair, hk, tok;
     bool ok;
 };
 __device__ __forceinline__ Unit find_unit(const AttnParams& p, int tokens, int64_t idx, bool tell) {
@@ -128,9 +174,10 @@ __device__ __forceinline__ Unit find_unit(const AttnParams& p, int tokens, int64
     int64_t base = 0;
     for (int b0 = 0; b0 < p.batch; b0 += 32) {
         const int b = b0 + lane;
-        int n = 0, len = 0;
+        int n = 0, len = 0, q0 = 0;
         if (b < p.batch) {
-            const int q0 = p.q_start[b], q1 = p.q_start[b + 1];
+            q0 = p.q_start[b];
+            const int q1 = p.q_start[b + 1];
             n = q1 - q0;
             len = p.kv_lens[b];
             if (n < 0 || n > p.max_q || len < 0 || len > p.max_kv || q0 < 0 || q1 > p.T) {
@@ -153,6 +200,7 @@ __device__ __forceinline__ Unit find_unit(const AttnParams& p, int tokens, int64
             u.b = b0 + src;
             u.n = __shfl_sync(~0u, n, src);
             u.len = __shfl_sync(~0u, len, src);
+            u.tok = __shfl_sync(~0u, q0, src);
             u.pair = (int)(all / p.kv_heads - 1 - r / p.kv_heads);
             u.hk = (int)(r % p.kv_heads);
             u.ok = true;
@@ -190,7 +238,186 @@ __device__ __forceinline__ Range unit_range(const AttnParams& p, const TcParams&
     return r;
 }
 
+// What the TMA warp tells the other roles about the CTA's next unit.
+struct alignas(16) Job {
+    Range rg;
+    int n, len, pair, hk, tok;     // tok: first token of the sequence in the call
+    int part;                      // unit * splits + split
+    int valid;
+};
+
+// Cluster launch control: take over a block of the grid that has not started.
+__device__ __forceinline__ void clc_try_cancel(uint32_t response, uint64_t* bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(response),
+                 "r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ bool clc_taken(uint32_t response, uint32_t* block) {
+    uint32_t ok, x;
+    asm volatile(
+        "{\n .reg .b128 r;\n .reg .pred p;\n ld.shared.b128 r, [%2];\n mov.u32 %1, 0;\n"
+        " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n selp.u32 %0, 1, 0, p;\n"
+        " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n}"
+        : "=r"(ok), "=r"(x)
+        : "r"(response)
+        : "memory");
+    *block = x;
+    return ok != 0;
+}
+
+// Shared memory: Q tiles, the ring, the jobs, the barriers.
+template <int DP>
+struct Shared {
+    using S = Shape<DP>;
+    static constexpr int R = S::kRing;
+    uint8_t* qs;    // [2][halves][128 rows][128 B]
+    uint8_t* ring;  // [R][halves][128 rows][128 B]
+    Job* jobs;      // [2]
+    uint8_t* response;
+    uint64_t *kv_full, *kv_empty;                   // [R]
+    uint64_t *q_full, *q_empty, *s_full;            // [2] per row tile, as those below
+    uint64_t *p_half, *p_ready;                     // P of the first 64 keys, of the others: one arrival per softmax warp
+    uint64_t *o_full, *o_free;
+    uint64_t *job_full, *job_empty;                 // [2] per slot
+    uint64_t *v_edge, *v_zeroed, *clc_bar, *done;
+    __device__ __forceinline__ explicit Shared(uint8_t* smem) {
+        qs = smem;
+        ring = smem + 2 * S::kTile;
+        jobs = reinterpret_cast<Job*>(ring + R * S::kTile);
+        response = reinterpret_cast<uint8_t*>(jobs + 2);
+        kv_full = reinterpret_cast<uint64_t*>(response + 16);
+        kv_empty = kv_full + R;
+        q_full = kv_empty + R;
+        q_empty = q_full + 2;
+        s_full = q_empty + 2;
+        p_half = s_full + 2;
+        p_ready = p_half + 2;
+        o_full = p_ready + 2;
+        o_free = o_full + 2;
+        job_full = o_free + 2;
+        job_empty = job_full + 2;
+        v_edge = job_empty + 2;
+        v_zeroed = v_edge + 1;
+        clc_bar = v_zeroed + 1;
+        done = clc_bar + 1;
+        static_assert(2 * sizeof(Job) + 16 + (2 * R + 22) * 8 + 8 <= kBarBytes, "barriers fit");
+    }
+};
+
+// Rows [z0, z1) of key tile j hold visible keys or lie in a box that was loaded for one.
+__device__ __forceinline__ bool zero_range(const Range& rg, int j, int box_log, int* z0, int* z1) {
+    const int kb = (rg.first + j) * kKeys;
+    *z0 = rg.lo > kb ? ((rg.lo - kb) >> box_log) << box_log : 0;
+    *z1 = rg.hi - kb < kKeys ? rg.hi - kb : kKeys;
+    return *z0 > 0 || *z1 < kKeys;
+}
+
+// The thread that issues all MMAs; false when a wait ran out.
 template <int DT, int DP>
+__device__ __forceinline__ bool mma_role(const Shared<DP>& sh, const AttnParams& p, uint32_t tmem, int box_log) {
+    using S = Shape<DP>;
+    constexpr int R = S::kRing;
+    constexpr uint64_t kTileStep = S::kTile >> 4;
+    const uint32_t id_s = tc::idesc_f16(DT == kBF16, kRows, kKeys);
+    const uint32_t id_o = tc::idesc_f16(DT == kBF16, kRows, DP) | (1u << 16);  // B is MN-major
+    const uint64_t q_desc = tc::sdesc_sw128(smem_u32(sh.qs)), k_desc = tc::sdesc_sw128(smem_u32(sh.ring));
+    const uint64_t v_desc = sdesc_mn_sw128(smem_u32(sh.ring));
+    // about two seconds of polls (or the call's own limit, when it is shortened)
+    const uint32_t limit = p.wait_limit >= (1u << 14) ? 1u << 26 : p.wait_limit;
+    auto issue_s = [&](int x, int slot) {  // S_x = Q_x . K
+        const uint64_t a = q_desc + (uint64_t)x * kTileStep, b = k_desc + (uint64_t)slot * kTileStep;
+#pragma unroll
+        for (int kk = 0; kk < DP / 16; ++kk) {
+            const uint64_t off = (uint64_t)(((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4);
+            mma_ss(tmem + (uint32_t)(x * 128), a + off, b + off, id_s, kk > 0 ? 1u : 0u);
+        }
+    };
+    auto issue_o = [&](int x, int slot, bool first, int part) {  // O_x += P_x . V, half of the keys
+        const uint64_t b = v_desc + (uint64_t)slot * kTileStep;
+#pragma unroll
+        for (int kk = part * (kKeys / 32); kk < (part + 1) * (kKeys / 32); ++kk)
+            tc::mma_ta(tmem + 256u + (uint32_t)(x * 128), tmem + (uint32_t)(x * 128 + kk * 8), b + (uint64_t)(kk * (2048 >> 4)), id_o,
+                       (!first || kk > 0) ? 1u : 0u);
+    };
+    int slot = 0;  // next ring entry, and the parity of its phase
+    uint32_t phase = 0, edges = 0;
+    uint32_t cnt_a = 0, cnt_b = 0, units_a = 0, units_b = 0;  // key tiles, and units with any, so far
+    for (uint32_t k = 0;; ++k) {
+        const Job* job = &sh.jobs[k & 1];
+        if (!spin_for(&sh.job_full[k & 1], (k >> 1) & 1u, limit)) return false;
+        if (!job->valid) return true;
+        const Range rg = job->rg;
+        mbar_arrive(&sh.job_empty[k & 1]);
+        const int steps = rg.na > rg.nb ? rg.na : rg.nb;
+        if (steps == 0) continue;
+        int z0, z1;
+        const int edge_lo = zero_range(rg, 0, box_log, &z0, &z1) ? 0 : -1;
+        const int edge_hi = zero_range(rg, steps - 1, box_log, &z0, &z1) ? steps - 1 : -1;
+        int sv = 0, sk = slot;
+        if (!spin_for(&sh.kv_full[slot], phase, limit)) return false;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int nx = x ? rg.nb : rg.na;
+            if (nx == 0) continue;
+            if (!spin_for(&sh.q_full[x], (x ? units_b : units_a) & 1u, limit)) return false;
+            tc::fence_after();
+            issue_s(x, sk);
+            tc::commit(&sh.s_full[x]);
+            if (nx == 1) tc::commit(&sh.q_empty[x]);
+        }
+        tc::commit(&sh.kv_empty[sk]);
+        for (int j = 0; j < steps; ++j) {
+            // V of this step, K of the next
+            if (++slot == R) {
+                slot = 0;
+                phase ^= 1u;
+            }
+            sv = slot;
+            if (!spin_for(&sh.kv_full[sv], phase, limit)) return false;
+            if (j == edge_lo || j == edge_hi) {  // warp 10 clears the V rows that no row sees
+                mbar_arrive(sh.v_edge);
+                if (!spin_for(sh.v_zeroed, edges++ & 1u, limit)) return false;
+            }
+            if (++slot == R) {
+                slot = 0;
+                phase ^= 1u;
+            }
+            sk = slot;
+            if (j + 1 < steps && !spin_for(&sh.kv_full[sk], phase, limit)) return false;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int nx = x ? rg.nb : rg.na;
+                uint32_t& cnt = x ? cnt_b : cnt_a;
+                if (j < nx) {
+                    const uint32_t un = x ? units_b : units_a;
+                    if (j == 0 && un > 0 && !spin_for(&sh.o_free[x], (un - 1) & 1u, limit)) return false;
+                    if (!spin_for(&sh.p_half[x], cnt & 1u, limit)) return false;
+                    tc::fence_after();
+                    issue_o(x, sv, j == 0, 0);
+                    if (!spin_for(&sh.p_ready[x], cnt & 1u, limit)) return false;
+                    tc::fence_after();
+                    issue_o(x, sv, false, 1);
+                    ++cnt;
+                    if (j + 1 < nx) {
+                        issue_s(x, sk);
+                        tc::commit(&sh.s_full[x]);
+                        if (j + 2 == nx) tc::commit(&sh.q_empty[x]);
+                    } else {
+                        tc::commit(&sh.o_full[x]);
+                    }
+                }
+            }
+            tc::commit(&sh.kv_empty[sv]);
+            if (j + 1 < steps) tc::commit(&sh.kv_empty[sk]);
+        }
+        // (slot is one past the last V: the first K of the next unit)
+        units_a += rg.na > 0;
+        units_b += rg.nb > 0;
+    }
+}
+
+// MIN: the scale is negative, a row's largest scaled score is its smallest score.
+template <int DT, int DP, bool MIN>
 __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p, const TcParams tp,
                                                               const __grid_constant__ CUtensorMap qmap,
                                                               const __grid_constant__ CUtensorMap kmap,
@@ -199,21 +426,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
     constexpr int R = S::kRing;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint8_t* qs = smem;                  // [2][halves][128 rows][128 B]
-    uint8_t* ring = smem + 2 * S::kTile; // [R][halves][128 rows][128 B]
-    uint64_t* bars = reinterpret_cast<uint64_t*>(ring + R * S::kTile);
-    uint64_t* kv_full = bars;
-    uint64_t* kv_empty = bars + R;
-    uint64_t* q_full = bars + 2 * R;     // [2]
-    uint64_t* s_full = q_full + 2;       // [2]
-    uint64_t* p_ready = s_full + 2;      // [2] one arrival per softmax warp
-    uint64_t* o_full = p_ready + 2;      // [2]
-    uint64_t* v_edge = o_full + 2;
-    uint64_t* v_zeroed = v_edge + 1;
-    uint64_t* done = v_zeroed + 1;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+    const Shared<DP> sh(smem);
+    uint8_t* const qs = sh.qs;
+    uint8_t* const ring = sh.ring;
+    Job* const jobs = sh.jobs;
+    uint8_t* const response = sh.response;
+    uint64_t *const kv_full = sh.kv_full, *const kv_empty = sh.kv_empty, *const q_full = sh.q_full, *const q_empty = sh.q_empty;
+    uint64_t *const s_full = sh.s_full, *const p_half = sh.p_half, *const p_ready = sh.p_ready, *const o_full = sh.o_full;
+    uint64_t *const o_free = sh.o_free, *const job_full = sh.job_full, *const job_empty = sh.job_empty;
+    uint64_t *const v_edge = sh.v_edge, *const v_zeroed = sh.v_zeroed, *const clc_bar = sh.clc_bar, *const done = sh.done;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sh.done + 1);
     int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
-    static_assert((2 * R + 11) * 8 + 8 <= 256, "barriers fit");
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
@@ -223,65 +446,84 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(&q_full[x], 1);
+            mbar_init(&q_empty[x], 1);
             mbar_init(&s_full[x], 1);
+            mbar_init(&p_half[x], 4);
             mbar_init(&p_ready[x], 4);
             mbar_init(&o_full[x], 1);
+            mbar_init(&o_free[x], 4);
+            mbar_init(&job_full[x], 1);
+            mbar_init(&job_empty[x], kSoftWarps + 2);
         }
         mbar_init(v_edge, 1);
         mbar_init(v_zeroed, 1);
+        mbar_init(clc_bar, 1);
         mbar_init(done, 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
-    griddep_wait();
-    griddep_launch_dependents();
-    const int64_t idx = blockIdx.x / (unsigned)tp.splits;
-    const int split = (int)(blockIdx.x % (unsigned)tp.splits);
-    const Unit u = find_unit(p, tp.tokens, idx, blockIdx.x == 0);
-    if (!u.ok) return;  // the same for the block
     if (warp == kMmaWarp) tc::alloc(tmem_slot, 512);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
     const uint32_t tmem = *tmem_slot;  // S_A | S_B | O_A | O_B, 128 columns each
     volatile int* abort_v = abort_flag;
-    const Range rg = unit_range(p, tp, u, split);
-    const int steps = rg.na > rg.nb ? rg.na : rg.nb;
+    griddep_wait();
+    griddep_launch_dependents();
 
     const int box_log = __ffs(tp.box_rows) - 1;
-    // rows [z0, z1) of key tile j hold visible keys or lie in a box that was loaded for one
-    auto zero_range = [&](int j, int* z0, int* z1) {
-        const int kb = (rg.first + j) * kKeys;
-        *z0 = rg.lo > kb ? ((rg.lo - kb) >> box_log) << box_log : 0;
-        *z1 = rg.hi - kb < kKeys ? rg.hi - kb : kKeys;
-        return *z0 > 0 || *z1 < kKeys;
-    };
     if (warp >= kSoftWarps) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtlRegs));
         if (warp == kTmaWarp) {
-            int issued = 0;
-            if (steps > 0) {
-                const uint32_t q_bytes = (uint32_t)(tp.tokens * p.group * 128 * S::kHalves);
-                const int tok = p.q_start[u.b] + u.pair * 2 * tp.tokens;
-                if (lane == 0) {
-                    for (int x = 0; x < 2; ++x) {
-                        if ((x ? rg.nb : rg.na) == 0) continue;
-                        mbar_arrive_expect_tx(&q_full[x], q_bytes);
-                        for (int h = 0; h < S::kHalves; ++h)
-                            tma_load_4d(smem_u32(qs + x * S::kTile + h * kHalfBytes), &qmap, h * 64, 0, u.hk, tok + x * tp.tokens, &q_full[x]);
+            const uint32_t q_bytes = (uint32_t)(tp.tokens * p.group * 128 * S::kHalves);
+            const int boxes = kKeys >> box_log, ps_mask = (1 << p.page_shift) - 1;
+            // a lane's box of the tile (at most 16 boxes): its page is read a tile ahead
+            const int box = lane / S::kHalves, half = lane % S::kHalves;
+            int i = 0, q_used[2] = {0, 0};  // ring entries, and Q tiles of each kind, issued so far
+            int k = 0, asked = 0;           // jobs told, blocks asked for
+            bool ok = true, more = true;
+            uint32_t block = blockIdx.x;
+            while (ok) {
+                Unit u{};
+                if (more) {  // ask for the next block before working on this one
+                    if (lane == 0) {
+                        fence_proxy_async_smem();  // the last response has been read
+                        mbar_arrive_expect_tx(clc_bar, 16);
+                        clc_try_cancel(smem_u32(response), clc_bar);
                     }
+                    __syncwarp();
+                    ++asked;
+                    u = find_unit(p, tp.tokens, block / (unsigned)tp.splits, blockIdx.x == 0 && k == 0);
                 }
+                Range rg{};
+                if (u.ok || !more) {  // (a block past the last unit only gives way to the next one)
+                    if (u.ok) rg = unit_range(p, tp, u, (int)(block % (unsigned)tp.splits));
+                    const int slot = k & 1;
+                    ok = k < 2 || __all_sync(~0u, wait_for(&job_empty[slot], (uint32_t)((k >> 1) - 1) & 1u, abort_v, p));
+                    if (!ok) break;
+                    if (lane == 0) {
+                        Job& job = jobs[slot];
+                        job.rg = rg;
+                        job.n = u.n;
+                        job.len = u.len;
+                        job.pair = u.pair;
+                        job.hk = u.hk;
+                        job.tok = u.tok;
+                        job.part = (int)block;
+                        job.valid = u.ok ? 1 : 0;
+                        mbar_arrive(&job_full[slot]);
+                    }
+                    __syncwarp();
+                    ++k;
+                    if (!more) break;
+                }
+                const int steps = rg.na > rg.nb ? rg.na : rg.nb;
                 const int32_t* table = p.tables + (int64_t)u.b * p.table_stride;
-                const int boxes = kKeys >> box_log;
-                // a lane's box of the tile (at most 16 boxes): its page is read a tile ahead
-                const int box = lane / S::kHalves, half = lane % S::kHalves;
-                const int ps_mask = (1 << p.page_shift) - 1;
                 auto page_of = [&](int j) -> int {
                     const int key = (rg.first + j) * kKeys + (box << box_log), col = key >> p.page_shift;
                     if (j >= steps || box >= boxes || key >= rg.hi || key + tp.box_rows <= rg.lo) return -1;
                     return col < p.table_stride ? __ldg(table + col) : -1;
                 };
-                bool ok = true;
                 int page = page_of(0);
                 for (int j = 0; j < steps && ok; ++j) {
                     const int next = page_of(j + 1);
@@ -298,272 +540,248 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
                     const int row = (kb + (box << box_log)) & ps_mask;
 #pragma unroll
                     for (int kv = 0; kv < 2; ++kv) {  // K, then V
-                        const int i = 2 * j + kv, slot = i % R;
-                        ok = ok && wait_for(&kv_empty[slot], (uint32_t)((i / R) & 1) ^ 1u, abort_v, p);
-                        ok = __all_sync(~0u, ok);
+                        const int slot = i % R;
+                        ok = __all_sync(~0u, wait_for(&kv_empty[slot], (uint32_t)((i / R) & 1) ^ 1u, abort_v, p));
                         if (!ok) break;
                         if (lane == 0) mbar_arrive_expect_tx(&kv_full[slot], bytes);
                         __syncwarp();
                         if (mine) tma_load_4d(dst + (uint32_t)(slot * S::kTile), kv ? &vmap : &kmap, half * 64, row, u.hk, page, &kv_full[slot]);
-                        issued = i + 1;
+                        ++i;
+                        if (j > 0 || kv > 0) continue;
+                        // the unit's Q behind its first K: its buffers come free with the last S of the unit before
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            if ((x ? rg.nb : rg.na) == 0) continue;
+                            if (q_used[x] > 0) ok = ok && __all_sync(~0u, wait_for(&q_empty[x], (uint32_t)(q_used[x] - 1) & 1u, abort_v, p));
+                            if (!ok) break;
+                            if (lane == 0) {
+                                mbar_arrive_expect_tx(&q_full[x], q_bytes);
+                                for (int h = 0; h < S::kHalves; ++h)
+                                    tma_load_4d(smem_u32(qs + x * S::kTile + h * kHalfBytes), &qmap, h * 64, 0, u.hk,
+                                                u.tok + (u.pair * 2 + x) * tp.tokens, &q_full[x]);
+                            }
+                            __syncwarp();
+                            ++q_used[x];
+                        }
+                        if (!ok) break;
                     }
                     page = next;
                 }
-                if (!ok) {
-                    *abort_v = 1;
-                    __syncwarp();
-                    if (rg.na) tc::drain_wait(&q_full[0], 0);
-                    if (rg.nb) tc::drain_wait(&q_full[1], 0);
-                    for (int i = issued - R < 0 ? 0 : issued - R; i < issued; ++i)
-                        tc::drain_wait(&kv_full[i % R], (uint32_t)((i / R) & 1));
-                }
+                if (!ok) break;
+                ok = __all_sync(~0u, wait_for(clc_bar, (uint32_t)(asked - 1) & 1u, abort_v, p));
+                if (!ok) break;
+                more = clc_taken(smem_u32(response), &block);
+                __syncwarp();
+            }
+            if (!ok) {  // let the copies in flight land
+                give_up(abort_v, p);
+                __syncwarp();
+                tc::drain_wait(clc_bar, (uint32_t)(asked - 1) & 1u);
+                for (int x = 0; x < 2; ++x)
+                    if (q_used[x]) tc::drain_wait(&q_full[x], (uint32_t)(q_used[x] - 1) & 1u);
+                for (int e = i - R < 0 ? 0 : i - R; e < i; ++e) tc::drain_wait(&kv_full[e % R], (uint32_t)((e / R) & 1));
             }
         } else if (warp == kMmaWarp) {
-            if (lane == 0 && steps > 0) {
-                const uint32_t id_s = tc::idesc_f16(DT == kBF16, kRows, kKeys);
-                const uint32_t id_o = tc::idesc_f16(DT == kBF16, kRows, DP) | (1u << 16);  // B is MN-major
-                const uint64_t q_desc = tc::sdesc_sw128(smem_u32(qs)), k_desc = tc::sdesc_sw128(smem_u32(ring));
-                const uint64_t v_desc = sdesc_mn_sw128(smem_u32(ring));
-                bool ok = true;
-                auto wait = [&](uint64_t* bar, uint32_t ph) {
-                    ok = ok && wait_for(bar, ph, abort_v, p);
-                    return ok;
-                };
-                auto issue_s = [&](int x, int slot) {  // S_x = Q_x . K
-                    const uint64_t a = q_desc + (uint64_t)(x * (S::kTile >> 4)), b = k_desc + (uint64_t)(slot * (S::kTile >> 4));
-#pragma unroll
-                    for (int kk = 0; kk < DP / 16; ++kk) {
-                        const uint64_t off = (uint64_t)(((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4);
-                        mma_ss(tmem + (uint32_t)(x * 128), a + off, b + off, id_s, kk > 0 ? 1u : 0u);
-                    }
-                };
-                auto issue_o = [&](int x, int slot, int step) {  // O_x += P_x . V
-                    const uint64_t b = v_desc + (uint64_t)(slot * (S::kTile >> 4));
-#pragma unroll
-                    for (int kk = 0; kk < kKeys / 16; ++kk)
-                        tc::mma_ta(tmem + 256u + (uint32_t)(x * 128), tmem + (uint32_t)(x * 128 + kk * 8), b + (uint64_t)(kk * (2048 >> 4)),
-                                   id_o, (step > 0 || kk > 0) ? 1u : 0u);
-                };
-                wait(&kv_full[0], 0);
-                for (int x = 0; x < 2 && ok; ++x) {
-                    if ((x ? rg.nb : rg.na) == 0 || !wait(&q_full[x], 0)) continue;
-                    tc::fence_after();
-                    issue_s(x, 0);
-                    tc::commit(&s_full[x]);
-                }
-                if (ok) tc::commit(&kv_empty[0]);
-                uint32_t edges = 0;
-                for (int j = 0; j < steps && ok; ++j) {
-                    const int iv = 2 * j + 1, ik = iv + 1;
-                    const int sv = iv % R, sk = ik % R;
-                    int z0, z1;
-                    if (!wait(&kv_full[sv], (uint32_t)((iv / R) & 1))) break;
-                    if (zero_range(j, &z0, &z1)) {  // warp 10 clears the V rows that no row of the unit sees
-                        mbar_arrive(v_edge);
-                        if (!wait(v_zeroed, edges++ & 1)) break;
-                    }
-                    if (j + 1 < steps && !wait(&kv_full[sk], (uint32_t)((ik / R) & 1))) break;
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const int nx = x ? rg.nb : rg.na;
-                        if (j >= nx || !wait(&p_ready[x], (uint32_t)(j & 1))) continue;
-                        tc::fence_after();
-                        issue_o(x, sv, j);
-                        if (j + 1 < nx) {
-                            issue_s(x, sk);
-                            tc::commit(&s_full[x]);
-                        } else {
-                            tc::commit(&o_full[x]);
-                        }
-                    }
-                    if (!ok) break;
-                    tc::commit(&kv_empty[sv]);
-                    if (j + 1 < steps) tc::commit(&kv_empty[sk]);
-                }
-                if (!ok) {
-                    *abort_v = 1;
-                    tc::commit(done);
-                    tc::drain_wait(done, 0);
-                }
+            if (elect_one() && !mma_role<DT, DP>(sh, p, tmem, box_log)) {
+                give_up(abort_v, p);
+                tc::commit(sh.done);
+                tc::drain_wait(sh.done, 0);
             }
         } else if (warp == kZeroWarp) {
             // Rows of V past the visible keys: their pages may hold anything, and 0 * NaN is NaN.
-            // The MMA thread asks for it once the tile has arrived.
+            // The MMA threads ask for it once the tile has arrived.
             uint32_t edges = 0;
-            for (int j = 0; j < steps; ++j) {
-                int z0, z1;
-                if (!zero_range(j, &z0, &z1)) continue;
-                const int iv = 2 * j + 1;
-                const bool ok = wait_for(v_edge, edges++ & 1, abort_v, p);
-                if (!__all_sync(~0u, ok)) break;
-                uint8_t* v = ring + (iv % R) * S::kTile;
-                for (int c = lane; c < kKeys * 8; c += 32) {
-                    const int r = c >> 3;
-                    if (r < z0 || r >= z1) {
-#pragma unroll
-                        for (int h = 0; h < S::kHalves; ++h)
-                            *reinterpret_cast<uint4*>(v + h * kHalfBytes + c * 16) = make_uint4(0, 0, 0, 0);
-                    }
-                }
-                fence_proxy_async_smem();
+            int base = 0;
+            bool ok = true;
+            for (int k = 0; ok; ++k) {
+                const Job* job = &jobs[k & 1];
+                ok = __all_sync(~0u, wait_for(&job_full[k & 1], (uint32_t)((k >> 1) & 1), abort_v, p));
+                if (!ok || !job->valid) break;
+                const Range rg = job->rg;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(v_zeroed);
+                if (lane == 0) mbar_arrive(&job_empty[k & 1]);
+                const int steps = rg.na > rg.nb ? rg.na : rg.nb;
+                for (int j = 0; j < steps; j = j + 1 < steps - 1 ? steps - 1 : j + 1) {  // the first and the last tile
+                    int z0, z1;
+                    if (!zero_range(rg, j, box_log, &z0, &z1)) continue;
+                    ok = __all_sync(~0u, wait_for(v_edge, edges++ & 1, abort_v, p));
+                    if (!ok) break;
+                    uint8_t* v = ring + ((base + 2 * j + 1) % R) * S::kTile;
+                    for (int c = lane; c < kKeys * 8; c += 32) {
+                        const int r = c >> 3;
+                        if (r < z0 || r >= z1) {
+#pragma unroll
+                            for (int h = 0; h < S::kHalves; ++h)
+                                *reinterpret_cast<uint4*>(v + h * kHalfBytes + c * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(v_zeroed);
+                }
+                base += 2 * steps;
             }
+            if (!ok) give_up(abort_v, p);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         const int x = warp >> 2;                 // row tile
         const int r = (warp & 3) * 32 + lane;    // row of the tile = TMEM lane
+        const int r_tok = r / p.group, r_head = r - r_tok * p.group;
         const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + (uint32_t)(x * 128) + lane_addr, to = tmem + 256u + (uint32_t)(x * 128) + lane_addr;
-        const int nx = x ? rg.nb : rg.na;
-        const int i0 = (u.pair * 2 + x) * tp.tokens, i = i0 + r / p.group;
-        const bool row_ok = r < tp.tokens * p.group && i < u.n;
-        int row_lo = 0, row_hi = 0;
-        if (row_ok) visible_range(p, u.n, u.len, i, i + 1, &row_lo, &row_hi);
-        int full_lo, full_hi, unused;  // keys that every row of the tile sees
-        {
-            const int i1 = i0 + tp.tokens < u.n ? i0 + tp.tokens : u.n;
-            visible_range(p, u.n, u.len, i0, i0 + 1, &unused, &full_hi);
-            visible_range(p, u.n, u.len, i1 - 1, i1, &full_lo, &unused);
-        }
-        float m = -INFINITY;
-        uint64_t l2a = pack2(0.f, 0.f), l2b = l2a;
+        uint32_t cnt = 0, units_of = 0;          // steps, and units with any, before this one
         bool ok = true;
-        for (int j = 0; j < nx; ++j) {
-            ok = __all_sync(~0u, wait_for(&s_full[x], (uint32_t)(j & 1), abort_v, p));
+        for (int k = 0;; ++k) {
+            // The job stays in shared memory until its epilogue is done: the key loop needs the registers.
+            const Job* job = &jobs[k & 1];
+            ok = __all_sync(~0u, wait_for(&job_full[k & 1], (uint32_t)((k >> 1) & 1), abort_v, p));
+            if (!ok || !job->valid) break;
+            const int nx = x ? job->rg.nb : job->rg.na;
+            const int i0 = (job->pair * 2 + x) * tp.tokens;
+            int row_lo = 0, row_hi = 0, full_lo = 0, full_hi = 0, unused;
+            if (i0 < job->n) {
+                const int i1 = i0 + tp.tokens < job->n ? i0 + tp.tokens : job->n;
+                if (r_tok < tp.tokens && i0 + r_tok < i1) visible_range(p, job->n, job->len, i0 + r_tok, i0 + r_tok + 1, &row_lo, &row_hi);
+                // keys that every row of the tile sees
+                visible_range(p, job->n, job->len, i0, i0 + 1, &unused, &full_hi);
+                visible_range(p, job->n, job->len, i1 - 1, i1, &full_lo, &unused);
+            }
+            const int kb0 = job->rg.first * kKeys;
+            float m = -INFINITY;
+            uint64_t l2a = pack2(0.f, 0.f), l2b = l2a;
+            for (int j = 0; j < nx; ++j) {
+                ok = __all_sync(~0u, wait_for(&s_full[x], (cnt + (uint32_t)j) & 1u, abort_v, p));
+                if (!ok) break;
+                tc::fence_after();
+                uint32_t s[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tc::ld_32x32b<32>(ts + (uint32_t)(c * 32), s[c]);
+                tc::wait_ld();
+                const int kb = kb0 + j * kKeys;
+                if (kb < full_lo || kb + kKeys > full_hi) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const int key = kb + c * 32 + e;
+                            if (key < row_lo || key >= row_hi) s[c][e] = MIN ? 0x7F800000u : 0xFF800000u;
+                        }
+                }
+                float t[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) t[c] = extreme32<MIN>(s[c]);
+                const float top = (MIN ? min3(t[0], t[1], fminf(t[2], t[3])) : max3(t[0], t[1], fmaxf(t[2], t[3]))) * p.scale_log2;
+                if (__any_sync(~0u, top > m + 8.f)) {
+                    const float mn = fmaxf(m, top);
+                    const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
+                    m = mn;
+                    const uint64_t f2 = pack2(f, f);
+                    l2a = ffma2(l2a, f2, pack2(0.f, 0.f));
+                    l2b = ffma2(l2b, f2, pack2(0.f, 0.f));
+                    if (j > 0) {
+#pragma unroll
+                        for (int c = 0; c < DP / 32; ++c) {
+                            uint32_t v[32];
+                            tc::ld_32x32b<32>(to + (uint32_t)(c * 32), v);
+                            tc::wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+                            tc::st_32x32b_x32(to + (uint32_t)(c * 32), v);
+                        }
+                    }
+                }
+                const float nb = m == -INFINITY ? 0.f : -m;
+                const uint64_t sc2 = pack2(p.scale_log2, p.scale_log2), nb2 = pack2(nb, nb);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    // 32 columns at a time, one kind of operation after the other: independent
+                    // instructions lie next to each other, so their latencies overlap
+                    float e[32];
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) {
+                        const float2 a = unpack2(ffma2(pack2u(s[c][2 * q], s[c][2 * q + 1]), sc2, nb2));
+                        e[2 * q] = a.x;
+                        e[2 * q + 1] = a.y;
+                    }
+#pragma unroll
+                    for (int q = 0; q < 32; ++q) e[q] = ex2(e[q]);
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) pk[q] = pack16<DT>(e[2 * q], e[2 * q + 1]);
+                    tc::st_32x32b_x16(ts + (uint32_t)(c * 16), pk);
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) {
+                        if (q & 1) l2a = fadd2(l2a, pack2(e[2 * q], e[2 * q + 1]));
+                        else l2b = fadd2(l2b, pack2(e[2 * q], e[2 * q + 1]));
+                    }
+                    if (c == 1 || c == 3) {  // P V of these 64 keys may start
+                        tc::wait_st();
+                        tc::fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(c == 1 ? &p_half[x] : &p_ready[x]);
+                    }
+                }
+            }
             if (!ok) break;
-            tc::fence_after();
-            uint32_t s[4][32];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tc::ld_32x32b<32>(ts + (uint32_t)(c * 32), s[c]);
-            tc::wait_ld();
-            const int kb = (rg.first + j) * kKeys;
-            if (kb < full_lo || kb + kKeys > full_hi) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        const int key = kb + c * 32 + k;
-                        if (key < row_lo || key >= row_hi) s[c][k] = p.scale_log2 < 0.f ? 0x7F800000u : 0xFF800000u;
-                    }
+            if (nx > 0) {
+                ok = __all_sync(~0u, wait_for(&o_full[x], units_of & 1u, abort_v, p));
+                if (!ok) break;
+                tc::fence_after();
             }
-            // the largest of scale * s: the largest or (negative scale) smallest s
-            float t[4];
-            if (p.scale_log2 >= 0.f) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    t[c] = __uint_as_float(s[c][0]);
-#pragma unroll
-                    for (int k = 1; k < 32; ++k) t[c] = fmaxf(t[c], __uint_as_float(s[c][k]));
-                }
-                t[0] = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
-            } else {
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    t[c] = __uint_as_float(s[c][0]);
-#pragma unroll
-                    for (int k = 1; k < 32; ++k) t[c] = fminf(t[c], __uint_as_float(s[c][k]));
-                }
-                t[0] = fminf(fminf(t[0], t[1]), fminf(t[2], t[3]));
-            }
-            const float top = t[0] * p.scale_log2;
-            if (__any_sync(~0u, top > m + 8.f)) {
-                const float mn = fmaxf(m, top);
-                const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
-                m = mn;
-                const uint64_t f2 = pack2(f, f);
-                l2a = ffma2(l2a, f2, pack2(0.f, 0.f));
-                l2b = ffma2(l2b, f2, pack2(0.f, 0.f));
-                if (j > 0) {
-#pragma unroll
-                    for (int c = 0; c < DP / 32; ++c) {
-                        uint32_t v[32];
-                        tc::ld_32x32b<32>(to + (uint32_t)(c * 32), v);
-                        tc::wait_ld();
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f);
-                        tc::st_32x32b_x32(to + (uint32_t)(c * 32), v);
-                    }
-                }
-            }
-            const float nb = m == -INFINITY ? 0.f : -m;
-            const uint64_t sc2 = pack2(p.scale_log2, p.scale_log2), nb2 = pack2(nb, nb);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                // 32 columns at a time, one kind of operation after the other: independent
-                // instructions lie next to each other, so their latencies overlap
-                float e[32];
-#pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    const float2 a = unpack2(ffma2(pack2u(s[c][2 * k], s[c][2 * k + 1]), sc2, nb2));
-                    e[2 * k] = a.x;
-                    e[2 * k + 1] = a.y;
-                }
-#pragma unroll
-                for (int k = 0; k < 32; ++k) e[k] = ex2(e[k]);
-                uint32_t pk[16];
-#pragma unroll
-                for (int k = 0; k < 16; ++k) pk[k] = pack16<DT>(e[2 * k], e[2 * k + 1]);
-                tc::st_32x32b_x16(ts + (uint32_t)(c * 16), pk);
-#pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    if (k & 1) l2a = fadd2(l2a, pack2(e[2 * k], e[2 * k + 1]));
-                    else l2b = fadd2(l2b, pack2(e[2 * k], e[2 * k + 1]));
-                }
-            }
-            tc::wait_st();
-            tc::fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_ready[x]);
-        }
-        const float2 la = unpack2(l2a), lb = unpack2(l2b);
-        const float l = (la.x + la.y) + (lb.x + lb.y);
-        bool fine = ok;
-        if (fine && nx > 0) fine = wait_for(&o_full[x], 0, abort_v, p);
-        fine = __all_sync(~0u, fine);
-        if (!fine) *abort_v = 1;
-        tc::fence_after();
-        if (fine && i0 < u.n) {
-            const int64_t tk = (int64_t)p.q_start[u.b] + i;
-            const int h = u.hk * p.group + r % p.group;
-            const int64_t part = (idx * tp.splits + split) * 256 + x * 128 + r;
+            const float2 la = unpack2(l2a), lb = unpack2(l2b);
+            const float l = (la.x + la.y) + (lb.x + lb.y);
+            const int i = i0 + r_tok;
+            const bool row_ok = r_tok < tp.tokens && i < job->n;
+            const int64_t tk = (int64_t)job->tok + i;
+            const int h = job->hk * p.group + r_head;
+            const int64_t part = (int64_t)job->part * 256 + x * 128 + r;
             const float inv = l > 0.f ? 1.f / l : 0.f;
+            uint16_t* orow = static_cast<uint16_t*>(p.o) + tk * p.o_ts + h * p.o_hs;
 #pragma unroll
             for (int c = 0; c < DP / 32; ++c) {
                 uint32_t v[32];
                 if (nx > 0) {
                     tc::ld_32x32b<32>(to + (uint32_t)(c * 32), v);
                     tc::wait_ld();
+                    if (c == DP / 32 - 1) {  // O may be written by the next unit
+                        tc::fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&o_free[x]);
+                    }
                 } else {
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) v[k] = 0u;
+                    for (int e = 0; e < 32; ++e) v[e] = 0u;
                 }
                 if (!row_ok) continue;
                 if (tp.splits == 1) {
-                    uint16_t* o = static_cast<uint16_t*>(p.o) + tk * p.o_ts + h * p.o_hs + c * 32;
 #pragma unroll
-                    for (int k = 0; k < 32; k += 8) {
-                        if (c * 32 + k < p.D) {
+                    for (int e = 0; e < 32; e += 8) {
+                        if (c * 32 + e < p.D) {
                             uint4 w;
-                            w.x = pack16<DT>(__uint_as_float(v[k]) * inv, __uint_as_float(v[k + 1]) * inv);
-                            w.y = pack16<DT>(__uint_as_float(v[k + 2]) * inv, __uint_as_float(v[k + 3]) * inv);
-                            w.z = pack16<DT>(__uint_as_float(v[k + 4]) * inv, __uint_as_float(v[k + 5]) * inv);
-                            w.w = pack16<DT>(__uint_as_float(v[k + 6]) * inv, __uint_as_float(v[k + 7]) * inv);
-                            *reinterpret_cast<uint4*>(o + k) = l > 0.f ? w : make_uint4(0, 0, 0, 0);
+                            w.x = pack16<DT>(__uint_as_float(v[e]) * inv, __uint_as_float(v[e + 1]) * inv);
+                            w.y = pack16<DT>(__uint_as_float(v[e + 2]) * inv, __uint_as_float(v[e + 3]) * inv);
+                            w.z = pack16<DT>(__uint_as_float(v[e + 4]) * inv, __uint_as_float(v[e + 5]) * inv);
+                            w.w = pack16<DT>(__uint_as_float(v[e + 6]) * inv, __uint_as_float(v[e + 7]) * inv);
+                            *reinterpret_cast<uint4*>(orow + c * 32 + e) = l > 0.f ? w : make_uint4(0, 0, 0, 0);
                         }
                     }
                 } else if (nx > 0) {
                     uint4* o = reinterpret_cast<uint4*>(tp.part_o + part * DP + c * 32);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) o[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                    for (int e = 0; e < 8; ++e) o[e] = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
                 }
             }
             if (row_ok) {
                 if (tp.splits > 1) tp.part_ml[part] = make_float2(m, l);
                 else if (p.lse) p.lse[tk * p.q_heads + h] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
             }
+            cnt += (uint32_t)nx;
+            units_of += nx > 0;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&job_empty[k & 1]);
         }
+        if (!ok) give_up(abort_v, p);
     }
     tc::fence_before();
     __syncthreads();
