@@ -327,61 +327,73 @@ def mnb_select_kernel(M, N, K, bits, block_size, act_dtype, accuracy_level=0) ->
 
 
 # ---- between the weight products: positions, cache, attention ----------------------------------
-# Sizes and strides come from the tensors: rows are [tokens, heads, dim] views with unit stride in dim.
+# Sizes and strides come from the tensors: rows are [tokens, heads, dim] views with unit stride in dim.  These calls
+# run between microsecond kernels, so their checks are a few attribute reads each.
 
-def _rows(t, what):
-    if t.dim() != 3 or t.stride(2) != 1:
-        raise ValueError(f"{what}: a [tokens, heads, dim] tensor with unit stride in dim is wanted")
-    return t.stride(0), t.stride(1)
-
-
-def _nbytes(t):
-    return 0 if t is None else t.numel() * t.element_size()
+_codes = {}  # torch dtype -> dtype code, filled on first use
+_int32 = _float32 = _device = _raw_stream = None
 
 
-def _i32(*named):
-    for what, t in named:
-        if t is not None and (str(t.dtype) != "torch.int32" or not t.is_contiguous()):
-            raise ValueError(f"{what}: a contiguous int32 tensor is wanted")
+def _setup():
+    global _int32, _float32, _device, _raw_stream
+    import torch
+    _int32, _float32 = torch.int32, torch.float32
+    _device, _raw_stream = getattr(torch._C, "_cuda_getDevice", None), getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _codes.update({torch.float32: MNB_F32, torch.float16: MNB_F16, torch.bfloat16: MNB_BF16})
 
 
-_DTYPE_OF = {"torch.float32": MNB_F32, "torch.float16": MNB_F16, "torch.bfloat16": MNB_BF16}
+def _current(stream):
+    """The call's stream: torch's current one by its raw handle, without making a Stream object."""
+    if stream is None and _raw_stream is not None and _device is not None:
+        return _raw_stream(_device())
+    return _stream(stream)
 
 
-def _same_dtype(code, *named):
-    for what, t in named:
-        if t is not None and _DTYPE_OF.get(str(t.dtype)) != code:
-            raise ValueError(f"{what}: {t.dtype} does not match the call's dtype code {code}")
+def _fail(what):
+    raise ValueError(what)
+
+
+def _i32(what, t):
+    if t.dtype is not _int32 or not t.is_contiguous():
+        _fail(f"{what}: a contiguous int32 tensor is wanted")
+    return t.data_ptr()
 
 
 def _table_pair(cos_table, sin_table):
-    for t in (cos_table, sin_table):
-        if t.dim() != 2 or not t.is_contiguous() or str(t.dtype) != "torch.float32" or t.shape != cos_table.shape:
-            raise ValueError("cos_table, sin_table: contiguous f32 [n_pos, rot_dim / 2] tensors of one shape are wanted")
-    return cos_table.shape[0], 2 * cos_table.shape[1]
+    shape = cos_table.shape
+    if len(shape) != 2 or sin_table.shape != shape or cos_table.dtype is not _float32 or sin_table.dtype is not _float32 or \
+            not cos_table.is_contiguous() or not sin_table.is_contiguous():
+        _fail("cos_table, sin_table: contiguous f32 [n_pos, rot_dim / 2] tensors of one shape are wanted")
+    return shape[0], 2 * shape[1]
+
+
+def _rows_fail(what):
+    _fail(f"{what}: a [tokens, heads, dim] tensor of the call's dtype with unit stride in dim is wanted")
 
 
 def kv_cache(k_pages, v_pages, tables, kv_lens, order, dtype) -> KvCache:
     """The cache descriptor of one layer.  Pages are [num_pages, heads, tokens, dim] (order "hnd") or
     [num_pages, tokens, heads, dim] ("nhd") tensors of one shape and one set of strides.  The descriptor holds the
     tensors' addresses (and the tensors): make it once per layer and keep it beside them."""
+    if not _codes:
+        _setup()
     if order not in ("hnd", "nhd"):
-        raise ValueError('order is "hnd" or "nhd"')
-    if k_pages.shape != v_pages.shape or k_pages.stride() != v_pages.stride() or k_pages.dim() != 4 or k_pages.stride(3) != 1:
-        raise ValueError("k_pages, v_pages: 4-d tensors of one shape and one set of strides are wanted")
-    _same_dtype(dtype, ("k_pages", k_pages), ("v_pages", v_pages))
-    _i32(("kv_lens", kv_lens))
-    if str(tables.dtype) != "torch.int32" or tables.dim() != 2 or (tables.shape[1] > 1 and tables.stride(1) != 1) or \
+        _fail('order is "hnd" or "nhd"')
+    if k_pages.shape != v_pages.shape or k_pages.stride() != v_pages.stride() or k_pages.dim() != 4 or k_pages.stride(3) != 1 or \
+            _codes.get(k_pages.dtype) != dtype or v_pages.dtype is not k_pages.dtype:
+        _fail("k_pages, v_pages: 4-d tensors of dtype, one shape and one set of strides are wanted")
+    lens_ptr = _i32("kv_lens", kv_lens)
+    if tables.dtype is not _int32 or tables.dim() != 2 or (tables.shape[1] > 1 and tables.stride(1) != 1) or \
             kv_lens.numel() < tables.shape[0]:
-        raise ValueError("tables: an int32 [batch, columns] tensor with a kv_len for each row is wanted")
+        _fail("tables: an int32 [batch, columns] tensor with a kv_len for each row is wanted")
     c = KvCache()
     head, tok = (1, 2) if order == "hnd" else (2, 1)
-    c.k_pages, c.v_pages, c.tables, c.kv_lens = k_pages.data_ptr(), v_pages.data_ptr(), tables.data_ptr(), kv_lens.data_ptr()
+    c.k_pages, c.v_pages, c.tables, c.kv_lens = k_pages.data_ptr(), v_pages.data_ptr(), tables.data_ptr(), lens_ptr
     c.batch = tables.shape[0]
-    # rows are table_stride apart; a single row, or rows apart by less than their width, take the width
+    # rows are table_stride apart; a single row takes its width
     c.table_stride = tables.stride(0) if tables.shape[0] > 1 else tables.shape[1]
     if c.table_stride < tables.shape[1]:
-        raise ValueError("tables: rows overlap")
+        _fail("tables: rows overlap")
     c.num_pages, c.page_stride = k_pages.shape[0], k_pages.stride(0)
     c.token_stride, c.head_stride = k_pages.stride(tok), k_pages.stride(head)
     c.page_size, c.kv_heads, c.head_dim, c.dtype = k_pages.shape[tok], k_pages.shape[head], k_pages.shape[3], dtype
@@ -396,7 +408,7 @@ def page_planes(pool) -> PagePlanes:
     inner = 1
     for n, st in zip(reversed(pool.shape[2:]), reversed(pool.stride()[2:])):
         if n > 1 and st != inner:
-            raise ValueError("pool: contiguous pages are wanted")
+            _fail("pool: contiguous pages are wanted")
         inner *= n
     p.base, p.num_planes, p.num_pages = pool.data_ptr(), pool.shape[0], pool.shape[1]
     p.plane_stride, p.page_stride, p.page_bytes = pool.stride(0) * e, pool.stride(1) * e, inner * e
@@ -406,11 +418,12 @@ def page_planes(pool) -> PagePlanes:
 
 def cache_state(refs, tables, lens, page_size) -> CacheState:
     """Reference counts [pages], page tables [sequences, columns] and lengths [sequences], contiguous int32."""
-    _i32(("refs", refs), ("tables", tables), ("lens", lens))
-    if tables.dim() != 2 or lens.numel() != tables.shape[0]:
-        raise ValueError("tables: [sequences, columns] with a length for each row is wanted")
+    if not _codes:
+        _setup()
     s = CacheState()
-    s.refs, s.tables, s.lens = refs.data_ptr(), tables.data_ptr(), lens.data_ptr()
+    s.refs, s.tables, s.lens = _i32("refs", refs), _i32("tables", tables), _i32("lens", lens)
+    if tables.dim() != 2 or lens.numel() != tables.shape[0]:
+        _fail("tables: [sequences, columns] with a length for each row is wanted")
     s.num_pages, s.num_seqs, s.table_stride, s.page_size = refs.numel(), tables.shape[0], tables.shape[1], page_size
     s.tensors = (refs, tables, lens)
     return s
@@ -419,43 +432,59 @@ def cache_state(refs, tables, lens, page_size) -> CacheState:
 def mnb_rotary_table(cos_table, sin_table, base=10000.0, scaling=MNB_ROPE_NONE, factor=1.0, trained_len=0.0, low=1.0,
                      high=32.0, attn_factor=1.0, stream=None):
     """Fill the f32 [n_pos, rot_dim / 2] tables (see mnb_rope_scaling for the long-context forms)."""
+    if not _codes:
+        _setup()
     n_pos, rot = _table_pair(cos_table, sin_table)
     _check(load().mnb_rotary_table(_ptr(cos_table), _ptr(sin_table), n_pos, rot, base, scaling, factor, trained_len,
-                                   low, high, attn_factor, _stream(stream)), "mnb_rotary_table")
+                                   low, high, attn_factor, _current(stream)), "mnb_rotary_table")
 
 
 def mnb_rotary(x, y, positions, cos_table, sin_table, dtype, flags=0, stream=None):
     """y = x with the first rot_dim = 2 * cos_table.shape[1] depths of each head turned; x, y [T, H, D]."""
+    if not _codes:
+        _setup()
     n_pos, rot = _table_pair(cos_table, sin_table)
-    _same_dtype(dtype, ("x", x), ("y", y))
-    _i32(("positions", positions))
-    if x.shape != y.shape or positions.numel() != x.shape[0]:
-        raise ValueError("x, y: one shape, with a position for each token, is wanted")
-    _check(load().mnb_rotary(_ptr(x), _ptr(y), _ptr(positions), _ptr(cos_table), _ptr(sin_table), *x.shape, rot, n_pos,
-                             *_rows(x, "x"), *_rows(y, "y"), dtype, flags, _stream(stream)), "mnb_rotary")
+    shape, xs, ys = x.shape, x.stride(), y.stride()
+    if y.shape != shape or len(shape) != 3 or xs[2] != 1 or ys[2] != 1 or _codes.get(x.dtype) != dtype or y.dtype is not x.dtype:
+        _rows_fail("x, y")
+    pos_ptr = _i32("positions", positions)
+    if positions.numel() != shape[0]:
+        _fail("positions: one for each token is wanted")
+    st = (_lib or load()).mnb_rotary(x.data_ptr(), y.data_ptr(), pos_ptr, cos_table.data_ptr(), sin_table.data_ptr(), shape[0], shape[1],
+                                     shape[2], rot, n_pos, xs[0], xs[1], ys[0], ys[1], dtype, flags, _current(stream))
+    if st:
+        _check(st, "mnb_rotary")
 
 
 def mnb_rotary_append(q, q_out, k, v, cos_table, sin_table, cache, q_start, positions=None, flags=0, stream=None):
     """Turn q into q_out (q None: append only) and k, and write k and v to the cache's pages."""
-    a = RotaryArgs()
-    a.n_pos, a.rot_dim = _table_pair(cos_table, sin_table)
-    _same_dtype(cache.dtype, ("q", q), ("q_out", q_out), ("k", k), ("v", v))
-    _i32(("q_start", q_start), ("positions", positions))
-    a.T = k.shape[0]
-    if k.shape != v.shape or tuple(k.shape[1:]) != (cache.kv_heads, cache.head_dim) or q_start.numel() != cache.batch + 1 or \
-            (positions is not None and positions.numel() != a.T):
-        raise ValueError("k, v: [T, kv_heads, head_dim] of the cache, and q_start [batch + 1], are wanted")
-    a.k_token_stride, a.k_head_stride = _rows(k, "k")
-    a.v_token_stride, a.v_head_stride = _rows(v, "v")
+    if not _codes:
+        _setup()
+    n_pos, rot = _table_pair(cos_table, sin_table)
+    dtype, ks, vs, shape = cache.dtype, k.stride(), v.stride(), k.shape
+    if v.shape != shape or len(shape) != 3 or ks[2] != 1 or vs[2] != 1 or _codes.get(k.dtype) != dtype or v.dtype is not k.dtype or \
+            shape[1] != cache.kv_heads or shape[2] != cache.head_dim:
+        _fail("k, v: [T, kv_heads, head_dim] rows of the cache's dtype are wanted")
+    start_ptr, pos_ptr = _i32("q_start", q_start), None
+    if q_start.numel() != cache.batch + 1:
+        _fail("q_start: batch + 1 entries are wanted")
+    if positions is not None:
+        pos_ptr = _i32("positions", positions)
+        if positions.numel() != shape[0]:
+            _fail("positions: one for each token is wanted")
+    qp = op = None
+    heads, qs, os_ = 0, (0, 0), (0, 0)
     if q is not None:
-        if q.shape != q_out.shape or q.shape[0] != a.T or q.shape[2] != cache.head_dim:
-            raise ValueError("q, q_out: [T, q_heads, head_dim] is wanted")
-        a.q, a.q_out, a.q_heads = q.data_ptr(), q_out.data_ptr(), q.shape[1]
-        a.q_token_stride, a.q_head_stride = _rows(q, "q")
-        a.q_out_token_stride, a.q_out_head_stride = _rows(q_out, "q_out")
-    a.k, a.v, a.cos_table, a.sin_table = k.data_ptr(), v.data_ptr(), cos_table.data_ptr(), sin_table.data_ptr()
-    a.q_start, a.positions, a.flags, a.stream = q_start.data_ptr(), _ptr(positions), flags, _stream(stream)
-    _check(load().mnb_rotary_append(ctypes.byref(a), ctypes.byref(cache)), "mnb_rotary_append")
+        qshape, qs, os_ = q.shape, q.stride(), q_out.stride()
+        if q_out.shape != qshape or len(qshape) != 3 or qs[2] != 1 or os_[2] != 1 or q.dtype is not k.dtype or q_out.dtype is not k.dtype or \
+                qshape[0] != shape[0] or qshape[2] != shape[2]:
+            _fail("q, q_out: [T, q_heads, head_dim] rows of the cache's dtype are wanted")
+        qp, op, heads = q.data_ptr(), q_out.data_ptr(), qshape[1]
+    a = RotaryArgs(qp, op, k.data_ptr(), v.data_ptr(), cos_table.data_ptr(), sin_table.data_ptr(), start_ptr, pos_ptr, shape[0], heads, rot,
+                   n_pos, qs[0], qs[1], os_[0], os_[1], ks[0], ks[1], vs[0], vs[1], flags, _current(stream))
+    st = (_lib or load()).mnb_rotary_append(a, cache)
+    if st:
+        _check(st, "mnb_rotary_append")
 
 
 def mnb_attention_workspace_size(batch, T, q_heads, kv_heads, head_dim, max_q, max_kv, dtype) -> int:
@@ -465,32 +494,46 @@ def mnb_attention_workspace_size(batch, T, q_heads, kv_heads, head_dim, max_q, m
 def mnb_paged_attention(q, o, cache, q_start, max_q, max_kv, scale, lse=None, causal=True, window=0, workspace=None,
                         stream=None):
     """Attention of the tokens q [T, q_heads, head_dim] over the cache; lse f32 [T, q_heads] or None."""
-    _same_dtype(cache.dtype, ("q", q), ("o", o))
-    _i32(("q_start", q_start))
-    if q.shape != o.shape or q.shape[2] != cache.head_dim or q_start.numel() != cache.batch + 1:
-        raise ValueError("q, o: [T, q_heads, head_dim] of the cache, and q_start [batch + 1], are wanted")
-    if lse is not None and (tuple(lse.shape) != tuple(q.shape[:2]) or not lse.is_contiguous() or str(lse.dtype) != "torch.float32"):
-        raise ValueError("lse: a contiguous f32 [T, q_heads] tensor is wanted")
-    a = AttentionArgs()
-    a.q, a.o, a.lse, a.q_start = q.data_ptr(), o.data_ptr(), _ptr(lse), q_start.data_ptr()
-    a.T, a.q_heads, a.max_q, a.max_kv, a.window = q.shape[0], q.shape[1], max_q, max_kv, window
-    a.q_token_stride, a.q_head_stride = _rows(q, "q")
-    a.o_token_stride, a.o_head_stride = _rows(o, "o")
-    a.scale, a.causal = scale, 1 if causal else 0
-    a.workspace, a.workspace_bytes, a.stream = _ptr(workspace), _nbytes(workspace), _stream(stream)
-    _check(load().mnb_paged_attention(ctypes.byref(a), ctypes.byref(cache)), "mnb_paged_attention")
+    if not _codes:
+        _setup()
+    shape, qs, os_ = q.shape, q.stride(), o.stride()
+    if o.shape != shape or len(shape) != 3 or qs[2] != 1 or os_[2] != 1 or _codes.get(q.dtype) != cache.dtype or o.dtype is not q.dtype or \
+            shape[2] != cache.head_dim:
+        _fail("q, o: [T, q_heads, head_dim] rows of the cache's dtype are wanted")
+    start_ptr, lse_ptr, ws_ptr, ws_bytes = _i32("q_start", q_start), None, None, 0
+    if q_start.numel() != cache.batch + 1:
+        _fail("q_start: batch + 1 entries are wanted")
+    if lse is not None:
+        if lse.dtype is not _float32 or lse.shape != shape[:2] or not lse.is_contiguous():
+            _fail("lse: a contiguous f32 [T, q_heads] tensor is wanted")
+        lse_ptr = lse.data_ptr()
+    if workspace is not None:
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    a = AttentionArgs(q.data_ptr(), o.data_ptr(), lse_ptr, start_ptr, shape[0], shape[1], max_q, max_kv, window, qs[0], qs[1], os_[0], os_[1],
+                      scale, 1 if causal else 0, ws_ptr, ws_bytes, _current(stream))
+    st = (_lib or load()).mnb_paged_attention(a, cache)
+    if st:
+        _check(st, "mnb_paged_attention")
 
 
 def _pair_lists(a, b, what):
-    _i32((what, a), (what, b))
-    if a.numel() != b.numel():
-        raise ValueError(f"{what}: two lists of one length are wanted")
-    return a.data_ptr(), b.data_ptr(), a.numel()
+    pa, pb, n = _i32(what, a), _i32(what, b), a.numel()
+    if b.numel() != n:
+        _fail(f"{what}: two lists of one length are wanted")
+    return pa, pb, n
+
+
+def _space(workspace):
+    return (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
 
 
 def mnb_pages_copy(planes, src, dst, stream=None):
     """Copy page src[i] to page dst[i] in every plane."""
-    _check(load().mnb_pages_copy(ctypes.byref(planes), *_pair_lists(src, dst, "src, dst"), _stream(stream)), "mnb_pages_copy")
+    if not _codes:
+        _setup()
+    st = (_lib or load()).mnb_pages_copy(planes, *_pair_lists(src, dst, "src, dst"), _current(stream))
+    if st:
+        _check(st, "mnb_pages_copy")
 
 
 def mnb_cache_workspace_size(num_pages, num_seqs, table_stride) -> int:
@@ -499,24 +542,26 @@ def mnb_cache_workspace_size(num_pages, num_seqs, table_stride) -> int:
 
 def mnb_cache_fork(state, src, dst, workspace=None, stream=None):
     """Sequence dst[i] becomes a fork of sequence src[i] (pages shared, nothing copied)."""
-    _check(load().mnb_cache_fork(ctypes.byref(state), *_pair_lists(src, dst, "src, dst"), _ptr(workspace), _nbytes(workspace),
-                                 _stream(stream)), "mnb_cache_fork")
+    st = (_lib or load()).mnb_cache_fork(state, *_pair_lists(src, dst, "src, dst"), *_space(workspace), _current(stream))
+    if st:
+        _check(st, "mnb_cache_fork")
 
 
 def mnb_cache_resize(state, planes, seqs, new_lens, workspace=None, stream=None):
     """Sequence seqs[i] gets new_lens[i] tokens: pages are taken, released, or copied where a shared one grows."""
-    _check(load().mnb_cache_resize(ctypes.byref(state), None if planes is None else ctypes.byref(planes),
-                                   *_pair_lists(seqs, new_lens, "seqs, new_lens"), _ptr(workspace), _nbytes(workspace),
-                                   _stream(stream)), "mnb_cache_resize")
+    st = (_lib or load()).mnb_cache_resize(state, planes, *_pair_lists(seqs, new_lens, "seqs, new_lens"), *_space(workspace), _current(stream))
+    if st:
+        _check(st, "mnb_cache_resize")
 
 
 def mnb_cache_compact(state, planes, refs_out, tables_out, counts, workspace=None, stream=None):
     """Press the held pages together; counts (int32 [2]) gets the held and the moved pages."""
-    _i32(("refs_out", refs_out), ("tables_out", tables_out), ("counts", counts))
+    ptrs = _i32("refs_out", refs_out), _i32("tables_out", tables_out), _i32("counts", counts)
     if refs_out.numel() != state.num_pages or tables_out.numel() != state.num_seqs * state.table_stride or counts.numel() != 2:
-        raise ValueError("refs_out, tables_out: arrays of the state's sizes, and counts [2], are wanted")
-    _check(load().mnb_cache_compact(ctypes.byref(state), ctypes.byref(planes), _ptr(refs_out), _ptr(tables_out),
-                                    _ptr(counts), _ptr(workspace), _nbytes(workspace), _stream(stream)), "mnb_cache_compact")
+        _fail("refs_out, tables_out: arrays of the state's sizes, and counts [2], are wanted")
+    st = (_lib or load()).mnb_cache_compact(state, planes, *ptrs, *_space(workspace), _current(stream))
+    if st:
+        _check(st, "mnb_cache_compact")
 
 
 def mnb_get_device_error() -> int:

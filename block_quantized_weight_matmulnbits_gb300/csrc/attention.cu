@@ -16,7 +16,7 @@ size_t mnb_attention_workspace_size(int64_t batch, int64_t T, int64_t q_heads, i
     if (dtype != MNB_F16 && dtype != MNB_BF16) return 0;
     // the few-row kernel also takes what the many-row one declines
     size_t n = attn::mma_workspace_bytes((int)head_dim);
-    if (attn::tc_serves(q_heads, kv_heads, head_dim, max_q, dtype)) {
+    if (attn::tc_serves(batch, q_heads, kv_heads, head_dim, max_q, max_kv, dtype)) {
         const size_t t = attn::tc_workspace_bytes(batch, T, q_heads, kv_heads, head_dim, max_kv);
         n = t > n ? t : n;
     }
@@ -88,7 +88,7 @@ mnb_status mnb_paged_attention(const mnb_attention_args* a, const mnb_kv_cache* 
     if (c->dtype == MNB_F32) {
         e = attn::launch_generic(p, s);
     } else {
-        if (attn::tc_serves(p.q_heads, p.kv_heads, p.D, p.max_q, p.dtype)) {
+        if (attn::tc_serves(p.batch, p.q_heads, p.kv_heads, p.D, p.max_q, p.max_kv, p.dtype)) {
             family = "attn_tc";
             e = attn::launch_tc(p, s);
         }

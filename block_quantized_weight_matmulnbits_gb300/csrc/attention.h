@@ -44,7 +44,7 @@ cudaError_t launch_mma(const AttnParams& p, cudaStream_t s);
 size_t mma_workspace_bytes(int D);
 // Many rows, bf16 / f16, head_dim up to 128 (attn_tc.cuh); cudaErrorNotSupported
 // (nothing launched) where a stride or size has no tensor map.
-bool tc_serves(int64_t q_heads, int64_t kv_heads, int64_t D, int64_t max_q, int dtype);
+bool tc_serves(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t D, int64_t max_q, int64_t max_kv, int dtype);
 cudaError_t launch_tc(const AttnParams& p, cudaStream_t s);
 size_t tc_workspace_bytes(int64_t batch, int64_t T, int64_t q_heads, int64_t kv_heads, int64_t D, int64_t max_kv);
 // Any type, CUDA cores (attn_generic.cu).

@@ -18,14 +18,26 @@ cudaError_t launch_as(const AttnParams& p, cudaStream_t s) {
     sp.min_tiles = 4;
     sp.part_o = static_cast<float*>(p.workspace);
     sp.part_ml = reinterpret_cast<float2*>(sp.part_o + (size_t)sp.ctas * 2 * mma::kRows * DP);
-    auto kern = mma::attn_mma_kernel<DT, DP>;
+    const int64_t some = p.T * p.group / mma::kRows + (p.batch < p.T ? p.batch : p.T);
+    const int64_t each = (int64_t)p.batch * (((int64_t)p.max_q * p.group + mma::kRows - 1) / mma::kRows);
+    const int64_t units = (int64_t)p.kv_heads * (some < each ? some : each);  // at most
+    const int64_t keys = p.window > 0 && (int64_t)p.window + p.max_q < p.max_kv ? (int64_t)p.window + p.max_q : p.max_kv;
+    // Few units of a moderate context: a cluster each.  Eight CTAs hold about 4 us of loads each at 8192 keys; beyond
+    // that (or with more units than slots for clusters of two) an even cut over all SMs is worth its second kernel.
+    int cl = 1;
+    while (cl < 8 && units * cl * 2 <= sp.ctas) cl *= 2;
+    if (cl > 1 && keys <= (int64_t)1024 * cl) {
+        auto kern = mma::attn_mma_kernel<DT, DP, true>;
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+        if (e != cudaSuccess) return e;
+        return dec::launch_pdl(kern, dim3((unsigned)(units * cl)), dim3(mma::kThreads), S::kSmem, s, cl, p, sp);
+    }
+    auto kern = mma::attn_mma_kernel<DT, DP, false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess) return e;
     e = dec::launch_pdl(kern, dim3(sp.ctas), dim3(mma::kThreads), S::kSmem, s, 1, p, sp);
     if (e != cudaSuccess) return e;
     // No unit is cut when the bounds already say that each is short and has a CTA.
-    const int64_t units = (int64_t)p.kv_heads * (p.T * p.group / mma::kRows + p.batch);
-    const int64_t keys = p.window > 0 && (int64_t)p.window + p.max_q < p.max_kv ? (int64_t)p.window + p.max_q : p.max_kv;
     if (units <= sp.ctas && keys / mma::kKeys + 2 <= sp.whole_tiles) return cudaSuccess;
     auto join = attn_join_kernel<DT, DP, mma::kRows, mma::kKeys>;
     return dec::launch_pdl(join, dim3(sp.ctas, mma::kRows / 4), dim3(128), 0, s, 1, p, sp);

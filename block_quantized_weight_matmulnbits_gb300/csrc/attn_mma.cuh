@@ -33,7 +33,8 @@ template <int DP> struct Shape {
     static constexpr int kHalf = 16 * DP * 2;              // K or V of a stage, bytes
     static constexpr int kStage = 2 * kHalf;
     static constexpr int kRing = kStages * kStage;         // of one warp
-    static constexpr int kSmem = kWarps * kRing + kRows * DP * 2 + kWarps * kRows * 8;
+    static constexpr int kRed = kRows * DP * 4;            // a CTA's joined O, for the cluster form
+    static constexpr int kSmem = kWarps * kRing + kRows * DP * 2 + (kWarps + 1) * kRows * 8 + kRed;
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
@@ -78,21 +79,47 @@ __device__ __forceinline__ float ex2(float x) {
 template <int DP>
 __device__ __forceinline__ uint32_t chunk_at(int r, int c) { return (uint32_t)(r * DP * 2 + ((c ^ (r & 7)) << 4)); }
 
-template <int DT, int DP>
+__device__ __forceinline__ float2 ld_peer2(const void* local, uint32_t rank) {
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(local)), "r"(rank));
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(remote) : "memory");
+    return v;
+}
+
+// CL: few units of a moderate context.  A cluster of 2, 4 or 8 CTAs takes one
+// unit, each CTA an equal range of its keys, and joins the partial results
+// through distributed shared memory: no division to work out, no second kernel.
+template <int DT, int DP, bool CL>
 __global__ void __launch_bounds__(kThreads, Shape<DP>::kCtasPerSm) attn_mma_kernel(const AttnParams p, const SplitParams sp) {
     using S = Shape<DP>;
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t* qs = smem + kWarps * S::kRing;
     float2* ml_s = reinterpret_cast<float2*>(qs + kRows * DP * 2);
+    float2* ml_c = ml_s + kWarps * kRows;         // the CTA's own (m, l) and O of a row, for its cluster
+    float* o_c = reinterpret_cast<float*>(ml_c + kRows);
     float* o_s = reinterpret_cast<float*>(smem);  // [warp][row][DP], once the rings are drained
     static_assert(kWarps * kRows * DP * 4 <= kWarps * S::kRing, "the partial results fit in the rings");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     griddep_wait();
     griddep_launch_dependents();
-    const Division dv = divide<kRows, kKeys, kThreads>(p, sp, blockIdx.x == 0);
-    const int64_t x0 = dv.begin(blockIdx.x), x1 = dv.begin((int64_t)blockIdx.x + 1);
-    if (x0 >= x1) return;
-    Place pl = locate<kRows, kKeys, kThreads>(p, dv, x0);
+    Division dv{};
+    int64_t x0 = blockIdx.x, x1 = 0;
+    int rank = 0, peers = 1;
+    if constexpr (CL) {
+        rank = (int)cluster_ctarank();
+        asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(peers));
+        x0 = blockIdx.x / (unsigned)peers;
+        x1 = x0 + 1;
+        dv.whole = true;
+    } else {
+        dv = divide<kRows, kKeys, kThreads>(p, sp, blockIdx.x == 0);
+        x0 = dv.begin(blockIdx.x);
+        x1 = dv.begin((int64_t)blockIdx.x + 1);
+        if (x0 >= x1) return;
+    }
+    Place pl = locate<kRows, kKeys, kThreads>(p, dv.whole, x0, CL && x0 == 0);
+    if (CL && pl.b < 0) return;  // past the last unit: the whole cluster
 
     const uint32_t ring = smem_u32(smem) + warp * S::kRing, qa = smem_u32(qs);
     const uint16_t* kp = static_cast<const uint16_t*>(p.k);
@@ -106,9 +133,11 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kCtasPerSm) attn_mma_kern
 
     for (int64_t x = x0;;) {
         const int rt = pl.unit / p.kv_heads, hk = pl.unit - rt * p.kv_heads;
-        const int t0 = pl.tile;
+        const int t0 = CL ? (int)((int64_t)pl.s.tiles * rank / peers) : pl.tile;
         const int64_t left = x1 - x;
-        const int t1 = dv.whole ? pl.s.tiles : (int)(left < pl.s.tiles - t0 ? t0 + left : pl.s.tiles);
+        const int t1 = CL         ? (int)((int64_t)pl.s.tiles * (rank + 1) / peers)
+                       : dv.whole ? pl.s.tiles
+                                  : (int)(left < pl.s.tiles - t0 ? t0 + left : pl.s.tiles);
         const int rows = pl.s.n * p.group - rt * kRows < kRows ? pl.s.n * p.group - rt * kRows : kRows;
         const int64_t tok0 = p.q_start[pl.b];
         const int i0 = rt * kRows / p.group, i1 = (rt * kRows + rows - 1) / p.group + 1;
@@ -305,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kCtasPerSm) attn_mma_kern
                 wt[w] = ex2(v.x - base);
                 sum = fmaf(v.y, wt[w], sum);
             }
-            if (r < rows) {
+            if (CL || r < rows) {
                 const int g = rt * kRows + r;
                 const int64_t tk = tok0 + g / p.group;
                 const int h = hk * p.group + g % p.group;
@@ -323,7 +352,11 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kCtasPerSm) attn_mma_kern
                         a[4] = fmaf(v.x, wt[w], a[4]); a[5] = fmaf(v.y, wt[w], a[5]);
                         a[6] = fmaf(v.z, wt[w], a[6]); a[7] = fmaf(v.w, wt[w], a[7]);
                     }
-                    if (done) {
+                    if (CL) {
+                        float4* dst = reinterpret_cast<float4*>(o_c + r * DP + c * 8);
+                        dst[0] = make_float4(a[0], a[1], a[2], a[3]);
+                        dst[1] = make_float4(a[4], a[5], a[6], a[7]);
+                    } else if (done) {
                         if (c * 8 < p.D) {
                             uint4 out;
                             out.x = pack16<DT>(a[0] * inv, a[1] * inv);
@@ -339,10 +372,44 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kCtasPerSm) attn_mma_kern
                     }
                 }
                 if (q8 == 0) {
-                    if (!done) sp.part_ml[at] = make_float2(top, sum);
+                    if (CL) ml_c[r] = make_float2(top, sum);
+                    else if (!done) sp.part_ml[at] = make_float2(top, sum);
                     else if (p.lse) p.lse[tk * p.q_heads + h] = sum > 0.f ? (base + log2f(sum)) * kLn2 : -INFINITY;
                 }
             }
+        }
+        if constexpr (CL) {
+            cluster_sync();
+            // CTA `rank` joins rows rank, rank + peers, ..., a warp a row
+            for (int r = rank + warp * peers; r < rows; r += peers * kWarps) {
+                float top = -INFINITY;
+                for (int c = 0; c < peers; ++c) top = fmaxf(top, ld_peer2(ml_c + r, (uint32_t)c).x);
+                const float base = top == -INFINITY ? 0.f : top;
+                float sum = 0.f, a[DP / 32] = {};
+                for (int c = 0; c < peers; ++c) {
+                    const float2 v = ld_peer2(ml_c + r, (uint32_t)c);
+                    const float w = ex2(v.x - base);
+                    sum = fmaf(v.y, w, sum);
+#pragma unroll
+                    for (int d = 0; d < DP / 64; ++d) {
+                        const float2 u = ld_peer2(o_c + r * DP + d * 64 + lane * 2, (uint32_t)c);
+                        a[2 * d] = fmaf(u.x, w, a[2 * d]);
+                        a[2 * d + 1] = fmaf(u.y, w, a[2 * d + 1]);
+                    }
+                }
+                const int g = rt * kRows + r;
+                const int64_t tk = tok0 + g / p.group;
+                const int h = hk * p.group + g % p.group;
+                const float inv = sum > 0.f ? 1.f / sum : 0.f;
+                uint16_t* dst = static_cast<uint16_t*>(p.o) + tk * p.o_ts + h * p.o_hs;
+#pragma unroll
+                for (int d = 0; d < DP / 64; ++d)
+                    if (d * 64 + lane * 2 < p.D)
+                        *reinterpret_cast<uint32_t*>(dst + d * 64 + lane * 2) = pack16<DT>(a[2 * d] * inv, a[2 * d + 1] * inv);
+                if (lane == 0 && p.lse) p.lse[tk * p.q_heads + h] = sum > 0.f ? (base + log2f(sum)) * kLn2 : -INFINITY;
+            }
+            cluster_sync();  // nobody leaves while its shared memory is read
+            return;
         }
         x += dv.whole ? 1 : t1 - t0;
         if (x >= x1) break;

@@ -106,20 +106,23 @@ struct Place {
     int64_t unit_begin;  // index of the unit's first tile (or of the unit, when whole)
 };
 
-// The place of index x < total, by all threads of the block.
+// The place of index x, by all threads of the block; b < 0 past the last one.
+// WHOLE: x is a unit, not a tile.
 template <int ROWS, int KEYS, int THREADS>
-__device__ Place locate(const AttnParams& p, const Division& d, int64_t x) {
+__device__ Place locate(const AttnParams& p, bool whole, int64_t x, bool tell) {
     __shared__ int64_t sh_s[THREADS / 32];
     __shared__ int sh_b;
     __shared__ int64_t sh_base;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int64_t base = 0;
+    if (threadIdx.x == 0) sh_b = -1;
     for (int b0 = 0; b0 < p.batch; b0 += THREADS) {
         const int b = b0 + threadIdx.x;
         int64_t v = 0;
         if (b < p.batch) {
             const Seq s = load_seq<ROWS, KEYS>(p, b);
-            v = (int64_t)s.row_tiles * p.kv_heads * (d.whole ? 1 : s.tiles);
+            if (s.bad && tell) set_status(p.status, MNB_ERR_INVALID_ARG);
+            v = (int64_t)s.row_tiles * p.kv_heads * (whole ? 1 : s.tiles);
             if (s.tiles == 0) v = 0;
         }
         int64_t incl = v;
@@ -146,11 +149,12 @@ __device__ Place locate(const AttnParams& p, const Division& d, int64_t x) {
     __syncthreads();
     Place pl;
     pl.b = sh_b;
+    if (pl.b < 0) return pl;
     pl.s = load_seq<ROWS, KEYS>(p, pl.b);
     const int64_t r = x - sh_base;
-    const int per = d.whole ? 1 : pl.s.tiles;
+    const int per = whole ? 1 : pl.s.tiles;
     pl.unit = (int)(r / per);
-    pl.tile = d.whole ? 0 : (int)(r - (int64_t)pl.unit * per);
+    pl.tile = whole ? 0 : (int)(r - (int64_t)pl.unit * per);
     pl.unit_begin = x - pl.tile;
     return pl;
 }
@@ -179,7 +183,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnParams p, cons
     const int64_t c = blockIdx.x;
     if (d.whole || c + 1 >= d.ctas) return;
     const int64_t cut = d.begin(c + 1);
-    const Place pl = locate<ROWS, KEYS, 128>(p, d, cut);
+    const Place pl = locate<ROWS, KEYS, 128>(p, d.whole, cut, false);
     if (pl.tile == 0 || d.begin(c) > pl.unit_begin) return;  // no cut, or not the unit's first
     const int64_t unit_end = pl.unit_begin + pl.s.tiles;
     const int row = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;

@@ -437,7 +437,7 @@ cudaError_t launch_copy(const CopyParams& c, cudaStream_t s) {
     // enough blocks for every chunk at once, at most four resident blocks per SM; loops beyond
     int64_t units = c.n * c.planes * c.chunks;
     if (c.name) units += (int64_t)c.num_seqs * ((c.stride + 31) / 32);
-    const int64_t most = (int64_t)dec::sm_count() * 4;
+    const int64_t most = (int64_t)dec::kSms * 4;
     int64_t blocks = (units + kCopyThreads / 32 - 1) / (kCopyThreads / 32);
     if (blocks > most) blocks = most;
     if (blocks < 1) blocks = 1;

@@ -16,7 +16,7 @@ inline bool valid_dt(int d) { return d == kF32 || d == kF16 || d == kBF16; }
 inline int dt_bytes(int d) { return d == kF32 ? 4 : 2; }
 inline bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 inline bool pow2(int64_t v) { return v > 0 && (v & (v - 1)) == 0; }
-inline int sm_count() { return device_info().sm_count > 0 ? device_info().sm_count : 152; }
+constexpr int kSms = 152;  // SMs the grids are sized for
 
 // Launch with programmatic stream serialisation.  Every kernel of these
 // operators runs griddep_wait() before its first access to memory that another

@@ -216,7 +216,7 @@ cudaError_t launch_as(RotParams p, int64_t D, cudaStream_t s) {
     p.per_head = p.n_pair + (int)((D - p.rot) / (WIDE ? V : 1));
     // Four heads a thread once that still leaves two full blocks' worth of
     // threads per SM; one below, where more threads hide more latency.
-    const bool many = WIDE && p.T * heads * p.per_head >= (int64_t)4 * 2048 * dec::sm_count();
+    const bool many = WIDE && p.T * heads * p.per_head >= (int64_t)4 * 2048 * dec::kSms;
     p.groups = many ? (heads + 3) / 4 : heads;
     const int64_t items = p.T * p.groups * p.per_head;
     const int64_t blocks = (items + kThreads - 1) / kThreads;
