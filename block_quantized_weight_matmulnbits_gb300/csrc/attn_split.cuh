@@ -190,30 +190,35 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnParams p, cons
     const int rt = pl.unit / p.kv_heads, hk = pl.unit - rt * p.kv_heads;
     const int r = rt * ROWS + row;
     if (r >= pl.s.n * p.group) return;
-    // CTA c's piece of the unit is its last one (slot 1) unless the CTA begins with it
+    // Pieces: CTAs c .. last, the last with begin(x) < unit_end.  CTA c's piece is its last one (slot 1)
+    // unless it begins with the unit; the others begin inside the unit (slot 0).
+    const int n = (int)((unit_end * d.ctas - 1) / d.total - c) + 1;
+    const int64_t at0 = (c * 2 + (d.begin(c) == pl.unit_begin ? 0 : 1)) * ROWS + row;
+    auto piece = [&](int k) { return k == 0 ? at0 : ((c + k) * 2) * ROWS + row; };
     float m = -INFINITY;
-    int last = (int)c;
-    for (int64_t x = c; x < d.ctas && d.begin(x) < unit_end; ++x) {
-        const int slot = x == c ? (d.begin(x) == pl.unit_begin ? 0 : 1) : 0;
-        m = fmaxf(m, sp.part_ml[((int64_t)x * 2 + slot) * ROWS + row].x);
-        last = (int)x;
-    }
+    for (int k = lane; k < n; k += 32) m = fmaxf(m, sp.part_ml[piece(k)].x);
+#pragma unroll
+    for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, x));
     const float base = m == -INFINITY ? 0.f : m;
     float l = 0.f;
     constexpr int PER = DP / 32;
     float acc[PER] = {};
-    for (int x = (int)c; x <= last; ++x) {
-        const int slot = x == c ? (d.begin(x) == pl.unit_begin ? 0 : 1) : 0;
-        const int64_t at = ((int64_t)x * 2 + slot) * ROWS + row;
-        const float2 ml = sp.part_ml[at];
-        const float w = exp2f(ml.x - base);
-        l = fmaf(ml.y, w, l);
-        const float* o = sp.part_o + at * DP + lane * 2;
+    for (int k0 = 0; k0 < n; k0 += 32) {
+        // a lane's weight of piece k0 + lane, then the pieces in order, eight loads in flight
+        const float2 ml = k0 + lane < n ? sp.part_ml[piece(k0 + lane)] : make_float2(-INFINITY, 0.f);
+        const float w = exp2f(ml.x - base), wl = ml.y * w;
+        const int cnt = n - k0 < 32 ? n - k0 : 32;
+#pragma unroll 8
+        for (int k = 0; k < cnt; ++k) {
+            const float wk = __shfl_sync(~0u, w, k);
+            l += __shfl_sync(~0u, wl, k);
+            const float* o = sp.part_o + piece(k0 + k) * DP + lane * 2;
 #pragma unroll
-        for (int i = 0; i < PER; i += 2) {
-            const float2 v = *reinterpret_cast<const float2*>(o + i * 32);
-            acc[i] = fmaf(v.x, w, acc[i]);
-            acc[i + 1] = fmaf(v.y, w, acc[i + 1]);
+            for (int i = 0; i < PER; i += 2) {
+                const float2 v = *reinterpret_cast<const float2*>(o + i * 32);
+                acc[i] = fmaf(v.x, wk, acc[i]);
+                acc[i + 1] = fmaf(v.y, wk, acc[i + 1]);
+            }
         }
     }
     const int64_t t = p.q_start[pl.b] + r / p.group;

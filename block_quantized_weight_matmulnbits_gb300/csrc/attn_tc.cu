@@ -103,7 +103,7 @@ cudaError_t launch_as(const AttnParams& p, const Plan& pl, cudaStream_t s) {
 bool tc_serves(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t D, int64_t max_q, int64_t max_kv, int dtype) {
     const int64_t group = q_heads / kv_heads, rows = max_q * group;
     if (dtype == kF32 || D > 128 || group > tca::kRows || rows <= 16) return false;
-    return rows > 32 || (double)batch * (double)max_kv * (double)(kv_heads * D) * 4.0 > 64e6;
+    return rows > 32 || (double)batch * (double)max_kv * (double)(kv_heads * D) * 4.0 > 100e6;
 }
 
 size_t tc_workspace_bytes(int64_t batch, int64_t T, int64_t q_heads, int64_t kv_heads, int64_t D, int64_t max_kv) {

@@ -804,22 +804,29 @@ __global__ void __launch_bounds__(256) attn_tc_join_kernel(const AttnParams p, c
     const int i = (u.pair * 2 + x) * tp.tokens + r / p.group;
     if (r >= tp.tokens * p.group || i >= u.n) return;
     const int64_t base = idx * tp.splits * 256 + row;
+    // a lane's (m, l) of split lane (at most 64: two rounds), then the splits in order
     float top = -INFINITY;
-    for (int s = 0; s < tp.splits; ++s) top = fmaxf(top, tp.part_ml[base + s * 256].x);
+    for (int s = lane; s < tp.splits; s += 32) top = fmaxf(top, tp.part_ml[base + s * 256].x);
+#pragma unroll
+    for (int k = 16; k; k >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, k));
     constexpr int PER = DP / 32;
     float acc[PER] = {}, l = 0.f;
-    if (top > -INFINITY) {
-        for (int s = 0; s < tp.splits; ++s) {
-            const float2 ml = tp.part_ml[base + s * 256];
-            if (ml.x == -INFINITY) continue;  // no key of the range is visible: its O may not be written
-            const float w = exp2f(ml.x - top);
-            l = fmaf(ml.y, w, l);
-            const float* o = tp.part_o + (base + s * 256) * DP + lane * PER;
-            float v[PER];
-            if constexpr (PER == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(o);
-            else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(o);
+    for (int s0 = 0; s0 < tp.splits && top > -INFINITY; s0 += 32) {
+        const float2 ml = s0 + lane < tp.splits ? tp.part_ml[base + (s0 + lane) * 256] : make_float2(-INFINITY, 0.f);
+        const float w = exp2f(ml.x - top), wl = ml.y * w;
+        const int cnt = tp.splits - s0 < 32 ? tp.splits - s0 : 32;
+#pragma unroll 4
+        for (int s = 0; s < cnt; ++s) {
+            const float ws = __shfl_sync(~0u, w, s);
+            l += __shfl_sync(~0u, wl, s);
+            const float* o = tp.part_o + (base + (s0 + s) * 256) * DP + lane * PER;
+            float v[PER] = {};
+            if (ws > 0.f) {  // (a range without a visible key leaves its O unwritten)
+                if constexpr (PER == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(o);
+                else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(o);
+            }
 #pragma unroll
-            for (int k = 0; k < PER; ++k) acc[k] = fmaf(v[k], w, acc[k]);
+            for (int k = 0; k < PER; ++k) acc[k] = fmaf(v[k], ws, acc[k]);
         }
     }
     const int64_t tk = (int64_t)p.q_start[u.b] + i;

@@ -121,6 +121,26 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotParams p) {
     const int g = (int)(r / (uint32_t)p.per_head);
     const int c = (int)(r - (uint32_t)g * (uint32_t)p.per_head);
 
+    const bool turns = c < p.n_pair;
+    const int i0 = turns ? c * V : p.rot + (c - p.n_pair) * (WIDE ? V : 1);  // first depth of the item
+    const int half = p.rot >> 1;
+    const int heads = p.h_q + 2 * p.h_k;
+
+    // The values first: their loads need nothing that is looked up below.
+    Pack<DT, V, WIDE> a[HPT], b[HPT];
+#pragma unroll
+    for (int j = 0; j < HPT; ++j) {
+        const int h = g + j * p.groups;
+        if (h < heads) {
+            const int seg = h < p.h_q ? 0 : h < p.h_q + p.h_k ? 1 : 2;
+            const int hh = h - (seg == 0 ? 0 : seg == 1 ? p.h_q : p.h_q + p.h_k);
+            const T* in = static_cast<const T*>(p.src[seg]) + t * p.src_ts[seg] + hh * p.src_hs[seg] + i0;
+            if (WIDE || turns) a[j].load(in);
+            else a[j].v[0] = *in;  // a copied depth; D - rot may be odd
+            if (NV == 2 && turns) b[j].load(in + half);
+        }
+    }
+
     int64_t pos, row = 0;  // position for the table, offset of the token's row in the pages
     if (p.q_start) {
         if (t >= p.q_start[p.batch]) return;
@@ -142,39 +162,6 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotParams p) {
         set_status(p.status, MNB_ERR_INVALID_ARG);
         return;
     }
-
-    const bool turns = c < p.n_pair;
-    const int i0 = turns ? c * V : p.rot + (c - p.n_pair) * (WIDE ? V : 1);  // first depth of the item
-    const int half = p.rot >> 1;
-    const int heads = p.h_q + 2 * p.h_k;
-
-    const T* in[HPT];
-    T* out[HPT];
-    bool turn[HPT];
-#pragma unroll
-    for (int j = 0; j < HPT; ++j) {
-        const int h = g + j * p.groups;
-        in[j] = nullptr;
-        out[j] = nullptr;
-        turn[j] = turns;
-        if (h < heads) {
-            const int seg = h < p.h_q ? 0 : h < p.h_q + p.h_k ? 1 : 2;
-            const int hh = h - (seg == 0 ? 0 : seg == 1 ? p.h_q : p.h_q + p.h_k);
-            in[j] = static_cast<const T*>(p.src[seg]) + t * p.src_ts[seg] + hh * p.src_hs[seg] + i0;
-            out[j] = static_cast<T*>(p.dst[seg]) +
-                     (seg == 0 ? t * p.out_ts + hh * p.out_hs : row + hh * p.head_stride) + i0;
-            turn[j] = turns && seg < 2;
-        }
-    }
-    Pack<DT, V, WIDE> a[HPT], b[HPT];
-#pragma unroll
-    for (int j = 0; j < HPT; ++j) {
-        if (in[j]) {
-            if (WIDE || turns) a[j].load(in[j]);
-            else a[j].v[0] = *in[j];  // a copied depth; D - rot may be odd
-            if (NV == 2 && turns) b[j].load(in[j] + half);
-        }
-    }
     float cs[NC], sn[NC];
     if (turns) {
         const int64_t at = pos * half + (INTER ? i0 / 2 : i0);
@@ -185,8 +172,11 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotParams p) {
     }
 #pragma unroll
     for (int j = 0; j < HPT; ++j) {
-        if (!in[j]) continue;
-        if (turn[j]) {
+        const int h = g + j * p.groups;
+        if (h >= heads) continue;
+        const int seg = h < p.h_q ? 0 : h < p.h_q + p.h_k ? 1 : 2;
+        const int hh = h - (seg == 0 ? 0 : seg == 1 ? p.h_q : p.h_q + p.h_k);
+        if (turns && seg < 2) {
             if constexpr (INTER) {
 #pragma unroll
                 for (int i = 0; i < V / 2; ++i) {
@@ -203,9 +193,10 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotParams p) {
                 }
             }
         }
-        if (WIDE || turns) a[j].store(out[j]);
-        else *out[j] = a[j].v[0];
-        if (NV == 2 && turns) b[j].store(out[j] + half);
+        T* out = static_cast<T*>(p.dst[seg]) + (seg == 0 ? t * p.out_ts + hh * p.out_hs : row + hh * p.head_stride) + i0;
+        if (WIDE || turns) a[j].store(out);
+        else *out = a[j].v[0];
+        if (NV == 2 && turns) b[j].store(out + half);
     }
 }
 
