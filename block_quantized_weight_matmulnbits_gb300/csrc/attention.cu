@@ -35,6 +35,7 @@ mnb_status mnb_paged_attention(const mnb_attention_args* a, const mnb_kv_cache* 
     for (int64_t x : st)
         if (x < 0 || x % vec != 0 || x >= (int64_t(1) << 38)) return MNB_ERR_INVALID_ARG;
     if (a->T == 0) return MNB_OK;
+    if (a->T * a->q_heads >= i31) return MNB_ERR_UNSUPPORTED;
     if (!a->q || !a->o || !a->q_start || !dec::aligned_to(a->q, 16) || !dec::aligned_to(a->o, 16) ||
         !dec::aligned_to(a->lse, 4) || !dec::aligned_to(a->q_start, 4))
         return MNB_ERR_INVALID_ARG;

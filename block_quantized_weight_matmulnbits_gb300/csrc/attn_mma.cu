@@ -18,6 +18,7 @@ cudaError_t launch_as(const AttnParams& p, cudaStream_t s) {
     sp.min_tiles = 4;
     sp.part_o = static_cast<float*>(p.workspace);
     sp.part_ml = reinterpret_cast<float2*>(sp.part_o + (size_t)sp.ctas * 2 * mma::kRows * DP);
+    sp.cut = reinterpret_cast<int4*>(sp.part_ml + (size_t)sp.ctas * 2 * mma::kRows);
     const int64_t some = p.T * p.group / mma::kRows + (p.batch < p.T ? p.batch : p.T);
     const int64_t each = (int64_t)p.batch * (((int64_t)p.max_q * p.group + mma::kRows - 1) / mma::kRows);
     const int64_t units = (int64_t)p.kv_heads * (some < each ? some : each);  // at most
@@ -39,8 +40,9 @@ cudaError_t launch_as(const AttnParams& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     // No unit is cut when the bounds already say that each is short and has a CTA.
     if (units <= sp.ctas && keys / mma::kKeys + 2 <= sp.whole_tiles) return cudaSuccess;
-    auto join = attn_join_kernel<DT, DP, mma::kRows, mma::kKeys>;
-    return dec::launch_pdl(join, dim3(sp.ctas, mma::kRows / 4), dim3(128), 0, s, 1, p, sp);
+    auto join = attn_join_kernel<DT, DP, mma::kRows>;
+    const int64_t rows = (int64_t)p.max_q * p.group;
+    return dec::launch_pdl(join, dim3(sp.ctas, (unsigned)(rows < mma::kRows ? rows : mma::kRows)), dim3(128), 0, s, 1, p, sp);
 }
 
 template <int DT>
@@ -54,7 +56,7 @@ cudaError_t launch_dt(const AttnParams& p, cudaStream_t s) {
 
 size_t mma_workspace_bytes(int D) {
     const int dp = D <= 64 ? 64 : D <= 128 ? 128 : 256;
-    return (size_t)ctas_of(dp) * 2 * mma::kRows * (dp + 2) * 4;
+    return (size_t)ctas_of(dp) * (2 * mma::kRows * (dp + 2) * 4 + sizeof(int4));
 }
 
 cudaError_t launch_mma(const AttnParams& p, cudaStream_t s) {

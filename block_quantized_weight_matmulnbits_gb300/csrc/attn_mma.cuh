@@ -116,6 +116,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kCtasPerSm) attn_mma_kern
         dv = divide<kRows, kKeys, kThreads>(p, sp, blockIdx.x == 0);
         x0 = dv.begin(blockIdx.x);
         x1 = dv.begin((int64_t)blockIdx.x + 1);
+        if (threadIdx.x == 0) sp.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
         if (x0 >= x1) return;
     }
     Place pl = locate<kRows, kKeys, kThreads>(p, dv.whole, x0, CL && x0 == 0);
@@ -412,6 +413,12 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kCtasPerSm) attn_mma_kern
             return;
         }
         x += dv.whole ? 1 : t1 - t0;
+        if (!CL && tid == 0 && !dv.whole && x >= x1 && x0 <= pl.unit_begin && t1 < pl.s.tiles) {
+            // this range's end is the first cut of the unit; its pieces end with the last CTA that begins before its end
+            const int64_t last = ((pl.unit_begin + pl.s.tiles) * dv.ctas - 1) / dv.total;
+            sp.cut[blockIdx.x] = make_int4((int)tok0, rt * kRows, hk | rows << 16,
+                                           (int)(last - blockIdx.x + 1) * 2 + (x0 == pl.unit_begin ? 0 : 1));
+        }
         if (x >= x1) break;
         __syncthreads();  // the exchange buffer becomes the rings again
         next_unit<kRows, kKeys>(p, dv, pl);

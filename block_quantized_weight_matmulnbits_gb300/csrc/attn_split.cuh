@@ -23,6 +23,8 @@ struct SplitParams {
     int min_tiles;   // otherwise a CTA takes at least this many tiles
     float* part_o;   // [ctas][2][rows][DP]
     float2* part_ml; // [ctas][2][rows]: maximum (log2 units) and sum
+    int4* cut;       // [ctas]: the unit that the end of CTA c's range is the first to cut, for the join:
+                     // first token of the sequence, first row inside it, key head + rows << 16, pieces * 2 + slot of the first
 };
 
 struct Seq {
@@ -172,65 +174,80 @@ __device__ __forceinline__ void next_unit(const AttnParams& p, const Division& d
     } while (pl.s.tiles == 0);
 }
 
-// Joins the partial results of the units that a boundary cuts.  Block (c, y)
-// looks at the boundary between CTA c and c + 1; if it is the first one inside
-// its unit, the block joins the unit's rows [y * 4, y * 4 + 4).
-template <int DT, int DP, int ROWS, int KEYS>
+// Joins the partial results of the units that a boundary cuts: block (c, y)
+// takes row y of the unit that CTA c is the first to leave unfinished.  The CTAs
+// of the first kernel wrote what it needs to know.  Each of the four warps adds
+// every fourth piece, eight loads ahead of their use (one warp a row, a load at a
+// time, took 20 us for the 38 pieces of a single long context), and the four sums
+// are added in order.
+template <int DT, int DP, int ROWS>
 __global__ void __launch_bounds__(128) attn_join_kernel(const AttnParams p, const SplitParams sp) {
+    constexpr int W = 4, AHEAD = 8, PER = DP / 64;  // warps, pieces loaded ahead, pairs of depths a lane owns
+    __shared__ float2 acc_s[W][DP / 2];
+    __shared__ float l_s[W];
     griddep_wait();
     griddep_launch_dependents();
-    const Division d = divide<ROWS, KEYS, 128>(p, sp, false);
-    const int64_t c = blockIdx.x;
-    if (d.whole || c + 1 >= d.ctas) return;
-    const int64_t cut = d.begin(c + 1);
-    const Place pl = locate<ROWS, KEYS, 128>(p, d.whole, cut, false);
-    if (pl.tile == 0 || d.begin(c) > pl.unit_begin) return;  // no cut, or not the unit's first
-    const int64_t unit_end = pl.unit_begin + pl.s.tiles;
-    const int row = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const int rt = pl.unit / p.kv_heads, hk = pl.unit - rt * p.kv_heads;
-    const int r = rt * ROWS + row;
-    if (r >= pl.s.n * p.group) return;
-    // Pieces: CTAs c .. last, the last with begin(x) < unit_end.  CTA c's piece is its last one (slot 1)
-    // unless it begins with the unit; the others begin inside the unit (slot 0).
-    const int n = (int)((unit_end * d.ctas - 1) / d.total - c) + 1;
-    const int64_t at0 = (c * 2 + (d.begin(c) == pl.unit_begin ? 0 : 1)) * ROWS + row;
-    auto piece = [&](int k) { return k == 0 ? at0 : ((c + k) * 2) * ROWS + row; };
+    const int c = blockIdx.x, row = blockIdx.y;
+    const int4 cut = sp.cut[c];
+    const int n = cut.w >> 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (n == 0 || row >= cut.z >> 16) return;
+    // CTA c's piece is its last one (slot 1) unless its range begins with the unit; those after it begin inside the unit
+    const int64_t at0 = (int64_t)(c * 2 + (cut.w & 1)) * ROWS + row;
+    auto piece = [&](int k) { return k == 0 ? at0 : (int64_t)((c + k) * 2) * ROWS + row; };
     float m = -INFINITY;
     for (int k = lane; k < n; k += 32) m = fmaxf(m, sp.part_ml[piece(k)].x);
 #pragma unroll
     for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, x));
     const float base = m == -INFINITY ? 0.f : m;
     float l = 0.f;
-    constexpr int PER = DP / 32;
-    float acc[PER] = {};
-    for (int k0 = 0; k0 < n; k0 += 32) {
-        // a lane's weight of piece k0 + lane, then the pieces in order, eight loads in flight
-        const float2 ml = k0 + lane < n ? sp.part_ml[piece(k0 + lane)] : make_float2(-INFINITY, 0.f);
-        const float w = exp2f(ml.x - base), wl = ml.y * w;
-        const int cnt = n - k0 < 32 ? n - k0 : 32;
-#pragma unroll 8
-        for (int k = 0; k < cnt; ++k) {
-            const float wk = __shfl_sync(~0u, w, k);
-            l += __shfl_sync(~0u, wl, k);
-            const float* o = sp.part_o + piece(k0 + k) * DP + lane * 2;
+    float2 acc[PER] = {};
+    for (int k0 = warp; k0 < n; k0 += W * AHEAD) {
+        float2 v[AHEAD][PER], ml[AHEAD];
 #pragma unroll
-            for (int i = 0; i < PER; i += 2) {
-                const float2 v = *reinterpret_cast<const float2*>(o + i * 32);
-                acc[i] = fmaf(v.x, wk, acc[i]);
-                acc[i + 1] = fmaf(v.y, wk, acc[i + 1]);
+        for (int a = 0; a < AHEAD; ++a) {
+            const int k = k0 + a * W;
+            ml[a] = make_float2(-INFINITY, 0.f);
+            if (k < n) {
+                const int64_t at = piece(k);
+                ml[a] = sp.part_ml[at];
+#pragma unroll
+                for (int i = 0; i < PER; ++i) v[a][i] = *reinterpret_cast<const float2*>(sp.part_o + at * DP + i * 64 + lane * 2);
+            }
+        }
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a) {
+            if (k0 + a * W >= n) continue;
+            const float w = exp2f(ml[a].x - base);
+            l = fmaf(ml[a].y, w, l);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                acc[i].x = fmaf(v[a][i].x, w, acc[i].x);
+                acc[i].y = fmaf(v[a][i].y, w, acc[i].y);
             }
         }
     }
-    const int64_t t = p.q_start[pl.b] + r / p.group;
-    const int h = hk * p.group + r % p.group;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    const int64_t ob = t * p.o_ts + h * p.o_hs;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int dd = (i / 2) * 64 + lane * 2 + (i & 1);
-        if (dd < p.D) store_f32(p.o, ob + dd, acc[i] * inv, DT);
+    for (int i = 0; i < PER; ++i) acc_s[warp][i * 32 + lane] = acc[i];
+    if (lane == 0) l_s[warp] = l;
+    __syncthreads();
+    const int r = cut.y + row;
+    const int64_t t = (int64_t)cut.x + r / p.group;
+    const int h = (cut.z & 0xFFFF) * p.group + r % p.group;
+    l = (l_s[0] + l_s[1]) + (l_s[2] + l_s[3]);
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    for (int d = threadIdx.x; d * 2 < p.D; d += W * 32) {
+        float2 a = acc_s[0][d];
+#pragma unroll
+        for (int w = 1; w < W; ++w) {
+            a.x += acc_s[w][d].x;
+            a.y += acc_s[w][d].y;
+        }
+        const int64_t o = t * p.o_ts + h * p.o_hs + d * 2;
+        store_f32(p.o, o, a.x * inv, DT);
+        store_f32(p.o, o + 1, a.y * inv, DT);
     }
-    if (lane == 0 && p.lse) p.lse[t * p.q_heads + h] = l > 0.f ? (base + log2f(l)) * kLn2 : -INFINITY;
+    if (threadIdx.x == 0 && p.lse) p.lse[t * p.q_heads + h] = l > 0.f ? (base + log2f(l)) * kLn2 : -INFINITY;
 }
 
 }  // namespace attn

@@ -513,6 +513,7 @@ MNB_API mnb_status mnb_rotary_append(const mnb_rotary_args* args, const mnb_kv_c
  * type for the product with V, as its operand.
  *   q, o       device [T, q_heads, head_dim] of the cache's dtype, 16-byte
  *              aligned, strides in elements, multiples of 16 bytes
+ *              (T * q_heads below 2^31, else MNB_ERR_UNSUPPORTED)
  *   lse        device f32 [T, q_heads] or NULL
  *   q_start    device int32 [batch + 1], as for mnb_rotary_append; o and lse
  *              of tokens from q_start[batch] on are left alone
