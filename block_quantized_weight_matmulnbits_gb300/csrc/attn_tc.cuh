@@ -573,14 +573,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
                 more = clc_taken(smem_u32(response), &block);
                 __syncwarp();
             }
-            if (!ok) {  // let the copies in flight land
+            if (!ok) {
                 give_up(abort_v, p);
                 __syncwarp();
                 tc::drain_wait(clc_bar, (uint32_t)(asked - 1) & 1u);
-                for (int x = 0; x < 2; ++x)
-                    if (q_used[x]) tc::drain_wait(&q_full[x], (uint32_t)(q_used[x] - 1) & 1u);
-                for (int e = i - R < 0 ? 0 : i - R; e < i; ++e) tc::drain_wait(&kv_full[e % R], (uint32_t)((e / R) & 1));
             }
+            // every copy has landed before the CTA ends (at once, unless a role gave up)
+            for (int x = 0; x < 2; ++x)
+                if (q_used[x]) tc::drain_wait(&q_full[x], (uint32_t)(q_used[x] - 1) & 1u);
+            for (int e = i - R < 0 ? 0 : i - R; e < i; ++e) tc::drain_wait(&kv_full[e % R], (uint32_t)((e / R) & 1));
         } else if (warp == kMmaWarp) {
             if (elect_one() && !mma_role<DT, DP>(sh, p, tmem, box_log)) {
                 give_up(abort_v, p);
