@@ -47,13 +47,14 @@ constexpr int kSoftWarps = 8, kMmaWarp = 8, kTmaWarp = 9, kZeroWarp = 10, kThrea
 // 88 of each of its threads back, the softmax warpgroups take 40 more: 256 * 208 + 128 * 80 = 63488.
 constexpr int kSoftRegs = 208, kCtlRegs = 80;
 constexpr int kBarBytes = 512;         // jobs and barriers
+constexpr int kStageBytes = 4096;      // of one softmax warp: its 32 rows, 128 bytes at a time, on their way out
 constexpr int kHalfBytes = 128 * 128;  // 128 rows of 64 values: one swizzled half of a Q, K or V tile
 
 template <int DP> struct Shape {
     static constexpr int kHalves = DP / 64;
     static constexpr int kTile = kHalves * kHalfBytes;
-    static constexpr int kRing = DP == 128 ? 5 : 8;
-    static constexpr int kSmem = 1024 + 2 * kTile + kRing * kTile + kBarBytes;
+    static constexpr int kRing = DP == 128 ? 4 : 8;
+    static constexpr int kSmem = 1024 + 2 * kTile + kRing * kTile + kSoftWarps * kStageBytes + kBarBytes;
 };
 
 struct TcParams {
@@ -272,6 +273,7 @@ struct Shared {
     static constexpr int R = S::kRing;
     uint8_t* qs;    // [2][halves][128 rows][128 B]
     uint8_t* ring;  // [R][halves][128 rows][128 B]
+    uint8_t* stage; // [8 softmax warps][32 rows][128 B]
     Job* jobs;      // [2]
     uint8_t* response;
     uint64_t *kv_full, *kv_empty;                   // [R]
@@ -283,7 +285,8 @@ struct Shared {
     __device__ __forceinline__ explicit Shared(uint8_t* smem) {
         qs = smem;
         ring = smem + 2 * S::kTile;
-        jobs = reinterpret_cast<Job*>(ring + R * S::kTile);
+        stage = ring + R * S::kTile;
+        jobs = reinterpret_cast<Job*>(stage + kSoftWarps * kStageBytes);
         response = reinterpret_cast<uint8_t*>(jobs + 2);
         kv_full = reinterpret_cast<uint64_t*>(response + 16);
         kv_empty = kv_full + R;
@@ -738,40 +741,59 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
             const int h = job->hk * p.group + r_head;
             const int64_t part = (int64_t)job->part * 256 + x * 128 + r;
             const float inv = l > 0.f ? 1.f / l : 0.f;
-            uint16_t* orow = static_cast<uint16_t*>(p.o) + tk * p.o_ts + h * p.o_hs;
-#pragma unroll
-            for (int c = 0; c < DP / 32; ++c) {
+            // O leaves through shared memory, 128 bytes of the warp's 32 rows at a time, so that eight lanes store a row's
+            // whole lines.  (A thread storing its own row touches 32 lines an instruction: 7000 cycles a unit for bf16,
+            // 14000 for the f32 partial results, with the tensor pipe idle.)
+            const bool whole = tp.splits == 1;
+            uint8_t* const row = whole ? reinterpret_cast<uint8_t*>(static_cast<uint16_t*>(p.o) + tk * p.o_ts + h * p.o_hs)
+                                       : reinterpret_cast<uint8_t*>(tp.part_o + part * DP);
+            const uint32_t rows_ok = __ballot_sync(~0u, row_ok && (whole || nx > 0));
+            uint8_t* const stage = sh.stage + warp * kStageBytes;
+            const int depths = whole ? 64 : 32;  // in 128 bytes
+            for (int c = 0; c < DP; c += depths) {
                 uint32_t v[32];
                 if (nx > 0) {
-                    tc::ld_32x32b<32>(to + (uint32_t)(c * 32), v);
+                    tc::ld_32x32b<32>(to + (uint32_t)c, v);
                     tc::wait_ld();
-                    if (c == DP / 32 - 1) {  // O may be written by the next unit
-                        tc::fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&o_free[x]);
-                    }
                 } else {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) v[e] = 0u;
                 }
-                if (!row_ok) continue;
-                if (tp.splits == 1) {
+                if (whole) {
+                    uint32_t w[32];
+                    if (nx > 0) {
+                        tc::ld_32x32b<32>(to + (uint32_t)c + 32u, w);
+                        tc::wait_ld();
+                    } else {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        if (c * 32 + e < p.D) {
-                            uint4 w;
-                            w.x = pack16<DT>(__uint_as_float(v[e]) * inv, __uint_as_float(v[e + 1]) * inv);
-                            w.y = pack16<DT>(__uint_as_float(v[e + 2]) * inv, __uint_as_float(v[e + 3]) * inv);
-                            w.z = pack16<DT>(__uint_as_float(v[e + 4]) * inv, __uint_as_float(v[e + 5]) * inv);
-                            w.w = pack16<DT>(__uint_as_float(v[e + 6]) * inv, __uint_as_float(v[e + 7]) * inv);
-                            *reinterpret_cast<uint4*>(orow + c * 32 + e) = l > 0.f ? w : make_uint4(0, 0, 0, 0);
-                        }
+                        for (int e = 0; e < 32; ++e) w[e] = 0u;
                     }
-                } else if (nx > 0) {
-                    uint4* o = reinterpret_cast<uint4*>(tp.part_o + part * DP + c * 32);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) o[e] = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                    for (int e = 0; e < 16; ++e) {
+                        v[e] = pack16<DT>(__uint_as_float(v[2 * e]) * inv, __uint_as_float(v[2 * e + 1]) * inv);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[16 + e] = pack16<DT>(__uint_as_float(w[2 * e]) * inv, __uint_as_float(w[2 * e + 1]) * inv);
                 }
+                if (c + depths >= DP && nx > 0) {  // O may be written by the next unit
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&o_free[x]);
+                }
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    *reinterpret_cast<uint4*>(stage + lane * 128 + ((q ^ (lane & 7)) << 4)) = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                __syncwarp();
+                const int q = lane & 7;
+#pragma unroll
+                for (int it = 0; it < 8; ++it) {
+                    const int rr = it * 4 + (lane >> 3);
+                    const uint4 u = *reinterpret_cast<const uint4*>(stage + rr * 128 + ((q ^ (rr & 7)) << 4));
+                    uint8_t* const to_row = reinterpret_cast<uint8_t*>(__shfl_sync(~0u, reinterpret_cast<unsigned long long>(row), rr));
+                    if ((rows_ok >> rr & 1u) && (!whole || c + q * 8 < p.D))
+                        *reinterpret_cast<uint4*>(to_row + c * (whole ? 2 : 4) + q * 16) = u;
+                }
+                __syncwarp();
             }
             if (row_ok) {
                 if (tp.splits > 1) tp.part_ml[part] = make_float2(m, l);
