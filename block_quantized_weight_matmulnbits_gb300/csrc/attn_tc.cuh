@@ -28,8 +28,10 @@
 //                have not started (cluster launch control) and tells the others
 //                what is next, so a unit's first loads and products overlap the
 //                epilogue of the one before and nothing is set up twice
-//   warp 10      zeroes V rows past the visible keys, whose pages may hold
-//                anything (0 * NaN is NaN); warp 11 completes the warpgroup
+//   warp 10      watches the ring, so that the MMA thread polls one barrier a
+//                step for it, and zeroes V rows past the visible keys, whose
+//                pages may hold anything (0 * NaN is NaN); warp 11 completes the
+//                warpgroup
 // Few units (a short chunk over a long context) are cut into ranges of key
 // tiles; attn_tc_join adds their (m, l, O) in order.
 #pragma once
@@ -42,10 +44,11 @@ namespace attn {
 namespace tca {
 
 constexpr int kRows = 128, kKeys = 128;
-constexpr int kSoftWarps = 8, kMmaWarp = 8, kTmaWarp = 9, kZeroWarp = 10, kThreads = 384;
+constexpr int kSoftWarps = 8, kMmaWarp = 8, kTmaWarp = 9, kRingWarp = 10, kThreads = 384;
 // Registers: 384 threads start with 168 each (64512); the third warpgroup (MMA, TMA, zeroing) gives
 // 88 of each of its threads back, the softmax warpgroups take 40 more: 256 * 208 + 128 * 80 = 63488.
 constexpr int kSoftRegs = 208, kCtlRegs = 80;
+constexpr int kReady = 8;              // steps that may be announced ahead: more than the ring holds
 constexpr int kBarBytes = 512;         // jobs and barriers
 constexpr int kStageBytes = 4096;      // of one softmax warp: its 32 rows, 128 bytes at a time, on their way out
 constexpr int kHalfBytes = 128 * 128;  // 128 rows of 64 values: one swizzled half of a Q, K or V tile
@@ -281,7 +284,7 @@ struct Shared {
     uint64_t *p_half, *p_ready;                     // P of the first 64 keys, of the others: one arrival per softmax warp
     uint64_t *o_full, *o_free;
     uint64_t *job_full, *job_empty;                 // [2] per slot
-    uint64_t *v_edge, *v_zeroed, *clc_bar, *done;
+    uint64_t *kv_ready, *clc_bar, *done;            // kv_ready [kReady] by step
     __device__ __forceinline__ explicit Shared(uint8_t* smem) {
         qs = smem;
         ring = smem + 2 * S::kTile;
@@ -299,11 +302,10 @@ struct Shared {
         o_free = o_full + 2;
         job_full = o_free + 2;
         job_empty = job_full + 2;
-        v_edge = job_empty + 2;
-        v_zeroed = v_edge + 1;
-        clc_bar = v_zeroed + 1;
+        kv_ready = job_empty + 2;
+        clc_bar = kv_ready + kReady;
         done = clc_bar + 1;
-        static_assert(2 * sizeof(Job) + 16 + (2 * R + 22) * 8 + 8 <= kBarBytes, "barriers fit");
+        static_assert(2 * sizeof(Job) + 16 + (2 * R + 20 + kReady) * 8 + 8 <= kBarBytes, "barriers fit");
     }
 };
 
@@ -317,7 +319,7 @@ __device__ __forceinline__ bool zero_range(const Range& rg, int j, int box_log, 
 
 // The thread that issues all MMAs; false when a wait ran out.
 template <int DT, int DP>
-__device__ __forceinline__ bool mma_role(const Shared<DP>& sh, const AttnParams& p, uint32_t tmem, int box_log) {
+__device__ __forceinline__ bool mma_role(const Shared<DP>& sh, const AttnParams& p, uint32_t tmem) {
     using S = Shape<DP>;
     constexpr int R = S::kRing;
     constexpr uint64_t kTileStep = S::kTile >> 4;
@@ -343,7 +345,7 @@ __device__ __forceinline__ bool mma_role(const Shared<DP>& sh, const AttnParams&
                        (!first || kk > 0) ? 1u : 0u);
     };
     int slot = 0;  // next ring entry, and the parity of its phase
-    uint32_t phase = 0, edges = 0;
+    uint32_t phase = 0, seen = 0;  // (seen: steps of all units so far)
     uint32_t cnt_a = 0, cnt_b = 0, units_a = 0, units_b = 0;  // key tiles, and units with any, so far
     for (uint32_t k = 0;; ++k) {
         const Job* job = &sh.jobs[k & 1];
@@ -353,9 +355,6 @@ __device__ __forceinline__ bool mma_role(const Shared<DP>& sh, const AttnParams&
         mbar_arrive(&sh.job_empty[k & 1]);
         const int steps = rg.na > rg.nb ? rg.na : rg.nb;
         if (steps == 0) continue;
-        int z0, z1;
-        const int edge_lo = zero_range(rg, 0, box_log, &z0, &z1) ? 0 : -1;
-        const int edge_hi = zero_range(rg, steps - 1, box_log, &z0, &z1) ? steps - 1 : -1;
         int sv = 0, sk = slot;
         if (!spin_for(&sh.kv_full[slot], phase, limit)) return false;
 #pragma unroll
@@ -370,23 +369,19 @@ __device__ __forceinline__ bool mma_role(const Shared<DP>& sh, const AttnParams&
         }
         tc::commit(&sh.kv_empty[sk]);
         for (int j = 0; j < steps; ++j) {
-            // V of this step, K of the next
+            // V of this step and K of the next: warp 10 watches for them
             if (++slot == R) {
                 slot = 0;
                 phase ^= 1u;
             }
             sv = slot;
-            if (!spin_for(&sh.kv_full[sv], phase, limit)) return false;
-            if (j == edge_lo || j == edge_hi) {  // warp 10 clears the V rows that no row sees
-                mbar_arrive(sh.v_edge);
-                if (!spin_for(sh.v_zeroed, edges++ & 1u, limit)) return false;
-            }
             if (++slot == R) {
                 slot = 0;
                 phase ^= 1u;
             }
             sk = slot;
-            if (j + 1 < steps && !spin_for(&sh.kv_full[sk], phase, limit)) return false;
+            if (!spin_for(&sh.kv_ready[seen & (kReady - 1)], (seen / kReady) & 1u, limit)) return false;
+            ++seen;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const int nx = x ? rg.nb : rg.na;
@@ -437,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
     uint64_t *const kv_full = sh.kv_full, *const kv_empty = sh.kv_empty, *const q_full = sh.q_full, *const q_empty = sh.q_empty;
     uint64_t *const s_full = sh.s_full, *const p_half = sh.p_half, *const p_ready = sh.p_ready, *const o_full = sh.o_full;
     uint64_t *const o_free = sh.o_free, *const job_full = sh.job_full, *const job_empty = sh.job_empty;
-    uint64_t *const v_edge = sh.v_edge, *const v_zeroed = sh.v_zeroed, *const clc_bar = sh.clc_bar, *const done = sh.done;
+    uint64_t *const kv_ready = sh.kv_ready, *const clc_bar = sh.clc_bar, *const done = sh.done;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sh.done + 1);
     int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
 
@@ -458,8 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
             mbar_init(&job_full[x], 1);
             mbar_init(&job_empty[x], kSoftWarps + 2);
         }
-        mbar_init(v_edge, 1);
-        mbar_init(v_zeroed, 1);
+        for (int i = 0; i < kReady; ++i) mbar_init(&kv_ready[i], 1);
         mbar_init(clc_bar, 1);
         mbar_init(done, 1);
         *abort_flag = 0;
@@ -586,17 +580,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
                 if (q_used[x]) tc::drain_wait(&q_full[x], (uint32_t)(q_used[x] - 1) & 1u);
             for (int e = i - R < 0 ? 0 : i - R; e < i; ++e) tc::drain_wait(&kv_full[e % R], (uint32_t)((e / R) & 1));
         } else if (warp == kMmaWarp) {
-            if (elect_one() && !mma_role<DT, DP>(sh, p, tmem, box_log)) {
+            if (elect_one() && !mma_role<DT, DP>(sh, p, tmem)) {
                 give_up(abort_v, p);
                 tc::commit(sh.done);
                 tc::drain_wait(sh.done, 0);
             }
-        } else if (warp == kZeroWarp) {
-            // Rows of V past the visible keys: their pages may hold anything, and 0 * NaN is NaN.
-            // The MMA threads ask for it once the tile has arrived.
-            uint32_t edges = 0;
-            int base = 0;
+        } else if (warp == kRingWarp) {
+            // Watches the ring for the MMA thread (V of a step, K of the next), and clears the V rows past the visible
+            // keys: their pages may hold anything, and 0 * NaN is NaN.
+            int e = 0;           // ring entries so far
+            uint32_t told = 0;   // steps so far
             bool ok = true;
+            auto full = [&](int i) { return __all_sync(~0u, wait_for(&kv_full[i % R], (uint32_t)((i / R) & 1), abort_v, p)); };
             for (int k = 0; ok; ++k) {
                 const Job* job = &jobs[k & 1];
                 ok = __all_sync(~0u, wait_for(&job_full[k & 1], (uint32_t)((k >> 1) & 1), abort_v, p));
@@ -605,25 +600,30 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&job_empty[k & 1]);
                 const int steps = rg.na > rg.nb ? rg.na : rg.nb;
-                for (int j = 0; j < steps; j = j + 1 < steps - 1 ? steps - 1 : j + 1) {  // the first and the last tile
-                    int z0, z1;
-                    if (!zero_range(rg, j, box_log, &z0, &z1)) continue;
-                    ok = __all_sync(~0u, wait_for(v_edge, edges++ & 1, abort_v, p));
+                for (int j = 0; j < steps; ++j) {
+                    const int iv = e + 2 * j + 1;
+                    ok = full(iv);
                     if (!ok) break;
-                    uint8_t* v = ring + ((base + 2 * j + 1) % R) * S::kTile;
-                    for (int c = lane; c < kKeys * 8; c += 32) {
-                        const int r = c >> 3;
-                        if (r < z0 || r >= z1) {
+                    int z0, z1;
+                    if (zero_range(rg, j, box_log, &z0, &z1)) {
+                        uint8_t* v = ring + (iv % R) * S::kTile;
+                        for (int c = lane; c < kKeys * 8; c += 32) {
+                            const int r = c >> 3;
+                            if (r < z0 || r >= z1) {
 #pragma unroll
-                            for (int h = 0; h < S::kHalves; ++h)
-                                *reinterpret_cast<uint4*>(v + h * kHalfBytes + c * 16) = make_uint4(0, 0, 0, 0);
+                                for (int h = 0; h < S::kHalves; ++h)
+                                    *reinterpret_cast<uint4*>(v + h * kHalfBytes + c * 16) = make_uint4(0, 0, 0, 0);
+                            }
                         }
+                        fence_proxy_async_smem();
+                        __syncwarp();
                     }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(v_zeroed);
+                    ok = j + 1 == steps || full(iv + 1);
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive(&kv_ready[told & (kReady - 1)]);
+                    ++told;
                 }
-                base += 2 * steps;
+                e += 2 * steps;
             }
             if (!ok) give_up(abort_v, p);
         }
