@@ -281,7 +281,7 @@ struct Shared {
     uint8_t* response;
     uint64_t *kv_full, *kv_empty;                   // [R]
     uint64_t *q_full, *q_empty, *s_full;            // [2] per row tile, as those below
-    uint64_t *p_half, *p_ready;                     // P of the first 64 keys, of the others: one arrival per softmax warp
+    uint64_t* p_full;                               // one arrival per softmax warp
     uint64_t *o_full, *o_free;
     uint64_t *job_full, *job_empty;                 // [2] per slot
     uint64_t *kv_ready, *clc_bar, *done;            // kv_ready [kReady] by step
@@ -296,16 +296,15 @@ struct Shared {
         q_full = kv_empty + R;
         q_empty = q_full + 2;
         s_full = q_empty + 2;
-        p_half = s_full + 2;
-        p_ready = p_half + 2;
-        o_full = p_ready + 2;
+        p_full = s_full + 2;
+        o_full = p_full + 2;
         o_free = o_full + 2;
         job_full = o_free + 2;
         job_empty = job_full + 2;
         kv_ready = job_empty + 2;
         clc_bar = kv_ready + kReady;
         done = clc_bar + 1;
-        static_assert(2 * sizeof(Job) + 16 + (2 * R + 20 + kReady) * 8 + 8 <= kBarBytes, "barriers fit");
+        static_assert(2 * sizeof(Job) + 16 + (2 * R + 18 + kReady) * 8 + 8 <= kBarBytes, "barriers fit");
     }
 };
 
@@ -337,10 +336,10 @@ __device__ __forceinline__ bool mma_role(const Shared<DP>& sh, const AttnParams&
             mma_ss(tmem + (uint32_t)(x * 128), a + off, b + off, id_s, kk > 0 ? 1u : 0u);
         }
     };
-    auto issue_o = [&](int x, int slot, bool first, int part) {  // O_x += P_x . V, half of the keys
+    auto issue_o = [&](int x, int slot, bool first) {  // O_x += P_x . V
         const uint64_t b = v_desc + (uint64_t)slot * kTileStep;
 #pragma unroll
-        for (int kk = part * (kKeys / 32); kk < (part + 1) * (kKeys / 32); ++kk)
+        for (int kk = 0; kk < kKeys / 16; ++kk)
             tc::mma_ta(tmem + 256u + (uint32_t)(x * 128), tmem + (uint32_t)(x * 128 + kk * 8), b + (uint64_t)(kk * (2048 >> 4)), id_o,
                        (!first || kk > 0) ? 1u : 0u);
     };
@@ -389,12 +388,9 @@ __device__ __forceinline__ bool mma_role(const Shared<DP>& sh, const AttnParams&
                 if (j < nx) {
                     const uint32_t un = x ? units_b : units_a;
                     if (j == 0 && un > 0 && !spin_for(&sh.o_free[x], (un - 1) & 1u, limit)) return false;
-                    if (!spin_for(&sh.p_half[x], cnt & 1u, limit)) return false;
+                    if (!spin_for(&sh.p_full[x], cnt & 1u, limit)) return false;
                     tc::fence_after();
-                    issue_o(x, sv, j == 0, 0);
-                    if (!spin_for(&sh.p_ready[x], cnt & 1u, limit)) return false;
-                    tc::fence_after();
-                    issue_o(x, sv, false, 1);
+                    issue_o(x, sv, j == 0);
                     ++cnt;
                     if (j + 1 < nx) {
                         issue_s(x, sk);
@@ -430,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
     Job* const jobs = sh.jobs;
     uint8_t* const response = sh.response;
     uint64_t *const kv_full = sh.kv_full, *const kv_empty = sh.kv_empty, *const q_full = sh.q_full, *const q_empty = sh.q_empty;
-    uint64_t *const s_full = sh.s_full, *const p_half = sh.p_half, *const p_ready = sh.p_ready, *const o_full = sh.o_full;
+    uint64_t *const s_full = sh.s_full, *const p_full = sh.p_full, *const o_full = sh.o_full;
     uint64_t *const o_free = sh.o_free, *const job_full = sh.job_full, *const job_empty = sh.job_empty;
     uint64_t *const kv_ready = sh.kv_ready, *const clc_bar = sh.clc_bar, *const done = sh.done;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sh.done + 1);
@@ -446,8 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
             mbar_init(&q_full[x], 1);
             mbar_init(&q_empty[x], 1);
             mbar_init(&s_full[x], 1);
-            mbar_init(&p_half[x], 4);
-            mbar_init(&p_ready[x], 4);
+            mbar_init(&p_full[x], 4);
             mbar_init(&o_full[x], 1);
             mbar_init(&o_free[x], 4);
             mbar_init(&job_full[x], 1);
@@ -719,13 +714,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
                         if (q & 1) l2a = fadd2(l2a, pack2(e[2 * q], e[2 * q + 1]));
                         else l2b = fadd2(l2b, pack2(e[2 * q], e[2 * q + 1]));
                     }
-                    if (c == 1 || c == 3) {  // P V of these 64 keys may start
-                        tc::wait_st();
-                        tc::fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(c == 1 ? &p_half[x] : &p_ready[x]);
-                    }
                 }
+                tc::wait_st();
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[x]);
             }
             if (!ok) break;
             if (nx > 0) {
