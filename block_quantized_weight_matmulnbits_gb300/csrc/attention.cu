@@ -84,10 +84,10 @@ mnb_status mnb_paged_attention(const mnb_attention_args* a, const mnb_kv_cache* 
     if (inject_launch_failure()) return MNB_ERR_CUDA;
     ProfileScope prof("mnb_paged_attention", (cudaStream_t)a->stream);
     const cudaStream_t s = (cudaStream_t)a->stream;
-    const char* family = "attn_generic";
+    const char* family = "attn_f32";
     cudaError_t e = cudaErrorNotSupported;
     if (c->dtype == MNB_F32) {
-        e = attn::launch_generic(p, s);
+        e = attn::launch_f32(p, s);
     } else {
         if (attn::tc_serves(p.batch, p.q_heads, p.kv_heads, p.D, p.max_q, p.max_kv, p.dtype)) {
             family = "attn_tc";

@@ -47,8 +47,8 @@ size_t mma_workspace_bytes(int D);
 bool tc_serves(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t D, int64_t max_q, int64_t max_kv, int dtype);
 cudaError_t launch_tc(const AttnParams& p, cudaStream_t s);
 size_t tc_workspace_bytes(int64_t batch, int64_t T, int64_t q_heads, int64_t kv_heads, int64_t D, int64_t max_kv);
-// Any type, CUDA cores (attn_generic.cu).
-cudaError_t launch_generic(const AttnParams& p, cudaStream_t s);
+// f32, CUDA cores (attn_f32.cu).
+cudaError_t launch_f32(const AttnParams& p, cudaStream_t s);
 
 }  // namespace attn
 }  // namespace mnb

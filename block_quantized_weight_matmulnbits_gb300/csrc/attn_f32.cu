@@ -1,5 +1,5 @@
-// Paged attention on CUDA cores: any type (f32 above all), any head_dim that
-// is a multiple of 8 up to 256.
+// Paged attention in f32, on CUDA cores: any head_dim that is a multiple of 8
+// up to 256.
 //
 // One CTA of 8 warps per (token, query head).  Each warp walks every eighth
 // block of 32 keys with an online softmax: a lane scores one key (its whole
@@ -18,15 +18,9 @@ constexpr int kWarps = 8;
 constexpr int kMaxD = 256;
 constexpr int kPer = kMaxD / 32;  // depths a lane owns
 
-template <int DT>
-__device__ __forceinline__ float at(const void* p, int64_t i) {
-    if constexpr (DT == kF32) return static_cast<const float*>(p)[i];
-    else if constexpr (DT == kF16) return __half2float(static_cast<const __half*>(p)[i]);
-    else return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-}
+__device__ __forceinline__ float at(const void* p, int64_t i) { return static_cast<const float*>(p)[i]; }
 
-template <int DT>
-__global__ void __launch_bounds__(kWarps * 32) attn_generic_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(kWarps * 32) attn_f32_kernel(const AttnParams p) {
     __shared__ float qs[kMaxD];
     __shared__ float os[kWarps][kMaxD];
     __shared__ float ms[kWarps], ls[kWarps];
@@ -45,7 +39,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_generic_kernel(const AttnPar
     const int i = (int)(t - p.q_start[b]);
     int lo, hi;
     visible_range(p, n, len, i, i + 1, &lo, &hi);
-    for (int d = threadIdx.x; d < p.D; d += kWarps * 32) qs[d] = at<DT>(p.q, t * p.q_ts + h * p.q_hs + d) * p.scale;
+    for (int d = threadIdx.x; d < p.D; d += kWarps * 32) qs[d] = at(p.q, t * p.q_ts + h * p.q_hs + d) * p.scale;
     __syncthreads();
 
     float m = -INFINITY, l = 0.f, o[kPer] = {};
@@ -60,7 +54,13 @@ __global__ void __launch_bounds__(kWarps * 32) attn_generic_kernel(const AttnPar
             s = 0.f;
             if ((unsigned)page < (unsigned)p.num_pages) {
                 row = page * p.page_stride + (j & (ps - 1)) * p.token_stride + hk * p.head_stride;
-                for (int d = 0; d < p.D; ++d) s = fmaf(qs[d], at<DT>(p.k, row + d), s);
+                for (int d = 0; d < p.D; d += 4) {
+                    const float4 kk = *reinterpret_cast<const float4*>(static_cast<const float*>(p.k) + row + d);
+                    s = fmaf(qs[d], kk.x, s);
+                    s = fmaf(qs[d + 1], kk.y, s);
+                    s = fmaf(qs[d + 2], kk.z, s);
+                    s = fmaf(qs[d + 3], kk.w, s);
+                }
             } else {
                 set_status(p.status, MNB_ERR_INVALID_ARG);
             }
@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_generic_kernel(const AttnPar
 #pragma unroll
             for (int c = 0; c < kPer; ++c) {
                 const int d = c * 32 + lane;
-                if (d < p.D) o[c] = fmaf(w, at<DT>(p.v, r + d), o[c]);
+                if (d < p.D) o[c] = fmaf(w, at(p.v, r + d), o[c]);
             }
         }
     }
@@ -106,18 +106,18 @@ __global__ void __launch_bounds__(kWarps * 32) attn_generic_kernel(const AttnPar
     for (int d = threadIdx.x; d < p.D; d += kWarps * 32) {
         float a = 0.f;
         for (int w = 0; w < kWarps; ++w) a = fmaf(os[w][d], expf(ms[w] - base), a);
-        store_f32(p.o, t * p.o_ts + h * p.o_hs + d, hi > lo ? a / total : 0.f, DT);
+        static_cast<float*>(p.o)[t * p.o_ts + h * p.o_hs + d] = hi > lo ? a / total : 0.f;
     }
     if (threadIdx.x == 0 && p.lse) p.lse[t * p.q_heads + h] = hi > lo ? top + logf(total) : -INFINITY;
 }
 
 }  // namespace
 
-cudaError_t launch_generic(const AttnParams& p, cudaStream_t s) {
+cudaError_t launch_f32(const AttnParams& p, cudaStream_t s) {
     const int64_t blocks = p.T * p.q_heads;
     if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     const dim3 grid((unsigned)blocks), block(kWarps * 32);
-    return dec::launch_pdl(attn_generic_kernel<kF32>, grid, block, 0, s, 1, p);
+    return dec::launch_pdl(attn_f32_kernel, grid, block, 0, s, 1, p);
 }
 
 }  // namespace attn

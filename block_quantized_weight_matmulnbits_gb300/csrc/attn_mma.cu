@@ -23,11 +23,13 @@ cudaError_t launch_as(const AttnParams& p, cudaStream_t s) {
     const int64_t each = (int64_t)p.batch * (((int64_t)p.max_q * p.group + mma::kRows - 1) / mma::kRows);
     const int64_t units = (int64_t)p.kv_heads * (some < each ? some : each);  // at most
     const int64_t keys = p.window > 0 && (int64_t)p.window + p.max_q < p.max_kv ? (int64_t)p.window + p.max_q : p.max_kv;
-    // Few units of a moderate context: a cluster each.  Eight CTAs hold about 4 us of loads each at 8192 keys; beyond
-    // that (or with more units than slots for clusters of two) an even cut over all SMs is worth its second kernel.
+    // Few units of a moderate context: a cluster each.  A CTA takes about 5 us and 0.6 us for each 64 keys of its range;
+    // the even cut over all SMs starts at about 14 us (its division, its second kernel) and wins beyond 12 tiles a CTA
+    // (56 sequences of up to 2106 keys, two key heads: 20.5 us cut evenly, 22.0 us on clusters of two; one of 777 keys,
+    // eight key heads: 7.6 us on clusters of eight, 16.8 us cut evenly).
     int cl = 1;
     while (cl < 8 && units * cl * 2 <= sp.ctas) cl *= 2;
-    if (cl > 1 && keys <= (int64_t)1024 * cl) {
+    if (cl > 1 && keys <= (int64_t)768 * cl) {
         auto kern = mma::attn_mma_kernel<DT, DP, true>;
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
         if (e != cudaSuccess) return e;

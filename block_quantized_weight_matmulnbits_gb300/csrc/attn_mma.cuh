@@ -121,6 +121,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kCtasPerSm) attn_mma_kern
     }
     Place pl = locate<kRows, kKeys, kThreads>(p, dv.whole, x0, CL && x0 == 0);
     if (CL && pl.b < 0) return;  // past the last unit: the whole cluster
+    if (!dv.whole && x1 <= pl.unit_begin) return;  // a range inside what a unit is counted longer
 
     const uint32_t ring = smem_u32(smem) + warp * S::kRing, qa = smem_u32(qs);
     const uint16_t* kp = static_cast<const uint16_t*>(p.k);
@@ -132,13 +133,13 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kCtasPerSm) attn_mma_kern
     const int lrow = lane / kLanes, lchunk = lane % kLanes;
     const bool col_ok = lchunk * 8 < p.D;
 
-    for (int64_t x = x0;;) {
+    for (bool first = true;; first = false) {
         const int rt = pl.unit / p.kv_heads, hk = pl.unit - rt * p.kv_heads;
         const int t0 = CL ? (int)((int64_t)pl.s.tiles * rank / peers) : pl.tile;
-        const int64_t left = x1 - x;
-        const int t1 = CL         ? (int)((int64_t)pl.s.tiles * (rank + 1) / peers)
-                       : dv.whole ? pl.s.tiles
-                                  : (int)(left < pl.s.tiles - t0 ? t0 + left : pl.s.tiles);
+        const int64_t end = x1 - pl.unit_begin;
+        const int t1 = CL                                 ? (int)((int64_t)pl.s.tiles * (rank + 1) / peers)
+                       : dv.whole || end >= pl.s.tiles ? pl.s.tiles
+                                                          : (int)end;
         const int rows = pl.s.n * p.group - rt * kRows < kRows ? pl.s.n * p.group - rt * kRows : kRows;
         const int64_t tok0 = p.q_start[pl.b];
         const int i0 = rt * kRows / p.group, i1 = (rt * kRows + rows - 1) / p.group + 1;
@@ -339,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kCtasPerSm) attn_mma_kern
                 const int g = rt * kRows + r;
                 const int64_t tk = tok0 + g / p.group;
                 const int h = hk * p.group + g % p.group;
-                const int slot = x == x0 ? 0 : 1;
+                const int slot = first ? 0 : 1;
                 const int64_t at = ((int64_t)blockIdx.x * 2 + slot) * kRows + r;
                 const float inv = sum > 0.f ? 1.f / sum : 0.f;
                 for (int c = q8; c < DP / 8; c += 8) {
@@ -412,16 +413,17 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kCtasPerSm) attn_mma_kern
             cluster_sync();  // nobody leaves while its shared memory is read
             return;
         }
-        x += dv.whole ? 1 : t1 - t0;
-        if (!CL && tid == 0 && !dv.whole && x >= x1 && x0 <= pl.unit_begin && t1 < pl.s.tiles) {
+        if (dv.whole) break;
+        if (tid == 0 && t1 < pl.s.tiles && x0 <= pl.unit_begin) {
             // this range's end is the first cut of the unit; its pieces end with the last CTA that begins before its end
             const int64_t last = ((pl.unit_begin + pl.s.tiles) * dv.ctas - 1) / dv.total;
             sp.cut[blockIdx.x] = make_int4((int)tok0, rt * kRows, hk | rows << 16,
-                                           (int)(last - blockIdx.x + 1) * 2 + (x0 == pl.unit_begin ? 0 : 1));
+                                           (int)(last - blockIdx.x + 1) * 2 + (first ? 0 : 1));
         }
-        if (x >= x1) break;
+        if (x1 <= pl.unit_begin + pl.s.tiles) break;
+        next_unit<kRows, kKeys>(p, pl);
+        if (x1 <= pl.unit_begin) break;
         __syncthreads();  // the exchange buffer becomes the rings again
-        next_unit<kRows, kKeys>(p, dv, pl);
     }
 }
 

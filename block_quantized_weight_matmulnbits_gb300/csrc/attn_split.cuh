@@ -17,6 +17,11 @@
 namespace mnb {
 namespace attn {
 
+// What a unit costs beside its tiles (its lookups, Q, first loads and exchange), in tiles: the division counts each
+// unit that much longer, or a range of many short units would take several times as long as one of few long units
+// (256 sequences of 49 to 600 keys, 8 key heads: 92 us without it, 63 with).
+constexpr int kUnitCost = 6;
+
 struct SplitParams {
     int ctas;        // grid of the first kernel
     int whole_tiles; // units of at most this many tiles are not cut, when each can have a CTA
@@ -50,7 +55,7 @@ __device__ __forceinline__ Seq load_seq(const AttnParams& p, int b) {
 }
 
 struct Division {
-    int64_t total;  // tiles, or units when whole
+    int64_t total;  // tiles (kUnitCost more for each unit), or units when whole
     int64_t ctas;   // CTAs that have work
     bool whole;     // one unit per CTA, uncut
     __device__ int64_t begin(int64_t c) const { return c >= ctas ? total : whole ? c : c * total / ctas; }
@@ -68,7 +73,7 @@ __device__ Division divide(const AttnParams& p, const SplitParams& sp, bool tell
         if (s.bad && tell) set_status(p.status, MNB_ERR_INVALID_ARG);
         const int64_t units = (int64_t)s.row_tiles * p.kv_heads;
         u += units;
-        w += units * s.tiles;
+        if (s.tiles) w += units * (s.tiles + kUnitCost);
         t = max(t, s.tiles);
     }
 #pragma unroll
@@ -105,7 +110,7 @@ struct Place {
     Seq s;
     int unit;         // row tile * kv_heads + key head, inside the sequence
     int tile;
-    int64_t unit_begin;  // index of the unit's first tile (or of the unit, when whole)
+    int64_t unit_begin;  // index of the unit's first tile
 };
 
 // The place of index x, by all threads of the block; b < 0 past the last one.
@@ -124,7 +129,7 @@ __device__ Place locate(const AttnParams& p, bool whole, int64_t x, bool tell) {
         if (b < p.batch) {
             const Seq s = load_seq<ROWS, KEYS>(p, b);
             if (s.bad && tell) set_status(p.status, MNB_ERR_INVALID_ARG);
-            v = (int64_t)s.row_tiles * p.kv_heads * (whole ? 1 : s.tiles);
+            v = (int64_t)s.row_tiles * p.kv_heads * (whole ? 1 : s.tiles + kUnitCost);
             if (s.tiles == 0) v = 0;
         }
         int64_t incl = v;
@@ -154,17 +159,18 @@ __device__ Place locate(const AttnParams& p, bool whole, int64_t x, bool tell) {
     if (pl.b < 0) return pl;
     pl.s = load_seq<ROWS, KEYS>(p, pl.b);
     const int64_t r = x - sh_base;
-    const int per = whole ? 1 : pl.s.tiles;
+    const int per = whole ? 1 : pl.s.tiles + kUnitCost;
     pl.unit = (int)(r / per);
-    pl.tile = whole ? 0 : (int)(r - (int64_t)pl.unit * per);
-    pl.unit_begin = x - pl.tile;
+    const int off = whole ? 0 : (int)(r - (int64_t)pl.unit * per) - kUnitCost;
+    pl.tile = off > 0 ? off : 0;
+    pl.unit_begin = x - off;
     return pl;
 }
 
 // The next unit after pl (the caller knows that there is one).
 template <int ROWS, int KEYS>
-__device__ __forceinline__ void next_unit(const AttnParams& p, const Division& d, Place& pl) {
-    pl.unit_begin += d.whole ? 1 : pl.s.tiles;
+__device__ __forceinline__ void next_unit(const AttnParams& p, Place& pl) {
+    pl.unit_begin += pl.s.tiles + kUnitCost;
     pl.tile = 0;
     if (++pl.unit < pl.s.row_tiles * p.kv_heads) return;
     pl.unit = 0;
