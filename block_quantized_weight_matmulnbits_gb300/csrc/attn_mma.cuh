@@ -13,6 +13,11 @@
 //   - 2 CTAs per SM with 3 stages of 8 KB a warp (D = 128) hold 128 KB of loads
 //     in flight per SM while a third of the ring is computed on.
 //   - Page numbers are read one stage ahead of the loads that need them.
+// Measured on a GB300 (6800 GB/s copy): 64 sequences of 684 to 8192 keys, 8 key
+// heads x 128, 4 queries each, bf16: 131 us, 6040 GB/s (the even cut; 5 us of it
+// the join); one sequence of 131001 keys, f16: 93 us, 5780 GB/s; one of 777 keys
+// on clusters of 8: 7.6 us.  Bound by DRAM in the first two, by the chain of
+// dependent loads (length, page number, keys) in the last.
 // The maximum a row is scaled by follows the true one only when it falls more
 // than 8 (log2) behind, so O is rarely rescaled; p then stays below 2^8, exact
 // in the f32 sums and rounded once to the MMA's type for the product with V.

@@ -12,7 +12,11 @@
 // neighbouring vectors of neighbouring heads, so a warp's accesses are whole
 // lines.  The append is the same pass with another address for k and v.
 //
-// Measured (GB300): see the table of operators beside the measurements.
+// Measured on a GB300 (6800 GB/s copy): 10031 tokens of 48 heads x 128 in bf16,
+// half layout, turned and appended: 41.3 us, 6030 GB/s (48 us with one head a
+// thread, 42.5 with two); 4999 x 18 x 96 in f32, interleaved, 64 of 96 depths:
+// 14.2 us, 4950 GB/s, the ramp and tail of a short kernel.  One token: 7 us, the
+// launch and a chain of lookups (length, page, table row).
 #include <cmath>
 
 #include "decoder.h"
