@@ -367,6 +367,7 @@ def _table_pair(cos_table, sin_table):
     return shape[0], 2 * shape[1]
 
 
+# Rows' strides are checked where there are rows: an empty tensor's mean nothing (one made from numpy has zeros).
 def _rows_fail(what):
     _fail(f"{what}: a [tokens, heads, dim] tensor of the call's dtype with unit stride in dim is wanted")
 
@@ -445,7 +446,8 @@ def mnb_rotary(x, y, positions, cos_table, sin_table, dtype, flags=0, stream=Non
         _setup()
     n_pos, rot = _table_pair(cos_table, sin_table)
     shape, xs, ys = x.shape, x.stride(), y.stride()
-    if y.shape != shape or len(shape) != 3 or xs[2] != 1 or ys[2] != 1 or _codes.get(x.dtype) != dtype or y.dtype is not x.dtype:
+    if y.shape != shape or len(shape) != 3 or xs[2] != 1 and shape[0] or ys[2] != 1 and shape[0] or _codes.get(x.dtype) != dtype or \
+            y.dtype is not x.dtype:
         _rows_fail("x, y")
     pos_ptr = _i32("positions", positions)
     if positions.numel() != shape[0]:
@@ -462,7 +464,8 @@ def mnb_rotary_append(q, q_out, k, v, cos_table, sin_table, cache, q_start, posi
         _setup()
     n_pos, rot = _table_pair(cos_table, sin_table)
     dtype, ks, vs, shape = cache.dtype, k.stride(), v.stride(), k.shape
-    if v.shape != shape or len(shape) != 3 or ks[2] != 1 or vs[2] != 1 or _codes.get(k.dtype) != dtype or v.dtype is not k.dtype or \
+    if v.shape != shape or len(shape) != 3 or ks[2] != 1 and shape[0] or vs[2] != 1 and shape[0] or _codes.get(k.dtype) != dtype or \
+            v.dtype is not k.dtype or \
             shape[1] != cache.kv_heads or shape[2] != cache.head_dim:
         _fail("k, v: [T, kv_heads, head_dim] rows of the cache's dtype are wanted")
     start_ptr, pos_ptr = _i32("q_start", q_start), None
@@ -476,8 +479,8 @@ def mnb_rotary_append(q, q_out, k, v, cos_table, sin_table, cache, q_start, posi
     heads, qs, os_ = 0, (0, 0), (0, 0)
     if q is not None:
         qshape, qs, os_ = q.shape, q.stride(), q_out.stride()
-        if q_out.shape != qshape or len(qshape) != 3 or qs[2] != 1 or os_[2] != 1 or q.dtype is not k.dtype or q_out.dtype is not k.dtype or \
-                qshape[0] != shape[0] or qshape[2] != shape[2]:
+        if q_out.shape != qshape or len(qshape) != 3 or qs[2] != 1 and shape[0] or os_[2] != 1 and shape[0] or \
+                q.dtype is not k.dtype or q_out.dtype is not k.dtype or qshape[0] != shape[0] or qshape[2] != shape[2]:
             _fail("q, q_out: [T, q_heads, head_dim] rows of the cache's dtype are wanted")
         qp, op, heads = q.data_ptr(), q_out.data_ptr(), qshape[1]
     a = RotaryArgs(qp, op, k.data_ptr(), v.data_ptr(), cos_table.data_ptr(), sin_table.data_ptr(), start_ptr, pos_ptr, shape[0], heads, rot,
@@ -497,8 +500,8 @@ def mnb_paged_attention(q, o, cache, q_start, max_q, max_kv, scale, lse=None, ca
     if not _codes:
         _setup()
     shape, qs, os_ = q.shape, q.stride(), o.stride()
-    if o.shape != shape or len(shape) != 3 or qs[2] != 1 or os_[2] != 1 or _codes.get(q.dtype) != cache.dtype or o.dtype is not q.dtype or \
-            shape[2] != cache.head_dim:
+    if o.shape != shape or len(shape) != 3 or qs[2] != 1 and shape[0] or os_[2] != 1 and shape[0] or \
+            _codes.get(q.dtype) != cache.dtype or o.dtype is not q.dtype or shape[2] != cache.head_dim:
         _fail("q, o: [T, q_heads, head_dim] rows of the cache's dtype are wanted")
     start_ptr, lse_ptr, ws_ptr, ws_bytes = _i32("q_start", q_start), None, None, 0
     if q_start.numel() != cache.batch + 1:

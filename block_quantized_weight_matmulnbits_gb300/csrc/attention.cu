@@ -31,7 +31,10 @@ mnb_status mnb_paged_attention(const mnb_attention_args* a, const mnb_kv_cache* 
         (a->causal != 0 && a->causal != 1) || !std::isfinite(a->scale) || c->head_dim % 8 != 0 || c->head_dim > 256)
         return MNB_ERR_INVALID_ARG;
     const int64_t vec = 16 / dec::dt_bytes(c->dtype);
-    const int64_t st[4] = {a->q_token_stride, a->q_head_stride, a->o_token_stride, a->o_head_stride};
+    // a stride along one token or one head steps nowhere: it is not judged, and a plain one stands in for it
+    const int64_t D = c->head_dim, HD = a->q_heads * D;
+    const int64_t st[4] = {a->T > 1 ? a->q_token_stride : HD, a->q_heads > 1 ? a->q_head_stride : D,
+                           a->T > 1 ? a->o_token_stride : HD, a->q_heads > 1 ? a->o_head_stride : D};
     for (int64_t x : st)
         if (x < 0 || x % vec != 0 || x >= (int64_t(1) << 38)) return MNB_ERR_INVALID_ARG;
     if (a->T == 0) return MNB_OK;
@@ -56,10 +59,10 @@ mnb_status mnb_paged_attention(const mnb_attention_args* a, const mnb_kv_cache* 
     p.q_start = a->q_start;
     p.T = a->T;
     p.table_stride = c->table_stride;
-    p.q_ts = a->q_token_stride;
-    p.q_hs = a->q_head_stride;
-    p.o_ts = a->o_token_stride;
-    p.o_hs = a->o_head_stride;
+    p.q_ts = st[0];
+    p.q_hs = st[1];
+    p.o_ts = st[2];
+    p.o_hs = st[3];
     p.page_stride = c->page_stride;
     p.token_stride = c->token_stride;
     p.head_stride = c->head_stride;

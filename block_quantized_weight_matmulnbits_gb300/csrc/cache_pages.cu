@@ -13,7 +13,7 @@
 // The pages themselves are moved by a second kernel, a programmatic dependent
 // of the first, that reads the (source, destination) list the first one wrote.
 // It is bound by DRAM: 2 * page bytes * planes for each pair (700 pages of 32 KB
-// in 32 planes: 233 us, 6310 GB/s; a compaction that moves 715 pages of 16 KB:
+// in 32 planes: 233 us, 6310 GB/s; a compaction that moves 716 pages of 16 KB:
 // 130 us, 5760 GB/s, the bookkeeping before the copy included).  A warp moves 4 KB
 // at a time, eight 16-byte loads per lane before the first store, which keeps
 // about 128 KB in flight on an SM.

@@ -183,3 +183,78 @@ def test_in_a_graph_with_lengths_that_change(mnb):
         g.replay()
         torch.cuda.synchronize()
         p.check(o, lse)
+
+
+def _ragged(n, most, seed):
+    return [int(x) for x in np.random.default_rng(seed).integers(0, most + 1, n)]
+
+
+@pytest.mark.parametrize("q_lens,kv_lens,hq,hkv,D,page,window", [
+    ([1], [20011], 8, 2, 128, 16, 0),                                   # one context over every CTA, joined
+    ([1, 1], [9001, 12], 12, 2, 80, 32, 0),
+    ([1] * 40, _ragged(40, 700, 1), 16, 8, 128, 16, 0),                 # many short units: ranges that hold several, empty ones
+    ([1] * 70, _ragged(70, 90, 2), 10, 10, 64, 8, 0),
+    ([1] * 90, _ragged(90, 300, 3), 16, 2, 256, 64, 0),
+    ([20, 3], [2500, 30], 4, 4, 64, 16, 300),                           # two row tiles of few rows
+    ([3] * 50, [n + 3 for n in _ragged(50, 400, 4)], 6, 3, 128, 16, 100),
+    ([40], [9000], 4, 2, 128, 16, 0),                                   # many rows, keys cut into ranges
+    ([70, 1, 0, 33], [5000, 40, 0, 33], 6, 2, 96, 32, 0),
+    ([500], [2100], 4, 1, 64, 128, 777)])
+def test_long_and_many(mnb, q_lens, kv_lens, hq, hkv, D, page, window):
+    p = Problem(mnb, q_lens, kv_lens, hq, hkv, D, "bf16", page, "hnd", seed=D + len(q_lens))
+    heads = sorted({0, hq // 2, hq - 1})
+    some = range(0, len(q_lens), max(1, len(q_lens) // 25))
+    p.check(*p.run(window=window), window=window, heads=heads, seqs=set(some) | {len(q_lens) - 1})
+
+
+@pytest.mark.parametrize("q,hq,dtype", [(1, 8, "bf16"), (1, 8, "f32"), (60, 8, "f16")])
+def test_pages_before_the_window_are_not_read(mnb, q, hq, dtype):
+    """A server under a sliding window frees the pages that no row sees any more."""
+    n, window, page = 3000, 500, 16
+    p = Problem(mnb, [q], [n], hq, 2, 128, dtype, page, "hnd", seed=13)
+    gone = (n - q - window + 1) // page
+    keep = p.np_tables[0, :gone].copy()
+    p.tables[0, :gone] = -1
+    p.k[torch.from_numpy(keep).long().cuda()] = float("nan")
+    p.v[torch.from_numpy(keep).long().cuda()] = float("nan")
+    o, lse = p.run(window=window)
+    # (the plain form reads the freed pages' places, masked: give it zeros)
+    p.k[torch.from_numpy(keep).long().cuda()] = 0
+    p.v[torch.from_numpy(keep).long().cuda()] = 0
+    p.check(o, lse, window=window)
+
+
+@pytest.mark.parametrize("q,kv", [(120, 900), (300, 300)])
+def test_many_rows_in_a_graph_with_lengths_that_change(mnb, q, kv):
+    p = Problem(mnb, [q, 7], [kv, 90], 8, 2, 128, "bf16", 16, "hnd", seed=14, poison=False)
+    o, lse = torch.zeros_like(p.q), torch.zeros(p.q.shape[:2], device="cuda")
+    ws = torch.empty(mnb.mnb_attention_workspace_size(2, p.T, 8, 2, 128, q, kv, 2) + 256, dtype=torch.uint8, device="cuda")
+    step = lambda: mnb.mnb_paged_attention(p.q, o, p.cache, p.start, q, kv, p.scale(), lse=lse, workspace=ws)  # noqa: E731
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for lens in ([kv, 90], [q, 7], [kv - 13, 30]):
+        p.kv_lens = lens
+        p.lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        g.replay()
+        torch.cuda.synchronize()
+        p.check(o, lse, heads=[0, 5])
+
+
+@pytest.mark.parametrize("T,q_lens", [(3, [0, 0]), (300, [0, 0]), (0, [0, 0])])
+def test_padding_alone(mnb, T, q_lens):
+    """Nothing but tokens past q_start[batch]: nothing is written."""
+    p = Problem(mnb, q_lens, [5, 40], 4, 2, 128, "bf16", 16, "hnd", seed=15, pad=T)
+    o, lse = p.run(max_q=max(1, T))
+    p.check(o, lse)
+
+
+def test_strides_along_one_token_or_head_do_not_matter(mnb):
+    p = Problem(mnb, [1], [45], 1, 1, 64, "bf16", 16, "hnd", seed=16)
+    q = torch.as_strided(p.q.clone(), (1, 1, 64), (3, 5, 1))
+    p.check(*p.run(q=q))

@@ -179,3 +179,18 @@ def test_zero_tokens(mnb):
     cos, sin = _tables(10, 32)
     x = torch.empty((0, 2, 32), device="cuda")
     mnb.mnb_rotary(x, x, torch.empty(0, dtype=torch.int32, device="cuda"), cos, sin, 0)
+
+
+def test_no_tokens(mnb):
+    """An empty batch is a call that does nothing, whatever its tensors' strides are (numpy's empty ones have zeros)."""
+    cos, sin = _tables(50, 64)
+    none = torch.from_numpy(np.zeros((0, 2, 64), dtype=np.float32)).cuda()
+    pos = torch.zeros(0, dtype=torch.int32, device="cuda")
+    mnb.mnb_rotary(none, torch.empty_like(none), pos, cos, sin, 0)
+    pages = torch.full((2, 2, 16, 64), 5.0, device="cuda")
+    start, lens = torch.zeros(2, dtype=torch.int32, device="cuda"), torch.tensor([3], dtype=torch.int32).cuda()
+    cache = mnb.kv_cache(pages, pages.clone(), torch.zeros(1, 1, dtype=torch.int32, device="cuda"), lens, "hnd", 0)
+    mnb.mnb_rotary_append(none, none.clone(), none, none, cos, sin, cache, start)
+    mnb.mnb_rotary_append(None, None, none, none, cos, sin, cache, start)
+    torch.cuda.synchronize()
+    assert (pages == 5).all()
