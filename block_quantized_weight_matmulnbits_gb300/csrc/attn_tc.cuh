@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
             int i = 0, q_used[2] = {0, 0};  // ring entries, and Q tiles of each kind, issued so far
             int k = 0, asked = 0;           // jobs told, blocks asked for
             bool ok = true, more = true;
-            uint32_t block = blockIdx.x;
+            uint32_t block = blockIdx.x, unit = 0, split = 0;
             while (ok) {
                 Unit u{};
                 if (more) {  // ask for the next block before working on this one
@@ -492,11 +492,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
                     }
                     __syncwarp();
                     ++asked;
-                    u = find_unit(p, tp.tokens, block / (unsigned)tp.splits, blockIdx.x == 0 && k == 0);
+                    // a range of all units before the next range: units that share keys read them at one time
+                    unit = block % (unsigned)tp.units, split = block / (unsigned)tp.units;
+                    u = find_unit(p, tp.tokens, unit, blockIdx.x == 0 && k == 0);
                 }
                 Range rg{};
                 if (u.ok || !more) {  // (a block past the last unit only gives way to the next one)
-                    if (u.ok) rg = unit_range(p, tp, u, (int)(block % (unsigned)tp.splits));
+                    if (u.ok) rg = unit_range(p, tp, u, (int)split);
                     const int slot = k & 1;
                     ok = k < 2 || __all_sync(~0u, wait_for(&job_empty[slot], (uint32_t)((k >> 1) - 1) & 1u, abort_v, p));
                     if (!ok) break;
@@ -508,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
                         job.pair = u.pair;
                         job.hk = u.hk;
                         job.tok = u.tok;
-                        job.part = (int)block;
+                        job.part = (int)(unit * (unsigned)tp.splits + split);
                         job.valid = u.ok ? 1 : 0;
                         mbar_arrive(&job_full[slot]);
                     }
