@@ -1,5 +1,6 @@
 // Host side of the many-row attention kernel: tensor maps, the cut of few
 // units into ranges of keys, workspace and launches.
+#include <cmath>
 #include <cstring>
 
 #include "attn_tc.cuh"
@@ -55,13 +56,37 @@ Plan make_plan(int64_t batch, int64_t T, int64_t q_heads, int64_t kv_heads, int6
     return pl;
 }
 
-template <int DT, int DP>
+// How one box can bring both halves of 128 depths: rows split into groups of 8, halves and groups as dimensions of their
+// own, which leaves one more for pages and key heads.  The heads go beside the halves where a head follows the other
+// at once (tokens before heads), or beside the pages where a page is a number of heads (heads before tokens).
+struct OneBox {
+    bool ok;
+    int64_t page_step, head_step;  // in the last dimension
+    int head_halves;               // in the dimension of halves
+    int64_t halves, last, last_stride;
+};
+OneBox one_box(const AttnParams& p) {
+    OneBox b{};
+    if (p.D != 128) return b;
+    const int64_t pages = p.num_pages;
+    if (p.kv_heads == 1 || p.head_stride == 128) {
+        b = {true, 1, 0, 2, 2 * (int64_t)p.kv_heads, pages, p.page_stride};
+    } else if (p.head_stride > 0 && p.page_stride % p.head_stride == 0) {
+        const int64_t ratio = p.page_stride / p.head_stride;
+        // (the page after the last one stands for none: it has to lie past the last head of the last page)
+        b = {ratio >= p.kv_heads && (pages + 1) * ratio < (int64_t(1) << 31), ratio, 1, 0, 2, (pages - 1) * ratio + p.kv_heads,
+             p.head_stride};
+    }
+    return b;
+}
+
+template <int DT, int DP, bool ONE>
 cudaError_t launch_as(const AttnParams& p, const Plan& pl, cudaStream_t s) {
-    using S = tca::Shape<DP>;
+    using S = tca::Shape<DP, ONE>;
     EncodeTiledFn enc = encode_fn();
     if (!enc) return cudaErrorNotSupported;
     const CUtensorMapDataType dt = DT == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
     CUtensorMap maps[3];
     std::memset(maps, 0, sizeof(maps));
     {
@@ -73,7 +98,21 @@ cudaError_t launch_as(const AttnParams& p, const Plan& pl, cudaStream_t s) {
             return cudaErrorNotSupported;
     }
     const int page = 1 << p.page_shift, rows = page < tca::kKeys ? page : tca::kKeys;
+    tca::TcParams tp{};
     for (int i = 0; i < 2; ++i) {
+        if constexpr (ONE) {
+            const OneBox b = one_box(p);
+            const cuuint64_t dims[5] = {64, 8, (cuuint64_t)b.halves, (cuuint64_t)(page / 8), (cuuint64_t)b.last};
+            const cuuint64_t st[4] = {(cuuint64_t)p.token_stride * 2, 128, (cuuint64_t)p.token_stride * 16, (cuuint64_t)b.last_stride * 2};
+            const cuuint32_t box[5] = {64, 8, 2, (cuuint32_t)(rows / 8), 1};
+            if (enc(&maps[1 + i], dt, 5, const_cast<void*>(i ? p.v : p.k), dims, st, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+                return cudaErrorNotSupported;
+            tp.page_step = b.page_step;
+            tp.head_step = b.head_step;
+            tp.head_halves = b.head_halves;
+            continue;
+        }
         const cuuint64_t dims[4] = {(cuuint64_t)p.D, (cuuint64_t)page, (cuuint64_t)p.kv_heads, (cuuint64_t)p.num_pages};
         const cuuint64_t st[3] = {(cuuint64_t)p.token_stride * 2, (cuuint64_t)p.head_stride * 2, (cuuint64_t)p.page_stride * 2};
         const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1};
@@ -81,17 +120,19 @@ cudaError_t launch_as(const AttnParams& p, const Plan& pl, cudaStream_t s) {
                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return cudaErrorNotSupported;
     }
-    tca::TcParams tp{};
     tp.tokens = pl.tokens;
     tp.units = (int)pl.units;
     tp.splits = pl.splits;
     tp.box_rows = rows;
     tp.part_o = static_cast<float*>(p.workspace);
     tp.part_ml = reinterpret_cast<float2*>(tp.part_o + (size_t)pl.units * pl.splits * 256 * DP);
-    auto kern = p.scale_log2 < 0.f ? tca::attn_tc_kernel<DT, DP, true> : tca::attn_tc_kernel<DT, DP, false>;
+    AttnParams q = p;
+    tp.negate = p.scale_log2 < 0.f;
+    q.scale_log2 = std::fabs(p.scale_log2);
+    auto kern = tca::attn_tc_kernel<DT, DP, ONE>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess) return e;
-    e = dec::launch_pdl(kern, dim3((unsigned)(pl.units * pl.splits)), dim3(tca::kThreads), S::kSmem, s, 1, p, tp, maps[0], maps[1], maps[2]);
+    e = dec::launch_pdl(kern, dim3((unsigned)(pl.units * pl.splits)), dim3(tca::kThreads), S::kSmem, s, 1, q, tp, maps[0], maps[1], maps[2]);
     if (e != cudaSuccess || pl.splits == 1) return e;
     return dec::launch_pdl(tca::attn_tc_join_kernel<DT, DP>, dim3((unsigned)(pl.units * 32)), dim3(256), 0, s, 1, p, tp);
 }
@@ -114,8 +155,12 @@ size_t tc_workspace_bytes(int64_t batch, int64_t T, int64_t q_heads, int64_t kv_
 cudaError_t launch_tc(const AttnParams& p, cudaStream_t s) {
     const Plan pl = make_plan(p.batch, p.T, p.q_heads, p.kv_heads, p.max_kv);
     if (pl.units * pl.splits * 32 > 0x7FFFFFFF) return cudaErrorNotSupported;
-    if (p.dtype == kF16) return p.D <= 64 ? launch_as<kF16, 64>(p, pl, s) : launch_as<kF16, 128>(p, pl, s);
-    return p.D <= 64 ? launch_as<kBF16, 64>(p, pl, s) : launch_as<kBF16, 128>(p, pl, s);
+    if (p.D <= 64) return p.dtype == kF16 ? launch_as<kF16, 64, false>(p, pl, s) : launch_as<kBF16, 64, false>(p, pl, s);
+    if (one_box(p).ok) {
+        const cudaError_t e = p.dtype == kF16 ? launch_as<kF16, 128, true>(p, pl, s) : launch_as<kBF16, 128, true>(p, pl, s);
+        if (e != cudaErrorNotSupported) return e;
+    }
+    return p.dtype == kF16 ? launch_as<kF16, 128, false>(p, pl, s) : launch_as<kBF16, 128, false>(p, pl, s);
 }
 
 }  // namespace attn

@@ -9,7 +9,8 @@
 // query head of the group), token-major: the Q tile is one TMA box of
 // [tokens][heads of the group][64 depths], so a key tile read once serves the
 // whole group.  Keys come in tiles of 128, K and V through one ring of TMA
-// boxes (a box is the part of a page that lies in the tile).
+// boxes: a box is the part of a page that lies in the tile, both halves of its
+// depths at once where head_dim is 128 and one tensor map can describe that.
 //
 //   S_X = Q_X K^T        (M 128, N 128; both operands K-major in shared memory)
 //   P_X = 2^(s S_X - m)  (written as bf16 / f16 over S_X in TMEM)
@@ -33,12 +34,13 @@
 //                pages may hold anything (0 * NaN is NaN); warp 11 completes the
 //                warpgroup
 // Measured on a GB300: two prompts of 4096 tokens, 32 query and 8 key heads x
-// 128, bf16, pages of 64: 196 us in bursts, 208 sustained (1320 TFLOP/s, the
-// tensor pipe 61 % active); 500 tokens over 32000 keys: 232 us with pages of 16,
-// 197 with pages of 64 (a TMA box for each page and half).  A step (128 keys of
-// both row tiles) takes about 2800 cycles against 2048 of the tensor pipe: the
-// chain wait, softmax (1350), P V and S (1024) of a row tile, and the MMA
-// thread's polls, which take 160 to 250 cycles each.
+// 128, bf16, pages of 64: 196 us in bursts, 205 sustained (1340 TFLOP/s, the
+// tensor pipe 61 % active); 500 tokens over 32000 keys: 199 us with pages of 16,
+// 190 with pages of 64.  A box for each page and half took 224 and 191 us there
+// (and the prompts 233 us with pages of 16): the ring waited for 32 boxes a
+// step.  A step (128 keys of both row tiles) takes about 2800 cycles against
+// 2048 of the tensor pipe: the chain wait, softmax (1350), P V and S (1024) of a
+// row tile, and the MMA thread's polls, which take 160 to 250 cycles each.
 // Few units (a short chunk over a long context) are cut into ranges of key
 // tiles; attn_tc_join adds their (m, l, O) in order.
 #pragma once
@@ -60,8 +62,12 @@ constexpr int kBarBytes = 512;         // jobs and barriers
 constexpr int kStageBytes = 4096;      // of one softmax warp: its 32 rows, 128 bytes at a time, on their way out
 constexpr int kHalfBytes = 128 * 128;  // 128 rows of 64 values: one swizzled half of a Q, K or V tile
 
-template <int DP> struct Shape {
+// ONE: a box brings both halves of its rows, as [8 rows][half] groups; otherwise a box brings one half, and the halves of
+// a tile follow each other.
+template <int DP, bool ONE> struct Shape {
     static constexpr int kHalves = DP / 64;
+    static constexpr int kGroup = ONE ? 2048 : 1024;        // from 8 rows of a K / V tile to the next 8
+    static constexpr int kHalf = ONE ? 1024 : kHalfBytes;   // from one half of a K / V tile to the other
     static constexpr int kTile = kHalves * kHalfBytes;
     static constexpr int kRing = DP == 128 ? 4 : 8;
     static constexpr int kSmem = 1024 + 2 * kTile + kRing * kTile + kSoftWarps * kStageBytes + kBarBytes;
@@ -73,13 +79,23 @@ struct TcParams {
     int splits;
     float* part_o;   // [units][splits][256][DP]
     float2* part_ml; // [units][splits][256]
+    int negate;      // 1: S = -Q K^T
     int box_rows;    // rows of a K / V box: the part of a page in a tile
+    int64_t page_step, head_step; // ONE: steps of the box's last coordinate, and
+    int head_halves; // of its coordinate of halves with the key head
 };
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar) {
     asm volatile(
         "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, int v, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(smem_u32(bar))
         : "memory");
 }
 
@@ -99,14 +115,18 @@ __device__ __forceinline__ bool elect_one() {
     return ok != 0;
 }
 
-// MN-major, 128-byte swizzle: 64 values of the M / N dimension by 8 of K are a
-// 1024-byte atom; atoms follow each other along K every 1024 bytes (stride
-// byte offset), blocks of 64 along N every kHalfBytes (leading byte offset).
-__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
+// K, K-major with a 128-byte swizzle as tc::sdesc_sw128, its groups of 8 rows `group` bytes apart.
+__device__ __forceinline__ uint64_t sdesc_k_sw128(uint32_t saddr, int group) {
+    return (tc::sdesc_sw128(saddr) & ~(0x3FFFull << 32)) | (uint64_t)(group >> 4) << 32;
+}
+// V, MN-major, 128-byte swizzle: 64 values of the M / N dimension by 8 of K are a
+// 1024-byte atom; atoms follow each other along K every `group` bytes (stride
+// byte offset), blocks of 64 along N every `half` bytes (leading byte offset).
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, int group, int half) {
     uint64_t d = 0;
     d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)(kHalfBytes >> 4) << 16;
-    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)(half >> 4) << 16;
+    d |= (uint64_t)(group >> 4) << 32;
     d |= (uint64_t)1 << 46;
     d |= (uint64_t)2 << 61;
     return d;
@@ -144,11 +164,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
-__device__ __forceinline__ float min3(float a, float b, float c) {
-    float d;
-    asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
 template <int DT>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
     uint32_t d;
@@ -157,20 +172,15 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
     return d;
 }
 
-// Largest (MIN: smallest) of 32 scores.
-template <bool MIN>
-__device__ __forceinline__ float extreme32(const uint32_t (&v)[32]) {
+// Largest of 32 scores.
+__device__ __forceinline__ float largest32(const uint32_t (&v)[32]) {
     float a = __uint_as_float(v[0]), b = __uint_as_float(v[1]);
 #pragma unroll
     for (int k = 2; k < 32; k += 4) {
-        const float w = __uint_as_float(v[k]), x = __uint_as_float(v[k + 1]);
-        a = MIN ? min3(a, w, x) : max3(a, w, x);
-        if (k + 3 < 32) {
-            const float y = __uint_as_float(v[k + 2]), z = __uint_as_float(v[k + 3]);
-            b = MIN ? min3(b, y, z) : max3(b, y, z);
-        }
+        a = max3(a, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+        if (k + 3 < 32) b = max3(b, __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
     }
-    return MIN ? fminf(a, b) : fmaxf(a, b);
+    return fmaxf(a, b);
 }
 
 // Unit `idx`: sequence, row-tile pair and key head.  The pairs of a sequence
@@ -277,12 +287,12 @@ __device__ __forceinline__ bool clc_taken(uint32_t response, uint32_t* block) {
 }
 
 // Shared memory: Q tiles, the ring, the jobs, the barriers.
-template <int DP>
+template <int DP, bool ONE>
 struct Shared {
-    using S = Shape<DP>;
+    using S = Shape<DP, ONE>;
     static constexpr int R = S::kRing;
     uint8_t* qs;    // [2][halves][128 rows][128 B]
-    uint8_t* ring;  // [R][halves][128 rows][128 B]
+    uint8_t* ring;  // [R][halves][128 rows][128 B], or (ONE) [R][16][halves][8 rows][128 B]
     uint8_t* stage; // [8 softmax warps][32 rows][128 B]
     Job* jobs;      // [2]
     uint8_t* response;
@@ -324,30 +334,32 @@ __device__ __forceinline__ bool zero_range(const Range& rg, int j, int box_log, 
 }
 
 // The thread that issues all MMAs; false when a wait ran out.
-template <int DT, int DP>
-__device__ __forceinline__ bool mma_role(const Shared<DP>& sh, const AttnParams& p, uint32_t tmem) {
-    using S = Shape<DP>;
+template <int DT, int DP, bool ONE>
+__device__ __forceinline__ bool mma_role(const Shared<DP, ONE>& sh, const AttnParams& p, const TcParams& tp, uint32_t tmem) {
+    using S = Shape<DP, ONE>;
     constexpr int R = S::kRing;
     constexpr uint64_t kTileStep = S::kTile >> 4;
-    const uint32_t id_s = tc::idesc_f16(DT == kBF16, kRows, kKeys);
+    // (under a negative scale Q is negated, so that the softmax knows positive ones alone)
+    const uint32_t id_s = tc::idesc_f16(DT == kBF16, kRows, kKeys) | (uint32_t)tp.negate << 13;
     const uint32_t id_o = tc::idesc_f16(DT == kBF16, kRows, DP) | (1u << 16);  // B is MN-major
-    const uint64_t q_desc = tc::sdesc_sw128(smem_u32(sh.qs)), k_desc = tc::sdesc_sw128(smem_u32(sh.ring));
-    const uint64_t v_desc = sdesc_mn_sw128(smem_u32(sh.ring));
+    const uint64_t q_desc = tc::sdesc_sw128(smem_u32(sh.qs)), k_desc = sdesc_k_sw128(smem_u32(sh.ring), S::kGroup);
+    const uint64_t v_desc = sdesc_mn_sw128(smem_u32(sh.ring), S::kGroup, S::kHalf);
     // about two seconds of polls (or the call's own limit, when it is shortened)
     const uint32_t limit = p.wait_limit >= (1u << 14) ? 1u << 26 : p.wait_limit;
     auto issue_s = [&](int x, int slot) {  // S_x = Q_x . K
         const uint64_t a = q_desc + (uint64_t)x * kTileStep, b = k_desc + (uint64_t)slot * kTileStep;
 #pragma unroll
         for (int kk = 0; kk < DP / 16; ++kk) {
-            const uint64_t off = (uint64_t)(((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4);
-            mma_ss(tmem + (uint32_t)(x * 128), a + off, b + off, id_s, kk > 0 ? 1u : 0u);
+            const uint64_t off_q = (uint64_t)(((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4);
+            const uint64_t off_k = (uint64_t)(((kk >> 2) * S::kHalf + (kk & 3) * 32) >> 4);
+            mma_ss(tmem + (uint32_t)(x * 128), a + off_q, b + off_k, id_s, kk > 0 ? 1u : 0u);
         }
     };
     auto issue_o = [&](int x, int slot, bool first) {  // O_x += P_x . V
         const uint64_t b = v_desc + (uint64_t)slot * kTileStep;
 #pragma unroll
         for (int kk = 0; kk < kKeys / 16; ++kk)
-            tc::mma_ta(tmem + 256u + (uint32_t)(x * 128), tmem + (uint32_t)(x * 128 + kk * 8), b + (uint64_t)(kk * (2048 >> 4)), id_o,
+            tc::mma_ta(tmem + 256u + (uint32_t)(x * 128), tmem + (uint32_t)(x * 128 + kk * 8), b + (uint64_t)(kk * (2 * S::kGroup >> 4)), id_o,
                        (!first || kk > 0) ? 1u : 0u);
     };
     int slot = 0;  // next ring entry, and the parity of its phase
@@ -417,17 +429,16 @@ __device__ __forceinline__ bool mma_role(const Shared<DP>& sh, const AttnParams&
     }
 }
 
-// MIN: the scale is negative, a row's largest scaled score is its smallest score.
-template <int DT, int DP, bool MIN>
+template <int DT, int DP, bool ONE>
 __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p, const TcParams tp,
                                                               const __grid_constant__ CUtensorMap qmap,
                                                               const __grid_constant__ CUtensorMap kmap,
                                                               const __grid_constant__ CUtensorMap vmap) {
-    using S = Shape<DP>;
+    using S = Shape<DP, ONE>;
     constexpr int R = S::kRing;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    const Shared<DP> sh(smem);
+    const Shared<DP, ONE> sh(smem);
     uint8_t* const qs = sh.qs;
     uint8_t* const ring = sh.ring;
     Job* const jobs = sh.jobs;
@@ -476,8 +487,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
         if (warp == kTmaWarp) {
             const uint32_t q_bytes = (uint32_t)(tp.tokens * p.group * 128 * S::kHalves);
             const int boxes = kKeys >> box_log, ps_mask = (1 << p.page_shift) - 1;
-            // a lane's box of the tile (at most 16 boxes): its page is read a tile ahead
-            const int box = lane / S::kHalves, half = lane % S::kHalves;
+            // a lane's box of the tile (at most 16, or 16 of each half): its page is read a tile ahead
+            const int box = ONE ? lane : lane / S::kHalves, half = ONE ? 0 : lane % S::kHalves;
             int i = 0, q_used[2] = {0, 0};  // ring entries, and Q tiles of each kind, issued so far
             int k = 0, asked = 0;           // jobs told, blocks asked for
             bool ok = true, more = true;
@@ -537,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
                         page = p.num_pages;  // past the last page: the box is filled with zeros
                     }
                     const uint32_t bytes = (uint32_t)(((hi - lo) << box_log) * 128 * S::kHalves);
-                    const uint32_t dst = smem_u32(ring) + (uint32_t)(half * kHalfBytes + (box << box_log) * 128);
+                    const uint32_t dst = smem_u32(ring) + (uint32_t)(half * S::kHalf + (box << box_log) * (S::kGroup / 8));
                     const int row = (kb + (box << box_log)) & ps_mask;
 #pragma unroll
                     for (int kv = 0; kv < 2; ++kv) {  // K, then V
@@ -546,7 +557,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
                         if (!ok) break;
                         if (lane == 0) mbar_arrive_expect_tx(&kv_full[slot], bytes);
                         __syncwarp();
-                        if (mine) tma_load_4d(dst + (uint32_t)(slot * S::kTile), kv ? &vmap : &kmap, half * 64, row, u.hk, page, &kv_full[slot]);
+                        if (mine) {
+                            const CUtensorMap* map = kv ? &vmap : &kmap;
+                            const uint32_t to = dst + (uint32_t)(slot * S::kTile);
+                            if constexpr (ONE) {
+                                tma_load_5d(to, map, 0, 0, u.hk * tp.head_halves, row >> 3, (int)(page * tp.page_step + u.hk * tp.head_step), &kv_full[slot]);
+                            } else {
+                                tma_load_4d(to, map, half * 64, row, u.hk, page, &kv_full[slot]);
+                            }
+                        }
                         ++i;
                         if (j > 0 || kv > 0) continue;
                         // the unit's Q behind its first K: its buffers come free with the last S of the unit before
@@ -584,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
                 if (q_used[x]) tc::drain_wait(&q_full[x], (uint32_t)(q_used[x] - 1) & 1u);
             for (int e = i - R < 0 ? 0 : i - R; e < i; ++e) tc::drain_wait(&kv_full[e % R], (uint32_t)((e / R) & 1));
         } else if (warp == kMmaWarp) {
-            if (elect_one() && !mma_role<DT, DP>(sh, p, tmem)) {
+            if (elect_one() && !mma_role<DT, DP, ONE>(sh, p, tp, tmem)) {
                 give_up(abort_v, p);
                 tc::commit(sh.done);
                 tc::drain_wait(sh.done, 0);
@@ -616,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
                             if (r < z0 || r >= z1) {
 #pragma unroll
                                 for (int h = 0; h < S::kHalves; ++h)
-                                    *reinterpret_cast<uint4*>(v + h * kHalfBytes + c * 16) = make_uint4(0, 0, 0, 0);
+                                    *reinterpret_cast<uint4*>(v + h * S::kHalf + (r >> 3) * S::kGroup + (c & 63) * 16) = make_uint4(0, 0, 0, 0);
                             }
                         }
                         fence_proxy_async_smem();
@@ -673,13 +692,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
                             const int key = kb + c * 32 + e;
-                            if (key < row_lo || key >= row_hi) s[c][e] = MIN ? 0x7F800000u : 0xFF800000u;
+                            if (key < row_lo || key >= row_hi) s[c][e] = 0xFF800000u;
                         }
                 }
                 float t[4];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) t[c] = extreme32<MIN>(s[c]);
-                const float top = (MIN ? min3(t[0], t[1], fminf(t[2], t[3])) : max3(t[0], t[1], fmaxf(t[2], t[3]))) * p.scale_log2;
+                for (int c = 0; c < 4; ++c) t[c] = largest32(s[c]);
+                const float top = max3(t[0], t[1], fmaxf(t[2], t[3])) * p.scale_log2;
                 if (__any_sync(~0u, top > m + 8.f)) {
                     const float mn = fmaxf(m, top);
                     const float f = mn == -INFINITY ? 1.f : ex2(m - mn);

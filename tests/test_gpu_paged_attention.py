@@ -258,3 +258,37 @@ def test_strides_along_one_token_or_head_do_not_matter(mnb):
     p = Problem(mnb, [1], [45], 1, 1, 64, "bf16", 16, "hnd", seed=16)
     q = torch.as_strided(p.q.clone(), (1, 1, 64), (3, 5, 1))
     p.check(*p.run(q=q))
+
+
+@pytest.mark.parametrize("order", ["hnd", "nhd"])
+@pytest.mark.parametrize("inside", ["page pairs", "padded heads", "padded pages", "one head of many"])
+@pytest.mark.parametrize("q_lens,kv_lens", [([70, 40], [70, 333]), ([1, 1], [45, 700])])
+def test_pools_with_gaps(mnb, order, inside, q_lens, kv_lens):
+    """Keys and values of a page side by side, and strides that are no multiples of each other."""
+    hkv = 1 if inside == "one head of many" else 2
+    p = Problem(mnb, q_lens, kv_lens, 4, hkv, 128, "bf16", 16, order, seed=17)
+    pages, b, c, D = p.k.shape
+    if inside == "page pairs":
+        pool = torch.full((pages, 2, b, c, D), float("nan"), dtype=p.k.dtype, device="cuda")
+        k, v = pool[:, 0], pool[:, 1]
+    elif inside == "one head of many":
+        at = 1 if order == "hnd" else 2
+        wide = list(p.k.shape)
+        wide[at] = 3
+        k, v = (torch.full(wide, float("nan"), dtype=p.k.dtype, device="cuda").narrow(at, 1, 1) for _ in range(2))
+    else:
+        pad = 8 if inside == "padded pages" else 0
+        row = D + 8 if inside == "padded heads" else D
+        k, v = (torch.full((pages * (b * c * row + pad),), float("nan"), dtype=p.k.dtype, device="cuda").as_strided(
+            p.k.shape, (b * c * row + pad, c * row, row, 1)) for _ in range(2))
+    k.copy_(p.k)
+    v.copy_(p.v)
+    p.cache = mnb.kv_cache(k, v, p.tables, p.lens, order, R.CODE["bf16"])
+    p.check(*p.run())
+
+
+@pytest.mark.parametrize("D", [64, 80, 128])
+@pytest.mark.parametrize("scale", [-0.3, 0.0, -1e-38])
+def test_many_rows_under_scales_that_are_not_positive(mnb, D, scale):
+    p = Problem(mnb, [90], [400], 4, 2, D, "f16", 16, "hnd", seed=18)
+    p.check(*p.run(scale=scale), scale=scale)
