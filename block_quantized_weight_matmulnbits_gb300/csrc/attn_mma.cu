@@ -11,7 +11,6 @@ constexpr int ctas_of(int dp) { return dp == 256 ? 152 : 304; }
 
 template <int DT, int DP>
 cudaError_t launch_as(const AttnParams& p, cudaStream_t s) {
-    using S = mma::Shape<DP>;
     SplitParams sp{};
     sp.ctas = ctas_of(DP);
     sp.whole_tiles = 16;
@@ -28,17 +27,19 @@ cudaError_t launch_as(const AttnParams& p, cudaStream_t s) {
     // (56 sequences of up to 2106 keys, two key heads: 20.5 us cut evenly, 22.0 us on clusters of two; one of 777 keys,
     // eight key heads: 7.6 us on clusters of eight, 16.8 us cut evenly).
     int cl = 1;
-    while (cl < 8 && units * cl * 2 <= sp.ctas) cl *= 2;
+    while (cl < 8 && units * cl * 2 <= 152 * mma::Shape<DP, true>::kCtasPerSm) cl *= 2;
     if (cl > 1 && keys <= (int64_t)768 * cl) {
         auto kern = mma::attn_mma_kernel<DT, DP, true>;
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+        constexpr int smem = mma::Shape<DP, true>::kSmem;
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
-        return dec::launch_pdl(kern, dim3((unsigned)(units * cl)), dim3(mma::kThreads), S::kSmem, s, cl, p, sp);
+        return dec::launch_pdl(kern, dim3((unsigned)(units * cl)), dim3(mma::kThreads), smem, s, cl, p, sp);
     }
     auto kern = mma::attn_mma_kernel<DT, DP, false>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    constexpr int smem = mma::Shape<DP, false>::kSmem;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    e = dec::launch_pdl(kern, dim3(sp.ctas), dim3(mma::kThreads), S::kSmem, s, 1, p, sp);
+    e = dec::launch_pdl(kern, dim3(sp.ctas), dim3(mma::kThreads), smem, s, 1, p, sp);
     if (e != cudaSuccess) return e;
     // No unit is cut when the bounds already say that each is short and has a CTA.
     if (units <= sp.ctas && keys / mma::kKeys + 2 <= sp.whole_tiles) return cudaSuccess;
