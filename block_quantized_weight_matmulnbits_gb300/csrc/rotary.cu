@@ -8,12 +8,12 @@
 // bound by the bytes of x and y, so all it has to do is keep enough wide loads
 // in flight.  A thread owns one 16-byte vector (half layout: the two vectors of
 // its pairs) of up to four heads of one token: the table values are read once
-// for the four, and their loads are independent.  Neighbouring threads take
+// for them, and their loads are independent.  Neighbouring threads take
 // neighbouring vectors of neighbouring heads, so a warp's accesses are whole
 // lines.  The append is the same pass with another address for k and v.
 //
 // Measured on a GB300 (6800 GB/s copy): 10031 tokens of 48 heads x 128 in bf16,
-// half layout, turned and appended: 41.3 us, 6030 GB/s (48 us with one head a
+// half layout, turned and appended: 40.1 us, 6210 GB/s (48 us with one head a
 // thread, 42.5 with two); 4999 x 18 x 96 in f32, interleaved, 64 of 96 depths:
 // 14.2 us, 4950 GB/s, the ramp and tail of a short kernel.  One token: 7 us, the
 // launch and a chain of lookups (length, page, table row).
@@ -209,16 +209,20 @@ cudaError_t launch_as(RotParams p, int64_t D, cudaStream_t s) {
     const int heads = p.h_q + 2 * p.h_k;
     p.n_pair = INTER ? p.rot / V : p.rot / 2 / V;
     p.per_head = p.n_pair + (int)((D - p.rot) / (WIDE ? V : 1));
-    // Four heads a thread once that still leaves two full blocks' worth of
-    // threads per SM; one below, where more threads hide more latency.
+    // Several heads a thread once that still leaves two full blocks' worth of
+    // threads per SM; one below, where more threads hide more latency.  Four of
+    // one vector each (interleaved pairs), three of two vectors (halves): 10031
+    // tokens x 48 heads x 128, bf16: halves 40.2 us with three, 41.5 with four,
+    // 44.2 with six; interleaved 43.2 with four, 47.4 with three.
+    constexpr int kMany = INTER ? 4 : 3;
     const bool many = WIDE && p.T * heads * p.per_head >= (int64_t)4 * 2048 * dec::kSms;
-    p.groups = many ? (heads + 3) / 4 : heads;
+    p.groups = many ? (heads + kMany - 1) / kMany : heads;
     const int64_t items = p.T * p.groups * p.per_head;
     const int64_t blocks = (items + kThreads - 1) / kThreads;
     if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     if constexpr (WIDE) {
         if (many)
-            return dec::launch_pdl(rotary_kernel<DT, V, WIDE, INTER, 4>, dim3((unsigned)blocks), dim3(kThreads), 0, s, 1, p);
+            return dec::launch_pdl(rotary_kernel<DT, V, WIDE, INTER, kMany>, dim3((unsigned)blocks), dim3(kThreads), 0, s, 1, p);
     }
     return dec::launch_pdl(rotary_kernel<DT, V, WIDE, INTER, 1>, dim3((unsigned)blocks), dim3(kThreads), 0, s, 1, p);
 }
