@@ -12,7 +12,8 @@
 //     through shared memory when the CTA leaves a unit.
 //   - 2 CTAs per SM with 3 stages of 8 KB a warp (D = 128) hold 128 KB of loads
 //     in flight per SM while a third of the ring is computed on.
-//   - Page numbers are read one stage ahead of the loads that need them.
+//   - Page numbers are read one stage ahead of the loads that need them, and a
+//     unit's first loads are issued before the unit before it is joined.
 // Measured on a GB300 (6800 GB/s copy): 64 sequences of 684 to 8192 keys, 8 key
 // heads x 128, 4 queries each, bf16: 131 us, 6040 GB/s (the even cut; 5 us of it
 // the join); one sequence of 131001 keys, f16: 93 us, 5780 GB/s; one of 777 keys
@@ -106,8 +107,8 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, CL>::kCtasPerSm) attn_mma_
     float2* ml_s = reinterpret_cast<float2*>(qs + kRows * DP * 2);
     float2* ml_c = ml_s + kWarps * kRows;         // the CTA's own (m, l) and O of a row, for its cluster
     float* o_c = reinterpret_cast<float*>(ml_c + kRows);
-    float* o_s = reinterpret_cast<float*>(smem);  // [warp][row][DP], once the rings are drained
-    static_assert(kWarps * kRows * DP * 4 <= kWarps * S::kRing, "the partial results fit in the rings");
+    // A warp's O [row][DP], for the others, lies in the stage of its ring that held the unit's last tile.
+    static_assert(kRows * DP * 4 == S::kStage, "a warp's partial results take a stage");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     griddep_wait();
     griddep_launch_dependents();
@@ -141,73 +142,97 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, CL>::kCtasPerSm) attn_mma_
     const int lrow = lane / kLanes, lchunk = lane % kLanes;
     const bool col_ok = lchunk * 8 < p.D;
 
-    for (bool first = true;; first = false) {
-        const int rt = pl.unit / p.kv_heads, hk = pl.unit - rt * p.kv_heads;
-        const int t0 = CL ? (int)((int64_t)pl.s.tiles * rank / peers) : pl.tile;
+    // the unit at hand
+    int rt, hk, t0, t1, rows, i0, i1, lo, hi, key_w;
+    int64_t tok0, head_off;
+    const int32_t* table;
+    int c0 = 0;  // the stage of its first tile
+    auto begin_unit = [&]() {
+        rt = pl.unit / p.kv_heads;
+        hk = pl.unit - rt * p.kv_heads;
+        t0 = CL ? (int)((int64_t)pl.s.tiles * rank / peers) : pl.tile;
         const int64_t end = x1 - pl.unit_begin;
-        const int t1 = CL                                 ? (int)((int64_t)pl.s.tiles * (rank + 1) / peers)
-                       : dv.whole || end >= pl.s.tiles ? pl.s.tiles
-                                                          : (int)end;
-        const int rows = pl.s.n * p.group - rt * kRows < kRows ? pl.s.n * p.group - rt * kRows : kRows;
-        const int64_t tok0 = p.q_start[pl.b];
-        const int i0 = rt * kRows / p.group, i1 = (rt * kRows + rows - 1) / p.group + 1;
-        int lo, hi;  // keys that a row of the tile sees
-        visible_range(p, pl.s.n, pl.s.len, i0, i1, &lo, &hi);
-        const int32_t* table = p.tables + (int64_t)pl.b * p.table_stride;
-        const int key_w = pl.s.lo + warp * 16;
-        const int64_t head_off = (int64_t)hk * p.head_stride;
+        t1 = CL ? (int)((int64_t)pl.s.tiles * (rank + 1) / peers) : dv.whole || end >= pl.s.tiles ? pl.s.tiles : (int)end;
+        rows = pl.s.n * p.group - rt * kRows < kRows ? pl.s.n * p.group - rt * kRows : kRows;
+        tok0 = p.q_start[pl.b];
+        i0 = rt * kRows / p.group;
+        i1 = (rt * kRows + rows - 1) / p.group + 1;
+        visible_range(p, pl.s.n, pl.s.len, i0, i1, &lo, &hi);  // keys that a row of the tile sees
+        table = p.tables + (int64_t)pl.b * p.table_stride;
+        key_w = pl.s.lo + warp * 16;
+        head_off = (int64_t)hk * p.head_stride;
+    };
+    auto stage = [&](int t) { return ring + (uint32_t)(((c0 + t - t0) % S::kStages) * S::kStage); };
 
-        // page numbers of the 16 keys from key0 on: rows 0-7 in lane 0, 8-15 in lane 1 (and so on)
-        auto pages_at = [&](int t) -> int {
-            const int key = key_w + t * kKeys + (lane & 1) * 8;
-            if (t >= t1 || key >= hi || key + 8 <= lo) return -1;
-            const int col = key >> p.page_shift;
-            int page = col < p.table_stride ? __ldg(table + col) : -1;
-            if ((unsigned)page >= (unsigned)p.num_pages) {
-                set_status(p.status, MNB_ERR_INVALID_ARG);
-                page = -1;
-            }
-            return page;
-        };
-        auto load = [&](int t, int pages) {
-            const int key0 = key_w + t * kKeys;
-            if (t < t1 && key0 < hi && key0 + 16 > lo) {
-                const int pa = __shfl_sync(~0u, pages, 0), pb = __shfl_sync(~0u, pages, 1);
-                const int64_t offa = pa * p.page_stride + head_off + (key0 & ps_mask) * p.token_stride + lchunk * 8;
-                const int64_t offb = pb * p.page_stride + head_off + ((key0 + 8) & ps_mask) * p.token_stride + lchunk * 8;
-                const uint32_t dst = ring + ((t - t0) % S::kStages) * S::kStage;
+    // page numbers of the 16 keys from key0 on: rows 0-7 in lane 0, 8-15 in lane 1 (and so on)
+    auto pages_at = [&](int t) -> int {
+        const int key = key_w + t * kKeys + (lane & 1) * 8;
+        if (t >= t1 || key >= hi || key + 8 <= lo) return -1;
+        const int col = key >> p.page_shift;
+        int page = col < p.table_stride ? __ldg(table + col) : -1;
+        if ((unsigned)page >= (unsigned)p.num_pages) {
+            set_status(p.status, MNB_ERR_INVALID_ARG);
+            page = -1;
+        }
+        return page;
+    };
+    auto load = [&](int t, int pages) {
+        const int key0 = key_w + t * kKeys;
+        if (t < t1 && key0 < hi && key0 + 16 > lo) {
+            const int pa = __shfl_sync(~0u, pages, 0), pb = __shfl_sync(~0u, pages, 1);
+            const int64_t offa = pa * p.page_stride + head_off + (key0 & ps_mask) * p.token_stride + lchunk * 8;
+            const int64_t offb = pb * p.page_stride + head_off + ((key0 + 8) & ps_mask) * p.token_stride + lchunk * 8;
+            const uint32_t dst = stage(t);
 #pragma unroll
-                for (int i = 0; i < 16 / kRpi; ++i) {
-                    const int r = i * kRpi + lrow;
-                    const bool b = r >= 8;
-                    const bool ok = (b ? pb : pa) >= 0 && key0 + r < hi && col_ok;
-                    const int64_t off = ok ? (b ? offb : offa) + (r & 7) * p.token_stride : 0;
-                    const uint32_t to = dst + chunk_at<DP>(r, lchunk);
-                    cp16(to, kp + off, ok);
-                    cp16(to + S::kHalf, vp + off, ok);
-                }
+            for (int i = 0; i < 16 / kRpi; ++i) {
+                const int r = i * kRpi + lrow;
+                const bool b = r >= 8;
+                const bool ok = (b ? pb : pa) >= 0 && key0 + r < hi && col_ok;
+                const int64_t off = ok ? (b ? offb : offa) + (r & 7) * p.token_stride : 0;
+                const uint32_t to = dst + chunk_at<DP>(r, lchunk);
+                cp16(to, kp + off, ok);
+                cp16(to + S::kHalf, vp + off, ok);
             }
-            cp_commit();
-        };
+        }
+        cp_commit();
+    };
 
-        int pg = pages_at(t0);
+    int pg;
+    auto first_loads = [&]() {
+        pg = pages_at(t0);
 #pragma unroll
         for (int s = 0; s < S::kStages - 1; ++s) {
             const int nx = pages_at(t0 + s + 1);
             load(t0 + s, pg);
             pg = nx;
         }
-        // the unit's rows of Q (past the last row or depth: zero)
-        for (int c = tid; c < kRows * kChunks; c += kThreads) {
-            const int r = c / kChunks, ch = c % kChunks;
-            uint4 v = make_uint4(0, 0, 0, 0);
+    };
+    // the unit's rows of Q (past the last row or depth: zero), through registers
+    constexpr int kQ = kRows * kChunks / kThreads;
+    static_assert(kQ * kThreads == kRows * kChunks, "Q divides among the threads");
+    uint4 qv[kQ];
+    auto load_q = [&]() {
+#pragma unroll
+        for (int i = 0; i < kQ; ++i) {
+            const int c = tid + i * kThreads, r = c / kChunks, ch = c % kChunks;
+            qv[i] = make_uint4(0, 0, 0, 0);
             if (r < rows && ch * 8 < p.D) {
                 const int g = rt * kRows + r;
                 const int64_t t = tok0 + g / p.group;
                 const int h = hk * p.group + g % p.group;
-                v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + t * p.q_ts + h * p.q_hs + ch * 8);
+                qv[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + t * p.q_ts + h * p.q_hs + ch * 8);
             }
-            *reinterpret_cast<uint4*>(qs + chunk_at<DP>(r, ch)) = v;
+        }
+    };
+    begin_unit();
+    first_loads();
+    load_q();
+
+    for (bool first = true;; first = false) {
+#pragma unroll
+        for (int i = 0; i < kQ; ++i) {
+            const int c = tid + i * kThreads;
+            *reinterpret_cast<uint4*>(qs + chunk_at<DP>(c / kChunks, c % kChunks)) = qv[i];
         }
         __syncthreads();
         const int mi = lane >> 3;
@@ -241,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, CL>::kCtasPerSm) attn_mma_
             __syncwarp();
             const int key0 = key_w + t * kKeys;
             if (key0 < hi && key0 + 16 > lo) {
-                const uint32_t ka = ring + ((t - t0) % S::kStages) * S::kStage, va = ka + S::kHalf;
+                const uint32_t ka = stage(t), va = ka + S::kHalf;
                 float s[2][4] = {};
                 const uint32_t k_row = (mi >> 1) * 8 + (lane & 7);
 #pragma unroll
@@ -317,20 +342,47 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, CL>::kCtasPerSm) attn_mma_
             }
             __syncwarp();  // the stage is free for the next load
         }
-        cp_wait<0>();
-        __syncthreads();  // every warp is done with its ring: it becomes the exchange buffer
+        // (the range may be empty: any stage then, all loads have landed)
+        const int n_tiles = t1 > t0 ? t1 - t0 : 0;
+        if (n_tiles == 0) cp_wait<0>();
+        const int last = (c0 + (n_tiles ? n_tiles - 1 : S::kStages - 1)) % S::kStages;
+        auto o_of = [&](int w) { return reinterpret_cast<float*>(smem + w * S::kRing + last * S::kStage); };
+        __syncwarp();
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             l[j] += __shfl_xor_sync(~0u, l[j], 1);
             l[j] += __shfl_xor_sync(~0u, l[j], 2);
             const int r = (lane >> 2) + 8 * j;
             if ((lane & 3) == 0) ml_s[warp * kRows + r] = make_float2(m[j], l[j]);
-            float* row = o_s + (warp * kRows + r) * DP + (lane & 3) * 2;
+            float* row = o_of(warp) + r * DP + (lane & 3) * 2;
 #pragma unroll
             for (int n = 0; n < DP / 8; ++n) *reinterpret_cast<float2*>(row + ((n ^ (r & 7)) * 8)) = make_float2(o[n][2 * j], o[n][2 * j + 1]);
         }
-        __syncthreads();
         const bool done = dv.whole || (t0 == 0 && t1 == pl.s.tiles);
+        const int e_rt = rt, e_hk = hk, e_rows = rows;
+        const int64_t e_tok0 = tok0;
+        bool more = false;
+        if constexpr (!CL) {
+            if (tid == 0 && !dv.whole && t1 < pl.s.tiles && x0 <= pl.unit_begin) {
+                // this range's end is the first cut of the unit; its pieces end with the last CTA that begins before its end
+                const int64_t end = ((pl.unit_begin + pl.s.tiles) * dv.ctas - 1) / dv.total;
+                sp.cut[blockIdx.x] = make_int4((int)tok0, rt * kRows, hk | rows << 16,
+                                               (int)(end - blockIdx.x + 1) * 2 + (first ? 0 : 1));
+            }
+            // the next unit's first loads are on their way while this one is joined and written
+            more = !dv.whole && x1 > pl.unit_begin + pl.s.tiles;
+            if (more) {
+                next_unit<kRows, kKeys>(p, pl);
+                more = x1 > pl.unit_begin;
+            }
+            if (more) {
+                c0 = (last + 1) % S::kStages;
+                begin_unit();
+                first_loads();
+                load_q();
+            }
+        }
+        __syncthreads();
         {
             const int r = tid >> 3, q8 = tid & 7;  // 8 threads a row, groups of 8 columns each
             float top = -INFINITY;
@@ -344,10 +396,10 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, CL>::kCtasPerSm) attn_mma_
                 wt[w] = ex2(v.x - base);
                 sum = fmaf(v.y, wt[w], sum);
             }
-            if (CL || r < rows) {
-                const int g = rt * kRows + r;
-                const int64_t tk = tok0 + g / p.group;
-                const int h = hk * p.group + g % p.group;
+            if (CL || r < e_rows) {
+                const int g = e_rt * kRows + r;
+                const int64_t tk = e_tok0 + g / p.group;
+                const int h = e_hk * p.group + g % p.group;
                 const int slot = first ? 0 : 1;
                 const int64_t at = ((int64_t)blockIdx.x * 2 + slot) * kRows + r;
                 const float inv = sum > 0.f ? 1.f / sum : 0.f;
@@ -355,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, CL>::kCtasPerSm) attn_mma_
                     float a[8] = {};
 #pragma unroll
                     for (int w = 0; w < kWarps; ++w) {
-                        const float4* src = reinterpret_cast<const float4*>(o_s + (w * kRows + r) * DP + ((c ^ (r & 7)) * 8));
+                        const float4* src = reinterpret_cast<const float4*>(o_of(w) + r * DP + ((c ^ (r & 7)) * 8));
                         const float4 u = src[0], v = src[1];
                         a[0] = fmaf(u.x, wt[w], a[0]); a[1] = fmaf(u.y, wt[w], a[1]);
                         a[2] = fmaf(u.z, wt[w], a[2]); a[3] = fmaf(u.w, wt[w], a[3]);
@@ -391,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, CL>::kCtasPerSm) attn_mma_
         if constexpr (CL) {
             cluster_sync();
             // CTA `rank` joins rows rank, rank + peers, ..., a warp a row
-            for (int r = rank + warp * peers; r < rows; r += peers * kWarps) {
+            for (int r = rank + warp * peers; r < e_rows; r += peers * kWarps) {
                 float top = -INFINITY;
                 for (int c = 0; c < peers; ++c) top = fmaxf(top, ld_peer2(ml_c + r, (uint32_t)c).x);
                 const float base = top == -INFINITY ? 0.f : top;
@@ -407,9 +459,9 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, CL>::kCtasPerSm) attn_mma_
                         a[2 * d + 1] = fmaf(u.y, w, a[2 * d + 1]);
                     }
                 }
-                const int g = rt * kRows + r;
-                const int64_t tk = tok0 + g / p.group;
-                const int h = hk * p.group + g % p.group;
+                const int g = e_rt * kRows + r;
+                const int64_t tk = e_tok0 + g / p.group;
+                const int h = e_hk * p.group + g % p.group;
                 const float inv = sum > 0.f ? 1.f / sum : 0.f;
                 uint16_t* dst = static_cast<uint16_t*>(p.o) + tk * p.o_ts + h * p.o_hs;
 #pragma unroll
@@ -421,17 +473,8 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, CL>::kCtasPerSm) attn_mma_
             cluster_sync();  // nobody leaves while its shared memory is read
             return;
         }
-        if (dv.whole) break;
-        if (tid == 0 && t1 < pl.s.tiles && x0 <= pl.unit_begin) {
-            // this range's end is the first cut of the unit; its pieces end with the last CTA that begins before its end
-            const int64_t last = ((pl.unit_begin + pl.s.tiles) * dv.ctas - 1) / dv.total;
-            sp.cut[blockIdx.x] = make_int4((int)tok0, rt * kRows, hk | rows << 16,
-                                           (int)(last - blockIdx.x + 1) * 2 + (first ? 0 : 1));
-        }
-        if (x1 <= pl.unit_begin + pl.s.tiles) break;
-        next_unit<kRows, kKeys>(p, pl);
-        if (x1 <= pl.unit_begin) break;
-        __syncthreads();  // the exchange buffer becomes the rings again
+        if (!more) break;
+        // (the barrier behind the next Q keeps the exchange's stage and ml_s until all have read them)
     }
 }
 

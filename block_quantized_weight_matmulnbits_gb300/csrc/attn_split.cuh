@@ -17,10 +17,11 @@
 namespace mnb {
 namespace attn {
 
-// What a unit costs beside its tiles (its lookups, Q, first loads and exchange), in tiles: the division counts each
-// unit that much longer, or a range of many short units would take several times as long as one of few long units
-// (256 sequences of 49 to 600 keys, 8 key heads: 92 us without it, 63 with).
-constexpr int kUnitCost = 6;
+// What a unit costs beside its tiles (its lookups, Q and exchange; its first loads fly during the exchange before it), in
+// tiles: the division counts each unit that much longer, or a range of many short units would take several times as
+// long as one of few long units.  256 sequences of 49 to 600 keys, 8 key heads: 78 us at 0, 58, 54, 55, 57 at 1, 2, 3, 4;
+// 512 of up to 1000 keys: 162, 145, 136, 136, 139 us; 64 of up to 8192 keys: 129 us at each.
+constexpr int kUnitCost = 2;
 
 struct SplitParams {
     int ctas;        // grid of the first kernel
