@@ -31,7 +31,7 @@ mnb_status mnb_paged_attention(const mnb_attention_args* a, const mnb_kv_cache* 
         (a->causal != 0 && a->causal != 1) || !std::isfinite(a->scale) || c->head_dim % 8 != 0 || c->head_dim > 256)
         return MNB_ERR_INVALID_ARG;
     const int64_t vec = 16 / dec::dt_bytes(c->dtype);
-    // a stride along one token or one head steps nowhere: it is not judged, and a plain one stands in for it
+    // a stride along one token or one head steps nowhere: it is not checked, and a plain one stands in for it
     const int64_t D = c->head_dim, HD = a->q_heads * D;
     const int64_t st[4] = {a->T > 1 ? a->q_token_stride : HD, a->q_heads > 1 ? a->q_head_stride : D,
                            a->T > 1 ? a->o_token_stride : HD, a->q_heads > 1 ? a->o_head_stride : D};

@@ -25,7 +25,7 @@ cudaError_t launch_as(const AttnParams& p, cudaStream_t s) {
     // Few units of a moderate context: a cluster each.  A CTA takes about 5 us and 0.6 us for each 64 keys of its range;
     // the even cut over all SMs starts at about 14 us (its division, its second kernel) and wins beyond 12 tiles a CTA
     // (56 sequences of up to 2106 keys, two key heads: 20.5 us cut evenly, 22.0 us on clusters of two; one of 777 keys,
-    // eight key heads: 7.6 us on clusters of eight, 16.8 us cut evenly).
+    // eight key heads: 7.7 us on clusters of eight, 16.8 us cut evenly).
     int cl = 1;
     while (cl < 8 && units * cl * 2 <= 152 * mma::Shape<DP, true>::kCtasPerSm) cl *= 2;
     if (cl > 1 && keys <= (int64_t)768 * cl) {

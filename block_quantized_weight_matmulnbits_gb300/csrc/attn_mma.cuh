@@ -15,9 +15,10 @@
 //   - Page numbers are read one stage ahead of the loads that need them, and a
 //     unit's first loads are issued before the unit before it is joined.
 // Measured on a GB300 (6800 GB/s copy): 64 sequences of 684 to 8192 keys, 8 key
-// heads x 128, 4 queries each, bf16: 131 us, 6040 GB/s (the even cut; 5 us of it
-// the join); one sequence of 131001 keys, f16: 93 us, 5780 GB/s; one of 777 keys
-// on clusters of 8: 7.6 us.  Bound by DRAM in the first two, by the chain of
+// heads x 128, 4 queries each, bf16: 130 us, 6070 GB/s (the even cut; 5 us of it
+// the join); 256 of 49 to 600 keys: 54 us, 4520 GB/s (63 us without the overlap
+// of units); one of 131001 keys, f16: 92 us, 5860 GB/s; one of 777 keys on
+// clusters of 8: 7.7 us.  Bound by DRAM in the long ones, by the chain of
 // dependent loads (length, page number, keys) in the last.
 // The maximum a row is scaled by follows the true one only when it falls more
 // than 8 (log2) behind, so O is rarely rescaled; p then stays below 2^8, exact
