@@ -853,11 +853,13 @@ __global__ void __launch_bounds__(256) attn_tc_join_kernel(const AttnParams p, c
     for (int s = lane; s < tp.splits; s += 32) top = fmaxf(top, tp.part_ml[base + s * 256].x);
 #pragma unroll
     for (int k = 16; k; k >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, k));
+    // (-inf: no range has a visible key, or those that have hold NaN scores alone, which a maximum passes over)
+    const float ref = top == -INFINITY ? 0.f : top;
     constexpr int PER = DP / 32;
     float acc[PER] = {}, l = 0.f;
-    for (int s0 = 0; s0 < tp.splits && top > -INFINITY; s0 += 32) {
+    for (int s0 = 0; s0 < tp.splits; s0 += 32) {
         const float2 ml = s0 + lane < tp.splits ? tp.part_ml[base + (s0 + lane) * 256] : make_float2(-INFINITY, 0.f);
-        const float w = exp2f(ml.x - top), wl = ml.y * w;
+        const float w = exp2f(ml.x - ref), wl = ml.y * w;
         const int cnt = tp.splits - s0 < 32 ? tp.splits - s0 : 32;
 #pragma unroll 4
         for (int s = 0; s < cnt; ++s) {
@@ -865,7 +867,7 @@ __global__ void __launch_bounds__(256) attn_tc_join_kernel(const AttnParams p, c
             l += __shfl_sync(~0u, wl, s);
             const float* o = tp.part_o + (base + (s0 + s) * 256) * DP + lane * PER;
             float v[PER] = {};
-            if (ws > 0.f) {  // (a range without a visible key leaves its O unwritten)
+            if (__shfl_sync(~0u, ml.y, s) != 0.f) {  // (a range without a visible key leaves its O unwritten)
                 if constexpr (PER == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(o);
                 else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(o);
             }
@@ -875,7 +877,7 @@ __global__ void __launch_bounds__(256) attn_tc_join_kernel(const AttnParams p, c
     }
     const int64_t tk = (int64_t)p.q_start[u.b] + i;
     const int h = u.hk * p.group + r % p.group;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
     uint16_t* o = static_cast<uint16_t*>(p.o) + tk * p.o_ts + h * p.o_hs + lane * PER;
     if (lane * PER < p.D) {
         if constexpr (PER == 4) *reinterpret_cast<uint2*>(o) = make_uint2(pack16<DT>(acc[0] * inv, acc[1] * inv), pack16<DT>(acc[2] * inv, acc[3] * inv));

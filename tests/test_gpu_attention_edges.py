@@ -1,0 +1,92 @@
+"""Attention over the paged cache at its edges: NaN and infinities in queries and keys, rows that see nothing beside
+rows that do, windows wider than any sequence, batches wider than one look at them, workspaces of other calls."""
+
+import numpy as np
+import pytest
+import torch
+
+from tests import _decoder_ref as R
+from tests.test_gpu_paged_attention import Problem
+
+pytestmark = pytest.mark.gpu
+
+
+def _rows(p):
+    """(token, sequence, position) of each row of the call."""
+    t = 0
+    for b, (m, n) in enumerate(zip(p.q_lens, p.kv_lens)):
+        for i in range(m):
+            yield t, b, n - m + i
+            t += 1
+
+
+def _check(p, o, lse, nan_rows, empty_rows=(), window=0, heads=None):
+    """Rows (token, head) of nan_rows are NaN in every depth and in lse, those of empty_rows 0 and -inf, and all others
+    within the 64-bit form's bounds."""
+    go, gl = R.f64(o), R.f64(lse)
+    k, v = {}, {}
+    for t, b, pos in _rows(p):
+        for h in range(p.hq) if heads is None else heads:
+            if (t, h) in nan_rows:
+                assert np.isnan(go[t, h]).all() and np.isnan(gl[t, h]), ("NaN", t, h, go[t, h][:4], gl[t, h])
+                continue
+            if (t, h) in empty_rows:
+                assert (go[t, h] == 0).all() and np.isneginf(gl[t, h]), ("empty", t, h, go[t, h][:4], gl[t, h])
+                continue
+            hk = h // (p.hq // p.hkv)
+            if (b, hk) not in k:
+                k[b, hk], v[b, hk] = p.rows(p.k, b, hk), p.rows(p.v, b, hk)
+            lo = max(0, pos - window + 1) if window else 0
+            ro, rl, bo, bl = R.attention(R.f64(p.q[t:t + 1, h]), k[b, hk][lo:pos + 1], v[b, hk][lo:pos + 1], pos - lo,
+                                         np.float32(p.scale()).astype(np.float64), True, 0)
+            assert (np.abs(go[t, h] - ro[0]) <= bo[p.dtype][0]).all(), (t, h)
+            assert (np.isneginf(gl[t, h]) and np.isneginf(rl[0])) or abs(gl[t, h] - rl[0]) <= bl[0], (t, h, gl[t, h], rl[0])
+
+
+def _set_keys(p, b, keys, value, what="k", head=slice(None)):
+    """Keys (or values) of a sequence's tokens."""
+    pages = p.k if what == "k" else p.v
+    for j in keys:
+        page, row = int(p.np_tables[b, j // p.page]), j % p.page
+        if p.order == "hnd":
+            pages[page, head, row] = value
+        else:
+            pages[page, row, head] = value
+
+
+#: one call of each kernel and form: clusters, the even cut and its join, the many-row kernel whole and cut, f32
+FORMS = [("bf16", [1, 1], [300, 40], 8, 2, 128), ("f16", [1] * 5, [9000, 31, 700, 64, 5], 8, 2, 64), ("bf16", [1], [3000], 2, 1, 256),
+         ("bf16", [1] * 40, [37 * (i + 1) for i in range(40)], 16, 8, 128), ("bf16", [260], [260], 2, 1, 64), ("f16", [40], [2500], 4, 2, 128),
+         ("bf16", [70, 3], [1900, 40], 6, 2, 96), ("bf16", [90], [100], 4, 2, 128), ("f32", [1, 9], [500, 30], 4, 2, 64)]
+
+
+def _form(mnb, form, seed, **kw):
+    dtype, q_lens, kv_lens, hq, hkv, D = form
+    return Problem(mnb, q_lens, kv_lens, hq, hkv, D, dtype, 16, "hnd", seed=seed, **kw)
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_a_nan_query_gives_nan(mnb, form):
+    """Never the zeros of a row that sees no key, however the keys are divided."""
+    p = _form(mnb, form, 21)
+    bad = {(0, 0), (p.T - 1, p.hq - 1), (p.T // 2, 1)}
+    for t, h in bad:
+        p.q[t, h, 3] = float("nan")
+    o, _ = p.run()
+    for t, h in bad:
+        assert torch.isnan(o[t, h]).all(), (t, h, o[t, h, :4])
+    o[torch.tensor([t for t, _ in bad]), torch.tensor([h for _, h in bad])] = 0
+    assert not torch.isnan(o).any()
+
+
+@pytest.mark.parametrize("tiles", [1, 2, 3, 4])
+@pytest.mark.parametrize("form", [f for f in FORMS if max(f[2]) >= 1900])
+def test_nan_in_every_key_of_a_range_gives_nan(mnb, form, tiles):
+    """The first 128, 256, .. keys of the longest sequence hold NaN, so that for one of the counts at least a range of its
+    keys holds nothing else: every row of the sequence is NaN, and none of the others."""
+    p = _form(mnb, form, 22)
+    b = int(np.argmax(p.kv_lens))
+    _set_keys(p, b, range(128 * tiles), float("nan"))
+    o, _ = p.run()
+    for t, s, _ in _rows(p):
+        assert torch.isnan(o[t]).all() if s == b else not torch.isnan(o[t]).any(), t
