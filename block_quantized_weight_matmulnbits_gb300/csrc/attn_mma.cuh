@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, CL>::kCtasPerSm) attn_mma_
                 const int h = e_hk * p.group + g % p.group;
                 const int slot = first ? 0 : 1;
                 const int64_t at = ((int64_t)blockIdx.x * 2 + slot) * kRows + r;
-                const float inv = sum > 0.f ? 1.f / sum : 0.f;
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
                 for (int c = q8; c < DP / 8; c += 8) {
                     float a[8] = {};
 #pragma unroll
@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, CL>::kCtasPerSm) attn_mma_
                 if (q8 == 0) {
                     if (CL) ml_c[r] = make_float2(top, sum);
                     else if (!done) sp.part_ml[at] = make_float2(top, sum);
-                    else if (p.lse) p.lse[tk * p.q_heads + h] = sum > 0.f ? (base + log2f(sum)) * kLn2 : -INFINITY;
+                    else if (p.lse) p.lse[tk * p.q_heads + h] = sum == 0.f ? -INFINITY : (base + log2f(sum)) * kLn2;
                 }
             }
         }
@@ -463,13 +463,13 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, CL>::kCtasPerSm) attn_mma_
                 const int g = e_rt * kRows + r;
                 const int64_t tk = e_tok0 + g / p.group;
                 const int h = e_hk * p.group + g % p.group;
-                const float inv = sum > 0.f ? 1.f / sum : 0.f;
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
                 uint16_t* dst = static_cast<uint16_t*>(p.o) + tk * p.o_ts + h * p.o_hs;
 #pragma unroll
                 for (int d = 0; d < DP / 64; ++d)
                     if (d * 64 + lane * 2 < p.D)
                         *reinterpret_cast<uint32_t*>(dst + d * 64 + lane * 2) = pack16<DT>(a[2 * d] * inv, a[2 * d + 1] * inv);
-                if (lane == 0 && p.lse) p.lse[tk * p.q_heads + h] = sum > 0.f ? (base + log2f(sum)) * kLn2 : -INFINITY;
+                if (lane == 0 && p.lse) p.lse[tk * p.q_heads + h] = sum == 0.f ? -INFINITY : (base + log2f(sum)) * kLn2;
             }
             cluster_sync();  // nobody leaves while its shared memory is read
             return;

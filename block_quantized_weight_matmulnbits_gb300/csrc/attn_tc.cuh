@@ -761,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
             const int64_t tk = (int64_t)job->tok + i;
             const int h = job->hk * p.group + r_head;
             const int64_t part = (int64_t)job->part * 256 + x * 128 + r;
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
             // O leaves through shared memory, 128 bytes of the warp's 32 rows at a time, so that eight lanes store a row's
             // whole lines.  (A thread storing its own row touches 32 lines an instruction: 7000 cycles a unit for bf16,
             // 14000 for the f32 partial results, with the tensor pipe idle.)
@@ -818,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
             }
             if (row_ok) {
                 if (tp.splits > 1) tp.part_ml[part] = make_float2(m, l);
-                else if (p.lse) p.lse[tk * p.q_heads + h] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+                else if (p.lse) p.lse[tk * p.q_heads + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
             }
             cnt += (uint32_t)nx;
             units_of += nx > 0;
@@ -883,7 +883,7 @@ __global__ void __launch_bounds__(256) attn_tc_join_kernel(const AttnParams p, c
         if constexpr (PER == 4) *reinterpret_cast<uint2*>(o) = make_uint2(pack16<DT>(acc[0] * inv, acc[1] * inv), pack16<DT>(acc[2] * inv, acc[3] * inv));
         else *reinterpret_cast<uint32_t*>(o) = pack16<DT>(acc[0] * inv, acc[1] * inv);
     }
-    if (lane == 0 && p.lse) p.lse[tk * p.q_heads + h] = l > 0.f ? (top + log2f(l)) * kLn2 : -INFINITY;
+    if (lane == 0 && p.lse) p.lse[tk * p.q_heads + h] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
 }
 
 }  // namespace tca

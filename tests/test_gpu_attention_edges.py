@@ -90,3 +90,27 @@ def test_nan_in_every_key_of_a_range_gives_nan(mnb, form, tiles):
     o, _ = p.run()
     for t, s, _ in _rows(p):
         assert torch.isnan(o[t]).all() if s == b else not torch.isnan(o[t]).any(), t
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_lse_of_a_nan_row_is_nan(mnb, form):
+    """And not the -inf of a row that sees no key; the other rows keep theirs."""
+    p = _form(mnb, form, 23)
+    bad = {(0, 0), (p.T - 1, p.hq - 1), (p.T // 2, 1)}
+    for t, h in bad:
+        p.q[t, h, p.D - 1] = float("nan")
+    o, lse = p.run()
+    _check(p, o, lse, bad, heads=sorted({0, 1, p.hq - 1}) if p.T <= 10 else [0])
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_an_infinite_score_gives_nan(mnb, form):
+    """exp(inf - inf): the row has no value, in o and in lse."""
+    p = _form(mnb, form, 24)
+    p.q[:, :, 0] = 1.0
+    _set_keys(p, 0, [0], 0.0)
+    p.k[int(p.np_tables[0, 0]), :, 0, 0] = float("inf")
+    o, lse = p.run()
+    for t, b, _ in _rows(p):
+        bad = torch.isnan(o[t]).all() and torch.isnan(lse[t]).all()
+        assert bad if b == 0 else not (torch.isnan(o[t]).any() or torch.isnan(lse[t]).any()), t
