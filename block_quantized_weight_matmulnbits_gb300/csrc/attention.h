@@ -36,7 +36,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 __host__ __device__ inline void visible_range(const AttnParams& p, int n, int len, int i0, int i1, int* lo, int* hi) {
     const int first = len - n + i0, last = len - n + i1 - 1;  // positions of the first and last row
     *hi = p.causal ? (last + 1 < len ? last + 1 : len) : len;
-    *lo = p.window > 0 && first - p.window + 1 > 0 ? first - p.window + 1 : 0;
+    *lo = p.window > 0 && first >= p.window ? first - p.window + 1 : 0;  // (first may be negative and the window 2^31 - 1)
 }
 
 // Few rows a key head, bf16 / f16 (attn_mma.cuh); its workspace.

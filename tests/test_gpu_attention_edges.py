@@ -114,3 +114,12 @@ def test_an_infinite_score_gives_nan(mnb, form):
     for t, b, _ in _rows(p):
         bad = torch.isnan(o[t]).all() and torch.isnan(lse[t]).all()
         assert bad if b == 0 else not (torch.isnan(o[t]).any() or torch.isnan(lse[t]).any()), t
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 3, 2 ** 30])
+@pytest.mark.parametrize("dtype,q_lens,kv_lens,hq,hkv,D", [
+    ("bf16", [5], [2], 4, 2, 128), ("f16", [5, 1], [2, 20000], 4, 2, 64), ("bf16", [300, 4], [130, 1], 4, 2, 128), ("f32", [5, 40], [2, 7], 2, 1, 64)])
+def test_a_window_past_every_sequence_is_no_window(mnb, window, dtype, q_lens, kv_lens, hq, hkv, D):
+    """The largest int stands for "no limit", and more new tokens than keys put the first rows before the sequence."""
+    p = Problem(mnb, q_lens, kv_lens, hq, hkv, D, dtype, 16, "hnd", seed=25)
+    p.check(*p.run(window=window), window=window)
