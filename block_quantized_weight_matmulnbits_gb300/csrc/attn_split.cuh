@@ -152,7 +152,7 @@ __device__ Place locate(const AttnParams& p, bool whole, int64_t x, bool tell) {
             sh_base = before + incl - v;
         }
         base += sum;
-        if (x < base) break;
+        if (x < base && !tell) break;  // (the block that reports bad sequences looks at all of them)
     }
     __syncthreads();
     Place pl;

@@ -123,3 +123,17 @@ def test_a_window_past_every_sequence_is_no_window(mnb, window, dtype, q_lens, k
     """The largest int stands for "no limit", and more new tokens than keys put the first rows before the sequence."""
     p = Problem(mnb, q_lens, kv_lens, hq, hkv, D, dtype, 16, "hnd", seed=25)
     p.check(*p.run(window=window), window=window)
+
+
+@pytest.mark.parametrize("dtype,batch,q,hq,hkv,D", [
+    ("bf16", 140, 1, 4, 1, 128), ("f16", 300, 1, 2, 1, 64),      # clusters
+    ("bf16", 200, 1, 4, 4, 128), ("bf16", 150, 20, 2, 1, 128),   # the even cut, the many-row kernel
+    ("f32", 140, 1, 2, 1, 64)])
+@pytest.mark.parametrize("at", [0, 127, 128, -1])
+def test_any_sequence_past_the_bounds_is_reported(mnb, dtype, batch, q, hq, hkv, D, at):
+    lens = [q + (7 * i) % 90 for i in range(batch)]
+    lens[at] = 300
+    p = Problem(mnb, [q] * batch, lens, hq, hkv, D, dtype, 16, "hnd", seed=26)
+    o, lse = p.run(max_kv=299)
+    assert mnb.mnb_get_device_error() == mnb.MNB_ERR_INVALID_ARG
+    p.check(o, lse, seqs={0, 1, 63, 126, batch - 2} - {at % batch}, heads=[0, hq - 1])
