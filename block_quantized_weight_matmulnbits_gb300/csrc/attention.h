@@ -39,6 +39,11 @@ __host__ __device__ inline void visible_range(const AttnParams& p, int n, int le
     *lo = p.window > 0 && first >= p.window ? first - p.window + 1 : 0;  // (first may be negative and the window 2^31 - 1)
 }
 
+// A sequence of tokens [q0, q1) and len keys that is no sequence, or exceeds the call's bounds.
+__device__ inline bool bad_sequence(const AttnParams& p, int q0, int q1, int len) {
+    return q0 < 0 || q1 < q0 || q1 - q0 > p.max_q || q1 > p.T || len < 0 || len > p.max_kv;
+}
+
 // Few rows a key head, bf16 / f16 (attn_mma.cuh); its workspace.
 cudaError_t launch_mma(const AttnParams& p, cudaStream_t s);
 size_t mma_workspace_bytes(int D);

@@ -29,13 +29,13 @@ __global__ void __launch_bounds__(kWarps * 32) attn_f32_kernel(const AttnParams 
     const int64_t t = blockIdx.x / (unsigned)p.q_heads;
     const int h = (int)(blockIdx.x % (unsigned)p.q_heads), hk = h / p.group;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (blockIdx.x == 0)  // reports bad sequences, those without a new token among them
+        for (int b = threadIdx.x; b < p.batch; b += kWarps * 32)
+            if (bad_sequence(p, p.q_start[b], p.q_start[b + 1], p.kv_lens[b])) set_status(p.status, MNB_ERR_INVALID_ARG);
     if (t >= p.q_start[p.batch]) return;
     const int b = dec::sequence_of(p.q_start, p.batch, t);
     const int n = p.q_start[b + 1] - p.q_start[b], len = p.kv_lens[b];
-    if (n > p.max_q || len > p.max_kv || len < 0) {
-        if (threadIdx.x == 0) set_status(p.status, MNB_ERR_INVALID_ARG);
-        return;
-    }
+    if (bad_sequence(p, p.q_start[b], p.q_start[b + 1], len)) return;
     const int i = (int)(t - p.q_start[b]);
     int lo, hi;
     visible_range(p, n, len, i, i + 1, &lo, &hi);

@@ -45,7 +45,7 @@ __device__ __forceinline__ Seq load_seq(const AttnParams& p, int b) {
     Seq s;
     s.n = p.q_start[b + 1] - p.q_start[b];
     s.len = p.kv_lens[b];
-    s.bad = s.n < 0 || s.n > p.max_q || s.len < 0 || s.len > p.max_kv || p.q_start[b] < 0 || p.q_start[b + 1] > p.T;
+    s.bad = bad_sequence(p, p.q_start[b], p.q_start[b + 1], s.len);
     if (s.bad) s.n = 0;
     int lo, hi;
     visible_range(p, s.n, s.len, 0, s.n, &lo, &hi);

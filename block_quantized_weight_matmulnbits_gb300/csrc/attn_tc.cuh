@@ -201,7 +201,7 @@ __device__ __forceinline__ Unit find_unit(const AttnParams& p, int tokens, int64
             const int q1 = p.q_start[b + 1];
             n = q1 - q0;
             len = p.kv_lens[b];
-            if (n < 0 || n > p.max_q || len < 0 || len > p.max_kv || q0 < 0 || q1 > p.T) {
+            if (bad_sequence(p, q0, q1, len)) {
                 set_status(p.status, MNB_ERR_INVALID_ARG);
                 n = 0;
             }

@@ -137,3 +137,11 @@ def test_any_sequence_past_the_bounds_is_reported(mnb, dtype, batch, q, hq, hkv,
     o, lse = p.run(max_kv=299)
     assert mnb.mnb_get_device_error() == mnb.MNB_ERR_INVALID_ARG
     p.check(o, lse, seqs={0, 1, 63, 126, batch - 2} - {at % batch}, heads=[0, hq - 1])
+
+
+@pytest.mark.parametrize("dtype,q", [("bf16", 1), ("bf16", 60), ("f32", 1)])
+def test_a_sequence_without_new_tokens_is_reported_too(mnb, dtype, q):
+    p = Problem(mnb, [q, 0, q], [80, 300, 70], 4, 2, 128, dtype, 16, "hnd", seed=27)
+    o, lse = p.run(max_kv=200)
+    assert mnb.mnb_get_device_error() == mnb.MNB_ERR_INVALID_ARG
+    p.check(o, lse, seqs=[0, 2])
