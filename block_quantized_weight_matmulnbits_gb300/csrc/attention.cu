@@ -42,8 +42,9 @@ mnb_status mnb_paged_attention(const mnb_attention_args* a, const mnb_kv_cache* 
     if (!a->q || !a->o || !a->q_start || !dec::aligned_to(a->q, 16) || !dec::aligned_to(a->o, 16) ||
         !dec::aligned_to(a->lse, 4) || !dec::aligned_to(a->q_start, 4))
         return MNB_ERR_INVALID_ARG;
-    const size_t need = mnb_attention_workspace_size(c->batch, a->T, a->q_heads, c->kv_heads, c->head_dim, a->max_q, a->max_kv, c->dtype);
-    if (need && (!a->workspace || a->workspace_bytes < need)) return MNB_ERR_NO_MEM;
+    // the least: the few-row kernel's; the many-row one cuts the context as far as the rest goes
+    const size_t least = c->dtype == MNB_F32 ? 0 : attn::mma_workspace_bytes(c->head_dim);
+    if (least && (!a->workspace || a->workspace_bytes < least)) return MNB_ERR_NO_MEM;
     if (a->workspace && !dec::aligned_to(a->workspace, 256)) return MNB_ERR_INVALID_ARG;
 
     attn::AttnParams p{};
@@ -82,6 +83,7 @@ mnb_status mnb_paged_attention(const mnb_attention_args* a, const mnb_kv_cache* 
     // a masked score is -inf before it is scaled; 2^-100 leaves every finite score at 0
     if (std::fabs(p.scale_log2) < 0x1p-100f) p.scale_log2 = 0x1p-100f;
     p.workspace = a->workspace;
+    p.workspace_bytes = a->workspace_bytes;
     p.dtype = c->dtype;
     wait_limits(&p.wait_limit, &p.wait_hint_ns);
     if (inject_launch_failure()) return MNB_ERR_CUDA;

@@ -25,6 +25,7 @@ struct AttnParams {
     float scale, scale_log2;                         // scale, scale * log2(e)
     int* status;
     void* workspace;
+    size_t workspace_bytes;
     uint32_t wait_limit, wait_hint_ns;
     int dtype;
 };

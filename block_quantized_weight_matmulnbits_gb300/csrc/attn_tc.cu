@@ -1,5 +1,6 @@
 // Host side of the many-row attention kernel: tensor maps, the cut of few
 // units into ranges of keys, workspace and launches.
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -35,8 +36,9 @@ struct Plan {
 // Units and splits from the bounds of a call.  A wave of 152 CTAs takes as
 // long as its key tiles plus about four tiles' worth of prologue and epilogue;
 // the cut with the least waves * (tiles + 4) is taken, and one with as many
-// tiles again must save a tenth to be worth its partial results.
-Plan make_plan(int64_t batch, int64_t T, int64_t q_heads, int64_t kv_heads, int64_t max_kv) {
+// tiles again must save a tenth to be worth its partial results.  max_pieces:
+// the partial results (units x ranges) that the workspace has room for.
+Plan make_plan(int64_t batch, int64_t T, int64_t q_heads, int64_t kv_heads, int64_t max_kv, int64_t max_pieces) {
     Plan pl;
     const int64_t group = q_heads / kv_heads;
     pl.tokens = (int)(tca::kRows / group);
@@ -45,6 +47,7 @@ Plan make_plan(int64_t batch, int64_t T, int64_t q_heads, int64_t kv_heads, int6
     const int64_t tiles = (max_kv + tca::kKeys - 1) / tca::kKeys;
     double best = 0;
     for (int64_t s = 1; s <= 64 && s <= tiles; ++s) {
+        if (s > 1 && pl.units * s > max_pieces) break;
         const int64_t waves = (pl.units * s + 151) / 152;
         double cost = (double)waves * (double)((tiles + s - 1) / s + 4);
         if (s > 1) cost = cost * 1.02 + (double)(pl.units * s) / 152.0;
@@ -79,6 +82,9 @@ OneBox one_box(const AttnParams& p) {
     }
     return b;
 }
+
+// Partial results of 256 rows: O and (m, l).
+size_t piece_bytes(int64_t D) { return (size_t)256 * ((D <= 64 ? 64 : 128) + 2) * 4; }
 
 template <int DT, int DP, bool ONE>
 cudaError_t launch_as(const AttnParams& p, const Plan& pl, cudaStream_t s) {
@@ -147,13 +153,20 @@ bool tc_serves(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t D, int6
     return rows > 32 || (double)batch * (double)max_kv * (double)(kv_heads * D) * 4.0 > 100e6;
 }
 
+// A call with more units may want fewer pieces than one with less (a full wave is not cut), so the size reported is no
+// less than kSharedPieces as soon as that many could be of use: a buffer sized for the largest call of a program then
+// serves its smaller ones at full speed (81 MB at 128 depths), up to those that want more than four waves of pieces.
+constexpr int64_t kSharedPieces = 4 * 152;
+
 size_t tc_workspace_bytes(int64_t batch, int64_t T, int64_t q_heads, int64_t kv_heads, int64_t D, int64_t max_kv) {
-    const Plan pl = make_plan(batch, T, q_heads, kv_heads, max_kv);
-    return pl.splits == 1 ? 0 : (size_t)pl.units * pl.splits * 256 * ((D <= 64 ? 64 : 128) + 2) * 4;
+    const Plan pl = make_plan(batch, T, q_heads, kv_heads, max_kv, INT64_MAX);
+    const int64_t tiles = (max_kv + tca::kKeys - 1) / tca::kKeys, most = pl.units * std::min<int64_t>(64, tiles);
+    const int64_t shared = tiles > 1 ? std::min(kSharedPieces, most) : 0;
+    return (size_t)std::max(shared, pl.splits == 1 ? 0 : pl.units * pl.splits) * piece_bytes(D);
 }
 
 cudaError_t launch_tc(const AttnParams& p, cudaStream_t s) {
-    const Plan pl = make_plan(p.batch, p.T, p.q_heads, p.kv_heads, p.max_kv);
+    const Plan pl = make_plan(p.batch, p.T, p.q_heads, p.kv_heads, p.max_kv, (int64_t)(p.workspace_bytes / piece_bytes(p.D)));
     if (pl.units * pl.splits * 32 > 0x7FFFFFFF) return cudaErrorNotSupported;
     if (p.D <= 64) return p.dtype == kF16 ? launch_as<kF16, 64, false>(p, pl, s) : launch_as<kBF16, 64, false>(p, pl, s);
     if (one_box(p).ok) {

@@ -523,9 +523,15 @@ MNB_API mnb_status mnb_rotary_append(const mnb_rotary_args* args, const mnb_kv_c
  *              status word (its rows are unspecified).
  *   head_dim   a multiple of 8, at most 256; q_heads a multiple of kv_heads;
  *              scale finite
- *   workspace  device, 256-byte aligned, mnb_attention_workspace_size() bytes
- *              of the same sizes, for the partial results of a split context;
- *              its contents need no preparation
+ *   workspace  device, 256-byte aligned, for the partial results of a divided
+ *              context; its contents need no preparation.  With
+ *              mnb_attention_workspace_size() bytes of the call's sizes the
+ *              context is divided as far as it pays.  The size for a larger
+ *              call (none of batch, T, max_q and max_kv smaller) serves as
+ *              well: with less than its own size a call divides its context as
+ *              far as the buffer goes, so its last bits may depend on
+ *              workspace_bytes.  MNB_ERR_NO_MEM below what every bf16 / f16
+ *              call of a head_dim needs (5.1 MB for 65 to 128).
  * A page number outside [0, num_pages) sets the status word; its keys count as
  * zeros.  NaN or infinities in visible values of the cache reach every row of
  * their sequence that the same tile of keys covers.  A row with a NaN or +inf
@@ -546,8 +552,8 @@ typedef struct mnb_attention_args {
 
 MNB_API mnb_status mnb_paged_attention(const mnb_attention_args* args, const mnb_kv_cache* cache);
 
-/* Workspace bytes of mnb_paged_attention for a call of these sizes (0 if they
- * are invalid or none is needed). */
+/* Workspace bytes of mnb_paged_attention for a call of these sizes, enough for
+ * calls of smaller ones too (0 if the sizes are invalid or none is needed). */
 MNB_API size_t mnb_attention_workspace_size(int64_t batch, int64_t T, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
                                     int64_t max_q, int64_t max_kv, mnb_dtype dtype);
 

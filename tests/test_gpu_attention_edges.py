@@ -145,3 +145,32 @@ def test_a_sequence_without_new_tokens_is_reported_too(mnb, dtype, q):
     o, lse = p.run(max_kv=200)
     assert mnb.mnb_get_device_error() == mnb.MNB_ERR_INVALID_ARG
     p.check(o, lse, seqs=[0, 2])
+
+
+def test_a_workspace_of_a_larger_call_serves_smaller_ones(mnb):
+    """A server sizes its buffer once, for the largest call; that call may have units enough and cut none of them."""
+    heads, kv_heads, D, code = 4, 2, 128, R.CODE["bf16"]
+    size = mnb.mnb_attention_workspace_size(1, 8000, heads, kv_heads, D, 8000, 9000, code)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    for q, kv in ((70, 9000), (300, 2500), (1, 9000), (20, 3000)):
+        p = Problem(mnb, [q], [kv], heads, kv_heads, D, "bf16", 16, "hnd", seed=q)
+        o, lse = torch.empty_like(p.q), torch.empty(p.q.shape[:2], device="cuda")
+        mnb.mnb_paged_attention(p.q, o, p.cache, p.start, q, kv, p.scale(), lse=lse, workspace=ws)
+        p.check(o, lse, heads=[0, heads - 1])
+
+
+@pytest.mark.parametrize("part", [0.0, 0.3, 0.7, 1.0])
+def test_a_smaller_workspace_cuts_into_fewer_ranges(mnb, part):
+    """Between the least and the full size a call is cut as far as the buffer goes, and no byte past it is written."""
+    p = Problem(mnb, [70], [9000], 4, 2, 128, "bf16", 16, "hnd", seed=28)
+    full = mnb.mnb_attention_workspace_size(1, 70, 4, 2, 128, 70, 9000, R.CODE["bf16"])
+    least = mnb.mnb_attention_workspace_size(1, 1, 4, 2, 128, 1, 9000, R.CODE["bf16"])
+    size = least + int((full - least) * part) // 256 * 256
+    ws = torch.full((size + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+    o, lse = torch.empty_like(p.q), torch.empty(p.q.shape[:2], device="cuda")
+    mnb.mnb_paged_attention(p.q, o, p.cache, p.start, 70, 9000, p.scale(), lse=lse, workspace=ws[:size])
+    p.check(o, lse, heads=[0, 3])
+    assert (ws[size:] == 0x5A).all()
+    with pytest.raises(mnb.MnbError) as e:
+        mnb.mnb_paged_attention(p.q, o, p.cache, p.start, 70, 9000, p.scale(), lse=lse, workspace=ws[:least - 256])
+    assert e.value.status == mnb.MNB_ERR_NO_MEM
