@@ -37,14 +37,17 @@ struct Plan {
 // long as its key tiles plus about four tiles' worth of prologue and epilogue;
 // the cut with the least waves * (tiles + 4) is taken, and one with as many
 // tiles again must save a tenth to be worth its partial results.  max_pieces:
-// the partial results (units x ranges) that the workspace has room for.
-Plan make_plan(int64_t batch, int64_t T, int64_t q_heads, int64_t kv_heads, int64_t max_kv, int64_t max_pieces) {
+// the partial results (units x ranges) that the workspace has room for.  seen:
+// most keys that a unit sees where a window bounds them (they may begin inside
+// a tile), or 0.
+Plan make_plan(int64_t batch, int64_t T, int64_t q_heads, int64_t kv_heads, int64_t max_kv, int64_t max_pieces, int64_t seen) {
     Plan pl;
     const int64_t group = q_heads / kv_heads;
     pl.tokens = (int)(tca::kRows / group);
     pl.units = (T / (2 * pl.tokens) + (batch < T ? batch : T)) * kv_heads;
     pl.splits = 1;
-    const int64_t tiles = (max_kv + tca::kKeys - 1) / tca::kKeys;
+    int64_t tiles = (max_kv + tca::kKeys - 1) / tca::kKeys;
+    if (seen > 0) tiles = std::min(tiles, (seen + tca::kKeys - 1) / tca::kKeys + 1);
     double best = 0;
     for (int64_t s = 1; s <= 64 && s <= tiles; ++s) {
         if (s > 1 && pl.units * s > max_pieces) break;
@@ -159,14 +162,17 @@ bool tc_serves(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t D, int6
 constexpr int64_t kSharedPieces = 4 * 152;
 
 size_t tc_workspace_bytes(int64_t batch, int64_t T, int64_t q_heads, int64_t kv_heads, int64_t D, int64_t max_kv) {
-    const Plan pl = make_plan(batch, T, q_heads, kv_heads, max_kv, INT64_MAX);
+    const Plan pl = make_plan(batch, T, q_heads, kv_heads, max_kv, INT64_MAX, 0);
     const int64_t tiles = (max_kv + tca::kKeys - 1) / tca::kKeys, most = pl.units * std::min<int64_t>(64, tiles);
     const int64_t shared = tiles > 1 ? std::min(kSharedPieces, most) : 0;
     return (size_t)std::max(shared, pl.splits == 1 ? 0 : pl.units * pl.splits) * piece_bytes(D);
 }
 
 cudaError_t launch_tc(const AttnParams& p, cudaStream_t s) {
-    const Plan pl = make_plan(p.batch, p.T, p.q_heads, p.kv_heads, p.max_kv, (int64_t)(p.workspace_bytes / piece_bytes(p.D)));
+    // (a unit's first row sees window keys, its last one as many further on, or the sequence to its end)
+    const int64_t rows = p.causal ? std::min<int64_t>(2 * (tca::kRows / p.group), p.max_q) : p.max_q;
+    const int64_t seen = p.window > 0 ? p.window + rows - 1 : 0;
+    const Plan pl = make_plan(p.batch, p.T, p.q_heads, p.kv_heads, p.max_kv, (int64_t)(p.workspace_bytes / piece_bytes(p.D)), seen);
     if (pl.units * pl.splits * 32 > 0x7FFFFFFF) return cudaErrorNotSupported;
     if (p.D <= 64) return p.dtype == kF16 ? launch_as<kF16, 64, false>(p, pl, s) : launch_as<kBF16, 64, false>(p, pl, s);
     if (one_box(p).ok) {

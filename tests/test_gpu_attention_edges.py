@@ -174,3 +174,13 @@ def test_a_smaller_workspace_cuts_into_fewer_ranges(mnb, part):
     with pytest.raises(mnb.MnbError) as e:
         mnb.mnb_paged_attention(p.q, o, p.cache, p.start, 70, 9000, p.scale(), lse=lse, workspace=ws[:least - 256])
     assert e.value.status == mnb.MNB_ERR_NO_MEM
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_under_a_window_the_cut_does_not_follow_the_context(mnb, causal):
+    """A chunk under a window sees as many keys of a long context as of a short one: the same bits, whatever max_kv is."""
+    p = Problem(mnb, [500], [3000], 32, 8, 128, "bf16", 16, "hnd", seed=29)
+    got = [p.run(causal, 1024, max_kv=n) for n in (3000, 32000, 100000)]
+    p.check(*got[0], causal=causal, window=1024, heads=[31])
+    for o, lse in got[1:]:
+        assert torch.equal(o, got[0][0]) and torch.equal(lse, got[0][1])
