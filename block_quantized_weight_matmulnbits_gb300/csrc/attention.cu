@@ -1,4 +1,5 @@
 // mnb_paged_attention: argument checks and the choice of a kernel.
+#include <algorithm>
 #include <cmath>
 
 #include "attention.h"
@@ -94,7 +95,9 @@ mnb_status mnb_paged_attention(const mnb_attention_args* a, const mnb_kv_cache* 
     if (c->dtype == MNB_F32) {
         e = attn::launch_f32(p, s);
     } else {
-        if (attn::tc_serves(p.batch, p.q_heads, p.kv_heads, p.D, p.max_q, p.max_kv, p.dtype)) {
+        // the keys that a sequence's new tokens see
+        const int64_t keys = a->window > 0 ? std::min(a->max_kv, a->window + a->max_q) : a->max_kv;
+        if (attn::tc_serves(p.batch, p.q_heads, p.kv_heads, p.D, p.max_q, keys, p.dtype)) {
             family = "attn_tc";
             e = attn::launch_tc(p, s);
         }

@@ -49,8 +49,9 @@ __device__ inline bool bad_sequence(const AttnParams& p, int q0, int q1, int len
 cudaError_t launch_mma(const AttnParams& p, cudaStream_t s);
 size_t mma_workspace_bytes(int D);
 // Many rows, bf16 / f16, head_dim up to 128 (attn_tc.cuh); cudaErrorNotSupported
-// (nothing launched) where a stride or size has no tensor map.
-bool tc_serves(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t D, int64_t max_q, int64_t max_kv, int dtype);
+// (nothing launched) where a stride or size has no tensor map.  keys: those
+// that the new tokens of a sequence see, at most.
+bool tc_serves(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t D, int64_t max_q, int64_t keys, int dtype);
 cudaError_t launch_tc(const AttnParams& p, cudaStream_t s);
 size_t tc_workspace_bytes(int64_t batch, int64_t T, int64_t q_heads, int64_t kv_heads, int64_t D, int64_t max_kv);
 // f32, CUDA cores (attn_f32.cu).

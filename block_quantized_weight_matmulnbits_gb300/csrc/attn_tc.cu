@@ -148,12 +148,18 @@ cudaError_t launch_as(const AttnParams& p, const Plan& pl, cudaStream_t s) {
 
 }  // namespace
 
-// From 17 rows a key head on; from 33 on where the keys fit in L2, because there two row tiles of 16 that each read
-// the keys cost less than this kernel's longer start (16 sequences of 8 tokens, window 1024: 18.2 against 13.1 us).
-bool tc_serves(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t D, int64_t max_q, int64_t max_kv, int dtype) {
+// From 33 rows a key head on; from 17 on where the keys that the call sees are many.  There the few-row kernel reads and
+// walks them twice (two row tiles of 16), which costs less than this kernel's longer start while they are few.  By their
+// bytes, this kernel against the few-row one, us (16 sequences of 8 new tokens unless said):
+//   16 / 4 heads x 64:  17 MB 25 - 17, 33 MB 29 - 21, 66 MB 37 - 44, 131 MB 54 - 72, 524 MB 150 - 203;
+//                       32000 keys under a window of 1024 (17 MB) 25 - 17, of 4096 (67 MB) 37 - 46
+//   32 / 8 x 128:       33 MB 21 - 21, 66 MB 29 - 35, 131 MB 42 - 70; under a window of 1024 (68 MB) 29 - 44
+//   4 sequences of it:  33 MB 27 - 21, 66 MB 35 - 35, 131 MB 48 - 52;  one: 33 MB 29 - 27, 66 MB 37 - 34, 131 MB 50 - 49
+bool tc_serves(int64_t batch, int64_t q_heads, int64_t kv_heads, int64_t D, int64_t max_q, int64_t keys, int dtype) {
     const int64_t group = q_heads / kv_heads, rows = max_q * group;
     if (dtype == kF32 || D > 128 || group > tca::kRows || rows <= 16) return false;
-    return rows > 32 || (double)batch * (double)max_kv * (double)(kv_heads * D) * 4.0 > 100e6;
+    const double bytes = (double)batch * (double)keys * (double)(kv_heads * D) * 4.0;
+    return rows > 32 || bytes > 100e6 || (bytes > 50e6 && batch * kv_heads >= 32);
 }
 
 // A call with more units may want fewer pieces than one with less (a full wave is not cut), so the size reported is no

@@ -184,3 +184,20 @@ def test_under_a_window_the_cut_does_not_follow_the_context(mnb, causal):
     p.check(*got[0], causal=causal, window=1024, heads=[31])
     for o, lse in got[1:]:
         assert torch.equal(o, got[0][0]) and torch.equal(lse, got[0][1])
+
+
+def test_the_window_and_not_the_context_chooses_the_kernel(mnb, monkeypatch, capfd):
+    """Drafted tokens (17 to 32 rows a key head) under a window read the same keys of a long context as of a short one."""
+    families = []
+    for kv in (2000, 40000):
+        p = Problem(mnb, [8] * 16, [600] * 16, 16, 4, 64, "f16", 32, "nhd", seed=30)
+        monkeypatch.setenv("MNB_PROFILE", "1")
+        monkeypatch.setenv("MNB_PROFILE_EVERY", "1")
+        capfd.readouterr()
+        o, lse = p.run(window=500, max_kv=kv)
+        torch.cuda.synchronize()
+        p.run(window=500, max_kv=kv)
+        monkeypatch.delenv("MNB_PROFILE")
+        families.append({x for x in ("attn_mma", "attn_tc") if f"kernel={x} " in capfd.readouterr().err})
+        p.check(o, lse, window=500, heads=[0, 15], seqs=[0, 15])
+    assert families[0] and families[0] == families[1]
