@@ -86,7 +86,9 @@ mnb_status mnb_paged_attention(const mnb_attention_args* a, const mnb_kv_cache* 
     p.workspace = a->workspace;
     p.workspace_bytes = a->workspace_bytes;
     p.dtype = c->dtype;
-    wait_limits(&p.wait_limit, &p.wait_hint_ns);
+    uint32_t hint;
+    wait_limits(&p.wait_limit, &hint);
+    if (hint) p.wait_limit = kWaitTries;  // the waits of these kernels take no hint, whatever MNB_WAIT_MODE says
     if (inject_launch_failure()) return MNB_ERR_CUDA;
     ProfileScope prof("mnb_paged_attention", (cudaStream_t)a->stream);
     const cudaStream_t s = (cudaStream_t)a->stream;

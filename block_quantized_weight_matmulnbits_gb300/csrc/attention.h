@@ -26,7 +26,7 @@ struct AttnParams {
     int* status;
     void* workspace;
     size_t workspace_bytes;
-    uint32_t wait_limit, wait_hint_ns;
+    uint32_t wait_limit;  // tries without a hint
     int dtype;
 };
 

@@ -165,8 +165,8 @@ void wait_limits(uint32_t* limit, uint32_t* hint_ns) {
     // hint, 2 busy polling with test_wait; the limits keep every mode near two seconds.
     switch (env_int("MNB_WAIT_MODE", 1)) {
         case 0: *limit = kWaitLimit; *hint_ns = kWaitHintNs; break;
-        case 2: *limit = 1u << 26; *hint_ns = kWaitPoll; break;
-        default: *limit = 1u << 24; *hint_ns = 0; break;  // measured fastest on the tcgen05 GEMMs
+        case 2: *limit = kWaitPolls; *hint_ns = kWaitPoll; break;
+        default: *limit = kWaitTries; *hint_ns = 0; break;  // measured fastest on the tcgen05 GEMMs
     }
 }
 

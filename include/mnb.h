@@ -654,9 +654,9 @@ MNB_API mnb_status mnb_cache_compact(const mnb_cache_state* state, const mnb_pag
  *   MNB_TC_BT=32|64|128    token tile of the block-scaled prefill GEMM
  *   MNB_TC_SPLITK=1|2      K split over a 2-CTA cluster in the hi/lo GEMM
  *                          (1: never, 2: always)
- *   MNB_WAIT_MODE=0|1|2    bounded mbarrier waits: suspend with a time hint,
- *                          try_wait without a hint (the default), or
- *                          test_wait polling
+ *   MNB_WAIT_MODE=0|1|2    bounded mbarrier waits of the matmul kernels:
+ *                          suspend with a time hint, try_wait without a hint
+ *                          (the default), or test_wait polling
  *   MNB_WAIT_LIMIT=n       test hook: n tries per bounded wait (then
  *                          MNB_ERR_TIMEOUT in the status word)
  *   MNB_GEMV_STAGE_BUFS, MNB_GEMV_MAX_SLOTS  ring shape of the f32 GEMV

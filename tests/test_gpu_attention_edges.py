@@ -201,3 +201,21 @@ def test_the_window_and_not_the_context_chooses_the_kernel(mnb, monkeypatch, cap
         families.append({x for x in ("attn_mma", "attn_tc") if f"kernel={x} " in capfd.readouterr().err})
         p.check(o, lse, window=500, heads=[0, 15], seqs=[0, 15])
     assert families[0] and families[0] == families[1]
+
+
+@pytest.mark.parametrize("mode", ["0", "1", "2"])
+def test_roles_wait_while_a_large_batch_is_searched(mnb, monkeypatch, mode):
+    """Four million sequences of which the last one alone has new tokens: the warps that wait for their unit do so for as
+    long as the search takes, whatever the matmul kernels' way of waiting is."""
+    batch, n, kv, page = 1 << 22, 60, 1000, 1024
+    p = Problem(mnb, [n], [kv], 4, 1, 64, "bf16", page, "hnd", seed=38)
+    start = torch.zeros(batch + 1, dtype=torch.int32, device="cuda")
+    lens, tables = torch.zeros(batch, dtype=torch.int32, device="cuda"), torch.zeros((batch, 1), dtype=torch.int32, device="cuda")
+    start[-1], lens[-1], tables[-1, 0] = n, kv, p.tables[0, 0]
+    cache = mnb.kv_cache(p.k, p.v, tables, lens, "hnd", R.CODE["bf16"])
+    o, lse = torch.empty_like(p.q), torch.empty(p.q.shape[:2], device="cuda")
+    ws = torch.empty(mnb.mnb_attention_workspace_size(batch, n, 4, 1, 64, n, kv, R.CODE["bf16"]), dtype=torch.uint8, device="cuda")
+    monkeypatch.setenv("MNB_WAIT_MODE", mode)
+    mnb.mnb_paged_attention(p.q, o, cache, start, n, kv, p.scale(), lse=lse, workspace=ws)
+    torch.cuda.synchronize()
+    p.check(o, lse)
