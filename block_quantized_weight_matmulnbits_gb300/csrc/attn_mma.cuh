@@ -188,7 +188,8 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, CL>::kCtasPerSm) attn_mma_
             for (int i = 0; i < 16 / kRpi; ++i) {
                 const int r = i * kRpi + lrow;
                 const bool b = r >= 8;
-                const bool ok = (b ? pb : pa) >= 0 && key0 + r < hi && col_ok;
+                // (zeros for keys that no row of the tile sees: 0 * NaN is NaN)
+                const bool ok = (b ? pb : pa) >= 0 && key0 + r >= lo && key0 + r < hi && col_ok;
                 const int64_t off = ok ? (b ? offb : offa) + (r & 7) * p.token_stride : 0;
                 const uint32_t to = dst + chunk_at<DP>(r, lchunk);
                 cp16(to, kp + off, ok);

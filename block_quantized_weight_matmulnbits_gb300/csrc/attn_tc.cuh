@@ -30,9 +30,9 @@
 //                what is next, so a unit's first loads and products overlap the
 //                epilogue of the one before and nothing is set up twice
 //   warp 10      watches the ring, so that the MMA thread polls one barrier a
-//                step for it, and zeroes V rows past the visible keys, whose
-//                pages may hold anything (0 * NaN is NaN); warp 11 completes the
-//                warpgroup
+//                step for it, and zeroes V rows before and past the visible keys,
+//                whose pages may hold anything (0 * NaN is NaN); warp 11
+//                completes the warpgroup
 // Measured on a GB300: two prompts of 4096 tokens, 32 query and 8 key heads x
 // 128, bf16, pages of 64: 196 us in bursts, 205 sustained (1340 TFLOP/s, the
 // tensor pipe 61 % active); 500 tokens over 32000 keys: 199 us with pages of 16,
@@ -327,10 +327,10 @@ struct Shared {
     }
 };
 
-// Rows [z0, z1) of key tile j hold visible keys or lie in a box that was loaded for one.
-__device__ __forceinline__ bool zero_range(const Range& rg, int j, int box_log, int* z0, int* z1) {
+// Rows [z0, z1) of key tile j hold visible keys.
+__device__ __forceinline__ bool zero_range(const Range& rg, int j, int* z0, int* z1) {
     const int kb = (rg.first + j) * kKeys;
-    *z0 = rg.lo > kb ? ((rg.lo - kb) >> box_log) << box_log : 0;
+    *z0 = rg.lo > kb ? rg.lo - kb : 0;
     *z1 = rg.hi - kb < kKeys ? rg.hi - kb : kKeys;
     return *z0 > 0 || *z1 < kKeys;
 }
@@ -611,8 +611,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
                 tc::drain_wait(sh.done, 0);
             }
         } else if (warp == kRingWarp) {
-            // Watches the ring for the MMA thread (V of a step, K of the next), and clears the V rows past the visible
-            // keys: their pages may hold anything, and 0 * NaN is NaN.
+            // Watches the ring for the MMA thread (V of a step, K of the next), and clears the V rows before and past the
+            // visible keys: their pages may hold anything, and 0 * NaN is NaN.
             int e = 0;           // ring entries so far
             uint32_t told = 0;   // steps so far
             bool ok = true;
@@ -630,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
                     ok = full(iv);
                     if (!ok) break;
                     int z0, z1;
-                    if (zero_range(rg, j, box_log, &z0, &z1)) {
+                    if (zero_range(rg, j, &z0, &z1)) {
                         uint8_t* v = ring + (iv % R) * S::kTile;
                         for (int c = lane; c < kKeys * 8; c += 32) {
                             const int r = c >> 3;

@@ -410,7 +410,8 @@ MNB_API mnb_status mnb_matmul_fp_ex(const void* x, const void* packed, const voi
  *   page_size         a power of two, 8 .. 1024
  * Entries of tables at or past ceil(kv_len / page_size) are not read (under a
  * window of mnb_paged_attention, those of pages that no row sees neither), and
- * cached rows past kv_len never reach a result, whatever they hold. */
+ * cached rows past kv_len, or before every row's window, never reach a result,
+ * whatever they hold. */
 typedef struct mnb_kv_cache {
     void* k_pages;
     void* v_pages;

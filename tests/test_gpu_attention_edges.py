@@ -219,3 +219,17 @@ def test_roles_wait_while_a_large_batch_is_searched(mnb, monkeypatch, mode):
     mnb.mnb_paged_attention(p.q, o, cache, start, n, kv, p.scale(), lse=lse, workspace=ws)
     torch.cuda.synchronize()
     p.check(o, lse)
+
+
+@pytest.mark.parametrize("what", ["k", "v"])
+@pytest.mark.parametrize("dtype,page,q,kv,window", [
+    ("bf16", 16, 1, 500, 97), ("f16", 64, 1, 5000, 1003), ("bf16", 128, 60, 900, 333), ("f16", 16, 60, 9000, 1003), ("f32", 32, 1, 500, 100),
+    ("bf16", 8, 3, 77, 5)])
+def test_a_nan_before_the_window_reaches_no_row(mnb, what, dtype, page, q, kv, window):
+    """Tokens that no row of the call sees any more, up to the last of them: inside a page and a tile that rows do read."""
+    p = Problem(mnb, [q], [kv], 4, 2, 128, dtype, page, "hnd", seed=31)
+    gone = kv - q - window + 1
+    _set_keys(p, 0, range(max(0, gone - 300), gone), float("nan"), what)
+    o, lse = p.run(window=window)
+    _set_keys(p, 0, range(max(0, gone - 300), gone), 0.0, what)  # (the plain form multiplies them by nought)
+    p.check(o, lse, window=window)
