@@ -106,9 +106,9 @@ __global__ void __launch_bounds__(kWarps * 32) attn_f32_kernel(const AttnParams 
     for (int d = threadIdx.x; d < p.D; d += kWarps * 32) {
         float a = 0.f;
         for (int w = 0; w < kWarps; ++w) a = fmaf(os[w][d], expf(ms[w] - base), a);
-        static_cast<float*>(p.o)[t * p.o_ts + h * p.o_hs + d] = hi > lo ? a / total : 0.f;
+        static_cast<float*>(p.o)[t * p.o_ts + h * p.o_hs + d] = total == 0.f ? 0.f : a / total;  // (no key, or none above -inf)
     }
-    if (threadIdx.x == 0 && p.lse) p.lse[t * p.q_heads + h] = hi > lo ? top + logf(total) : -INFINITY;
+    if (threadIdx.x == 0 && p.lse) p.lse[t * p.q_heads + h] = total == 0.f ? -INFINITY : base + logf(total);
 }
 
 }  // namespace

@@ -510,7 +510,8 @@ MNB_API mnb_status mnb_rotary_append(const mnb_rotary_args* args, const mnb_kv_c
  * h / (q_heads / kv_heads):
  *     O[t, h, :] = sum_j p_j V[j, :] / sum_j p_j,   p_j = exp(scale * Q[t, h, :] . K[j, :])
  *     lse[t, h]  = ln sum_j p_j
- * A row that sees no key (kv_len 0, or pos < 0) is O = 0, lse = -inf.  Scores,
+ * A row that sees no key (kv_len 0, or, causal, pos < 0), or none with a score
+ * above -inf, is O = 0, lse = -inf.  Scores,
  * maxima, sums and O are held in f32; the bf16 / f16 kernels round p_j to that
  * type for the product with V, as its operand.
  *   q, o       device [T, q_heads, head_dim] of the cache's dtype, 16-byte

@@ -1,6 +1,8 @@
 """Attention over the paged cache at its edges: NaN and infinities in queries and keys, rows that see nothing beside
 rows that do, windows wider than any sequence, batches wider than one look at them, workspaces of other calls."""
 
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -233,3 +235,32 @@ def test_a_nan_before_the_window_reaches_no_row(mnb, what, dtype, page, q, kv, w
     o, lse = p.run(window=window)
     _set_keys(p, 0, range(max(0, gone - 300), gone), 0.0, what)  # (the plain form multiplies them by nought)
     p.check(o, lse, window=window)
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_scores_of_minus_infinity_alone_are_no_keys(mnb, form):
+    """Every visible score -inf: nothing to weigh, o = 0 and lse = -inf, in every kernel; beside a finite score such keys
+    weigh nothing."""
+    p = _form(mnb, form, 32)
+    p.q[:, :, 0] = 1.0
+    n = p.kv_lens[0]
+    _set_keys(p, 0, range(n), 0.0)
+    keys = range(n) if p.q_lens[0] == 1 else range(n - p.q_lens[0] + 3)
+    for j in keys:
+        page, row = int(p.np_tables[0, j // p.page]), j % p.page
+        p.k[page, :, row, 0] = float("-inf")
+    o, lse = p.run()
+    go, gl = R.f64(o), R.f64(lse)
+    values = {hk: p.rows(p.v, 0, hk) for hk in range(p.hkv)}
+    for t, b, pos in _rows(p):
+        if b:
+            continue
+        left = np.arange(len(keys), pos + 1)  # these weigh alike: their scores are q . (0, ..) = 0
+        for h in range(p.hq):
+            if not len(left):
+                assert (go[t, h] == 0).all() and np.isneginf(gl[t, h]), (t, h)
+            else:
+                v = values[h // (p.hq // p.hkv)][left]
+                assert (np.abs(go[t, h] - v.mean(0)) <= 1.02 * R.ROUND[p.dtype] * np.abs(v).mean(0) + 2 * R.ROUND[p.dtype] * np.abs(v.mean(0))
+                        + 2.0 ** -18).all()
+                assert abs(gl[t, h] - math.log(len(left))) <= 2.0 ** -18
