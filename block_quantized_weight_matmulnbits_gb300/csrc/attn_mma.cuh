@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, CL>::kCtasPerSm) attn_mma_
                 const int h = e_hk * p.group + g % p.group;
                 const int slot = first ? 0 : 1;
                 const int64_t at = ((int64_t)blockIdx.x * 2 + slot) * kRows + r;
-                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                const float inv = 1.f / sum;
                 for (int c = q8; c < DP / 8; c += 8) {
                     float a[8] = {};
 #pragma unroll
@@ -422,11 +422,13 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, CL>::kCtasPerSm) attn_mma_
                         dst[1] = make_float4(a[4], a[5], a[6], a[7]);
                     } else if (done) {
                         if (c * 8 < p.D) {
-                            uint4 out;
-                            out.x = pack16<DT>(a[0] * inv, a[1] * inv);
-                            out.y = pack16<DT>(a[2] * inv, a[3] * inv);
-                            out.z = pack16<DT>(a[4] * inv, a[5] * inv);
-                            out.w = pack16<DT>(a[6] * inv, a[7] * inv);
+                            uint4 out = make_uint4(0, 0, 0, 0);  // without a key: its a may be 0 * NaN
+                            if (sum != 0.f) {
+                                out.x = pack16<DT>(a[0] * inv, a[1] * inv);
+                                out.y = pack16<DT>(a[2] * inv, a[3] * inv);
+                                out.z = pack16<DT>(a[4] * inv, a[5] * inv);
+                                out.w = pack16<DT>(a[6] * inv, a[7] * inv);
+                            }
                             *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + tk * p.o_ts + h * p.o_hs + c * 8) = out;
                         }
                     } else {
@@ -464,12 +466,12 @@ __global__ void __launch_bounds__(kThreads, Shape<DP, CL>::kCtasPerSm) attn_mma_
                 const int g = e_rt * kRows + r;
                 const int64_t tk = e_tok0 + g / p.group;
                 const int h = e_hk * p.group + g % p.group;
-                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                const float inv = 1.f / sum;
                 uint16_t* dst = static_cast<uint16_t*>(p.o) + tk * p.o_ts + h * p.o_hs;
 #pragma unroll
                 for (int d = 0; d < DP / 64; ++d)
                     if (d * 64 + lane * 2 < p.D)
-                        *reinterpret_cast<uint32_t*>(dst + d * 64 + lane * 2) = pack16<DT>(a[2 * d] * inv, a[2 * d + 1] * inv);
+                        *reinterpret_cast<uint32_t*>(dst + d * 64 + lane * 2) = sum == 0.f ? 0u : pack16<DT>(a[2 * d] * inv, a[2 * d + 1] * inv);
                 if (lane == 0 && p.lse) p.lse[tk * p.q_heads + h] = sum == 0.f ? -INFINITY : (base + log2f(sum)) * kLn2;
             }
             cluster_sync();  // nobody leaves while its shared memory is read

@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnParams p, cons
     const int64_t t = (int64_t)cut.x + r / p.group;
     const int h = (cut.z & 0xFFFF) * p.group + r % p.group;
     l = (l_s[0] + l_s[1]) + (l_s[2] + l_s[3]);
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const float inv = 1.f / l;
     for (int d = threadIdx.x; d * 2 < p.D; d += W * 32) {
         float2 a = acc_s[0][d];
 #pragma unroll
@@ -251,8 +251,8 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnParams p, cons
             a.y += acc_s[w][d].y;
         }
         const int64_t o = t * p.o_ts + h * p.o_hs + d * 2;
-        store_f32(p.o, o, a.x * inv, DT);
-        store_f32(p.o, o + 1, a.y * inv, DT);
+        store_f32(p.o, o, l == 0.f ? 0.f : a.x * inv, DT);  // (without a key a may be 0 * NaN)
+        store_f32(p.o, o + 1, l == 0.f ? 0.f : a.y * inv, DT);
     }
     if (threadIdx.x == 0 && p.lse) p.lse[t * p.q_heads + h] = l == 0.f ? -INFINITY : (base + log2f(l)) * kLn2;
 }

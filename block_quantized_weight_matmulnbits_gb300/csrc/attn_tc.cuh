@@ -763,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
             const int64_t tk = (int64_t)job->tok + i;
             const int h = job->hk * p.group + r_head;
             const int64_t part = (int64_t)job->part * 256 + x * 128 + r;
-            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const float inv = 1.f / l;
             // O leaves through shared memory, 128 bytes of the warp's 32 rows at a time, so that eight lanes store a row's
             // whole lines.  (A thread storing its own row touches 32 lines an instruction: 7000 cycles a unit for bf16,
             // 14000 for the f32 partial results, with the tensor pipe idle.)
@@ -797,6 +797,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const AttnParams p
                     }
 #pragma unroll
                     for (int e = 0; e < 16; ++e) v[16 + e] = pack16<DT>(__uint_as_float(w[2 * e]) * inv, __uint_as_float(w[2 * e + 1]) * inv);
+                }
+                if (l == 0.f) {  // without a key O may be 0 * NaN
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = 0u;
                 }
                 if (c + depths >= DP && nx > 0) {  // O may be written by the next unit
                     tc::fence_before();

@@ -536,8 +536,8 @@ MNB_API mnb_status mnb_rotary_append(const mnb_rotary_args* args, const mnb_kv_c
  *              call of a head_dim needs (5.1 MB for 65 to 128).
  * A page number outside [0, num_pages) sets the status word; its keys count as
  * zeros.  NaN or infinities in visible values of the cache reach every row of
- * their sequence that the same tile of keys covers.  A row with a NaN or +inf
- * score is NaN, in o and in lse. */
+ * their sequence that sees a key and that the same tile of keys covers.  A row
+ * with a NaN or +inf score is NaN, in o and in lse. */
 typedef struct mnb_attention_args {
     const void* q;
     void* o;

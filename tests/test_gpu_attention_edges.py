@@ -264,3 +264,15 @@ def test_scores_of_minus_infinity_alone_are_no_keys(mnb, form):
                 assert (np.abs(go[t, h] - v.mean(0)) <= 1.02 * R.ROUND[p.dtype] * np.abs(v).mean(0) + 2 * R.ROUND[p.dtype] * np.abs(v.mean(0))
                         + 2.0 ** -18).all()
                 assert abs(gl[t, h] - math.log(len(left))) <= 2.0 ** -18
+
+
+@pytest.mark.parametrize("dtype,q_lens,kv_lens,hq,hkv", [
+    ("bf16", [5], [3], 4, 2), ("f16", [7, 1], [3, 9000], 2, 1), ("bf16", [300], [200], 4, 2), ("bf16", [300], [100], 4, 2), ("f16", [60, 1], [40, 3000], 4, 2), ("f32", [5], [3], 4, 2)])
+def test_a_row_without_a_key_is_zero_beside_rows_that_are_nan(mnb, dtype, q_lens, kv_lens, hq, hkv):
+    p = Problem(mnb, q_lens, kv_lens, hq, hkv, 128, dtype, 16, "hnd", seed=33)
+    _set_keys(p, 0, [0], float("nan"), "v")
+    o, lse = p.run()
+    none = q_lens[0] - kv_lens[0]
+    assert (o[:none] == 0).all() and torch.isneginf(lse[:none]).all()
+    assert torch.isnan(o[none:q_lens[0]]).all() and torch.isfinite(lse[none:q_lens[0]]).all()
+    assert not torch.isnan(o[q_lens[0]:]).any()
