@@ -59,6 +59,7 @@ class MatmulArgs(ctypes.Structure):
 
 class KvCache(ctypes.Structure):
     """mnb_kv_cache; made by kv_cache()."""
+    max_len = (1 << 30) - 1  # tokens that a row of the tables has columns for
     _fields_ = [
         ("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("tables", ctypes.c_void_p),
         ("kv_lens", ctypes.c_void_p), ("batch", ctypes.c_int64), ("table_stride", ctypes.c_int64),
@@ -375,7 +376,9 @@ def _rows_fail(what):
 def kv_cache(k_pages, v_pages, tables, kv_lens, order, dtype) -> KvCache:
     """The cache descriptor of one layer.  Pages are [num_pages, heads, tokens, dim] (order "hnd") or
     [num_pages, tokens, heads, dim] ("nhd") tensors of one shape and one set of strides.  The descriptor holds the
-    tensors' addresses (and the tensors): make it once per layer and keep it beside them."""
+    tensors' addresses (and the tensors): make it once per layer and keep it beside them.  tables may be some columns of
+    a wider array: a kv_len that needs more of them sets the status word (with positions of its own, the append takes
+    the array's next column instead)."""
     if not _codes:
         _setup()
     if order not in ("hnd", "nhd"):
@@ -398,6 +401,7 @@ def kv_cache(k_pages, v_pages, tables, kv_lens, order, dtype) -> KvCache:
     c.num_pages, c.page_stride = k_pages.shape[0], k_pages.stride(0)
     c.token_stride, c.head_stride = k_pages.stride(tok), k_pages.stride(head)
     c.page_size, c.kv_heads, c.head_dim, c.dtype = k_pages.shape[tok], k_pages.shape[head], k_pages.shape[3], dtype
+    c.max_len = min(c.max_len, tables.shape[1] * c.page_size)
     c.tensors = (k_pages, v_pages, tables, kv_lens)
     return c
 
@@ -475,6 +479,8 @@ def mnb_rotary_append(q, q_out, k, v, cos_table, sin_table, cache, q_start, posi
         pos_ptr = _i32("positions", positions)
         if positions.numel() != shape[0]:
             _fail("positions: one for each token is wanted")
+    elif n_pos > cache.max_len:
+        n_pos = cache.max_len  # a token's position is its place, and the table's columns end there
     qp = op = None
     heads, qs, os_ = 0, (0, 0), (0, 0)
     if q is not None:
@@ -512,6 +518,8 @@ def mnb_paged_attention(q, o, cache, q_start, max_q, max_kv, scale, lse=None, ca
         lse_ptr = lse.data_ptr()
     if workspace is not None:
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if max_kv > cache.max_len:
+        max_kv = cache.max_len  # (a longer sequence has pages past its row of the tables)
     a = AttentionArgs(q.data_ptr(), o.data_ptr(), lse_ptr, start_ptr, shape[0], shape[1], max_q, max_kv, window, qs[0], qs[1], os_[0], os_[1],
                       scale, 1 if causal else 0, ws_ptr, ws_bytes, _current(stream))
     st = (_lib or load()).mnb_paged_attention(a, cache)

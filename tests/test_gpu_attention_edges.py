@@ -276,3 +276,29 @@ def test_a_row_without_a_key_is_zero_beside_rows_that_are_nan(mnb, dtype, q_lens
     assert (o[:none] == 0).all() and torch.isneginf(lse[:none]).all()
     assert torch.isnan(o[none:q_lens[0]]).all() and torch.isfinite(lse[none:q_lens[0]]).all()
     assert not torch.isnan(o[q_lens[0]:]).any()
+
+
+@pytest.mark.parametrize("q,dtype", [(1, "bf16"), (60, "f16"), (1, "f32")])
+def test_a_row_of_a_strided_table_ends_with_its_columns(mnb, q, dtype):
+    """Tables that are some columns of a wider array: a length past them sets the status, and what stands behind them is
+    not taken for pages."""
+    p = Problem(mnb, [q, q], [200, 90], 4, 2, 128, dtype, 16, "hnd", seed=34)
+    wide = torch.full((2, 40), 1, dtype=torch.int32, device="cuda")
+    cols = wide[:, 3:3 + 13]
+    cols.copy_(p.tables[:, :13])
+    p.cache = mnb.kv_cache(p.k, p.v, cols, p.lens, "hnd", R.CODE[dtype])
+    p.check(*p.run())
+    cols = wide[:, 3:3 + 12]  # a page short for the first sequence, and enough for the second
+    p.cache = mnb.kv_cache(p.k, p.v, cols, p.lens, "hnd", R.CODE[dtype])
+    o, lse = p.run()
+    assert mnb.mnb_get_device_error() == mnb.MNB_ERR_INVALID_ARG
+    p.check(o, lse, seqs=[1])
+    before = p.k.clone(), p.v.clone()
+    x = torch.ones((2, 2, 128), dtype=p.k.dtype, device="cuda")
+    start = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+    one = torch.ones((300, 64), device="cuda")
+    mnb.mnb_rotary_append(None, None, x, x, one, torch.zeros_like(one), p.cache, start)
+    assert mnb.mnb_get_device_error() == mnb.MNB_ERR_INVALID_ARG
+    page, row = int(p.np_tables[1, 89 // 16]), 89 % 16
+    before[0][page, :, row], before[1][page, :, row] = 1, 1
+    assert torch.equal(torch.nan_to_num(before[0]), torch.nan_to_num(p.k)) and torch.equal(torch.nan_to_num(before[1]), torch.nan_to_num(p.v))
