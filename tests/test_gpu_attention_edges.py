@@ -302,3 +302,46 @@ def test_a_row_of_a_strided_table_ends_with_its_columns(mnb, q, dtype):
     page, row = int(p.np_tables[1, 89 // 16]), 89 % 16
     before[0][page, :, row], before[1][page, :, row] = 1, 1
     assert torch.equal(torch.nan_to_num(before[0]), torch.nan_to_num(p.k)) and torch.equal(torch.nan_to_num(before[1]), torch.nan_to_num(p.v))
+
+
+@pytest.mark.parametrize("dtype,page,order", [("bf16", 64, "nhd"), ("f16", 16, "hnd"), ("f32", 32, "nhd")])
+@pytest.mark.parametrize("q_lens,kv_lens,hq,hkv,D", [
+    ([1, 1], [500, 64], 8, 2, 128), ([1], [6000], 4, 1, 64), ([150, 20, 0, 7], [400, 20, 9, 3], 2, 1, 64), ([4, 1], [300, 2], 8, 1, 128),
+    ([90], [1500], 4, 2, 96), ([3, 40], [90, 700], 2, 2, 256)])
+@pytest.mark.parametrize("window", [0, 65])
+def test_not_causal(mnb, dtype, page, order, q_lens, kv_lens, hq, hkv, D, window):
+    """Encoders and cross attention: every row sees every key (from its window on)."""
+    p = Problem(mnb, q_lens, kv_lens, hq, hkv, D, dtype, page, order, seed=35)
+    p.check(*p.run(False, window), causal=False, window=window)
+
+
+@pytest.mark.parametrize("dtype,page,order", [("f16", 32, "nhd"), ("f32", 8, "nhd"), ("bf16", 128, "nhd")])
+@pytest.mark.parametrize("window", [1, 64, 200])
+@pytest.mark.parametrize("q_lens,kv_lens,hq,hkv,D", [([1, 1], [500, 64], 8, 2, 128), ([150, 20], [400, 20], 2, 1, 64), ([4, 1], [2, 300], 8, 1, 80)])
+def test_windows_of_other_types_and_orders(mnb, dtype, page, order, window, q_lens, kv_lens, hq, hkv, D):
+    p = Problem(mnb, q_lens, kv_lens, hq, hkv, D, dtype, page, order, seed=window)
+    p.check(*p.run(window=window), window=window)
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_nan_in_a_key_reaches_the_rows_that_see_it(mnb, form):
+    """And no other row: the scores of keys that a row does not see are not looked at."""
+    p = _form(mnb, form, 36)
+    b = len(p.q_lens) - 1
+    j = p.kv_lens[b] - max(1, p.q_lens[b] // 2)
+    _set_keys(p, b, [j], float("nan"))
+    heads = [0, p.hq - 1]
+    bad = {(t, h) for t, s, pos in _rows(p) for h in heads if s == b and pos >= j}
+    o, lse = p.run()
+    if p.T > 60:  # many rows: who is NaN, and no row in part
+        assert all(torch.isnan(o[t, h]).all() and torch.isnan(lse[t, h]) for t, h in bad)
+        assert torch.isnan(o[:, heads]).all(-1).sum() == len(bad) and torch.equal(torch.isnan(o).any(-1), torch.isnan(o).all(-1))
+        return
+    _check(p, o, lse, bad, heads=heads)
+
+
+@pytest.mark.parametrize("form", [("bf16", [1] * 200, [1 + (11 * i) % 250 for i in range(200)], 2, 1, 64),
+                                  ("f16", [1] * 150, [1 + (13 * i) % 400 for i in range(150)], 4, 1, 128)])
+def test_clusters_of_more_than_128_sequences(mnb, form):
+    p = _form(mnb, form, 37)
+    p.check(*p.run(), seqs=set(range(0, len(p.q_lens), 9)) | {127, 128, 129, len(p.q_lens) - 1})
