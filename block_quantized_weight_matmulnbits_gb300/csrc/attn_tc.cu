@@ -34,9 +34,17 @@ struct Plan {
 };
 
 // Units and splits from the bounds of a call.  A wave of 152 CTAs takes as
-// long as its key tiles plus about four tiles' worth of prologue and epilogue;
-// the cut with the least waves * (tiles + 4) is taken, and one with as many
-// tiles again must save a tenth to be worth its partial results.  max_pieces:
+// long as its key tiles plus about four tiles' worth of prologue and epilogue
+// (2 to 8 choose the same cut in most cases); the cut with the least waves *
+// (tiles + 4) is taken.  A cut pays its partial results, a tile a wave, and the
+// join, about four tiles, and it must save 5 % beyond them, because unequal
+// units (a causal chunk's) pack better than whole waves.  32 / 8 heads x 128,
+// cut against uncut, us:
+//   not cut for it: 300 tokens 19 - 12, 500 over 1000 keys 27 - 20, 1500 over
+//     3000 85 - 63, 4096 over 8192 345 - 281, 32 sequences of 64 over 8000 281 - 227
+//   still cut: 40 over 1000 15.5 - 18.6, 300 over 2000 26 - 31, 500 over 4000
+//     43 - 52, 2048 over 32000 700 - 733, 500 over 32000 194 - 367
+// max_pieces:
 // the partial results (units x ranges) that the workspace has room for.  seen:
 // most keys that a unit sees where a window bounds them (they may begin inside
 // a tile), or 0.
@@ -53,7 +61,7 @@ Plan make_plan(int64_t batch, int64_t T, int64_t q_heads, int64_t kv_heads, int6
         if (s > 1 && pl.units * s > max_pieces) break;
         const int64_t waves = (pl.units * s + 151) / 152;
         double cost = (double)waves * (double)((tiles + s - 1) / s + 4);
-        if (s > 1) cost = cost * 1.02 + (double)(pl.units * s) / 152.0;
+        if (s > 1) cost = cost * 1.05 + (double)(pl.units * s) / 152.0 + 4;
         if (s == 1 || cost < best) {
             best = cost;
             pl.splits = (int)s;
