@@ -88,7 +88,8 @@ mnb_status mnb_paged_attention(const mnb_attention_args* a, const mnb_kv_cache* 
     p.dtype = c->dtype;
     uint32_t hint;
     wait_limits(&p.wait_limit, &hint);
-    if (hint) p.wait_limit = kWaitTries;  // the waits of these kernels take no hint, whatever MNB_WAIT_MODE says
+    // these kernels' waits take no hint, whatever MNB_WAIT_MODE says, and begin behind the preceding kernel
+    if (hint || p.wait_limit > kWaitTries) p.wait_limit = kWaitTries;
     if (inject_launch_failure()) return MNB_ERR_CUDA;
     ProfileScope prof("mnb_paged_attention", (cudaStream_t)a->stream);
     const cudaStream_t s = (cudaStream_t)a->stream;

@@ -162,11 +162,12 @@ void wait_limits(uint32_t* limit, uint32_t* hint_ns) {
         return;
     }
     // MNB_WAIT_MODE (tuning): 0 suspend with a time hint, 1 try_wait without a
-    // hint, 2 busy polling with test_wait; the limits keep every mode near two seconds.
+    // hint, 2 busy polling with test_wait.  Two seconds in modes 0 and 2, a minute in mode 1 (3.8 us a try): warps that wait
+    // for the producer of a programmatic dependent wait for as long as the preceding kernel runs.
     switch (env_int("MNB_WAIT_MODE", 1)) {
         case 0: *limit = kWaitLimit; *hint_ns = kWaitHintNs; break;
         case 2: *limit = kWaitPolls; *hint_ns = kWaitPoll; break;
-        default: *limit = kWaitTries; *hint_ns = 0; break;  // measured fastest on the tcgen05 GEMMs
+        default: *limit = 1u << 24; *hint_ns = 0; break;  // measured fastest on the tcgen05 GEMMs
     }
 }
 
