@@ -6,6 +6,12 @@
 // row against the query in shared memory), the warp takes the block's maximum
 // and sum with shuffles, then the lanes turn to the depths and add p_j V[j].
 // The 8 partial (m, l, O) are joined at the end in a fixed order.
+//
+// The plain kernel for a type that decoders rarely cache in.  Nothing is shared
+// between rows or the heads of a group, so it is bound by its loads from L2 (a
+// lane reads a key row by itself).  Measured on a GB300, 32 / 8 heads x 128: 8
+// single tokens over 2000 keys 305 us (19 us of DRAM time), a prompt of 256
+// tokens 293 us, one of 2048 11.7 ms (3 TFLOP/s).
 #include <cmath>
 
 #include "attention.h"

@@ -431,7 +431,11 @@ typedef struct mnb_kv_cache {
  *   BY_PARTS  g f_i + (1 - g) f_i / s with g = clamp((L f_i / 2 pi - low) / (high - low), 0, 1):
  *             depths that turn more than `high` times over L keep their
  *             frequency, those below `low` turns are interpolated (the
- *             by-parts interpolation of the YaRN paper; low 1, high 32 there) */
+ *             by-parts interpolation of the YaRN paper; low 1, high 32 there).
+ *             g is linear in the number of turns, as in the paper.  Models
+ *             whose frequencies ramp linearly in the depth index i between two
+ *             correction depths are not of this form: give mnb_rotary tables
+ *             of their own. */
 typedef enum mnb_rope_scaling {
     MNB_ROPE_NONE = 0,
     MNB_ROPE_LINEAR = 1,
