@@ -44,10 +44,9 @@ struct Plan {
 //     3000 85 - 63, 4096 over 8192 345 - 281, 32 sequences of 64 over 8000 281 - 227
 //   still cut: 40 over 1000 15.5 - 18.6, 300 over 2000 26 - 31, 500 over 4000
 //     43 - 52, 2048 over 32000 700 - 733, 500 over 32000 194 - 367
-// max_pieces:
-// the partial results (units x ranges) that the workspace has room for.  seen:
-// most keys that a unit sees where a window bounds them (they may begin inside
-// a tile), or 0.
+// max_pieces: the partial results (units x ranges) that the workspace has room
+// for.  seen: most keys that a unit sees where a window bounds them (they may
+// begin inside a tile), or 0.
 Plan make_plan(int64_t batch, int64_t T, int64_t q_heads, int64_t kv_heads, int64_t max_kv, int64_t max_pieces, int64_t seen) {
     Plan pl;
     const int64_t group = q_heads / kv_heads;
