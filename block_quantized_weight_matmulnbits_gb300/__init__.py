@@ -20,6 +20,7 @@ MNB_F32, MNB_F16, MNB_BF16 = 0, 1, 2
 MNB_FLAG_PDL = 1
 MNB_FLAG_KPERM = 2
 MNB_ROTARY_INTERLEAVED, MNB_ROTARY_INVERSE = 1, 2
+MNB_NORM_UNIT_OFFSET = 1
 MNB_ROPE_NONE, MNB_ROPE_LINEAR, MNB_ROPE_NTK, MNB_ROPE_BY_PARTS = range(4)
 MNB_WF_E4M3, MNB_WF_E5M2, MNB_WF_NVFP4 = 1, 2, 3
 KERNELS = {"auto": 0, "gemv": 1, "gemv_mma": 2, "gemm_tc": 3, "generic": 4, "gemv_i8": 5}
@@ -34,6 +35,7 @@ EXPORTS = [
     "mnb_matmul_fp_ex", "mnb_packed_size_gidx", "mnb_pack_weights_gidx", "mnb_workspace_size_ex",
     "mnb_rotary_table", "mnb_rotary", "mnb_rotary_append", "mnb_paged_attention", "mnb_attention_workspace_size",
     "mnb_pages_copy", "mnb_cache_fork", "mnb_cache_resize", "mnb_cache_compact", "mnb_cache_workspace_size",
+    "mnb_rms_norm",
 ]
 MNB_A8_STATIC_SCRATCH_BYTES = 1 << 20
 MNB_HOST_IO_X_BYTES = 8 << 20
@@ -110,6 +112,17 @@ class CacheState(ctypes.Structure):
     ]
 
 
+class RmsNormArgs(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("residual_out", ctypes.c_void_p),
+        ("weight", ctypes.c_void_p), ("y", ctypes.c_void_p), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+        ("T", ctypes.c_int64), ("width", ctypes.c_int64), ("block_size", ctypes.c_int64), ("x_stride", ctypes.c_int64),
+        ("residual_stride", ctypes.c_int64), ("residual_out_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64),
+        ("dtype", ctypes.c_int), ("weight_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int), ("eps", ctypes.c_float),
+        ("flags", ctypes.c_int), ("stream", ctypes.c_void_p),
+    ]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -158,6 +171,7 @@ def load(build: bool = True):
             "mnb_cache_fork": (ci, [ctypes.POINTER(CacheState), vp, vp, i64, vp, sz, vp]),
             "mnb_cache_resize": (ci, [ctypes.POINTER(CacheState), ctypes.POINTER(PagePlanes), vp, vp, i64, vp, sz, vp]),
             "mnb_cache_compact": (ci, [ctypes.POINTER(CacheState), ctypes.POINTER(PagePlanes), vp, vp, vp, vp, sz, vp]),
+            "mnb_rms_norm": (ci, [ctypes.POINTER(RmsNormArgs)]),
             "mnb_fp_packed_size": (sz, [i64, i64, ci]),
             "mnb_pack_fp_weights": (ci, [vp, vp, sz, i64, i64, ci, vp]),
             "mnb_matmul_fp": (ci, [vp, vp, vp, ctypes.c_float, vp, i64, i64, i64, ci, ci, ci, vp]),
@@ -332,13 +346,13 @@ def mnb_select_kernel(M, N, K, bits, block_size, act_dtype, accuracy_level=0) ->
 # run between microsecond kernels, so their checks are a few attribute reads each.
 
 _codes = {}  # torch dtype -> dtype code, filled on first use
-_int32 = _float32 = _device = _raw_stream = None
+_int8 = _int32 = _float32 = _device = _raw_stream = None
 
 
 def _setup():
-    global _int32, _float32, _device, _raw_stream
+    global _int8, _int32, _float32, _device, _raw_stream
     import torch
-    _int32, _float32 = torch.int32, torch.float32
+    _int8, _int32, _float32 = torch.int8, torch.int32, torch.float32
     _device, _raw_stream = getattr(torch._C, "_cuda_getDevice", None), getattr(torch._C, "_cuda_getCurrentRawStream", None)
     _codes.update({torch.float32: MNB_F32, torch.float16: MNB_F16, torch.bfloat16: MNB_BF16})
 
@@ -573,6 +587,62 @@ def mnb_cache_compact(state, planes, refs_out, tables_out, counts, workspace=Non
     st = (_lib or load()).mnb_cache_compact(state, planes, *ptrs, *_space(workspace), _current(stream))
     if st:
         _check(st, "mnb_cache_compact")
+
+
+# ---- around the attention: norm, experts, the next token ----------------------------------------
+
+def _here(what, t):
+    """The tensor's address; it has to live on the current device, whose stream the call goes to."""
+    d = t.get_device()
+    if d < 0 or (_device is not None and d != _device()):
+        _fail(f"{what}: a tensor on the current CUDA device is wanted")
+    return t.data_ptr()
+
+
+def _row_matrix(what, t, shape, dtype=None):
+    """(pointer, row stride) of a [rows, columns] tensor with unit stride in a row."""
+    st = t.stride()
+    if t.shape != shape or len(shape) != 2 or (st[1] != 1 and shape[1] > 1 and shape[0]) or (dtype is not None and t.dtype is not dtype):
+        _fail(f"{what}: a [rows, columns] tensor of the call's shape and dtype with unit stride in a row is wanted")
+    return _here(what, t), st[0]
+
+
+def mnb_rms_norm(x, weight, eps, residual=None, residual_out=None, y=None, codes=None, scales=None, block_size=0, flags=0,
+                 stream=None):
+    """S = x + residual to residual_out; its norm to y and, as int8 codes with a scale for each block of block_size values,
+    to codes [T, KB * block_size] and scales [T, KB].  x [T, width]; weight [width] or None."""
+    if not _codes:
+        _setup()
+    shape, dt = x.shape, x.dtype
+    code = _codes.get(dt)
+    if code is None:
+        _fail("x: a float32, float16 or bfloat16 tensor is wanted")
+    xp, xs = _row_matrix("x", x, shape)
+    rp, rs = (None, 0) if residual is None else _row_matrix("residual", residual, shape, dt)
+    sp, ss = (None, 0) if residual_out is None else _row_matrix("residual_out", residual_out, shape, dt)
+    yp, ys, yd = None, 0, 0
+    if y is not None:
+        yp, ys = _row_matrix("y", y, shape)
+        yd = _codes.get(y.dtype, -1)
+    wp, wd = None, 0
+    if weight is not None:
+        wd = _codes.get(weight.dtype, -1)
+        if weight.numel() != shape[1] or not weight.is_contiguous():
+            _fail("weight: a contiguous [width] tensor is wanted")
+        wp = _here("weight", weight)
+    cp = ap = None
+    if codes is not None or scales is not None:
+        if codes is None or scales is None or block_size < 1:
+            _fail("codes, scales: both, with a block_size, are wanted")
+        kb = -(-shape[1] // block_size)
+        if codes.dtype is not _int8 or codes.shape != (shape[0], kb * block_size) or not codes.is_contiguous() or \
+                scales.dtype is not _float32 or scales.shape != (shape[0], kb) or not scales.is_contiguous():
+            _fail("codes, scales: contiguous int8 [T, KB * block_size] and f32 [T, KB] tensors are wanted")
+        cp, ap = _here("codes", codes), _here("scales", scales)
+    a = RmsNormArgs(xp, rp, sp, wp, yp, cp, ap, shape[0], shape[1], block_size, xs, rs, ss, ys, code, wd, yd, eps, flags, _current(stream))
+    st = (_lib or load()).mnb_rms_norm(a)
+    if st:
+        _check(st, "mnb_rms_norm")
 
 
 def mnb_get_device_error() -> int:

@@ -634,6 +634,56 @@ MNB_API mnb_status mnb_cache_compact(const mnb_cache_state* state, const mnb_pag
                              int32_t* tables_out, int32_t* counts, void* workspace, size_t workspace_bytes,
                              mnb_stream_t stream);
 
+/* ---- around the attention: norm, experts, the next token ----------------
+ * What a decoder's step runs besides the products and the attention: the
+ * root-mean-square norm with the residual's addition, a mixture-of-experts
+ * layer for a few tokens, and the draw of the next tokens.  No page of the
+ * reference has a kernel for them.  As the calls above they use programmatic
+ * dependent launch on their own, and report what they find on the device in
+ * the status word. */
+
+/* Flags of mnb_rms_norm. */
+#define MNB_NORM_UNIT_OFFSET 1 /* gain 1 + weight instead of weight */
+
+/* S = X + residual (S = X without one);
+ * Y[t, i] = S[t, i] * gain[i] / sqrt(mean_i S[t, i]^2 + eps).
+ * Everything is computed in f32 from the unrounded S; residual_out, y and the
+ * codes are each rounded once from it.
+ *   x, residual   device [T, width] of dtype with the given row strides
+ *                 (elements, at least width), aligned to the element
+ *   residual      NULL: none, and residual_out is NULL too
+ *   residual_out  [T, width] of dtype, or NULL: S
+ *   weight        [width] of weight_dtype, or NULL: gain 1
+ *   y             [T, width] of out_dtype, or NULL
+ *   codes, scales int8 [T, KB * block_size] (16-byte aligned) and f32 [T, KB],
+ *                 KB = ceil(width / block_size), both or neither: Y as
+ *                 mnb_quantize_activations codes it (scale = max|y| / 127 of
+ *                 the block, round half away from zero, codes past width 0),
+ *                 but from the unrounded Y, and a block with an infinity or a
+ *                 NaN has scale NaN and codes 0.  block_size: a power of two,
+ *                 at least 16; a block as wide as the row gives one scale a row.
+ * residual_out and y may be x or residual (same pointer and strides); any
+ * other overlap is undefined.  width (with codes KB * block_size) is at most
+ * 32768, else MNB_ERR_UNSUPPORTED.  16-byte accesses where every base and
+ * stride allows them, narrower ones otherwise.  T == 0 is a no-op. */
+typedef struct mnb_rms_norm_args {
+    const void* x;
+    const void* residual;
+    void* residual_out;
+    const void* weight;
+    void* y;
+    int8_t* codes;
+    float* scales;
+    int64_t T, width, block_size;
+    int64_t x_stride, residual_stride, residual_out_stride, y_stride;
+    mnb_dtype dtype, weight_dtype, out_dtype;
+    float eps; /* >= 0 */
+    int flags; /* MNB_NORM_* */
+    mnb_stream_t stream;
+} mnb_rms_norm_args;
+
+MNB_API mnb_status mnb_rms_norm(const mnb_rms_norm_args* args);
+
 /* ---- diagnostics ------------------------------------------------------- */
 
 /* Environment overrides, read at each call (none changes a result beyond
