@@ -21,6 +21,8 @@ MNB_FLAG_PDL = 1
 MNB_FLAG_KPERM = 2
 MNB_ROTARY_INTERLEAVED, MNB_ROTARY_INVERSE = 1, 2
 MNB_NORM_UNIT_OFFSET = 1
+MNB_MOE_SOFTMAX, MNB_MOE_SIGMOID = 0, 1
+MNB_ACT_SILU, MNB_ACT_GELU_TANH = 0, 1
 MNB_ROPE_NONE, MNB_ROPE_LINEAR, MNB_ROPE_NTK, MNB_ROPE_BY_PARTS = range(4)
 MNB_WF_E4M3, MNB_WF_E5M2, MNB_WF_NVFP4 = 1, 2, 3
 KERNELS = {"auto": 0, "gemv": 1, "gemv_mma": 2, "gemm_tc": 3, "generic": 4, "gemv_i8": 5}
@@ -35,7 +37,7 @@ EXPORTS = [
     "mnb_matmul_fp_ex", "mnb_packed_size_gidx", "mnb_pack_weights_gidx", "mnb_workspace_size_ex",
     "mnb_rotary_table", "mnb_rotary", "mnb_rotary_append", "mnb_paged_attention", "mnb_attention_workspace_size",
     "mnb_pages_copy", "mnb_cache_fork", "mnb_cache_resize", "mnb_cache_compact", "mnb_cache_workspace_size",
-    "mnb_rms_norm",
+    "mnb_rms_norm", "mnb_moe_route", "mnb_moe", "mnb_moe_workspace_size",
 ]
 MNB_A8_STATIC_SCRATCH_BYTES = 1 << 20
 MNB_HOST_IO_X_BYTES = 8 << 20
@@ -123,6 +125,34 @@ class RmsNormArgs(ctypes.Structure):
     ]
 
 
+class MoeRouteArgs(ctypes.Structure):
+    _fields_ = [
+        ("logits", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("ids", ctypes.c_void_p), ("weights", ctypes.c_void_p),
+        ("T", ctypes.c_int64), ("E", ctypes.c_int64), ("S", ctypes.c_int64), ("logits_stride", ctypes.c_int64),
+        ("dtype", ctypes.c_int), ("scoring", ctypes.c_int), ("renormalize", ctypes.c_int), ("scale", ctypes.c_float),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
+class ExpertWeights(ctypes.Structure):
+    """mnb_expert_weights; made by expert_weights()."""
+    _fields_ = [
+        ("packed_b", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("zero_points", ctypes.c_void_p),
+        ("E", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("bits", ctypes.c_int),
+        ("block_size", ctypes.c_int), ("scale_dtype", ctypes.c_int),
+    ]
+
+
+class MoeArgs(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("gate", ctypes.POINTER(ExpertWeights)),
+        ("up", ctypes.POINTER(ExpertWeights)), ("down", ctypes.POINTER(ExpertWeights)), ("x_stride", ctypes.c_int64),
+        ("y_stride", ctypes.c_int64), ("act_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int),
+        ("activation", ctypes.c_int), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -172,6 +202,9 @@ def load(build: bool = True):
             "mnb_cache_resize": (ci, [ctypes.POINTER(CacheState), ctypes.POINTER(PagePlanes), vp, vp, i64, vp, sz, vp]),
             "mnb_cache_compact": (ci, [ctypes.POINTER(CacheState), ctypes.POINTER(PagePlanes), vp, vp, vp, vp, sz, vp]),
             "mnb_rms_norm": (ci, [ctypes.POINTER(RmsNormArgs)]),
+            "mnb_moe_route": (ci, [ctypes.POINTER(MoeRouteArgs)]),
+            "mnb_moe": (ci, [ctypes.POINTER(MoeArgs), ctypes.POINTER(MoeRouteArgs)]),
+            "mnb_moe_workspace_size": (sz, [i64, i64, i64, i64, i64]),
             "mnb_fp_packed_size": (sz, [i64, i64, ci]),
             "mnb_pack_fp_weights": (ci, [vp, vp, sz, i64, i64, ci, vp]),
             "mnb_matmul_fp": (ci, [vp, vp, vp, ctypes.c_float, vp, i64, i64, i64, ci, ci, ci, vp]),
@@ -643,6 +676,84 @@ def mnb_rms_norm(x, weight, eps, residual=None, residual_out=None, y=None, codes
     st = (_lib or load()).mnb_rms_norm(a)
     if st:
         _check(st, "mnb_rms_norm")
+
+
+def expert_weights(packed, scales, zero_points, E, N, K, bits, block_size) -> ExpertWeights:
+    """The weights [N, K] of E experts: packed back to back (mnb_packed_size(N, K, bits, block_size) bytes each), scales
+    [E, N, KB], zero points [E, N, ceil(KB * bits / 8)] uint8 or None.  The descriptor holds the tensors."""
+    if not _codes:
+        _setup()
+    kb = -(-K // block_size) if block_size > 0 else 0
+    size = load().mnb_packed_size(N, K, bits, block_size)
+    if E < 1 or size == 0 or packed.numel() * packed.element_size() < E * size or not packed.is_contiguous():
+        _fail("packed: a contiguous buffer of E packed weights is wanted")
+    if scales.dtype not in _codes or scales.numel() != E * N * kb or not scales.is_contiguous():
+        _fail("scales: a contiguous [E, N, KB] tensor is wanted")
+    if zero_points is not None and (zero_points.element_size() != 1 or zero_points.numel() != E * N * -(-kb * bits // 8) or
+                                    not zero_points.is_contiguous()):
+        _fail("zero_points: a contiguous uint8 [E, N, ceil(KB * bits / 8)] tensor is wanted")
+    w = ExpertWeights(_here("packed", packed), _here("scales", scales), None if zero_points is None else _here("zero_points", zero_points),
+                      E, N, K, bits, block_size, _codes[scales.dtype])
+    w.tensors = (packed, scales, zero_points)
+    w.ref = ctypes.pointer(w)
+    return w
+
+
+def _route(logits, top_k, ids, weights, bias, scoring, renormalize, scale, stream):
+    shape, code = logits.shape, _codes.get(logits.dtype)
+    if code is None:
+        _fail("logits: a float32, float16 or bfloat16 tensor is wanted")
+    lp, ls = _row_matrix("logits", logits, shape)
+    bp = ip = wp = None
+    if bias is not None:
+        if bias.dtype is not _float32 or bias.numel() != shape[1] or not bias.is_contiguous():
+            _fail("bias: a contiguous f32 [E] tensor is wanted")
+        bp = _here("bias", bias)
+    if ids is not None:
+        ip = _i32("ids", ids)
+        if ids.shape != (shape[0], top_k):
+            _fail("ids: an int32 [T, top_k] tensor is wanted")
+        _here("ids", ids)
+    if weights is not None:
+        if weights.dtype is not _float32 or weights.shape != (shape[0], top_k) or not weights.is_contiguous():
+            _fail("weights: a contiguous f32 [T, top_k] tensor is wanted")
+        wp = _here("weights", weights)
+    return MoeRouteArgs(lp, bp, ip, wp, shape[0], shape[1], top_k, ls, code, scoring, 1 if renormalize else 0, scale, stream)
+
+
+def mnb_moe_route(logits, ids, weights, bias=None, scoring=MNB_MOE_SOFTMAX, renormalize=True, scale=1.0, stream=None):
+    """The experts (int32 [T, S]) of each token's logits [T, E] and their weights (f32 [T, S])."""
+    if not _codes:
+        _setup()
+    a = _route(logits, ids.shape[-1], ids, weights, bias, scoring, renormalize, scale, _current(stream))
+    st = (_lib or load()).mnb_moe_route(a)
+    if st:
+        _check(st, "mnb_moe_route")
+
+
+def mnb_moe_workspace_size(T, S, E, hidden, inner) -> int:
+    return load().mnb_moe_workspace_size(T, S, E, hidden, inner)
+
+
+def mnb_moe(x, logits, gate, up, down, y, top_k, ids=None, weights=None, bias=None, scoring=MNB_MOE_SOFTMAX, renormalize=True,
+            scale=1.0, activation=MNB_ACT_SILU, workspace=None, stream=None):
+    """y [T, hidden] = the layer's experts (expert_weights() descriptors) on x [T, hidden], selected by logits [T, E];
+    ids and weights [T, top_k], where given, get the selection."""
+    if not _codes:
+        _setup()
+    s = _current(stream)
+    r = _route(logits, top_k, ids, weights, bias, scoring, renormalize, scale, s)
+    shape = x.shape
+    code, out = _codes.get(x.dtype, -1), _codes.get(y.dtype, -1)
+    if len(shape) != 2 or shape[0] != r.T or shape[1] != gate.K:
+        _fail("x: [T, hidden] rows, one for each row of logits, are wanted")
+    xp, xs = _row_matrix("x", x, shape)
+    yp, ys = _row_matrix("y", y, shape)
+    ws_ptr, ws_bytes = _space(workspace)
+    a = MoeArgs(xp, yp, gate.ref, up.ref, down.ref, xs, ys, code, out, activation, ws_ptr, ws_bytes, s)
+    st = (_lib or load()).mnb_moe(a, r)
+    if st:
+        _check(st, "mnb_moe")
 
 
 def mnb_get_device_error() -> int:

@@ -1,0 +1,12 @@
+// mnb_moe with 2-bit codes (kernels in moe.cuh).
+#include "moe.cuh"
+
+namespace mnb {
+namespace moe {
+
+cudaError_t launch_b2(const Params& gate_up, const Params& down, int act_bf16, cudaStream_t s) {
+    return launch_bits<2>(gate_up, down, act_bf16, s);
+}
+
+}  // namespace moe
+}  // namespace mnb

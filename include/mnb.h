@@ -684,6 +684,89 @@ typedef struct mnb_rms_norm_args {
 
 MNB_API mnb_status mnb_rms_norm(const mnb_rms_norm_args* args);
 
+/* Selection of experts from a router's logits, for mnb_moe_route and mnb_moe.
+ *   logits       device [T, E] of dtype with the given row stride (elements)
+ *   scoring      SOFTMAX: the S largest logits; SIGMOID: the S largest
+ *                sigmoid(logit) + bias (bias: device f32 [E] or NULL, for the
+ *                selection alone; with SOFTMAX it is NULL).  In descending
+ *                order; equal ones by ascending expert, a NaN after all others.
+ *   renormalize  1: a token's weights are its S scores (exp(logit) or the
+ *                sigmoids) divided by their sum; 0: the softmax over all E, or
+ *                the sigmoids as they are.  An expert of logit -inf weighs 0,
+ *                and where every selected one does, so do all.
+ *   scale        multiplies the weights
+ *   ids, weights device int32 and f32 [T, S]: the result.  NULL: not wanted
+ * S <= 32 and E <= 1024, else MNB_ERR_UNSUPPORTED.  ids is what
+ * mnb_matmul_grouped takes. */
+typedef enum mnb_moe_scoring { MNB_MOE_SOFTMAX = 0, MNB_MOE_SIGMOID = 1 } mnb_moe_scoring;
+
+typedef struct mnb_moe_route_args {
+    const void* logits;
+    const float* bias;
+    int32_t* ids;
+    float* weights;
+    int64_t T, E, S, logits_stride;
+    mnb_dtype dtype;
+    mnb_moe_scoring scoring;
+    int renormalize; /* 0 or 1 */
+    float scale;     /* finite */
+    mnb_stream_t stream; /* of mnb_moe_route */
+} mnb_moe_route_args;
+
+MNB_API mnb_status mnb_moe_route(const mnb_moe_route_args* args);
+
+/* E experts' [N, K] weights, as mnb_matmul_grouped takes them: packed back to
+ * back (256-byte aligned), scales [E, N, KB], zero_points [E, N,
+ * ceil(KB * bits / 8)] or NULL. */
+typedef struct mnb_expert_weights {
+    const void* packed_b;
+    const void* scales;
+    const uint8_t* zero_points;
+    int64_t E, N, K;
+    int bits, block_size;
+    mnb_dtype scale_dtype;
+} mnb_expert_weights;
+
+typedef enum mnb_activation { MNB_ACT_SILU = 0, MNB_ACT_GELU_TANH = 1 } mnb_activation;
+
+/* A whole mixture-of-experts layer for a few tokens, in two launches (three
+ * from 9 tokens on): with the experts ids[t, s] and weights w[t, s] of `route`,
+ *     Y[t] = sum_s w[t, s] * down_e ( act(gate_e X[t]) * (up_e X[t]) ),   e = ids[t, s].
+ * Products accumulate in f32; what lies between the products keeps 16 bits
+ * (two bf16 parts), whatever act_dtype is; Y is rounded once to out_dtype.
+ * Results repeat.  The weights of experts that no token selects are not read.
+ *   x, y         device [T, hidden] of act_dtype (bf16 or f16) and out_dtype
+ *                with the given row strides (elements, at least hidden),
+ *                aligned to the element; 16-byte rows (base, stride and
+ *                hidden) are read faster
+ *   gate, up     [inner, hidden] of each expert; down [hidden, inner]; one
+ *                bits, block_size and scale_dtype for the three
+ *   workspace    device, 256-byte aligned, mnb_moe_workspace_size() bytes; its
+ *                contents need no preparation.  Calls that overlap (streams,
+ *                graphs in flight together) need workspaces of their own.
+ * T <= 64 and T * S <= 1024, one bits, block_size and scale_dtype, and act_dtype
+ * not f32, else MNB_ERR_UNSUPPORTED (mnb_moe_route and mnb_matmul_grouped serve
+ * more tokens).  A weight whose header does not match sets
+ * MNB_ERR_LAYOUT_MISMATCH in the device status word.  T == 0 is a no-op. */
+typedef struct mnb_moe_args {
+    const void* x;
+    void* y;
+    const mnb_expert_weights* gate;
+    const mnb_expert_weights* up;
+    const mnb_expert_weights* down;
+    int64_t x_stride, y_stride;
+    mnb_dtype act_dtype, out_dtype;
+    mnb_activation activation;
+    void* workspace;
+    size_t workspace_bytes;
+    mnb_stream_t stream;
+} mnb_moe_args;
+
+MNB_API mnb_status mnb_moe(const mnb_moe_args* args, const mnb_moe_route_args* route);
+
+/* Workspace bytes of mnb_moe (0 if the sizes are invalid or not served). */
+MNB_API size_t mnb_moe_workspace_size(int64_t T, int64_t S, int64_t E, int64_t hidden, int64_t inner);
+
 /* ---- diagnostics ------------------------------------------------------- */
 
 /* Environment overrides, read at each call (none changes a result beyond
