@@ -37,7 +37,7 @@ EXPORTS = [
     "mnb_matmul_fp_ex", "mnb_packed_size_gidx", "mnb_pack_weights_gidx", "mnb_workspace_size_ex",
     "mnb_rotary_table", "mnb_rotary", "mnb_rotary_append", "mnb_paged_attention", "mnb_attention_workspace_size",
     "mnb_pages_copy", "mnb_cache_fork", "mnb_cache_resize", "mnb_cache_compact", "mnb_cache_workspace_size",
-    "mnb_rms_norm", "mnb_moe_route", "mnb_moe", "mnb_moe_workspace_size",
+    "mnb_rms_norm", "mnb_moe_route", "mnb_moe", "mnb_moe_workspace_size", "mnb_sample",
 ]
 MNB_A8_STATIC_SCRATCH_BYTES = 1 << 20
 MNB_HOST_IO_X_BYTES = 8 << 20
@@ -153,6 +153,15 @@ class MoeArgs(ctypes.Structure):
     ]
 
 
+class SampleArgs(ctypes.Structure):
+    _fields_ = [
+        ("logits", ctypes.c_void_p), ("u", ctypes.c_void_p), ("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p),
+        ("top_p", ctypes.c_void_p), ("min_p", ctypes.c_void_p), ("tokens", ctypes.c_void_p), ("probs", ctypes.c_void_p),
+        ("B", ctypes.c_int64), ("V", ctypes.c_int64), ("row_stride", ctypes.c_int64), ("dtype", ctypes.c_int),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -205,6 +214,7 @@ def load(build: bool = True):
             "mnb_moe_route": (ci, [ctypes.POINTER(MoeRouteArgs)]),
             "mnb_moe": (ci, [ctypes.POINTER(MoeArgs), ctypes.POINTER(MoeRouteArgs)]),
             "mnb_moe_workspace_size": (sz, [i64, i64, i64, i64, i64]),
+            "mnb_sample": (ci, [ctypes.POINTER(SampleArgs)]),
             "mnb_fp_packed_size": (sz, [i64, i64, ci]),
             "mnb_pack_fp_weights": (ci, [vp, vp, sz, i64, i64, ci, vp]),
             "mnb_matmul_fp": (ci, [vp, vp, vp, ctypes.c_float, vp, i64, i64, i64, ci, ci, ci, vp]),
@@ -754,6 +764,34 @@ def mnb_moe(x, logits, gate, up, down, y, top_k, ids=None, weights=None, bias=No
     st = (_lib or load()).mnb_moe(a, r)
     if st:
         _check(st, "mnb_moe")
+
+
+def _per_row(what, t, dtype, n):
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
+        _fail(f"{what}: a contiguous {dtype} tensor with a value for each row is wanted")
+    return _here(what, t)
+
+
+def mnb_sample(logits, u, tokens, temperature=None, top_k=None, top_p=None, min_p=None, probs=None, stream=None):
+    """A token (int32 [B]) of each row of logits [B, V] from the uniform numbers u (f32 [B]); the cuts are tensors with a
+    value for each row, or None; probs (f32 [B]) gets the tokens' probabilities after the cuts."""
+    if not _codes:
+        _setup()
+    shape, code = logits.shape, _codes.get(logits.dtype)
+    if code is None:
+        _fail("logits: a float32, float16 or bfloat16 tensor is wanted")
+    lp, ls = _row_matrix("logits", logits, shape)
+    if u is None or tokens is None:
+        _fail("u, tokens: a tensor with a value for each row is wanted")
+    n = shape[0]
+    a = SampleArgs(lp, _per_row("u", u, _float32, n), _per_row("temperature", temperature, _float32, n), _per_row("top_k", top_k, _int32, n),
+                   _per_row("top_p", top_p, _float32, n), _per_row("min_p", min_p, _float32, n), _per_row("tokens", tokens, _int32, n),
+                   _per_row("probs", probs, _float32, n), n, shape[1], ls, code, _current(stream))
+    st = (_lib or load()).mnb_sample(a)
+    if st:
+        _check(st, "mnb_sample")
 
 
 def mnb_get_device_error() -> int:

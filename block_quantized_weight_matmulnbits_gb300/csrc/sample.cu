@@ -1,0 +1,796 @@
+// mnb_sample: one token of each row of logits, by temperature, top-k, top-p and
+// min-p from a given uniform number.
+//
+// With the tokens in descending order of their logits (equal ones by ascending
+// index) and w_i = exp((x_i - max) / T), each cut keeps a start of that order,
+// and the token drawn is the first whose sum of weights passes u times the sum
+// of what is kept.  So a row needs sums of weights up to a place, not a sorted
+// row.  A cluster of CTAs takes a row, each CTA a range of its tokens:
+//
+//   1. the range goes to shared memory (one pass over memory) with its maximum;
+//   2. 2048 bins of equal width in max - x get the tokens' counts and the sums
+//      of their weights; the cluster adds them and each CTA forms the prefix;
+//   3. a place in the order (the k-th token, the share p, the draw) lies in one
+//      bin: its tokens, or those of all bins up to it, if at most 1024, go to
+//      the first CTA, which sorts them and takes their sums in order;
+//   4. a bin with more of them is divided again, over the range of its values,
+//      until it has few or one value, whose j-th token is counted out.
+//
+// A draw depends on sums of up to a million weights next to a border, so the
+// weights are integers: 2^-y in units of 2^-43, y = (max - x) / T * log2 e in two
+// floats, from a table of 2^(-j / 1024) and a cubic of the rest (relative error
+// below 2^-34, one rounding of half a unit).  Their sums are exact and no order
+// of atomics changes them: results repeat, and agree with 64-bit floats but for
+// places that those do not settle either.
+//
+// Bound: the logits' bytes for many rows, in principle; the arithmetic of the
+// weights (35 instructions a token) is longer than those.  With top-k alone or
+// first, step 2 only counts.
+#include <algorithm>
+#include <cmath>
+
+#include "decoder.h"
+
+namespace mnb {
+namespace {
+
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kBins = 2048, kPer = kBins / kThreads;  // bins of a thread in the prefix
+constexpr int kList = 1024;                            // tokens that the first CTA sorts
+constexpr int kUnit = 43;                              // a weight of 1 is 2^43 units
+constexpr int kMaxVocab = 1 << 24;
+constexpr float kCut = 46.f;                           // weights below 2^-46 are 0 units
+
+// 2^43 * 2^(-j / 1024), from the exponential series in double at compile time (good to 2^-50).
+struct Table {
+    unsigned long long v[1024];
+    constexpr Table() : v() {
+        for (int j = 0; j < 1024; ++j) {
+            const double a = -0.693147180559945309417232121458 * j / 1024.0;
+            double term = 1.0, sum = 1.0;
+            for (int n = 1; n < 24; ++n) {
+                term = term * a / n;
+                sum += term;
+            }
+            v[j] = (unsigned long long)(sum * 8796093022208.0 + 0.5);
+        }
+    }
+};
+__device__ const Table g_table = Table();
+
+struct SampleParams {
+    const void* logits;
+    const float* temperature;
+    const int32_t* top_k;
+    const float* top_p;
+    const float* min_p;
+    const float* u;
+    int32_t* tokens;
+    float* probs;
+    int64_t stride;
+    int V, C, seg, staged;
+    int extra;  // weights lose this many bits more, so that V of them fit 63
+    int* status;
+};
+
+// ---- distributed shared memory ----
+__device__ __forceinline__ uint32_t map_to(const void* p, int rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ uint32_t ld_u32(const uint32_t* p, int rank) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(map_to(p, rank)) : "memory");
+    return v;
+}
+__device__ __forceinline__ unsigned long long ld_u64(const unsigned long long* p, int rank) {
+    unsigned long long v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(map_to(p, rank)) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_u32(uint32_t* p, int rank, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_to(p, rank)), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_u64(unsigned long long* p, int rank, unsigned long long v) {
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(map_to(p, rank)), "l"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t add_u32(uint32_t* p, int rank, uint32_t v) {
+    uint32_t old;
+    asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(map_to(p, rank)), "r"(v) : "memory");
+    return old;
+}
+__device__ __forceinline__ void min_u32(uint32_t* p, int rank, uint32_t v) {
+    asm volatile("red.shared::cluster.min.u32 [%0], %1;" ::"r"(map_to(p, rank)), "r"(v) : "memory");
+}
+__device__ __forceinline__ void max_u32(uint32_t* p, int rank, uint32_t v) {
+    asm volatile("red.shared::cluster.max.u32 [%0], %1;" ::"r"(map_to(p, rank)), "r"(v) : "memory");
+}
+
+// Floats in ascending order as unsigned integers (-0 as 0), and back.
+__device__ __forceinline__ uint32_t key_of(float f) {
+    const uint32_t u = __float_as_uint(f + 0.f);
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float value_of(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k); }
+
+struct Scale {
+    float top, c_hi, c_lo, cut, per;  // maximum, log2 e / T in two floats, largest max - x of a weight above 0, bins per unit of max - x
+};
+
+// 2^-y of a token, y = (top - x) c, as `units` (43 bits) and a right shift.
+__device__ __forceinline__ long long weight_parts(float x, const Scale& s, const unsigned long long* table, int& shift) {
+    const float d = s.top - x;
+    // d's own rounding error (exact: d + e = top - x)
+    const float b = d - s.top;
+    const float e = x == s.top ? 0.f : (s.top - (d - b)) + (-x - b);
+    const float p = x == s.top ? 0.f : d * s.c_hi;
+    float rest = fmaf(d, s.c_hi, -p);
+    rest = fmaf(d, s.c_lo, rest);
+    rest = x == s.top ? 0.f : fmaf(e, s.c_hi, rest);
+    const float q = p + 12288.f;  // 1.5 * 2^13: p in units of 2^-10
+    const int k = __float_as_int(q) - 0x46400000;
+    const float z = (p - (q - 12288.f)) + rest;  // |z| <= 2^-11 and a little
+    // 2^-z - 1 = -z ln 2 + (z ln 2)^2 / 2 - (z ln 2)^3 / 6, in units of 2^-42
+    const float a = z * -0.69314718056f;
+    const int f = __float2int_rn(fmaf(a * a, fmaf(a, 0.16666667f, 0.5f), a) * 4398046511104.f);
+    const long long t = (long long)table[k & 1023];
+    shift = k >> 10;
+    return t + (((long long)(int)(t >> 13) * f) >> 29);  // (t / 2^43 in units of 2^-30) * f
+}
+
+__device__ __forceinline__ unsigned long long weight_of(float x, const Scale& s, const unsigned long long* table, int extra) {
+    if (!(s.top - x <= s.cut) && x != s.top) return 0ull;  // also NaN and -inf
+    int shift;
+    const unsigned long long t = (unsigned long long)weight_parts(x, s, table, shift);
+    shift += extra;
+    return shift > 0 ? (t + (1ull << (shift - 1))) >> shift : t;
+}
+
+__device__ __forceinline__ int bin_of(float x, const Scale& s) {
+    const float d = x == s.top ? 0.f : s.top - x;
+    return d <= s.cut ? min((int)(d * s.per), kBins - 1) : -1;  // NaN: -1
+}
+
+// Shared memory of a CTA, before its tokens.
+struct Shared {
+    unsigned long long table[1024];
+    unsigned long long mw[kBins];      // the cluster's sums, then their prefix
+    unsigned long long list[kList];    // (order, index) of gathered tokens
+    unsigned long long sums[kList];    // their weights' prefix
+    uint32_t mc[kBins];
+    uint32_t cnt[kBins], lo[kBins], hi[kBins];
+    unsigned long long scan_w[kWarps];
+    unsigned long long minp_w, total_w, res_w, found_w;
+    uint32_t scan_c[kWarps];
+    uint32_t top_key, listed, first_index, kmin, kmax, ties[8], found, found2, res_token;
+    uint32_t total_c;
+    float res_x;
+};
+
+template <int DT>
+struct Row {
+    static constexpr int E = DT == kF32 ? 4 : 8;  // tokens of a 16-byte window
+    const uint8_t* base;                           // first window (16-byte aligned)
+    int windows, skip, n, first;                   // windows; tokens before the range in the first; tokens; index of the first token
+    bool edges;                                    // the first and last windows hold other memory
+
+    __device__ __forceinline__ static void widen(const uint4& v, float (&x)[E]) {
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (DT == kF32) {
+                x[i] = __uint_as_float(u[i]);
+            } else if constexpr (DT == kBF16) {
+                x[2 * i] = __uint_as_float(u[i] << 16);
+                x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+            } else {
+                const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+                x[2 * i] = h.x;
+                x[2 * i + 1] = h.y;
+            }
+        }
+    }
+    // Window w, tokens outside the range as -inf.
+    __device__ __forceinline__ uint4 raw(int w) const {
+        if (!edges || (w * E >= skip && (w + 1) * E <= skip + n)) return *reinterpret_cast<const uint4*>(base + (size_t)w * 16);
+        constexpr uint32_t none = DT == kF32 ? 0xFF800000u : DT == kBF16 ? 0xFF80u : 0xFC00u;
+        uint32_t u[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+            const bool in = w * E + j >= skip && w * E + j < skip + n;
+            if constexpr (DT == kF32) {
+                u[j] = in ? reinterpret_cast<const uint32_t*>(base)[(size_t)w * E + j] : none;
+            } else {
+                const uint32_t h = in ? reinterpret_cast<const uint16_t*>(base)[(size_t)w * E + j] : none;
+                u[j >> 1] |= h << (16 * (j & 1));
+            }
+        }
+        return make_uint4(u[0], u[1], u[2], u[3]);
+    }
+    template <class F>
+    __device__ __forceinline__ void each(F&& f) const {
+        for (int w = threadIdx.x; w < windows; w += kThreads) {
+            float x[E];
+            widen(raw(w), x);
+#pragma unroll
+            for (int j = 0; j < E; ++j) f(x[j], w * E + j);
+        }
+    }
+    __device__ __forceinline__ int index(int at) const { return first + at - skip; }
+};
+
+template <int DT>
+struct Sampler {
+    Shared& S;
+    const SampleParams& p;
+    Row<DT> row;
+    Scale sc;
+    int rank;
+    int tid, lane, warp;
+
+    __device__ __forceinline__ void sync() const {
+        if (p.C > 1) cluster_sync();
+        else __syncthreads();
+    }
+
+    // Bins' counts (and sums of weights) over the cluster, then their prefix in mc and mw.  bin(x) < 0: not counted.
+    template <bool WEIGHTS, class B>
+    __device__ __forceinline__ void histogram(B&& bin, unsigned long long minp) {
+        for (int i = tid; i < kBins; i += kThreads) {
+            S.cnt[i] = 0u;
+            if (WEIGHTS) S.lo[i] = S.hi[i] = 0u;
+        }
+        if (tid == 0) S.minp_w = 0ull;
+        __syncthreads();
+        unsigned long long keep = 0ull;
+        row.each([&](float x, int) {
+            const int b = bin(x);
+            if (b < 0) return;
+            atomicAdd(&S.cnt[b], 1u);
+            if (WEIGHTS) {
+                const unsigned long long w = weight_of(x, sc, S.table, p.extra);
+                if (w >= minp) keep += w;
+                const uint32_t lo = (uint32_t)w;
+                const uint32_t old = atomicAdd(&S.lo[b], lo);
+                const uint32_t hi = (uint32_t)(w >> 32) + (old + lo < old ? 1u : 0u);
+                if (hi) atomicAdd(&S.hi[b], hi);
+            }
+        });
+        if (WEIGHTS && minp != ~0ull) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) keep += __shfl_xor_sync(0xFFFFFFFFu, keep, o);
+            if (lane == 0) atomicAdd(&S.minp_w, keep);
+        }
+        if (p.C > 1) {
+            cluster_sync();
+            // each CTA adds a slice of the bins and hands it to all
+            const int slice = kBins / p.C, b0 = rank * slice;
+            for (int i = tid; i < slice; i += kThreads) {
+                uint32_t c = 0;
+                unsigned long long w = 0;
+                for (int r = 0; r < p.C; ++r) {
+                    c += ld_u32(&S.cnt[b0 + i], r);
+                    if (WEIGHTS) w += ld_u32(&S.lo[b0 + i], r) + ((unsigned long long)ld_u32(&S.hi[b0 + i], r) << 32);
+                }
+                for (int r = 0; r < p.C; ++r) {
+                    st_u32(&S.mc[b0 + i], r, c);
+                    if (WEIGHTS) st_u64(&S.mw[b0 + i], r, w);
+                }
+            }
+            unsigned long long all = 0;
+            if (WEIGHTS && minp != ~0ull && tid == 0) {
+                for (int r = 0; r < p.C; ++r) all += ld_u64(&S.minp_w, r);
+            }
+            cluster_sync();
+            if (WEIGHTS && minp != ~0ull && tid == 0) S.minp_w = all;  // (every CTA has read the others' parts)
+        } else {
+            __syncthreads();
+            for (int i = tid; i < kBins; i += kThreads) {
+                S.mc[i] = S.cnt[i];
+                if (WEIGHTS) S.mw[i] = S.lo[i] + ((unsigned long long)S.hi[i] << 32);
+            }
+            __syncthreads();
+        }
+        // inclusive prefix: kPer bins a thread
+        uint32_t c[kPer], cs = 0;
+        unsigned long long w[kPer], ws = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            cs += S.mc[tid * kPer + i];
+            c[i] = cs;
+            if (WEIGHTS) ws += S.mw[tid * kPer + i];
+            w[i] = ws;
+        }
+        uint32_t ci = cs;
+        unsigned long long wi = ws;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t a = __shfl_up_sync(0xFFFFFFFFu, ci, o);
+            const unsigned long long b = __shfl_up_sync(0xFFFFFFFFu, wi, o);
+            if (lane >= o) {
+                ci += a;
+                wi += b;
+            }
+        }
+        if (lane == 31) {
+            S.scan_c[warp] = ci;
+            S.scan_w[warp] = wi;
+        }
+        __syncthreads();
+        uint32_t cb = ci - cs;
+        unsigned long long wb = wi - ws;
+        for (int k = 0; k < warp; ++k) {
+            cb += S.scan_c[k];
+            wb += S.scan_w[k];
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            S.mc[tid * kPer + i] = cb + c[i];
+            if (WEIGHTS) S.mw[tid * kPer + i] = wb + w[i];
+        }
+        __syncthreads();
+    }
+
+    // First bin whose prefix reaches `target` (-1: none does).
+    template <bool COUNT>
+    __device__ __forceinline__ int first_bin(unsigned long long target) {
+        if (tid == 0) S.found = ~0u;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int b = tid * kPer + i;
+            const unsigned long long upto = COUNT ? (unsigned long long)S.mc[b] : S.mw[b];
+            const unsigned long long before = b == 0 ? 0ull : COUNT ? (unsigned long long)S.mc[b - 1] : S.mw[b - 1];
+            if (upto >= target && before < target) S.found = (uint32_t)b;
+        }
+        __syncthreads();
+        const int b = (int)S.found;
+        __syncthreads();
+        return b;
+    }
+
+    // Tokens with in(x) into the first CTA's list, sorted there, with the prefix of their weights; their number.
+    template <class P>
+    __device__ __forceinline__ int gather(P&& in) {
+        if (tid == 0) S.listed = 0u;
+        sync();
+        row.each([&](float x, int at) {
+            if (!in(x)) return;
+            const unsigned long long v = ((unsigned long long)(~key_of(x)) << 32) | (uint32_t)row.index(at);
+            if (p.C > 1) {
+                const uint32_t i = add_u32(&S.listed, 0, 1u);
+                if (i < kList) st_u64(&S.list[i], 0, v);
+            } else {
+                const uint32_t i = atomicAdd(&S.listed, 1u);
+                if (i < kList) S.list[i] = v;
+            }
+        });
+        sync();
+        if (rank != 0) return 0;
+        const int n = min((int)S.listed, kList);
+        int size = 32;
+        while (size < n) size *= 2;
+        for (int i = n + tid; i < size; i += kThreads) S.list[i] = ~0ull;
+        __syncthreads();
+        for (int k = 2; k <= size; k *= 2) {
+            for (int j = k / 2; j > 0; j /= 2) {
+                for (int t = tid; t < size / 2; t += kThreads) {
+                    const int a = 2 * t - (t & (j - 1)), b = a + j;
+                    const unsigned long long x = S.list[a], y = S.list[b];
+                    if ((x > y) == ((a & k) == 0)) {
+                        S.list[a] = y;
+                        S.list[b] = x;
+                    }
+                }
+                __syncthreads();
+            }
+        }
+        // two tokens a thread
+        unsigned long long w[2], s = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int at = 2 * tid + i;
+            s += at < n ? weight_of(value_of(~(uint32_t)(S.list[at] >> 32)), sc, S.table, p.extra) : 0ull;
+            w[i] = s;
+        }
+        unsigned long long si = s;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned long long b = __shfl_up_sync(0xFFFFFFFFu, si, o);
+            if (lane >= o) si += b;
+        }
+        if (lane == 31) S.scan_w[warp] = si;
+        __syncthreads();
+        unsigned long long before = si - s;
+        for (int k = 0; k < warp; ++k) before += S.scan_w[k];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) S.sums[2 * tid + i] = before + w[i];
+        __syncthreads();
+        return n;
+    }
+
+    // (first CTA) First place of the sorted list whose prefix reaches `target`; n - 1 if none does.
+    __device__ __forceinline__ int first_listed(unsigned long long target, int n) {
+        if (tid == 0) S.found2 = (uint32_t)(n - 1);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int at = 2 * tid + i;
+            if (at < n && S.sums[at] >= target && (at == 0 || S.sums[at - 1] < target)) S.found2 = (uint32_t)at;
+        }
+        __syncthreads();
+        const int at = (int)S.found2;
+        __syncthreads();
+        return at;
+    }
+
+    __device__ __forceinline__ void write(int64_t r, int token, float x, unsigned long long total) {
+        if (tid != 0) return;
+        p.tokens[r] = token;
+        if (p.probs) {
+            int shift;
+            const double w = (double)weight_parts(x, sc, S.table, shift);
+            p.probs[r] = (float)(ldexp(w, -shift - p.extra) / (double)total);
+        }
+    }
+
+    // The token at a place of the order: the first whose prefix of counts (COUNT) or weights reaches `target`, which the
+    // prefix in mc / mw of the bins by max - x does in bin `b`.  Every CTA gets its index, its logit and the sum of weights up to it.
+    template <bool COUNT>
+    __device__ __forceinline__ void resolve(int b, unsigned long long target) {
+        unsigned long long base_w = b ? S.mw[b - 1] : 0ull;
+        uint32_t base_c = b ? S.mc[b - 1] : 0u, n = S.mc[b] - base_c;
+        __syncthreads();
+        const Scale s0 = sc;
+        uint32_t kmin = 0u, kmax = ~0u;
+        auto extent = [&](auto&& in) {  // lowest and highest key of the tokens in(x)
+            if (tid == 0) {
+                S.kmin = ~0u;
+                S.kmax = 0u;
+            }
+            sync();
+            uint32_t lo = ~0u, hi = 0u;
+            row.each([&](float x, int) {
+                if (!in(x)) return;
+                lo = min(lo, key_of(x));
+                hi = max(hi, key_of(x));
+            });
+            lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+            hi = __reduce_max_sync(0xFFFFFFFFu, hi);
+            if (lane == 0) {
+                for (int r = 0; r < p.C; ++r) {
+                    if (p.C > 1) {
+                        min_u32(&S.kmin, r, lo);
+                        max_u32(&S.kmax, r, hi);
+                    } else {
+                        atomicMin(&S.kmin, lo);
+                        atomicMax(&S.kmax, hi);
+                    }
+                }
+            }
+            sync();
+            kmin = S.kmin;
+            kmax = S.kmax;
+            __syncthreads();
+        };
+        extent([&](float x) { return bin_of(x, s0) == b; });
+        while (n > kList && kmin < kmax) {
+            const uint32_t k0 = kmin, k1 = kmax;
+            const unsigned long long span = (unsigned long long)(k1 - k0) + 1ull;
+            // NaN is in no bin: its key is above or below every finite one's, and x == x is asked
+            auto sub = [&](float x) {
+                const uint32_t k = key_of(x);
+                return x == x && k >= k0 && k <= k1 ? (int)((unsigned long long)(k1 - k) * kBins / span) : -1;
+            };
+            histogram<true>(sub, ~0ull);
+            const int f = max(first_bin<COUNT>(target - (COUNT ? (unsigned long long)base_c : base_w)), 0);  // (one always does)
+            n = S.mc[f] - (f ? S.mc[f - 1] : 0u);
+            base_c += f ? S.mc[f - 1] : 0u;
+            base_w += f ? S.mw[f - 1] : 0ull;
+            extent([&](float x) { return sub(x) == f; });
+        }
+        auto in = [&](float x) { return x == x && key_of(x) >= kmin && key_of(x) <= kmax; };
+        if (n <= kList) {
+            const int m = gather(in);
+            if (rank == 0) {
+                const int at = COUNT ? min((int)(target - base_c), m) - 1 : first_listed(target - base_w, m);
+                if (tid == 0) {
+                    S.res_w = base_w + S.sums[at];
+                    S.res_token = (uint32_t)S.list[at];
+                    S.res_x = value_of(~(uint32_t)(S.list[at] >> 32));
+                }
+            }
+        } else {
+            // one value, more than fits the list: the j-th of its tokens
+            const float x0 = value_of(kmin);
+            const unsigned long long w = weight_of(x0, sc, S.table, p.extra);
+            const unsigned long long j = COUNT ? target - base_c : (target - base_w + w - 1) / w;  // from 1; w > 0, else no target is here
+            // a thread counts windows that follow each other
+            const int per = (row.windows + kThreads - 1) / kThreads;
+            const int w0 = min(tid * per, row.windows), w1 = min(w0 + per, row.windows);
+            uint32_t c = 0;
+            for (int i = w0; i < w1; ++i) {
+                float x[Row<DT>::E];
+                Row<DT>::widen(row.raw(i), x);
+#pragma unroll
+                for (int e = 0; e < Row<DT>::E; ++e) c += in(x[e]) ? 1u : 0u;
+            }
+            uint32_t ci = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t a = __shfl_up_sync(0xFFFFFFFFu, ci, o);
+                if (lane >= o) ci += a;
+            }
+            if (lane == 31) S.scan_c[warp] = ci;
+            __syncthreads();
+            uint32_t before = ci - c, all = 0;
+            for (int k = 0; k < kWarps; ++k) {
+                if (k < warp) before += S.scan_c[k];
+                all += S.scan_c[k];
+            }
+            if (p.C > 1) {
+                if (tid == 0)
+                    for (int r = 0; r < p.C; ++r) st_u32(&S.ties[rank], r, all);
+                cluster_sync();
+                for (int r = 0; r < rank; ++r) before += S.ties[r];
+            }
+            if (j > before && j <= (unsigned long long)before + c) {
+                uint32_t left = (uint32_t)(j - before);
+                for (int i = w0; i < w1; ++i) {
+                    float x[Row<DT>::E];
+                    Row<DT>::widen(row.raw(i), x);
+#pragma unroll
+                    for (int e = 0; e < Row<DT>::E; ++e)
+                        if (in(x[e]) && --left == 0u) {
+                            const uint32_t token = (uint32_t)row.index(i * Row<DT>::E + e);
+                            if (p.C > 1) st_u32(&S.res_token, 0, token);
+                            else S.res_token = token;
+                        }
+                }
+            }
+            if (rank == 0 && tid == 0) {
+                S.res_w = base_w + j * w;
+                S.res_x = x0;
+            }
+        }
+        sync();
+        if (p.C > 1 && rank != 0 && tid == 0) S.found_w = ld_u64(&S.res_w, 0);
+        else if (tid == 0) S.found_w = S.res_w;
+        sync();  // (the next resolve writes the first CTA's result)
+    }
+};
+
+template <int DT>
+__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    Shared& S = *reinterpret_cast<Shared*>(smem);
+    uint8_t* data = smem + (sizeof(Shared) + 15) / 16 * 16;
+    constexpr int E = Row<DT>::E, esize = 16 / E;
+    const int tid = threadIdx.x;
+    const int rank = p.C > 1 ? (int)cluster_ctarank() : 0;
+    const int64_t r = blockIdx.x / p.C;
+    for (int i = tid; i < 1024; i += kThreads) S.table[i] = g_table.v[i];
+    if (tid == 0) {
+        S.top_key = 0u;
+        S.first_index = ~0u;
+    }
+    griddep_wait();
+    griddep_launch_dependents();
+
+    const float temperature = p.temperature ? p.temperature[r] : 1.f;
+    const int top_k = p.top_k ? p.top_k[r] : 0;
+    const float top_p = p.top_p ? p.top_p[r] : 1.f;
+    const float min_p = p.min_p ? p.min_p[r] : 0.f;
+    const float u = p.u[r];
+    if (!(temperature >= 0.f) || !(top_p == top_p) || !(min_p == min_p) || !(u >= 0.f && u < 1.f)) {
+        if (rank == 0 && tid == 0) {
+            p.tokens[r] = -1;
+            if (p.probs) p.probs[r] = 0.f;
+            set_status(p.status, 1 /* MNB_ERR_INVALID_ARG */);
+        }
+        return;  // the whole cluster does
+    }
+
+    // ---- 1. the range, and the row's maximum ----
+    Row<DT> row;
+    row.first = min(rank * p.seg, p.V);
+    row.n = min(p.seg, p.V - row.first);
+    const uint8_t* src = static_cast<const uint8_t*>(p.logits) + (size_t)(r * p.stride + row.first) * esize;
+    row.base = reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(src) & ~uintptr_t(15));
+    row.skip = (int)(src - row.base) / esize;
+    row.windows = row.n > 0 ? (row.skip + row.n + E - 1) / E : 0;
+    row.edges = true;
+    float top = -INFINITY;
+    for (int w = tid; w < row.windows; w += kThreads) {
+        const uint4 v = row.raw(w);
+        if (p.staged) *reinterpret_cast<uint4*>(data + (size_t)w * 16) = v;
+        float x[E];
+        Row<DT>::widen(v, x);
+#pragma unroll
+        for (int j = 0; j < E; ++j) top = fmaxf(top, x[j]);  // passes over NaN
+    }
+    if (p.staged) {
+        row.base = data;
+        row.edges = false;  // the ends hold -inf there
+    }
+    if (p.C > 1) cluster_sync();  // every CTA's shared memory is set up
+    else __syncthreads();
+    const uint32_t k = __reduce_max_sync(0xFFFFFFFFu, key_of(top));
+    if ((tid & 31) == 0) {
+        if (p.C > 1)
+            for (int c = 0; c < p.C; ++c) max_u32(&S.top_key, c, k);
+        else atomicMax(&S.top_key, k);
+    }
+    Sampler<DT> q{S, p, row, {}, rank, tid, tid & 31, tid >> 5};
+    q.sync();
+    top = value_of(S.top_key);
+    if (top == -INFINITY) {  // nothing can be drawn
+        if (rank == 0 && tid == 0) {
+            p.tokens[r] = -1;
+            if (p.probs) p.probs[r] = 0.f;
+        }
+        return;
+    }
+    q.sc.top = top;
+    if (temperature == 0.f) {
+        // the first token with the maximum
+        uint32_t at = ~0u;
+        row.each([&](float x, int i) {
+            if (x == top) at = min(at, (uint32_t)row.index(i));
+        });
+        at = __reduce_min_sync(0xFFFFFFFFu, at);
+        if ((tid & 31) == 0 && at != ~0u) {
+            if (p.C > 1) min_u32(&S.first_index, 0, at);
+            else atomicMin(&S.first_index, at);
+        }
+        q.sync();
+        if (rank == 0 && tid == 0) {
+            p.tokens[r] = (int32_t)S.first_index;
+            if (p.probs) p.probs[r] = 1.f;
+        }
+        return;
+    }
+    const double c = fmin(1.4426950408889634 / (double)temperature, 1e38);
+    q.sc.c_hi = (float)c;
+    q.sc.c_lo = (float)(c - (double)q.sc.c_hi);
+    q.sc.cut = fminf(__fdiv_rn(kCut, q.sc.c_hi), 3.4e38f);
+    q.sc.per = (float)kBins / q.sc.cut;
+
+    // ---- 2. bins ----
+    const unsigned long long one = 1ull << (kUnit - p.extra);
+    const unsigned long long minp = min_p > 0.f ? (unsigned long long)ceil((double)fminf(min_p, 1.f) * (double)one) : 0ull;
+    auto bin = [&](float x) { return bin_of(x, q.sc); };
+    bool by_k = top_k > 0 && top_k < p.V;
+    int last = -1;  // the list takes the bins up to this one
+    if (by_k) {
+        q.template histogram<false>(bin, 0ull);
+        const int b = q.template first_bin<true>((unsigned long long)top_k);
+        if (b < 0) by_k = false;  // every token of a weight above 0 is among the k
+        else if (S.mc[b] <= (uint32_t)kList) last = b;
+    }
+    unsigned long long total = 0ull, kept = 0ull, least = 0ull;  // sums: of the top k, of what is kept; of what min-p keeps
+    if (last < 0) {
+        q.template histogram<true>(bin, minp);
+        total = S.mw[kBins - 1];
+        least = minp ? S.minp_w : ~0ull;
+        if (by_k) {
+            q.template resolve<true>(q.template first_bin<true>((unsigned long long)top_k), (unsigned long long)top_k);
+            total = S.found_w;
+            q.template histogram<true>(bin, minp);  // (a divided bin took its place)
+        }
+        kept = total;
+        if (top_p < 1.f) {
+            unsigned long long target = (unsigned long long)ceil((double)fmaxf(top_p, 0.f) * (double)total);
+            target = min(max(target, 1ull), total);
+            const int b = q.template first_bin<false>(target);
+            if (S.mc[b] <= (uint32_t)kList) {
+                last = b;
+            } else {
+                q.template resolve<false>(b, target);
+                kept = S.found_w;
+                q.template histogram<true>(bin, minp);
+            }
+        }
+        if (last < 0) {
+            kept = min(kept, least);
+            const unsigned long long target = min((unsigned long long)((double)u * (double)kept) + 1ull, kept);
+            q.template resolve<false>(q.template first_bin<false>(target), target);
+            if (rank == 0) q.write(r, (int)S.res_token, S.res_x, kept);
+            return;
+        }
+    }
+
+    // ---- 3. all that can be kept fits the list ----
+    const int n = q.gather([&](float x) { return bin_of(x, q.sc) >= 0 && bin_of(x, q.sc) <= last; });
+    if (rank == 0) {
+        if (by_k && total == 0ull) total = S.sums[min(top_k, n) - 1];
+        kept = total;
+        if (top_p < 1.f) {
+            unsigned long long target = (unsigned long long)ceil((double)fmaxf(top_p, 0.f) * (double)total);
+            target = min(max(target, 1ull), total);
+            kept = S.sums[q.first_listed(target, n)];
+        }
+        if (minp) {  // weights descend along the list: the sum of those from minp on
+            if (tid == 0) S.minp_w = 0ull;
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int at = 2 * tid + i;
+                if (at < n) {
+                    const unsigned long long w = S.sums[at] - (at ? S.sums[at - 1] : 0ull);
+                    if (w >= minp) atomicAdd(&S.minp_w, w);
+                }
+            }
+            __syncthreads();
+            kept = min(kept, S.minp_w);
+        }
+        const unsigned long long target = min((unsigned long long)((double)u * (double)kept) + 1ull, kept);
+        const int at = q.first_listed(target, n);
+        q.write(r, (int)(uint32_t)S.list[at], value_of(~(uint32_t)(S.list[at] >> 32)), kept);
+    }
+}
+
+template <int DT>
+cudaError_t launch_sample(SampleParams p, int64_t rows, cudaStream_t s) {
+    constexpr int esize = DT == kF32 ? 4 : 2;
+    const size_t fixed = (sizeof(Shared) + 15) / 16 * 16;
+    const size_t limit = device_info().smem_optin;
+    // CTAs a row: until the row's ranges fit a third of an SM's shared memory each, or all SMs have one
+    p.C = 1;
+    auto seg_of = [&](int c) { return ((p.V + c - 1) / c + 7) / 8 * 8; };
+    while (p.C < 8 && ((size_t)seg_of(p.C) * esize > 40 * 1024 || rows * p.C * 2 <= dec::kSms) && p.V > p.C * 2048) p.C *= 2;
+    p.seg = seg_of(p.C);
+    size_t bytes = ((size_t)p.seg * esize + 15) / 16 * 16 + 16;
+    p.staged = fixed + bytes <= limit;  // else the passes read memory (L2)
+    if (!p.staged) bytes = 0;
+    auto kern = sample_kernel<DT>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(fixed + bytes));
+    if (e != cudaSuccess) return e;
+    return dec::launch_pdl(kern, dim3((unsigned)(rows * p.C)), dim3(kThreads), fixed + bytes, s, p.C, p);
+}
+
+}  // namespace
+}  // namespace mnb
+
+using namespace mnb;
+
+extern "C" {
+
+mnb_status mnb_sample(const mnb_sample_args* a) {
+    if (!a || a->B < 0 || a->V < 1 || !dec::valid_dt(a->dtype)) return MNB_ERR_INVALID_ARG;
+    if (a->B > 1 && (a->row_stride < a->V || a->row_stride >= (int64_t(1) << 38))) return MNB_ERR_INVALID_ARG;
+    if (a->V > kMaxVocab || a->B >= (int64_t(1) << 28)) return MNB_ERR_UNSUPPORTED;
+    if (a->B == 0) return MNB_OK;
+    if (!a->logits || !a->u || !a->tokens || !dec::aligned_to(a->logits, dec::dt_bytes(a->dtype)) || !dec::aligned_to(a->u, 4) ||
+        !dec::aligned_to(a->tokens, 4) || !dec::aligned_to(a->probs, 4) || !dec::aligned_to(a->temperature, 4) ||
+        !dec::aligned_to(a->top_k, 4) || !dec::aligned_to(a->top_p, 4) || !dec::aligned_to(a->min_p, 4))
+        return MNB_ERR_INVALID_ARG;
+    SampleParams p{};
+    p.status = device_status_word();
+    if (!p.status) return dec::status_of(cudaErrorUnknown);
+    p.logits = a->logits;
+    p.temperature = a->temperature;
+    p.top_k = a->top_k;
+    p.top_p = a->top_p;
+    p.min_p = a->min_p;
+    p.u = a->u;
+    p.tokens = a->tokens;
+    p.probs = a->probs;
+    p.V = (int)a->V;
+    p.stride = a->B > 1 ? a->row_stride : a->V;
+    while (((int64_t)p.V >> p.extra) >= (1 << 19)) ++p.extra;  // V * 2^(43 - extra) below 2^63
+    if (inject_launch_failure()) return MNB_ERR_CUDA;
+    const cudaStream_t s = (cudaStream_t)a->stream;
+    ProfileScope prof("mnb_sample", s);
+    cudaError_t e;
+    switch (a->dtype) {
+        case MNB_F32: e = launch_sample<kF32>(p, a->B, s); break;
+        case MNB_F16: e = launch_sample<kF16>(p, a->B, s); break;
+        default: e = launch_sample<kBF16>(p, a->B, s); break;
+    }
+    if (e == cudaSuccess) prof.done("sample");
+    return dec::status_of(e);
+}
+
+}  // extern "C"

@@ -767,6 +767,46 @@ MNB_API mnb_status mnb_moe(const mnb_moe_args* args, const mnb_moe_route_args* r
 /* Workspace bytes of mnb_moe (0 if the sizes are invalid or not served). */
 MNB_API size_t mnb_moe_workspace_size(int64_t T, int64_t S, int64_t E, int64_t hidden, int64_t inner);
 
+/* One token of each row of logits.  With x the row, T its temperature, the
+ * tokens in descending order of x (equal ones by ascending index) and
+ * w_i = exp((x_i - max x) / T):
+ *   top-k   keeps the first k tokens (k <= 0 or >= V: all)
+ *   top-p   then the shortest start of them whose weights sum to at least
+ *           top_p of theirs (never none; 1 and more: all)
+ *   min-p   of these, those with w_i >= min_p (0: all; above 1 acts as 1)
+ * and the token is the first in that order whose sum of kept weights, its own
+ * included, exceeds u times the sum of all kept ones.  T == 0 takes the first
+ * token of the order.  Weights below 2^-46 of the largest are never drawn; a
+ * NaN counts as -inf.  A row without a logit above -inf gets token -1,
+ * probability 0.  Sums are exact integers (units of 2^-43 of the largest
+ * weight for V below 2^19): results repeat, and agree with 64-bit arithmetic.
+ *   logits       device [B, V] of dtype, row stride in elements, aligned to the
+ *                element
+ *   u            device f32 [B], in [0, 1)
+ *   temperature, top_p, min_p  device f32 [B] or NULL (1, 1, 0 for every row)
+ *   top_k        device int32 [B] or NULL (0)
+ *   tokens       device int32 [B]
+ *   probs        device f32 [B] or NULL: the token's weight over the sum of
+ *                the kept ones
+ * A row whose temperature is negative or NaN, whose top_p or min_p is NaN, or
+ * whose u is outside [0, 1) sets the status word and gets token -1.  V is at
+ * most 2^24, else MNB_ERR_UNSUPPORTED.  B == 0 is a no-op. */
+typedef struct mnb_sample_args {
+    const void* logits;
+    const float* u;
+    const float* temperature;
+    const int32_t* top_k;
+    const float* top_p;
+    const float* min_p;
+    int32_t* tokens;
+    float* probs;
+    int64_t B, V, row_stride;
+    mnb_dtype dtype;
+    mnb_stream_t stream;
+} mnb_sample_args;
+
+MNB_API mnb_status mnb_sample(const mnb_sample_args* args);
+
 /* ---- diagnostics ------------------------------------------------------- */
 
 /* Environment overrides, read at each call (none changes a result beyond

@@ -109,3 +109,33 @@ def moe(x, ids, weights, gate, up, down, gelu):
                 y[t] += down[e] @ h
                 tol[t] += np.abs(down[e]) @ dh + unit(inner) * (np.abs(down[e]) @ np.abs(h))
     return y, tol
+
+
+def sample(x, t, k, p, m, u):
+    """(token, probability, distance): the draw from a float64 row; the distance of its sums from the nearest border that
+    would change it, relative to what is kept."""
+    x = np.where(np.isnan(x), -np.inf, x)
+    if x.max() == -np.inf:
+        return -1, 0.0, 1.0
+    order = np.lexsort((np.arange(len(x)), -x))
+    if t == 0:
+        return int(order[0]), 1.0, 1.0
+    with np.errstate(invalid="ignore"):
+        d = np.where(x[order] == x.max(), 0.0, x.max() - x[order])
+        w = np.where(np.isinf(d), 0.0, np.exp(-np.where(np.isinf(d), 0.0, d) / t))
+    near = 1.0
+    if 0 < k < len(x):
+        w[k:] = 0.0
+    if p < 1:
+        before = np.concatenate([[0.0], np.cumsum(w)[:-1]])
+        keep = before < p * w.sum()
+        keep[0] = True
+        near = min(near, np.abs(np.cumsum(w) - p * w.sum()).min() / w.sum())
+        w[~keep] = 0.0
+    if m > 0:
+        near = min(near, np.abs(w - min(m, 1.0))[w != 1].min(initial=1.0))
+        w[w < min(m, 1.0)] = 0.0
+    upto = np.cumsum(w)
+    near = min(near, np.abs(upto - u * upto[-1]).min() / upto[-1]) if u > 0 else near
+    at = int((upto <= u * upto[-1]).sum())
+    return int(order[at]), float(w[at] / upto[-1]), near

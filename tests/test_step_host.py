@@ -118,3 +118,25 @@ def test_moe_limits():
     assert call(_moe(workspace=None), _route()) == mnb.MNB_ERR_NO_MEM
     for bad in ((0, 2, 8, 64, 96), (65, 2, 8, 64, 96), (2, 9, 8, 64, 96), (2, 2, 8, 0, 96), (64, 32, 64, 64, 96), (2, 2, 8, 64, 0)):
         assert mnb.mnb_moe_workspace_size(*bad) == 0
+
+
+def _sample(**kw):
+    a = mnb.SampleArgs()
+    a.logits = a.u = a.tokens = a.temperature = a.top_k = a.top_p = a.min_p = a.probs = 4096
+    a.B, a.V, a.row_stride, a.dtype = 2, 100, 100, mnb.MNB_F32
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+@pytest.mark.parametrize("bad", [{"logits": None}, {"logits": 4098}, {"u": None}, {"tokens": None}, {"tokens": 4097}, {"probs": 4098}, {"B": -1},
+                                 {"V": 0}, {"row_stride": 99}, {"dtype": 3}, {"top_k": 4097}, {"top_p": 4097}, {"min_p": 4097}, {"temperature": 4097}])
+def test_sample_arguments(bad):
+    assert mnb.load().mnb_sample(ctypes.byref(_sample(**bad))) == mnb.MNB_ERR_INVALID_ARG
+
+
+def test_sample_limits():
+    lib = mnb.load()
+    assert lib.mnb_sample(None) == mnb.MNB_ERR_INVALID_ARG
+    assert lib.mnb_sample(ctypes.byref(_sample(B=0))) == mnb.MNB_OK
+    assert lib.mnb_sample(ctypes.byref(_sample(V=(1 << 24) + 1, row_stride=1 << 25))) == mnb.MNB_ERR_UNSUPPORTED
