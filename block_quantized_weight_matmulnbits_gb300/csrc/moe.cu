@@ -13,8 +13,8 @@ namespace {
 
 constexpr int kRouteWarps = 4;
 
-// A warp a token.  Written twice where a caller wants the result and a kernel reads the workspace's.
-__global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(Route r, int64_t T, int32_t* ids, float* w, int32_t* ids2, float* w2) {
+// mnb_moe_route: a warp a token.
+__global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(Route r, int64_t T, int32_t* ids, float* w) {
     const int64_t t = (int64_t)blockIdx.x * kRouteWarps + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     griddep_wait();
@@ -27,14 +27,79 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(Route r, int64_
         const int64_t at = t * r.S + lane;
         if (ids) ids[at] = e;
         if (w) w[at] = v;
-        if (ids2) ids2[at] = e;
-        if (w2) w2[at] = v;
     }
 }
 
-cudaError_t launch_route(const Route& r, int64_t T, int32_t* ids, float* w, int32_t* ids2, float* w2, cudaStream_t s) {
-    return dec::launch_pdl(route_kernel, dim3((unsigned)((T + kRouteWarps - 1) / kRouteWarps)), dim3(32 * kRouteWarps), 0, s, 1, r, T,
-                           ids, w, ids2, w2);
+// Routing of mnb_moe's tokens and its lists, in one CTA: a warp a token, then one warp counts the pairs of each expert,
+// 32 pairs at a time (equal ones find each other by a match), and cuts them into segments.
+constexpr int kPlanThreads = 512;
+
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(Route r, Plan* g, int32_t* ids_out, float* w_out) {
+    __shared__ int ids[kMaxPairs], place[kMaxPairs], cnt[kMaxExperts], first[kMaxExperts];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int S = r.S, P = r.T * S, E = r.E;
+    for (int i = tid; i < E; i += kPlanThreads) cnt[i] = 0;
+    griddep_wait();
+    griddep_launch_dependents();
+    for (int t = warp; t < r.T; t += kPlanThreads / 32) {
+        int e;
+        float w;
+        route_any(r, t, e, w);
+        if (lane < S) {
+            const int at = t * S + lane;
+            ids[at] = e;
+            g->w[at] = w;
+            if (ids_out) ids_out[at] = e;
+            if (w_out) w_out[at] = w;
+        }
+    }
+    __syncthreads();
+    if (warp == 0) {
+        for (int i0 = 0; i0 < P; i0 += 32) {
+            const int i = i0 + lane;
+            const int e = i < P ? ids[i] : -1 - lane;
+            const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
+            const int rank = __popc(same & ((1u << lane) - 1u));
+            const int before = i < P ? cnt[e] : 0;
+            __syncwarp();
+            if (i < P) {
+                place[i] = before + rank;  // among its expert's
+                if (rank == 0) cnt[e] = before + __popc(same);
+            }
+            __syncwarp();
+        }
+    }
+    __syncthreads();
+    if (warp < 2) {
+        PlanSegs& to = warp == 0 ? g->by8 : g->by4;
+        const int cap = warp == 0 ? 8 : 4;
+        int pairs = 0, segs = 0, most = 0;
+        for (int e0 = 0; e0 < E; e0 += 32) {
+            const int e = e0 + lane, c = e < E ? cnt[e] : 0, n = (c + cap - 1) / cap;
+            int fs = c, ss = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int a = __shfl_up_sync(0xFFFFFFFFu, fs, o), b = __shfl_up_sync(0xFFFFFFFFu, ss, o);
+                if (lane >= o) {
+                    fs += a;
+                    ss += b;
+                }
+            }
+            const int f = pairs + fs - c, s = segs + ss - n;
+            for (int k = 0; k < n; ++k) to.seg[s + k] = Seg{e, f + k * cap, min(cap, c - k * cap)};
+            if (warp == 0 && e < E) first[e] = f;
+            most = max(most, min(cap, c));
+            pairs += __shfl_sync(0xFFFFFFFFu, fs, 31);
+            segs += __shfl_sync(0xFFFFFFFFu, ss, 31);
+        }
+        most = __reduce_max_sync(0xFFFFFFFFu, most);
+        if (lane == 0) {
+            to.n = segs;
+            to.most = most;
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < P; i += kPlanThreads) g->sorted[first[ids[i]] + place[i]] = i;
 }
 
 mnb_status check_route(const mnb_moe_route_args* a) {
@@ -91,16 +156,6 @@ Weights make_weights(const mnb_expert_weights* w) {
     return q;
 }
 
-// The loads of an item's scales and zero points as one access, where a row's blocks are those of the loop, whole items
-// and aligned (blocks of 32 or 16).
-void set_vectors(Params& p, int bits) {
-    const int blocks = p.bs_shift == 4 ? 8 : 4;
-    const bool runs = p.bs_shift <= 5 && p.a.KB % blocks == 0;
-    auto all = [&](const void* a, const void* b, int n) { return dec::aligned_to(a, n) && dec::aligned_to(b, n); };
-    p.s_vec = runs && p.sdt != kF32 && all(p.a.scales, p.b.scales, 2 * blocks);
-    p.z_vec = runs && all(p.a.zp, p.b.zp, blocks * bits / 8);
-}
-
 size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
 
 }  // namespace
@@ -118,7 +173,9 @@ mnb_status mnb_moe_route(const mnb_moe_route_args* a) {
     if (inject_launch_failure()) return MNB_ERR_CUDA;
     const cudaStream_t s = (cudaStream_t)a->stream;
     ProfileScope prof("mnb_moe_route", s);
-    const cudaError_t e = moe::launch_route(moe::make_route(a), a->T, a->ids, a->weights, nullptr, nullptr, s);
+    const unsigned grid = (unsigned)((a->T + moe::kRouteWarps - 1) / moe::kRouteWarps);
+    const cudaError_t e = dec::launch_pdl(moe::route_kernel, dim3(grid), dim3(32 * moe::kRouteWarps), 0, s, 1, moe::make_route(a), a->T,
+                                          a->ids, a->weights);
     if (e == cudaSuccess) prof.done("moe_route");
     return dec::status_of(e);
 }
@@ -128,7 +185,7 @@ size_t mnb_moe_workspace_size(int64_t T, int64_t S, int64_t E, int64_t hidden, i
         hidden < 1 || hidden >= (int64_t(1) << 30) || inner < 1 || inner >= (int64_t(1) << 30))
         return 0;
     const size_t pairs = (size_t)(T * S);
-    return 2 * moe::round256(pairs * 4) + moe::round256(pairs * 4 * (((size_t)inner + 15) / 16 * 16));
+    return moe::round256(sizeof(moe::Plan)) + moe::round256(pairs * 4 * (((size_t)inner + 15) / 16 * 16));
 }
 
 mnb_status mnb_moe(const mnb_moe_args* a, const mnb_moe_route_args* route) {
@@ -158,11 +215,9 @@ mnb_status mnb_moe(const mnb_moe_args* a, const mnb_moe_route_args* route) {
     p.status = device_status_word();
     if (!p.status) return dec::status_of(cudaErrorUnknown);
     p.r = moe::make_route(route);
-    const int P = p.r.T * p.r.S;
     uint8_t* ws = static_cast<uint8_t*>(a->workspace);
-    int32_t* ids = reinterpret_cast<int32_t*>(ws);
-    float* w = reinterpret_cast<float*>(ws + moe::round256((size_t)P * 4));
-    p.h = reinterpret_cast<uint16_t*>(ws + 2 * moe::round256((size_t)P * 4));
+    moe::Plan* plan = reinterpret_cast<moe::Plan*>(ws);
+    p.h = reinterpret_cast<uint16_t*>(ws + moe::round256(sizeof(moe::Plan)));
     p.inner = (g->N + 15) / 16 * 16;
     p.x = a->x;
     p.x_stride = p.r.T > 1 ? a->x_stride : g->K;
@@ -177,17 +232,13 @@ mnb_status mnb_moe(const mnb_moe_args* a, const mnb_moe_route_args* route) {
     p.a = moe::make_weights(g);
     p.b = moe::make_weights(u);
     q.a = q.b = moe::make_weights(d);
-    moe::set_vectors(p, g->bits);
-    moe::set_vectors(q, g->bits);
     if (inject_launch_failure()) return MNB_ERR_CUDA;
     const cudaStream_t s = (cudaStream_t)a->stream;
     ProfileScope prof("mnb_moe", s);
     cudaError_t e = cudaSuccess;
-    if (p.r.T > moe::kRouteInside) {
-        // every CTA routing for itself takes as long as its warps have tokens: from two on a launch of its own is shorter
-        e = moe::launch_route(p.r, p.r.T, ids, w, route->ids, route->weights, s);
-        p.ids_in = q.ids_in = ids;
-        p.w_in = q.w_in = w;
+    if ((int64_t)p.r.T * p.r.E * p.r.E > moe::kInsideScores || p.r.T * p.r.S > moe::kInsidePairs) {
+        e = dec::launch_pdl(moe::plan_kernel, dim3(1), dim3(moe::kPlanThreads), 0, s, 1, p.r, plan, route->ids, route->weights);
+        p.plan = q.plan = plan;
     } else {
         p.ids_out = route->ids;
         p.w_out = route->weights;

@@ -7,30 +7,32 @@
 // their bytes bound both.  What a warp does for 512 bytes of packed 4-bit
 // codes (a tile of 16 rows x 64 depths): 4 k-steps of an unpack (7 shifts and
 // ands, 4 exact packed subtractions of the zero point) and one m16n8k16 MMA per
-// 8 columns.
+// 8 columns, so that the issue of instructions is the next bound.
 //
-// The work unit of a warp is an item: two row tiles that multiply the same
+// The work of a warp comes in items: two row tiles that multiply the same
 // columns (gate and up of one row tile; two neighbouring row tiles of down), 128
-// depths.  Its weights go straight from global memory into registers, its
-// scales and zero points too (a lane those of one of the 32 rows; as float and
-// subtraction constant they then pass through a table of the warp in shared
-// memory), and its columns through asynchronous copies into a slot of the warp
-// in shared memory, DEPTH items ahead.  Warps wait for no other warp while they
-// stream; sharing the columns between two row tiles halves what their fragments
-// cost in shared-memory cycles, which otherwise bound the loop before the
-// weights' bytes do.
+// depths (8-bit codes: 64).  Weights and columns go through a ring of the warp in shared
+// memory by asynchronous copies, a few items ahead: a lane copies the 16 bytes
+// of a packed tile that it alone reads, and warps wait for no other warp while
+// they stream.  Two row tiles share the fragments of the columns, which halves
+// what those cost in shared-memory cycles.  Scales and zero points (a lane loads
+// those of one of the 32 rows, one item ahead) pass through a table of the warp
+// as float and subtraction constant.  One copy of the loop, indexed by the
+// ring's slot, keeps the code in the instruction cache (with the weights in
+// registers, a copy a buffer, a quarter of the stalls were instruction fetches).
 //
 // The columns of an item are the tokens of its expert: its pairs (t, s), in
-// ascending order, at most 8 NG of them a segment (down: 4 NG, each as a high
-// and a low bf16 part, so that h keeps 16 bits and no f16 can overflow; the two
-// columns are added before they leave).  An expert with more pairs has more
+// ascending order, at most 8 of them a segment (down: 4, each as a high and a
+// low bf16 part, so that h keeps 16 bits and no f16 can overflow; a lane adds
+// the two columns before they leave).  An expert with more pairs has more
 // segments, whose weights come from L2.
 //
-// gate_up: teams of 1, 2, 4 or 8 warps take row tiles; a team's warps split the
-// depths and one of them adds the partial sums, in order.  down: a cluster of
-// CTAs owns 32 rows of y and its warps split the depths of all experts, each an
-// equal range; partial sums of tokens are added over the warps, then over the
-// cluster through distributed shared memory, in order.  So results repeat.
+// gate_up: a CTA takes consecutive row tiles and its warps equal runs of their
+// items.  A row tile inside a warp's run is finished there; the others' partial
+// sums are added in order after the runs.  down: a cluster of CTAs owns 32 rows
+// of y and its warps equal runs of the items of all experts; partial sums of
+// tokens are added over the warps, then over the cluster through distributed
+// shared memory, in order.  So results repeat.
 //
 // Both are launched as programmatic dependents.  down begins while gate_up
 // runs: it needs the experts only (from the logits, or from a routing kernel
@@ -50,106 +52,111 @@ using gmma::Unpack;
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kDepth = 128;                // depths of an item
-constexpr int kSlotRow = kDepth * 2 + 16;  // bytes of a column in a slot: padded, ldmatrix rows meet no bank twice
-
-struct Seg {
-    int e, first, cnt;  // expert, place of its first pair in the sorted list, pairs
-};
+constexpr int kRingBytes = 9216;  // of a warp: two CTAs fit an SM; two to four slots
 
 // Shared memory after the streaming buffers: the routing of the call.
 struct Lists {
-    int* nseg;
-    float* w;      // weight of pair p
-    int* ids;      // expert of pair p
-    int* sorted;   // pairs by expert, ascending
+    int *nseg, *most;  // segments; pairs of the largest
+    float* w;          // weight of pair p
+    int* sorted;       // pairs by expert, ascending
+    int* token;        // their tokens
     Seg* seg;
-    int* cnt;      // pairs of each expert, then its first place
+    int* ids;          // expert of pair p; whether it begins a segment (scratch of make_lists)
+    int* head;
     __device__ __forceinline__ Lists(uint8_t* at, int P) {
         nseg = reinterpret_cast<int*>(at);
+        most = nseg + 1;
         w = reinterpret_cast<float*>(at + 16);
-        ids = reinterpret_cast<int*>(w + P);
-        sorted = ids + P;
-        seg = reinterpret_cast<Seg*>(sorted + P);
-        cnt = reinterpret_cast<int*>(seg + P);
+        sorted = reinterpret_cast<int*>(w + P);
+        token = sorted + P;
+        seg = reinterpret_cast<Seg*>(token + P);
+        ids = reinterpret_cast<int*>(seg + P);
+        head = ids + P;
     }
-    static size_t bytes(int P, int E) { return 16 + (size_t)P * 24 + (size_t)E * 4; }
+    static size_t bytes(int P) { return 16 + (size_t)P * 32; }
 };
 
-// Routes (or reads the routing) and sorts the pairs by expert, in segments of at most `cap` pairs.  All threads call it.
-__device__ __forceinline__ void make_lists(const Params& p, const Lists& L, int cap) {
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int S = p.r.S, P = p.r.T * S, E = p.r.E;
-    for (int i = tid; i < E; i += kThreads) L.cnt[i] = 0;
-    if (p.ids_in) {
+// The lists of a call, with segments of at most `cap` pairs: from a routing kernel's, or (few tokens and experts) from the
+// logits.  All threads call it.  scratch: shared memory for T * E scores and T * E keys.
+__device__ __forceinline__ void make_lists(const Params& p, const Lists& L, int cap, uint32_t* scratch) {
+    const int tid = threadIdx.x;
+    const int S = p.r.S, T = p.r.T, P = T * S, E = p.r.E;
+    if (p.plan) {
+        const Plan& g = *p.plan;
+        const PlanSegs& from = cap == 8 ? g.by8 : g.by4;
+        const int n = from.n;
         for (int i = tid; i < P; i += kThreads) {
-            L.ids[i] = p.ids_in[i];
-            L.w[i] = p.w_in[i];
+            L.w[i] = g.w[i];
+            L.sorted[i] = g.sorted[i];
+            L.token[i] = g.sorted[i] / S;
         }
-    } else if (warp < p.r.T) {
-        int e;
-        float w;
-        route_any(p.r, warp, e, w);
-        if (lane < S) {
-            L.ids[warp * S + lane] = e;
-            L.w[warp * S + lane] = w;
-            if (p.ids_out && blockIdx.x == 0) p.ids_out[warp * S + lane] = e;
-            if (p.w_out && blockIdx.x == 0) p.w_out[warp * S + lane] = w;
+        for (int i = tid; i < n; i += kThreads) L.seg[i] = from.seg[i];
+        if (tid == 0) {
+            *L.nseg = n;
+            *L.most = from.most;
         }
+        __syncthreads();
+        return;
+    }
+    // The rank of a score among its token's is its place: a thread a score, no rounds that wait for each other.
+    float* score = reinterpret_cast<float*>(scratch + T * E);
+    for (int i = tid; i < T * E; i += kThreads) {
+        const int t = i / E, e = i - t * E;
+        const float l = load_f32(p.r.logits, t * p.r.stride + e, p.r.dt);
+        score[i] = l;
+        scratch[i] = route_key(p.r, l, e);
+    }
+    if (tid == 0) *L.most = 0;
+    __syncthreads();
+    for (int i = tid; i < T * E; i += kThreads) {
+        const int t = i / E, e = i - t * E;
+        const uint32_t mine = scratch[i], *all = scratch + t * E;
+        int rank = 0;
+#pragma unroll 8
+        for (int f = 0; f < E; ++f) rank += all[f] > mine || (all[f] == mine && f < e) ? 1 : 0;
+        if (rank < S) L.ids[t * S + rank] = e;
     }
     __syncthreads();
-    if (warp == 0) {
-        // rank of each pair among its expert's: a match over 32 pairs, after those of the chunks before
-        for (int i0 = 0; i0 < P; i0 += 32) {
-            const int i = i0 + lane;
-            const int e = i < P ? L.ids[i] : -1 - lane;
-            const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
-            const int rank = __popc(same & ((1u << lane) - 1u));
-            const int before = i < P ? L.cnt[e] : 0;
-            __syncwarp();
-            if (i < P) {
-                L.sorted[i] = before + rank;  // for now
-                if (rank == 0) L.cnt[e] = before + __popc(same);
-            }
-            __syncwarp();
+    int e = 0, less = 0, before = 0, same = 0;
+    bool head = false;
+    if (tid < P) {
+        // a thread a pair: its weight, and the pairs before it in the order of (expert, pair)
+        const int t = tid / S;
+        e = L.ids[tid];
+        const float w = route_weight(p.r, score + t * E, L.ids + t * S, tid - t * S);
+        L.w[tid] = w;
+        if (blockIdx.x == 0 && p.ids_out) p.ids_out[tid] = e;
+        if (blockIdx.x == 0 && p.w_out) p.w_out[tid] = w;
+#pragma unroll 8
+        for (int q = 0; q < P; ++q) {
+            const int f = L.ids[q];
+            less += f < e ? 1 : 0;
+            same += f == e ? 1 : 0;
+            before += f == e && q < tid ? 1 : 0;
         }
-        int first = 0, segs = 0;
-        for (int e0 = 0; e0 < E; e0 += 32) {
-            const int e = e0 + lane, c = e < E ? L.cnt[e] : 0, n = (c + cap - 1) / cap;
-            int fs = c, ss = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int a = __shfl_up_sync(0xFFFFFFFFu, fs, o), b = __shfl_up_sync(0xFFFFFFFFu, ss, o);
-                if (lane >= o) {
-                    fs += a;
-                    ss += b;
-                }
-            }
-            const int f = first + fs - c, s = segs + ss - n;
-            for (int k = 0; k < n; ++k) L.seg[s + k] = Seg{e, f + k * cap, min(cap, c - k * cap)};
-            if (e < E) L.cnt[e] = f;
-            first += __shfl_sync(0xFFFFFFFFu, fs, 31);
-            segs += __shfl_sync(0xFFFFFFFFu, ss, 31);
-        }
-        if (lane == 0) *L.nseg = segs;
+        head = before % cap == 0;
+        L.sorted[less + before] = tid;
+        L.token[less + before] = t;
+        L.head[tid] = head;
     }
-    __syncthreads();
-    int rank[kMaxPairs / kThreads];
-#pragma unroll
-    for (int k = 0; k < kMaxPairs / kThreads; ++k) {
-        const int i = tid + k * kThreads;
-        rank[k] = i < P ? L.sorted[i] + L.cnt[L.ids[i]] : 0;
+    const int heads = __syncthreads_count(head);
+    if (head) {
+        int at = 0;
+#pragma unroll 8
+        for (int q = 0; q < P; ++q) at += L.head[q] && (L.ids[q] < e || (L.ids[q] == e && q < tid)) ? 1 : 0;
+        const int cnt = min(cap, same - before);
+        L.seg[at] = Seg{e, less + before, cnt};
+        atomicMax(L.most, cnt);
     }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kMaxPairs / kThreads; ++k) {
-        const int i = tid + k * kThreads;
-        if (i < P) L.sorted[rank[k]] = i;
-    }
+    if (tid == 0) *L.nseg = heads;
     __syncthreads();
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// `bytes` of 16, the rest zeros (columns: through L1, where a CTA's warps meet)
+__device__ __forceinline__ void cp_async16_part(uint32_t dst, const void* src, int bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -157,167 +164,241 @@ template <int N>
 __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+// The oldest of `depth` groups is complete.
+__device__ __forceinline__ void cp_wait_oldest(int depth) {
+    if (depth == 2) cp_wait<1>();
+    else if (depth == 3) cp_wait<2>();
+    else cp_wait<3>();
+}
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t at) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(at)
                  : "memory");
 }
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
 
-// SUB: k-steps that one scale covers in the loop (2: blocks of 32 depths and more; 1: blocks of 16).
-template <int BITS, bool BF, int SUB, int NG>
-struct Item {
-    static constexpr int TPI = BITS / 2;   // packed tiles of 128 depths
-    static constexpr int SPT = 16 / BITS;  // k-steps of a packed tile
-    static constexpr int NSUB = 8 / SUB;   // scales of a row
-    // items in flight: what 128 registers hold (8-bit weights take 32 a buffer)
-    static constexpr int DEPTH = BITS == 8 || SUB == 1 || NG == 2 ? 2 : 3;
-    static constexpr int kSlotBytes = 8 * NG * kSlotRow;
-    static constexpr int kTabBytes = 2 * NSUB * 16 * 8;
-    using U = Unpack<BITS, BF>;
-
-    uint4 w[2][TPI];
-    uint32_t s[NSUB], z[NSUB];  // raw scales and zero points of the lane's row
-
-    // w0, w1: the lane's 16 bytes of the row tiles' first packed tile; srow, zrow: the lane's row (zrow null: none)
-    __device__ __forceinline__ void load(const Params& p, const uint8_t* w0, const uint8_t* w1, const uint8_t* srow,
-                                         const uint8_t* zrow, int c) {
-        const int kt = (int)p.a.k_tiles;
-#pragma unroll
-        for (int j = 0; j < TPI; ++j) {
-            // past the last tile the columns are zero: any codes do
-            const int64_t at = (int64_t)min(c * TPI + j, kt - 1) * kTileBytes;
-            w[0][j] = ldg_stream(w0 + at);
-            w[1][j] = ldg_stream(w1 + at);
-        }
-        if (p.s_vec) {
-            if constexpr (SUB == 2) {
-                const uint2 v = __ldg(reinterpret_cast<const uint2*>(srow) + c);
-                s[0] = v.x;
-                s[1] = v.y;
-            } else {
-                const uint4 v = __ldg(reinterpret_cast<const uint4*>(srow) + c);
-                s[0] = v.x;
-                s[1] = v.y;
-                s[2] = v.z;
-                s[3] = v.w;
-            }
-        } else {
-            const int every = max(1 << p.bs_shift >> (SUB == 2 ? 5 : 4), 1) - 1;
-#pragma unroll
-            for (int j = 0; j < NSUB; ++j) {
-                const int b = (c * kDepth + j * 16 * SUB) >> p.bs_shift;
-                if (j == 0 || (j & every) == 0) {
-                    s[j] = 0u;  // depths past the last block: scale 0
-                    if (b < p.a.KB)
-                        s[j] = p.sdt == kF32 ? __ldg(reinterpret_cast<const uint32_t*>(srow) + b)
-                                             : (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(srow) + b);
-                }
-            }
-        }
-        if (zrow != nullptr) {
-            if (p.z_vec) {
-                constexpr int ZB = NSUB * BITS / 8;  // bytes of an item
-                if constexpr (ZB == 1) z[0] = __ldg(zrow + c);
-                else if constexpr (ZB == 2) z[0] = __ldg(reinterpret_cast<const uint16_t*>(zrow) + c);
-                else if constexpr (ZB == 4) z[0] = __ldg(reinterpret_cast<const uint32_t*>(zrow) + c);
-                else {
-                    const uint2 v = __ldg(reinterpret_cast<const uint2*>(zrow) + c);
-                    z[0] = v.x;
-                    z[1] = v.y;
-                }
-            } else {
-                const int every = max(1 << p.bs_shift >> (SUB == 2 ? 5 : 4), 1) - 1;
-#pragma unroll
-                for (int j = 0; j < NSUB; ++j) {
-                    const int b = min((c * kDepth + j * 16 * SUB) >> p.bs_shift, p.a.KB - 1);
-                    if (j == 0 || (j & every) == 0) z[j] = (uint32_t)__ldg(zrow + ((b * BITS) >> 3)) >> ((b * BITS) & 7);
-                }
-            }
-        }
+// Read-only loads of scales and zero points: a miss brings 256 bytes of the row into L2, those of the items to come.
+template <class T>
+__device__ __forceinline__ T ldg_ahead(const T* p) {
+    T v;
+    if constexpr (sizeof(T) == 16) {
+        asm volatile("ld.global.nc.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    } else if constexpr (sizeof(T) == 8) {
+        asm volatile("ld.global.nc.L2::256B.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    } else if constexpr (sizeof(T) == 4) {
+        asm volatile("ld.global.nc.L2::256B.u32 %0, [%1];" : "=r"(v) : "l"(p));
+    } else if constexpr (sizeof(T) == 2) {
+        asm volatile("ld.global.nc.L2::256B.u16 %0, [%1];" : "=h"(v) : "l"(p));
+    } else {
+        uint32_t u;
+        asm volatile("ld.global.nc.L2::256B.u8 %0, [%1];" : "=r"(u) : "l"(p));
+        v = (T)u;
     }
-
-    static __device__ __forceinline__ float widen(uint32_t raw, int dt) {
-        if (dt == kF32) return __uint_as_float(raw);
-        return dt == kBF16 ? __uint_as_float(raw << 16) : __half2float(__ushort_as_half((unsigned short)raw));
-    }
-
-    // The lane's row into the warp's table: entry [row tile][j][row] = (scale, subtraction constant).
-    __device__ __forceinline__ void table(const Params& p, uint2* tab, bool has_z) const {
-        const int lane = threadIdx.x & 31;
-        uint2* dst = tab + (lane >> 4) * NSUB * 16 + (lane & 15);
-        const int every = max(1 << p.bs_shift >> (SUB == 2 ? 5 : 4), 1) - 1;
-        uint32_t sr = 0, zr = 0;
-#pragma unroll
-        for (int j = 0; j < NSUB; ++j) {
-            const bool own = j == 0 || (j & every) == 0;
-            if (p.s_vec) sr = (j & 1) ? s[j >> 1] >> 16 : s[j >> 1] & 0xFFFFu;
-            else if (own) sr = s[j];
-            if (p.z_vec) {
-                constexpr int per = 32 / BITS;
-                zr = z[j / per] >> ((j % per) * BITS);
-            } else if (own) {
-                zr = z[j];
-            }
-            const uint32_t zp = has_z ? zr & (uint32_t)((1 << BITS) - 1) : 1u << (BITS - 1);
-            dst[j * 16] = make_uint2(__float_as_uint(widen(sr, p.sdt)), U::zconst(zp));
-        }
-    }
-
-    // y[m][ng] += row tile m times column group ng.  slot: the warp's columns; tab: its table.
-    __device__ __forceinline__ void compute(uint32_t slot, const uint2* tab, float (&y)[2][NG][4]) const {
-        const int lane = threadIdx.x & 31, g = lane >> 2;
-        const float zero4[4] = {0.f, 0.f, 0.f, 0.f};
-        const uint32_t at = slot + (uint32_t)((lane & 7) * kSlotRow + (lane >> 3) * 16);
-        float acc[2][NG][4];
-        uint32_t x[NG][4];
-        uint2 lo[2], hi[2];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            if (k % SUB == 0) {
-#pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    lo[m] = tab[(m * NSUB + k / SUB) * 16 + g];
-                    hi[m] = tab[(m * NSUB + k / SUB) * 16 + g + 8];
-                }
-            }
-            if ((k & 1) == 0) {
-#pragma unroll
-                for (int n = 0; n < NG; ++n) ldmatrix4(x[n], at + (uint32_t)(n * 8 * kSlotRow + k * 32));
-            }
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                uint32_t a[4];
-                U::kstep(w[m][k / SPT], k % SPT, lo[m].y, hi[m].y, a);
-#pragma unroll
-                for (int n = 0; n < NG; ++n) {
-                    const uint32_t b0 = x[n][2 * (k & 1)], b1 = x[n][2 * (k & 1) + 1];
-                    if (k % SUB == 0) mma16816<BF>(acc[m][n], a, b0, b1, zero4);
-                    else mma16816<BF>(acc[m][n], a, b0, b1, acc[m][n]);
-                    if (k % SUB == SUB - 1) {
-                        const float sl = __uint_as_float(lo[m].x), sh = __uint_as_float(hi[m].x);
-                        y[m][n][0] = fmaf(sl, acc[m][n][0], y[m][n][0]);
-                        y[m][n][1] = fmaf(sl, acc[m][n][1], y[m][n][1]);
-                        y[m][n][2] = fmaf(sh, acc[m][n][2], y[m][n][2]);
-                        y[m][n][3] = fmaf(sh, acc[m][n][3], y[m][n][3]);
-                    }
-                }
-            }
-        }
-    }
-};
+    return v;
+}
 
 // Addresses of two row tiles of an expert for one lane (lanes 0-15: the first tile's rows, 16-31 the second's).
 struct RowTiles {
-    const uint8_t *w0, *w1, *srow, *zrow;
-    __device__ __forceinline__ void set(const Params& p, int e, int64_t rt0, int64_t rt1) {
+    const uint8_t *w0, *w1;
+    __device__ __forceinline__ void set(const Params& p, int e, int rt0, int rt1) {
+        const int lane = threadIdx.x & 31;
+        const int64_t bytes = p.a.k_tiles * kTileBytes;
+        w0 = p.a.packed + (size_t)e * p.a.expert_bytes + kHeaderBytes + rt0 * bytes + lane * 16;
+        w1 = p.b.packed + (size_t)e * p.b.expert_bytes + kHeaderBytes + rt1 * bytes + lane * 16;
+    }
+};
+struct RowScales {
+    const uint8_t *s, *z;  // z null: no zero points
+    __device__ __forceinline__ void set(const Params& p, int e, int rt0, int rt1) {
         const int lane = threadIdx.x & 31;
         const Weights& q = lane < 16 ? p.a : p.b;
-        const int n = min((int)(lane < 16 ? rt0 : rt1) * 16 + (lane & 15), q.N - 1);
-        w0 = p.a.packed + (size_t)e * p.a.expert_bytes + kHeaderBytes + (size_t)rt0 * p.a.k_tiles * kTileBytes + lane * 16;
-        w1 = p.b.packed + (size_t)e * p.b.expert_bytes + kHeaderBytes + (size_t)rt1 * p.b.k_tiles * kTileBytes + lane * 16;
-        srow = q.scales + (size_t)e * q.scale_bytes + (size_t)n * q.KB * (p.sdt == kF32 ? 4 : 2);
-        zrow = q.zp ? q.zp + (size_t)e * q.zp_bytes + (size_t)n * q.zp_row : nullptr;
+        const int n = min((lane < 16 ? rt0 : rt1) * 16 + (lane & 15), q.N - 1);
+        s = q.scales + (size_t)e * q.scale_bytes + (size_t)n * q.KB * (p.sdt == kF32 ? 4 : 2);
+        z = q.zp ? q.zp + (size_t)e * q.zp_bytes + (size_t)n * q.zp_row : nullptr;
+    }
+};
+
+// BSL: log2 of the block's k-steps, at most an item's (a longer block spans items).
+template <int BITS, bool BF, int BSL>
+struct Item {
+    static constexpr int KST = BITS == 8 ? 4 : 8;                // k-steps
+    static constexpr int kDepth = 16 * KST;
+    static constexpr int SPT = 16 / BITS;                        // k-steps of a packed tile
+    static constexpr int TPI = KST / SPT;                        // packed tiles of a row tile
+    static constexpr int SUB = (1 << BSL) < KST ? 1 << BSL : KST;  // k-steps of a scale
+    static constexpr int NB = KST / SUB;                         // scales of a row
+    static constexpr int PC = 2 * KST;                           // 16-byte pieces of a column
+    static constexpr int kColBytes = 16 * PC;
+    static constexpr int kWBytes = 2 * TPI * kTileBytes;
+    static constexpr int kTabBytes = 2 * NB * 16 * 8;
+    static_assert(NB * BITS <= 32, "an item's zero points of a row are one word");
+    using U = Unpack<BITS, BF>;
+    // Bytes of a slot: the weights, and as many columns as a segment of the call has.
+    static __device__ __forceinline__ int slot_bytes(int cols) { return kWBytes + cols * kColBytes; }
+    static_assert(2 * (kWBytes + 8 * kColBytes) <= kRingBytes, "two slots of 8 columns");
+
+    // Copies of the item's weights into a slot (w0, w1: the lane's 16 bytes of its first packed tiles; `tiles` of them
+    // are there).
+    static __device__ __forceinline__ void weights(const uint8_t* w0, const uint8_t* w1, int tiles, uint32_t slot) {
+        const uint32_t at = slot + (threadIdx.x & 31) * 16;
+        if (tiles >= TPI) {
+#pragma unroll
+            for (int j = 0; j < TPI; ++j) {
+                cp_async16(at + j * kTileBytes, w0 + j * kTileBytes);
+                cp_async16(at + (TPI + j) * kTileBytes, w1 + j * kTileBytes);
+            }
+        } else {  // past the last tile the columns are zero: any codes do
+#pragma unroll
+            for (int j = 0; j < TPI; ++j) {
+                cp_async16(at + j * kTileBytes, w0 + min(j, tiles - 1) * kTileBytes);
+                cp_async16(at + (TPI + j) * kTileBytes, w1 + min(j, tiles - 1) * kTileBytes);
+            }
+        }
+    }
+
+    // Raw scales (two a word, f32: one) and zero points of the lane's row.
+    struct Raw {
+        uint32_t s[NB], z;
+    };
+    static __device__ __forceinline__ void raw(const Params& p, const RowScales& r, int c, Raw& v) {
+        if (p.s_vec) {
+            if constexpr (NB == 8) {
+                const uint4 a = ldg_ahead(reinterpret_cast<const uint4*>(r.s) + c);
+                v.s[0] = a.x;
+                v.s[1] = a.y;
+                v.s[2] = a.z;
+                v.s[3] = a.w;
+            } else if constexpr (NB == 4) {
+                const uint2 a = ldg_ahead(reinterpret_cast<const uint2*>(r.s) + c);
+                v.s[0] = a.x;
+                v.s[1] = a.y;
+            } else if constexpr (NB == 2) {
+                v.s[0] = ldg_ahead(reinterpret_cast<const uint32_t*>(r.s) + c);
+            } else {
+                v.s[0] = ldg_ahead(reinterpret_cast<const uint16_t*>(r.s) + ((c * kDepth) >> p.bs_shift));
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                const int b = (c * kDepth + j * 16 * SUB) >> p.bs_shift;
+                uint32_t u = 0u;  // depths past the last block: scale 0
+                if (b < p.a.KB) u = p.sdt == kF32 ? ldg_ahead(reinterpret_cast<const uint32_t*>(r.s) + b) : ldg_ahead(reinterpret_cast<const uint16_t*>(r.s) + b);
+                if (p.sdt == kF32) v.s[j] = u;
+                else v.s[j >> 1] = (j & 1) ? v.s[j >> 1] | (u << 16) : u;
+            }
+        }
+        constexpr int ZBITS = NB * BITS;
+        if (r.z == nullptr) {
+            v.z = BITS == 2 ? 0xAAAAAAAAu : BITS == 4 ? 0x88888888u : 0x80808080u;  // 2^(bits - 1) in every field
+        } else if (ZBITS >= 8 && p.z_vec) {
+            if constexpr (ZBITS == 32) v.z = ldg_ahead(reinterpret_cast<const uint32_t*>(r.z) + c);
+            else if constexpr (ZBITS == 16) v.z = ldg_ahead(reinterpret_cast<const uint16_t*>(r.z) + c);
+            else v.z = ldg_ahead(r.z + c);
+        } else {
+            v.z = 0u;
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                const int b = min((c * kDepth + j * 16 * SUB) >> p.bs_shift, p.a.KB - 1) * BITS;
+                v.z |= (((uint32_t)ldg_ahead(r.z + (b >> 3)) >> (b & 7)) & (uint32_t)((1 << BITS) - 1)) << (j * BITS);
+            }
+        }
+    }
+
+    // The lane's row into the warp's table: entry [row tile][j][row] = (scale, subtraction constant).
+    static __device__ __forceinline__ void table(int sdt, const Raw& v, uint2* tab) {
+        const int lane = threadIdx.x & 31;
+        uint2* dst = tab + (lane >> 4) * NB * 16 + (lane & 15);
+        auto put = [&](int j, float s) {
+            const uint32_t z = (v.z >> (j * BITS)) & (uint32_t)((1 << BITS) - 1);
+            // U::zconst(z); in 16-bit lanes as one multiply-add
+            const uint32_t c = BITS == 8 && BF ? U::zconst(z) : z * 0x00010001u + U::kMagic16x2;
+            dst[j * 16] = make_uint2(__float_as_uint(s), c);
+        };
+        if (sdt == kF16) {
+#pragma unroll
+            for (int j = 0; j < NB; ++j) put(j, __half2float(__ushort_as_half((unsigned short)((j & 1) ? v.s[j >> 1] >> 16 : v.s[j >> 1]))));
+        } else if (sdt == kBF16) {
+#pragma unroll
+            for (int j = 0; j < NB; ++j) put(j, __uint_as_float((j & 1) ? v.s[j >> 1] & 0xFFFF0000u : v.s[j >> 1] << 16));
+        } else {
+#pragma unroll
+            for (int j = 0; j < NB; ++j) put(j, __uint_as_float(v.s[j]));
+        }
+    }
+
+    // Where piece `piece` of column `col` lies in a slot: pieces are permuted so that ldmatrix rows meet no bank twice.
+    static __device__ __forceinline__ uint32_t piece_at(int col, int piece) {
+        return (uint32_t)(kWBytes + col * kColBytes + ((piece ^ (col & 7)) << 4));
+    }
+
+    // y[m] += row tile m times the columns.  (Columns past the segment's hold anything: their sums are not used.)
+    static __device__ __forceinline__ void compute(uint32_t slot, const uint2* tab, float (&y)[2][4]) {
+        constexpr int KG = BITS == 2 ? 8 : 4;  // k-steps of a turn: with all 8 unrolled the loads of a whole item come first and spill
+        constexpr int TPG = KG / SPT;
+        const int lane = threadIdx.x & 31;
+        const float zero4[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t cols = slot + kWBytes + (lane & 7) * kColBytes, swz = (uint32_t)((lane >> 3) ^ (lane & 7)) << 4;
+        uint32_t mine = slot + lane * 16;
+        const uint2* row = tab + (lane >> 2);
+        float acc[2][4];
+        uint2 lo[2], hi[2];
+        if constexpr (SUB > KG) {
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                lo[m] = row[m * NB * 16];
+                hi[m] = row[m * NB * 16 + 8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[m][j] = 0.f;
+            }
+        }
+#pragma unroll 1
+        for (int k0 = 0; k0 < KST; k0 += KG) {
+            uint32_t x[4];
+            uint4 w[2];
+#pragma unroll
+            for (int k = 0; k < KG; ++k) {
+                if (k % SPT == 0) {
+                    w[0] = lds16(mine + (k / SPT) * kTileBytes);
+                    w[1] = lds16(mine + (TPI + k / SPT) * kTileBytes);
+                }
+                if (SUB <= KG && k % SUB == 0) {
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        lo[m] = row[(m * NB + k / SUB) * 16];
+                        hi[m] = row[(m * NB + k / SUB) * 16 + 8];
+                    }
+                }
+                if ((k & 1) == 0) ldmatrix4(x, cols + (swz ^ (uint32_t)(k * 32)));
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    uint32_t a[4];
+                    U::kstep(w[m], k % SPT, lo[m].y, hi[m].y, a);
+                    const uint32_t b0 = x[2 * (k & 1)], b1 = x[2 * (k & 1) + 1];
+                    if (SUB <= KG && k % SUB == 0) mma16816<BF>(acc[m], a, b0, b1, zero4);
+                    else mma16816<BF>(acc[m], a, b0, b1, acc[m]);
+                    if (SUB <= KG && k % SUB == SUB - 1) scale(acc[m], lo[m].x, hi[m].x, y[m]);
+                }
+            }
+            mine += TPG * kTileBytes;
+            swz ^= KG * 32;  // the next KG / 2 groups of 4 pieces (KG = 4: the pieces' third bit)
+            if constexpr (SUB <= KG) row += KG / SUB * 16;
+        }
+        if constexpr (SUB > KG) {
+#pragma unroll
+            for (int m = 0; m < 2; ++m) scale(acc[m], lo[m].x, hi[m].x, y[m]);
+        }
+    }
+
+    static __device__ __forceinline__ void scale(const float (&acc)[4], uint32_t lo, uint32_t hi, float (&y)[4]) {
+        y[0] = fmaf(__uint_as_float(lo), acc[0], y[0]);
+        y[1] = fmaf(__uint_as_float(lo), acc[1], y[1]);
+        y[2] = fmaf(__uint_as_float(hi), acc[2], y[2]);
+        y[3] = fmaf(__uint_as_float(hi), acc[3], y[3]);
     }
 };
 
@@ -333,180 +414,197 @@ __device__ __forceinline__ float activate(float g, int act) {
     return 0.5f * g * (1.f + tanhf(u));
 }
 
-__device__ __forceinline__ void team_barrier(int team, int threads) {
-    asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(threads) : "memory");
+// Start of part i of n things in `parts` parts that differ by at most one.
+__device__ __forceinline__ int part_start(int n, int i, int parts) {
+    const int q = n / parts;
+    return q * i + min(i, n - q * parts);
 }
 
-template <int BITS, bool BF, int SUB, int NG>
+// An item of a warp's run: its number, its unit and the unit's chunk.
+struct Cursor {
+    int i, u, c;
+    __device__ __forceinline__ void next(int chunks) {
+        ++i;
+        if (++c == chunks) {
+            c = 0;
+            ++u;
+        }
+    }
+};
+
+template <int BITS, bool BF, int BSL>
 __global__ void __launch_bounds__(kThreads, 2) gate_up_kernel(const __grid_constant__ Params p) {
-    using It = Item<BITS, BF, SUB, NG>;
-    constexpr int DEPTH = It::DEPTH;
+    using It = Item<BITS, BF, BSL>;
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t slots = smem_u32(smem) + (uint32_t)(warp * DEPTH * It::kSlotBytes);
-    uint8_t* at = smem + kWarps * DEPTH * It::kSlotBytes;
+    const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * kRingBytes);
+    uint8_t* at = smem + kWarps * kRingBytes;
     uint2* tab = reinterpret_cast<uint2*>(at + warp * It::kTabBytes);
     at += kWarps * It::kTabBytes;
-    float4* red = reinterpret_cast<float4*>(at);  // [warp][2 NG][lane]
-    at += kWarps * 2 * NG * 32 * 16;
+    float4* heads = reinterpret_cast<float4*>(at);  // [warp][gate, up][lane]: sums of the row tile that a run ends but did not begin
+    at += kWarps * 2 * 32 * 16;
     const Lists L(at, p.r.T * p.r.S);
 
     griddep_wait();
     griddep_launch_dependents();
-    make_lists(p, L, 8 * NG);
+    make_lists(p, L, 8, reinterpret_cast<uint32_t*>(smem));
+    const int slot_bytes = It::slot_bytes(*L.most), depth = min(4, kRingBytes / slot_bytes);
 
-    const int KC = (p.a.K + kDepth - 1) / kDepth, NT = (int)p.a.row_tiles;
+    const int KC = (p.a.K + It::kDepth - 1) / It::kDepth, NT = (int)p.a.row_tiles;
     const int units = *L.nseg * NT;
-    // warps a row tile: the fewest items in a row for any warp, then the fewest warps
-    int wpu = 1, cost = 0x7FFFFFFF;
-    for (int w = 1; w <= kWarps && w <= KC; w *= 2) {
-        const int teams = (int)gridDim.x * (kWarps / w);
-        const int c = ((units + teams - 1) / teams) * ((KC + w - 1) / w);
-        if (c < cost) {
-            cost = c;
-            wpu = w;
-        }
-    }
-    const int team = warp / wpu, wit = warp % wpu;
-    const int stride = (int)gridDim.x * (kWarps / wpu);
+    const int u0 = part_start(units, blockIdx.x, gridDim.x), items = (part_start(units, blockIdx.x + 1, gridDim.x) - u0) * KC;
+    const int i0 = part_start(items, warp, kWarps), i1 = part_start(items, warp + 1, kWarps);
+    Cursor cur{i0, u0 + i0 / KC, i0 % KC};
+    Cursor ahead = cur, next = cur;
 
-    // a warp's items: chunks wit, wit + wpu, ... of the team's row tiles
-    struct Cursor {
-        int u, c;
-    };
-    auto advance = [&](Cursor& i) {
-        i.c += wpu;
-        if (i.c >= KC) {
-            i.c = wit;
-            i.u += stride;
-        }
-    };
-    Cursor cur{(int)blockIdx.x + team * (int)gridDim.x, wit}, ahead = cur;
-    RowTiles rows;
+    const int piece = lane % It::PC, col0 = lane / It::PC;
+    const uint32_t to0 = It::piece_at(col0, piece);
+    RowTiles tiles;
     Seg ls{0, 0, 0};
-    int lu = -1;
-    auto load = [&](It& b, uint32_t slot) {
-        if (ahead.u < units) {
-            if (ahead.u != lu) {
-                lu = ahead.u;
-                const int sg = lu / NT, rt = lu - sg * NT;
+    const uint16_t* x0 = nullptr;
+    int tiles_u = -1, scales_u = -1;
+    // item `ahead` into a slot
+    auto load = [&](uint32_t slot) {
+        if (ahead.i < i1) {
+            if (ahead.u != tiles_u) {
+                tiles_u = ahead.u;
+                const int sg = tiles_u / NT, rt = tiles_u - sg * NT;
                 ls = L.seg[sg];
-                rows.set(p, ls.e, rt, rt);
+                tiles.set(p, ls.e, rt, rt);
+                tiles.w0 += (int64_t)ahead.c * (It::TPI * kTileBytes);
+                tiles.w1 += (int64_t)ahead.c * (It::TPI * kTileBytes);
+                x0 = static_cast<const uint16_t*>(p.x) + L.token[ls.first + min(col0, ls.cnt - 1)] * p.x_stride;
             }
-            b.load(p, rows.w0, rows.w1, rows.srow, rows.zrow, ahead.c);
-            const int piece = lane & 15, k = ahead.c * kDepth + piece * 8, left = p.a.K - k;
+            It::weights(tiles.w0, tiles.w1, (int)p.a.k_tiles - ahead.c * It::TPI, slot);
+            tiles.w0 += It::TPI * kTileBytes;
+            tiles.w1 += It::TPI * kTileBytes;
+            const int k = ahead.c * It::kDepth + piece * 8, left = p.a.K - k;
+            if (p.x_wide) {
+                const int bytes = left > 0 ? 16 : 0, from = left > 0 ? k : 0;  // (rows end on a whole vector)
+                if (col0 < ls.cnt) cp_async16_part(slot + to0, x0 + from, bytes);
 #pragma unroll 1
-            for (int col = lane >> 4; col < ls.cnt; col += 2) {
-                const int64_t row = (int64_t)(L.sorted[ls.first + col] / p.r.S) * p.x_stride;
-                const uint16_t* x = static_cast<const uint16_t*>(p.x) + row;
-                const uint32_t dst = slot + (uint32_t)(col * kSlotRow + piece * 16);
-                if (p.x_wide) {
-                    cp_async16(dst, left > 0 ? x + k : x, max(0, min(left * 2, 16)));
-                } else {
+                for (int col = col0 + 32 / It::PC; col < ls.cnt; col += 32 / It::PC)
+                    cp_async16_part(slot + It::piece_at(col, piece),
+                                    static_cast<const uint16_t*>(p.x) + L.token[ls.first + col] * p.x_stride + from, bytes);
+            } else {
+#pragma unroll 1
+                for (int col = col0; col < ls.cnt; col += 32 / It::PC) {
+                    const uint16_t* x = static_cast<const uint16_t*>(p.x) + L.token[ls.first + col] * p.x_stride;
                     uint32_t v[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const uint32_t lo = 2 * j < left ? x[k + 2 * j] : 0u, hi = 2 * j + 1 < left ? x[k + 2 * j + 1] : 0u;
-                        v[j] = lo | (hi << 16);
+                        const uint32_t a = 2 * j < left ? x[k + 2 * j] : 0u, b = 2 * j + 1 < left ? x[k + 2 * j + 1] : 0u;
+                        v[j] = a | (b << 16);
                     }
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(slot + It::piece_at(col, piece)), "r"(v[0]),
+                                 "r"(v[1]), "r"(v[2]), "r"(v[3])
                                  : "memory");
                 }
             }
-            advance(ahead);
+            ahead.next(KC);
         }
         cp_commit();
     };
+    RowScales rows;
+    typename It::Raw raw;
+    auto load_scales = [&] {
+        if (next.i < i1) {
+            if (next.u != scales_u) {
+                scales_u = next.u;
+                const int sg = scales_u / NT, rt = scales_u - sg * NT;
+                rows.set(p, L.seg[sg].e, rt, rt);
+            }
+            It::raw(p, rows, next.c, raw);
+            next.next(KC);
+        }
+    };
 
-    float y[2][NG][4];
+    float y[2][4];
     auto clear = [&] {
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
 #pragma unroll
-            for (int n = 0; n < NG; ++n) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) y[m][n][j] = 0.f;
-            }
+            for (int j = 0; j < 4; ++j) y[m][j] = 0.f;
         }
     };
-    clear();
-    // the row tile's sums are complete (in wpu warps): h of its rows
-    int turn = 0;
+    auto put = [&](float4* to) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) to[m * 32 + lane] = make_float4(y[m][0], y[m][1], y[m][2], y[m][3]);
+    };
+    // a row tile's sums are complete: h of its rows
     auto finish = [&](int u) {
         const int sg = u / NT, rt = u - sg * NT;
-        if (wpu > 1) {
-            team_barrier(team, wpu * 32);  // the partials of the row tile before are read
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-#pragma unroll
-                for (int n = 0; n < NG; ++n)
-                    red[(warp * 2 * NG + m * NG + n) * 32 + lane] = make_float4(y[m][n][0], y[m][n][1], y[m][n][2], y[m][n][3]);
-            }
-            team_barrier(team, wpu * 32);
-        }
-        if (wit == turn) {
-            if (wpu > 1) {
-                clear();
-                for (int w = 0; w < wpu; ++w) {
-#pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-#pragma unroll
-                        for (int n = 0; n < NG; ++n) {
-                            const float4 v = red[((team * wpu + w) * 2 * NG + m * NG + n) * 32 + lane];
-                            y[m][n][0] += v.x;
-                            y[m][n][1] += v.y;
-                            y[m][n][2] += v.z;
-                            y[m][n][3] += v.w;
-                        }
-                    }
-                }
-            }
-            const Seg sgm = L.seg[sg];
-#pragma unroll
-            for (int n = 0; n < NG; ++n) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int col = n * 8 + 2 * (lane & 3) + (j & 1), row = rt * 16 + (lane >> 2) + 8 * (j >> 1);
-                    if (col < sgm.cnt) {
-                        const int pair = L.sorted[sgm.first + col];
-                        const float v = row < p.a.N ? activate(y[0][n][j], p.act) * y[1][n][j] * L.w[pair] : 0.f;
-                        const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-                        const float rest = v - __bfloat162float(hi);  // exact; NaN beside an infinity
-                        uint16_t* dst = p.h + (int64_t)pair * 2 * p.inner + row;
-                        dst[0] = __bfloat16_as_ushort(hi);
-                        dst[p.inner] = isinf(__bfloat162float(hi)) ? 0 : __bfloat16_as_ushort(__float2bfloat16_rn(rest));
-                    }
-                }
+        const Seg s = L.seg[sg];
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j) {  // (one at a time: four abreast need 30 registers more)
+            const int col = 2 * (lane & 3) + (j & 1), row = rt * 16 + (lane >> 2) + 8 * (j >> 1);
+            const float g = j == 0 ? y[0][0] : j == 1 ? y[0][1] : j == 2 ? y[0][2] : y[0][3];
+            const float v0 = j == 0 ? y[1][0] : j == 1 ? y[1][1] : j == 2 ? y[1][2] : y[1][3];
+            if (col < s.cnt) {
+                const int pair = L.sorted[s.first + col];
+                const float v = row < p.a.N ? activate(g, p.act) * v0 * L.w[pair] : 0.f;
+                const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+                const float rest = v - __bfloat162float(hi);  // exact; NaN beside an infinity
+                uint16_t* dst = p.h + (int64_t)pair * 2 * p.inner + row;
+                dst[0] = __bfloat16_as_ushort(hi);
+                dst[p.inner] = isinf(__bfloat162float(hi)) ? 0 : __bfloat16_as_ushort(__float2bfloat16_rn(rest));
             }
         }
-        if (++turn == wpu) turn = 0;
-        clear();
     };
 
-    It buf[DEPTH];
-#pragma unroll
-    for (int d = 0; d < DEPTH; ++d) load(buf[d], slots + d * It::kSlotBytes);
-    const bool has_z = (lane < 16 ? p.a.zp : p.b.zp) != nullptr;
-    auto step = [&](It& b, uint32_t slot) {
-        if (cur.u >= units) return false;
-        cp_wait<DEPTH - 1>();
-        b.table(p, tab, has_z);
+    load_scales();
+#pragma unroll 1
+    for (int d = 0; d < depth; ++d) load(ring + d * slot_bytes);
+    clear();
+    const int first_u = cur.u, first_c = cur.c;
+    const uint32_t last_slot = ring + (depth - 1) * slot_bytes;
+    bool ends = false;  // the run ends a row tile that began in another
+    uint32_t slot = ring;
+#pragma unroll 1
+    while (cur.i < i1) {
+        cp_wait_oldest(depth);
+        It::table(p.sdt, raw, tab);
+        load_scales();
         __syncwarp();
-        b.compute(slot, tab, y);
+        It::compute(slot, tab, y);
         __syncwarp();
-        load(b, slot);
+        load(slot);
+        slot = slot == last_slot ? ring : slot + slot_bytes;
         const int u = cur.u;
-        advance(cur);
-        if (cur.u != u) finish(u);
-        return true;
-    };
-    bool more = true;
-    while (more) {
-#pragma unroll
-        for (int d = 0; d < DEPTH; ++d)
-            if (more) more = step(buf[d], slots + d * It::kSlotBytes);
+        cur.next(KC);
+        if (cur.c == 0) {  // the row tile's last item
+            if (u != first_u || first_c == 0) {
+                finish(u);
+            } else {
+                put(heads + warp * 64);
+                ends = true;
+            }
+            clear();
+        }
     }
     cp_wait<0>();
+    // the run that ends a row tile adds its parts in order
+    auto rest = [&](int w) { return reinterpret_cast<float4*>(smem + w * kRingBytes); };  // of the row tile that a run leaves unended
+    __syncwarp();
+    if (i1 > i0 && cur.c != 0) put(rest(warp));
+    __syncthreads();
+    if (ends) {
+        clear();
+        const int start = (first_u - u0) * KC;  // the row tile's first item
+        for (int w = 0; w <= warp; ++w) {
+            const int w0 = part_start(items, w, kWarps), w1 = part_start(items, w + 1, kWarps);
+            if (w1 <= start || w0 == w1) continue;
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const float4 v = (w < warp ? rest(w) : heads + warp * 64)[m * 32 + lane];
+                y[m][0] += v.x;
+                y[m][1] += v.y;
+                y[m][2] += v.z;
+                y[m][3] += v.w;
+            }
+        }
+        finish(first_u);
+    }
     if (blockIdx.x == 0)
         for (int i = tid; i < *L.nseg; i += kThreads) {
             check_headers(p, p.a, L.seg[i].e, BITS);
@@ -514,14 +612,13 @@ __global__ void __launch_bounds__(kThreads, 2) gate_up_kernel(const __grid_const
         }
 }
 
-template <int BITS, int SUB, int NG>
+template <int BITS, int BSL>
 __global__ void __launch_bounds__(kThreads, 2) down_kernel(const __grid_constant__ Params p) {
-    using It = Item<BITS, true, SUB, NG>;
-    constexpr int DEPTH = It::DEPTH;
+    using It = Item<BITS, true, BSL>;
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t slots = smem_u32(smem) + (uint32_t)(warp * DEPTH * It::kSlotBytes);
-    uint8_t* at = smem + kWarps * DEPTH * It::kSlotBytes;
+    const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * kRingBytes);
+    uint8_t* at = smem + kWarps * kRingBytes;
     uint2* tab = reinterpret_cast<uint2*>(at + warp * It::kTabBytes);
     at += kWarps * It::kTabBytes;
     const int T = p.r.T;
@@ -534,116 +631,118 @@ __global__ void __launch_bounds__(kThreads, 2) down_kernel(const __grid_constant
 
     for (int i = tid; i < kWarps * T * 32; i += kThreads) sums[i] = 0.f;
     // The routing's inputs were complete before the kernel that this one follows began: no wait.
-    make_lists(p, L, 4 * NG);
+    make_lists(p, L, 4, reinterpret_cast<uint32_t*>(smem));
+    const int slot_bytes = It::slot_bytes(2 * *L.most), depth = min(4, kRingBytes / slot_bytes);
 
-    const int IC = ((int)p.inner + kDepth - 1) / kDepth, items = *L.nseg * IC;
-    const int W = C * kWarps, me = rank * kWarps + warp;
-    const int i0 = (int)((int64_t)items * me / W), i1 = (int)((int64_t)items * (me + 1) / W);
-    const int64_t rt0 = 2 * group, rt1 = min(rt0 + 1, p.a.row_tiles - 1);
-    RowTiles rows;
+    const int KC = ((int)p.inner + It::kDepth - 1) / It::kDepth;
+    const int items = *L.nseg * KC, me = rank * kWarps + warp;
+    const int i0 = part_start(items, me, C * kWarps), i1 = part_start(items, me + 1, C * kWarps);
+    const int rt0 = 2 * group, rt1 = min(rt0 + 1, (int)p.a.row_tiles - 1);
+    Cursor cur{i0, i0 / KC, i0 % KC};
+    Cursor ahead = cur, next = cur, column = cur;
+    RowTiles tiles;
+    int tiles_u = -1, scales_u = -1, column_u = -1;
+    auto load_weights = [&](uint32_t slot) {
+        if (ahead.i < i1) {
+            if (ahead.u != tiles_u) {
+                tiles_u = ahead.u;
+                tiles.set(p, L.seg[tiles_u].e, rt0, rt1);
+                tiles.w0 += (int64_t)ahead.c * (It::TPI * kTileBytes);
+                tiles.w1 += (int64_t)ahead.c * (It::TPI * kTileBytes);
+            }
+            It::weights(tiles.w0, tiles.w1, (int)p.a.k_tiles - ahead.c * It::TPI, slot);
+            tiles.w0 += It::TPI * kTileBytes;
+            tiles.w1 += It::TPI * kTileBytes;
+            ahead.next(KC);
+        }
+    };
+    // columns 2 j and 2 j + 1: the high and the low part of the segment's pair j
+    const int piece = lane % It::PC, col0 = lane / It::PC;
+    const uint32_t to0 = It::piece_at(col0, piece);
+    const uint16_t* h0 = nullptr;
     Seg ls{0, 0, 0};
-    int lsg = -1, ahead = i0;
-    auto place = [&](int i) {  // the segment and chunk of item i, and the segment's addresses
-        const int sg = i / IC;
-        if (sg != lsg) {
-            lsg = sg;
-            ls = L.seg[sg];
-            rows.set(p, ls.e, rt0, rt1);
-        }
-        return i - sg * IC;
-    };
-    auto columns = [&](int i, int c, const Seg& sg, uint32_t slot) {
-        const int piece = lane & 15, k = c * kDepth + piece * 8, left = (int)p.inner - k;
+    auto load_columns = [&](uint32_t slot) {
+        if (column.i < i1) {
+            if (column.u != column_u) {
+                column_u = column.u;
+                ls = L.seg[column_u];
+                h0 = p.h + ((int64_t)L.sorted[ls.first + min(col0 >> 1, ls.cnt - 1)] * 2 + (col0 & 1)) * p.inner;
+            }
+            const int k = column.c * It::kDepth + piece * 8, left = (int)p.inner - k;
+            const int bytes = left > 0 ? 16 : 0, from = left > 0 ? k : 0;  // (rows of h are whole row tiles)
+            if (col0 < 2 * ls.cnt) cp_async16_part(slot + to0, h0 + from, bytes);
 #pragma unroll 1
-        for (int r = lane >> 4; r < 2 * sg.cnt; r += 2) {  // token r / 2, its high or low part
-            const int j = r >> 1, col = (j & 3) + 4 * (r & 1) + 8 * (j >> 2);
-            const uint16_t* h = p.h + ((int64_t)L.sorted[sg.first + j] * 2 + (r & 1)) * p.inner;
-            cp_async16(slot + (uint32_t)(col * kSlotRow + piece * 16), left > 0 ? h + k : h, max(0, min(left * 2, 16)));
+            for (int col = col0 + 32 / It::PC; col < 2 * ls.cnt; col += 32 / It::PC)
+                cp_async16_part(slot + It::piece_at(col, piece),
+                                p.h + ((int64_t)L.sorted[ls.first + (col >> 1)] * 2 + (col & 1)) * p.inner + from, bytes);
+            column.next(KC);
         }
-        (void)i;
     };
-    auto load = [&](It& b, uint32_t slot) {
-        if (ahead < i1) {
-            const int c = place(ahead);
-            b.load(p, rows.w0, rows.w1, rows.srow, rows.zrow, c);
-            columns(ahead, c, ls, slot);
-            ++ahead;
+    RowScales rows;
+    typename It::Raw raw;
+    auto load_scales = [&] {
+        if (next.i < i1) {
+            if (next.u != scales_u) {
+                scales_u = next.u;
+                rows.set(p, L.seg[scales_u].e, rt0, rt1);
+            }
+            It::raw(p, rows, next.c, raw);
+            next.next(KC);
         }
-        cp_commit();
     };
 
-    It buf[DEPTH];
-    // the first items' weights before the wait for h, their columns after it
-#pragma unroll
-    for (int d = 0; d < DEPTH; ++d)
-        if (i0 + d < i1) {
-            const int c = place(i0 + d);
-            buf[d].load(p, rows.w0, rows.w1, rows.srow, rows.zrow, c);
-        }
+    // the first items' weights before the wait for h (all in the first group), their columns after it
+    load_scales();
+#pragma unroll 1
+    for (int d = 0; d < depth; ++d) load_weights(ring + d * slot_bytes);
     griddep_wait();
     griddep_launch_dependents();
-#pragma unroll
-    for (int d = 0; d < DEPTH; ++d) {
-        if (ahead < i1) {
-            const int c = place(ahead);
-            columns(ahead, c, ls, slots + d * It::kSlotBytes);
-            ++ahead;
-        }
+#pragma unroll 1
+    for (int d = 0; d < depth; ++d) {
+        load_columns(ring + d * slot_bytes);
         cp_commit();
     }
 
-    float y[2][NG][4];
+    float y[2][4];
     auto clear = [&] {
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
 #pragma unroll
-            for (int n = 0; n < NG; ++n) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) y[m][n][j] = 0.f;
-            }
+            for (int j = 0; j < 4; ++j) y[m][j] = 0.f;
         }
     };
     clear();
     float* mine = sums + warp * T * 32;
-    // a segment ends: its columns' high and low parts are added and go to their tokens' sums
-    auto flush = [&](int sg) {
-        const Seg s = L.seg[sg];
+    const uint32_t last_slot = ring + (depth - 1) * slot_bytes;
+    uint32_t slot = ring;
+#pragma unroll 1
+    while (cur.i < i1) {
+        cp_wait_oldest(depth);
+        It::table(p.sdt, raw, tab);
+        load_scales();
+        __syncwarp();
+        It::compute(slot, tab, y);
+        __syncwarp();
+        load_weights(slot);
+        load_columns(slot);
+        cp_commit();
+        slot = slot == last_slot ? ring : slot + slot_bytes;
+        const int u = cur.u;
+        cur.next(KC);
+        if (cur.c == 0 || cur.i == i1) {
+            // the segment ends: its pairs' high and low parts are added and go to their tokens' sums
+            const Seg s = L.seg[u];
+            if ((lane & 3) < s.cnt) {
+                float* dst = mine + L.token[s.first + (lane & 3)] * 32 + (lane >> 2);
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-#pragma unroll
-            for (int n = 0; n < NG; ++n) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float v = y[m][n][j] + __shfl_xor_sync(0xFFFFFFFFu, y[m][n][j], 2);
-                    const int col = n * 4 + 2 * (lane & 3) + (j & 1);
-                    if ((lane & 3) < 2 && col < s.cnt)
-                        mine[L.sorted[s.first + col] / p.r.S * 32 + m * 16 + (lane >> 2) + 8 * (j >> 1)] += v;
+                for (int m = 0; m < 2; ++m) {
+                    dst[m * 16] += y[m][0] + y[m][1];
+                    dst[m * 16 + 8] += y[m][2] + y[m][3];
                 }
             }
+            clear();
+            __syncwarp();
         }
-        clear();
-        __syncwarp();
-    };
-    const bool has_z = p.a.zp != nullptr;
-    int cur = i0;
-    auto step = [&](It& b, uint32_t slot) {
-        if (cur >= i1) return false;
-        cp_wait<DEPTH - 1>();
-        b.table(p, tab, has_z);
-        __syncwarp();
-        b.compute(slot, tab, y);
-        __syncwarp();
-        load(b, slot);
-        const int sg = cur / IC;
-        ++cur;
-        if (cur == i1 || cur / IC != sg) flush(sg);
-        return true;
-    };
-    bool more = true;
-    while (more) {
-#pragma unroll
-        for (int d = 0; d < DEPTH; ++d)
-            if (more) more = step(buf[d], slots + d * It::kSlotBytes);
     }
     cp_wait<0>();
     __syncthreads();
@@ -670,12 +769,22 @@ __global__ void __launch_bounds__(kThreads, 2) down_kernel(const __grid_constant
         for (int i = tid; i < *L.nseg; i += kThreads) check_headers(p, p.a, L.seg[i].e, BITS);
 }
 
-template <int BITS, bool BF, int SUB, int NG>
-cudaError_t launch_gate_up(const Params& p, cudaStream_t s) {
-    using It = Item<BITS, BF, SUB, NG>;
-    auto kern = gate_up_kernel<BITS, BF, SUB, NG>;
+// The loads of an item's scales and zero points as one access, where a row's blocks come in whole items and aligned.
+template <class It>
+void set_vectors(Params& p, int bits) {
+    auto all = [&](const void* a, const void* b, int n) { return dec::aligned_to(a, n) && dec::aligned_to(b, n); };
+    const bool runs = It::NB == 1 || p.a.KB % It::NB == 0;
+    p.s_vec = runs && p.sdt != kF32 && all(p.a.scales, p.b.scales, 2 * It::NB);
+    p.z_vec = It::NB > 1 && runs && It::NB * bits >= 8 && all(p.a.zp, p.b.zp, It::NB * bits / 8);
+}
+
+template <int BITS, bool BF, int BSL>
+cudaError_t launch_gate_up(Params p, cudaStream_t s) {
+    using It = Item<BITS, BF, BSL>;
+    set_vectors<It>(p, BITS);
+    auto kern = gate_up_kernel<BITS, BF, BSL>;
     const int P = p.r.T * p.r.S;
-    const size_t smem = (size_t)kWarps * (It::DEPTH * It::kSlotBytes + It::kTabBytes + 2 * NG * 32 * 16) + Lists::bytes(P, p.r.E);
+    const size_t smem = (size_t)kWarps * (kRingBytes + It::kTabBytes + 2 * 32 * 16) + Lists::bytes(P);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     // two CTAs an SM; no more than the row tiles of the most experts that can be active
@@ -684,36 +793,38 @@ cudaError_t launch_gate_up(const Params& p, cudaStream_t s) {
     return dec::launch_pdl(kern, dim3(grid), dim3(kThreads), smem, s, 1, p);
 }
 
-template <int BITS, int SUB, int NG>
-cudaError_t launch_down(const Params& p, cudaStream_t s) {
-    using It = Item<BITS, true, SUB, NG>;
-    auto kern = down_kernel<BITS, SUB, NG>;
-    const size_t smem = (size_t)kWarps * (It::DEPTH * It::kSlotBytes + It::kTabBytes + p.r.T * 32 * 4) +
-                        Lists::bytes(p.r.T * p.r.S, p.r.E);
+template <int BITS, int BSL>
+cudaError_t launch_down(Params p, cudaStream_t s) {
+    using It = Item<BITS, true, BSL>;
+    set_vectors<It>(p, BITS);
+    auto kern = down_kernel<BITS, BSL>;
+    const size_t smem = (size_t)kWarps * (kRingBytes + It::kTabBytes + p.r.T * 32 * 4) + Lists::bytes(p.r.T * p.r.S);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const int64_t groups = (p.a.row_tiles + 1) / 2;
     // as many CTAs a group of 32 rows as two an SM hold, up to a portable cluster
-    Params q = p;
-    q.cluster = 1;
-    while (q.cluster < 8 && groups * q.cluster * 2 <= 2 * dec::kSms) q.cluster *= 2;
-    return dec::launch_pdl(kern, dim3((unsigned)(groups * q.cluster)), dim3(kThreads), smem, s, q.cluster, q);
+    p.cluster = 1;
+    while (p.cluster < 8 && groups * p.cluster * 2 <= 2 * dec::kSms) p.cluster *= 2;
+    return dec::launch_pdl(kern, dim3((unsigned)(groups * p.cluster)), dim3(kThreads), smem, s, p.cluster, p);
 }
 
-template <int BITS, int SUB>
-cudaError_t launch_sub(const Params& g, const Params& d, int bf, cudaStream_t s) {
-    // columns: one group of 8 (4 tokens in two parts) where no expert can have more pairs
-    const bool two = g.r.T > 8;
-    cudaError_t e;
-    if (bf) e = two ? launch_gate_up<BITS, true, SUB, 2>(g, s) : launch_gate_up<BITS, true, SUB, 1>(g, s);
-    else e = two ? launch_gate_up<BITS, false, SUB, 2>(g, s) : launch_gate_up<BITS, false, SUB, 1>(g, s);
-    if (e != cudaSuccess) return e;
-    return d.r.T > 4 ? launch_down<BITS, SUB, 2>(d, s) : launch_down<BITS, SUB, 1>(d, s);
+template <int BITS, int BSL>
+cudaError_t launch_block(const Params& g, const Params& d, int bf, cudaStream_t s) {
+    const cudaError_t e = bf ? launch_gate_up<BITS, true, BSL>(g, s) : launch_gate_up<BITS, false, BSL>(g, s);
+    return e == cudaSuccess ? launch_down<BITS, BSL>(d, s) : e;
 }
 
+// Blocks of 16, 32, 64, and 128 and more (8-bit codes: 64 and more, an item).
 template <int BITS>
 cudaError_t launch_bits(const Params& g, const Params& d, int bf, cudaStream_t s) {
-    return g.bs_shift == 4 ? launch_sub<BITS, 1>(g, d, bf, s) : launch_sub<BITS, 2>(g, d, bf, s);
+    switch (g.bs_shift) {
+        case 4: return launch_block<BITS, 0>(g, d, bf, s);
+        case 5: return launch_block<BITS, 1>(g, d, bf, s);
+        case 6: return launch_block<BITS, 2>(g, d, bf, s);
+        default:
+            if constexpr (BITS == 8) return launch_block<BITS, 2>(g, d, bf, s);
+            else return launch_block<BITS, 3>(g, d, bf, s);
+    }
 }
 
 }  // namespace moe

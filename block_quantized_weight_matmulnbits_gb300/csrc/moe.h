@@ -12,7 +12,9 @@ namespace mnb {
 namespace moe {
 
 constexpr int kMaxTokens = 64, kMaxTopK = 32, kMaxPairs = 1024, kMaxExperts = 1024;
-constexpr int kRouteInside = 8;  // tokens up to which every CTA routes for itself (a warp each)
+// Every CTA routes for itself up to so many comparisons (T * E^2; 64 a thread) and pairs; more are a launch of their own.
+constexpr int64_t kInsideScores = 1 << 14;
+constexpr int kInsidePairs = 64;
 
 // Experts' weights, back to back as mnb_matmul_grouped takes them.
 struct Weights {
@@ -34,10 +36,24 @@ struct Route {
     float scale;
 };
 
+struct Seg {
+    int e, first, cnt;  // expert, place of its first pair in the sorted list, pairs
+};
+
+// A routing kernel's lists: pairs sorted by expert, and segments of at most 8 (gate_up) and 4 (down) of them.
+struct PlanSegs {
+    int n, most;  // segments, pairs of the largest
+    Seg seg[kMaxPairs];
+};
+struct Plan {
+    float w[kMaxPairs];
+    int sorted[kMaxPairs];
+    PlanSegs by8, by4;
+};
+
 struct Params {
     Route r;
-    const int32_t* ids_in;  // routed before (null: route inside)
-    const float* w_in;
+    const Plan* plan;       // null: route inside
     int32_t* ids_out;       // optional outputs of a kernel that routes
     float* w_out;
     const void* x;

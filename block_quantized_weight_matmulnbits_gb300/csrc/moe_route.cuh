@@ -1,4 +1,4 @@
-// Selection of a token's experts by one warp.
+// Selection of a token's experts, by one warp or by a thread a score.
 //
 // The router's scores are the logits (softmax) or sigmoid(logit) + bias; the S
 // largest are taken in descending order, equal ones by ascending expert, a NaN
@@ -22,6 +22,26 @@ __device__ __forceinline__ uint32_t order_key(float f) {
 
 __device__ __forceinline__ float sigmoid(float v) { return 1.f / (1.f + expf(-v)); }
 
+// Key of expert e of logit l: what is ordered.
+__device__ __forceinline__ uint32_t route_key(const Route& r, float l, int e) {
+    if (r.sigmoid && r.bias) l = sigmoid(l) + __ldg(r.bias + e);
+    return order_key(l);
+}
+
+// Weight of place s of a token with the given logits, whose experts are ids[0 .. S - 1].
+__device__ __forceinline__ float route_weight(const Route& r, const float* logit, const int* ids, int s) {
+    const float top = logit[ids[0]];
+    auto score = [&](float l) { return r.sigmoid ? sigmoid(l) : l != -INFINITY ? expf(l - top) : 0.f; };
+    float w = score(logit[ids[s]]), sum = 0.f;
+    if (r.renorm) {
+        for (int j = 0; j < r.S; ++j) sum += score(logit[ids[j]]);
+    } else if (!r.sigmoid) {
+        for (int e = 0; e < r.E; ++e) sum += score(logit[e]);
+    }
+    if (!r.sigmoid || r.renorm) w = sum != 0.f ? __fdiv_rn(w, sum) : 0.f;
+    return w * r.scale;
+}
+
 // Lane s < S gets expert s and its weight.  VPL: scores a lane holds (E <= 32 VPL).
 template <int VPL>
 __device__ __forceinline__ void route_token(const Route& r, int64_t t, int& expert, float& weight) {
@@ -37,9 +57,7 @@ __device__ __forceinline__ void route_token(const Route& r, int64_t t, int& expe
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
         const int e = lane + 32 * j;
-        float score = l[j];
-        if (r.sigmoid && r.bias) score = sigmoid(score) + (e < r.E ? __ldg(r.bias + e) : 0.f);
-        key[j] = e < r.E ? order_key(score) : 0u;
+        key[j] = e < r.E ? route_key(r, l[j], e) : 0u;
     }
     expert = 0;
     float logit = 0.f;

@@ -730,7 +730,7 @@ typedef struct mnb_expert_weights {
 typedef enum mnb_activation { MNB_ACT_SILU = 0, MNB_ACT_GELU_TANH = 1 } mnb_activation;
 
 /* A whole mixture-of-experts layer for a few tokens, in two launches (three
- * from 9 tokens on): with the experts ids[t, s] and weights w[t, s] of `route`,
+ * where T * E * E > 16384 or T * S > 64): with the experts ids[t, s] and weights w[t, s] of `route`,
  *     Y[t] = sum_s w[t, s] * down_e ( act(gate_e X[t]) * (up_e X[t]) ),   e = ids[t, s].
  * Products accumulate in f32; what lies between the products keeps 16 bits
  * (two bf16 parts), whatever act_dtype is; Y is rounded once to out_dtype.
