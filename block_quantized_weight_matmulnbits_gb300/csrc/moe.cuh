@@ -4,22 +4,33 @@
 //   down:     y[t, :]    = sum_s down_e h[t, s, :]
 //
 // The active experts' weights are read once and everything else is small, so
-// their bytes bound both.  What a warp does for 512 bytes of packed 4-bit
-// codes (a tile of 16 rows x 64 depths): 4 k-steps of an unpack (7 shifts and
-// ands, 4 exact packed subtractions of the zero point) and one m16n8k16 MMA per
-// 8 columns, so that the issue of instructions is the next bound.
+// their bytes bound both, and the issue of instructions is the next bound.
+//
+// Arithmetic.  A code q in the low bits of a 16-bit lane is, read as an f16 or
+// bf16 number, q times the type's smallest subnormal (in bits 4 to 7, 16 q
+// times it; in bf16 the lowest exponent bit continues the scale up to 255).
+// Packed subtraction and the MMA take subnormal operands exactly, so an A
+// fragment of 4-bit codes is a shift, four ands and four subtractions of the
+// zero point, with no conversion; rows 8 to 15 come out 16 times as large, and
+// the sums are scaled at the end.  Columns of bf16 are scaled by 2^60 (h where
+// it is written, x in the loop), so that the products are normal numbers.
+//
+// The warp-level MMA of this part is slow (one m16n8k16 in 7 cycles an SM): 16
+// of them for the 2 KB of an item take about as long as its bytes from memory,
+// so none is spent on anything else (sums of x for the zero points by an MMA
+// with ones: half as long again).
 //
 // The work of a warp comes in items: two row tiles that multiply the same
 // columns (gate and up of one row tile; two neighbouring row tiles of down), 128
-// depths (8-bit codes: 64).  Weights and columns go through a ring of the warp in shared
-// memory by asynchronous copies, a few items ahead: a lane copies the 16 bytes
-// of a packed tile that it alone reads, and warps wait for no other warp while
-// they stream.  Two row tiles share the fragments of the columns, which halves
-// what those cost in shared-memory cycles.  Scales and zero points (a lane loads
-// those of one of the 32 rows, one item ahead) pass through a table of the warp
-// as float and subtraction constant.  One copy of the loop, indexed by the
-// ring's slot, keeps the code in the instruction cache (with the weights in
-// registers, a copy a buffer, a quarter of the stalls were instruction fetches).
+// depths (8-bit codes: 64).  Weights and columns go through a ring of the warp
+// in shared memory by asynchronous copies, two to four items ahead: a lane
+// copies the 16 bytes of a packed tile that it alone reads, and warps wait for
+// no other warp while they stream (bulk copies with barriers took a quarter more
+// instructions and 10% more time).  Two row tiles share the fragments of the
+// columns, which halves what those cost in shared-memory cycles.  Scales and
+// zero points (a lane loads those of one of the 32 rows, one item ahead) pass
+// through a table of the warp as floats.  One copy of the loop, indexed by the
+// ring's slot, keeps the code in the instruction cache.
 //
 // The columns of an item are the tokens of its expert: its pairs (t, s), in
 // ascending order, at most 8 of them a segment (down: 4, each as a high and a
@@ -48,11 +59,11 @@ namespace mnb {
 namespace moe {
 
 using gmma::mma16816;
-using gmma::Unpack;
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kRingBytes = 9216;  // of a warp: two CTAs fit an SM; two to four slots
+constexpr int kRingBytes = 9216;         // of a warp: two CTAs fit an SM beside 40 KB of L1 (for the scales); two to four slots
+constexpr float kColumnScale = 0x1p60f;  // of bf16 columns
 
 // Shared memory after the streaming buffers: the routing of the call.
 struct Lists {
@@ -223,8 +234,9 @@ struct RowScales {
     }
 };
 
-// BSL: log2 of the block's k-steps, at most an item's (a longer block spans items).
-template <int BITS, bool BF, int BSL>
+// BSL: log2 of the block's k-steps, at most an item's (a longer block spans items).  LIFT: the columns are bf16 values
+// that the loop scales.
+template <int BITS, bool BF, int BSL, bool LIFT>
 struct Item {
     static constexpr int KST = BITS == 8 ? 4 : 8;                // k-steps
     static constexpr int kDepth = 16 * KST;
@@ -233,14 +245,15 @@ struct Item {
     static constexpr int SUB = (1 << BSL) < KST ? 1 << BSL : KST;  // k-steps of a scale
     static constexpr int NB = KST / SUB;                         // scales of a row
     static constexpr int PC = 2 * KST;                           // 16-byte pieces of a column
-    static constexpr int kColBytes = 16 * PC;
+    static constexpr int kColBytes = 16 * PC, kColStride = kColBytes + 16;  // (padded: ldmatrix rows meet no bank twice)
     static constexpr int kWBytes = 2 * TPI * kTileBytes;
     static constexpr int kTabBytes = 2 * NB * 16 * 8;
+    static constexpr int kLift8 = BITS == 4 ? 16 : BITS == 2 ? 4 : 1;  // rows 8 to 15 of a tile: their codes stand higher
+    static constexpr float kUnscale = BF ? 0x1p73f : 0x1p24f;          // of y in rows 0 to 7: 2^133 / kColumnScale, 2^24
     static_assert(NB * BITS <= 32, "an item's zero points of a row are one word");
-    using U = Unpack<BITS, BF>;
     // Bytes of a slot: the weights, and as many columns as a segment of the call has.
-    static __device__ __forceinline__ int slot_bytes(int cols) { return kWBytes + cols * kColBytes; }
-    static_assert(2 * (kWBytes + 8 * kColBytes) <= kRingBytes, "two slots of 8 columns");
+    static __device__ __forceinline__ int slot_bytes(int cols) { return kWBytes + cols * kColStride; }
+    static_assert(2 * (kWBytes + 8 * kColStride) <= kRingBytes, "two slots of 8 columns");
 
     // Copies of the item's weights into a slot (w0, w1: the lane's 16 bytes of its first packed tiles; `tiles` of them
     // are there).
@@ -259,6 +272,31 @@ struct Item {
                 cp_async16(at + (TPI + j) * kTileBytes, w1 + min(j, tiles - 1) * kTileBytes);
             }
         }
+    }
+
+    // A fragment of k-step s of a lane's 16 packed bytes: q - zp as subnormal numbers, rows 8 to 15 times kLift8.
+    static __device__ __forceinline__ void fragment(const uint4& wv, int s, uint32_t zg, uint32_t zg8, uint32_t (&a)[4]) {
+        const uint32_t w[4] = {wv.x, wv.y, wv.z, wv.w};
+        if constexpr (BITS == 4) {
+            const uint32_t v = w[s], u = v >> 8;
+            a[0] = v & 0x000F000Fu;
+            a[1] = v & 0x00F000F0u;
+            a[2] = u & 0x000F000Fu;
+            a[3] = u & 0x00F000F0u;
+        } else if constexpr (BITS == 2) {
+            const uint32_t v = w[s >> 1] >> ((s & 1) * 8), u = v >> 4;
+            a[0] = v & 0x00030003u;
+            a[1] = v & 0x000C000Cu;
+            a[2] = u & 0x00030003u;
+            a[3] = u & 0x000C000Cu;
+        } else {
+            a[0] = prmt(w[2 * s], 0u, 0x4140u);
+            a[1] = prmt(w[2 * s], 0u, 0x4342u);
+            a[2] = prmt(w[2 * s + 1], 0u, 0x4140u);
+            a[3] = prmt(w[2 * s + 1], 0u, 0x4342u);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) a[r] = BF ? gmma::hsub2_bf16(a[r], (r & 1) ? zg8 : zg) : gmma::hsub2_f16(a[r], (r & 1) ? zg8 : zg);
     }
 
     // Raw scales (two a word, f32: one) and zero points of the lane's row.
@@ -309,15 +347,13 @@ struct Item {
         }
     }
 
-    // The lane's row into the warp's table: entry [row tile][j][row] = (scale, subtraction constant).
+    // The lane's row into the warp's table: entry [row tile][j][g] = (scale, zero point as the codes' numbers) of rows g and g + 8.
     static __device__ __forceinline__ void table(int sdt, const Raw& v, uint2* tab) {
         const int lane = threadIdx.x & 31;
-        uint2* dst = tab + (lane >> 4) * NB * 16 + (lane & 15);
+        uint2* dst = tab + (lane >> 4) * NB * 16 + (lane & 7) * 2 + ((lane >> 3) & 1);
+        const uint32_t lift = ((lane & 8) ? kLift8 : 1) * 0x00010001u;
         auto put = [&](int j, float s) {
-            const uint32_t z = (v.z >> (j * BITS)) & (uint32_t)((1 << BITS) - 1);
-            // U::zconst(z); in 16-bit lanes as one multiply-add
-            const uint32_t c = BITS == 8 && BF ? U::zconst(z) : z * 0x00010001u + U::kMagic16x2;
-            dst[j * 16] = make_uint2(__float_as_uint(s), c);
+            dst[j * 16] = make_uint2(__float_as_uint(s), ((v.z >> (j * BITS)) & (uint32_t)((1 << BITS) - 1)) * lift);
         };
         if (sdt == kF16) {
 #pragma unroll
@@ -331,74 +367,85 @@ struct Item {
         }
     }
 
-    // Where piece `piece` of column `col` lies in a slot: pieces are permuted so that ldmatrix rows meet no bank twice.
-    static __device__ __forceinline__ uint32_t piece_at(int col, int piece) {
-        return (uint32_t)(kWBytes + col * kColBytes + ((piece ^ (col & 7)) << 4));
-    }
+    // Where piece `piece` of column `col` lies in a slot.
+    static __device__ __forceinline__ uint32_t piece_at(int col, int piece) { return (uint32_t)(kWBytes + col * kColStride + piece * 16); }
 
-    // y[m] += row tile m times the columns.  (Columns past the segment's hold anything: their sums are not used.)
+    // y[m] += row tile m times the columns, in units of the codes' (times kColumnScale).  (Columns past the segment's hold
+    // anything: their sums are not used.)
     static __device__ __forceinline__ void compute(uint32_t slot, const uint2* tab, float (&y)[2][4]) {
         constexpr int KG = BITS == 2 ? 8 : 4;  // k-steps of a turn: with all 8 unrolled the loads of a whole item come first and spill
         constexpr int TPG = KG / SPT;
         const int lane = threadIdx.x & 31;
         const float zero4[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t cols = slot + kWBytes + (lane & 7) * kColBytes, swz = (uint32_t)((lane >> 3) ^ (lane & 7)) << 4;
-        uint32_t mine = slot + lane * 16;
-        const uint2* row = tab + (lane >> 2);
+        uint32_t cols = slot + kWBytes + (lane & 7) * kColStride + (lane >> 3) * 16, mine = slot + lane * 16;
+        const uint4* row = reinterpret_cast<const uint4*>(tab) + (lane >> 2);
         float acc[2][4];
-        uint2 lo[2], hi[2];
+        uint4 e[2];  // of the block: scale and zero point of rows g and g + 8
         if constexpr (SUB > KG) {
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
-                lo[m] = row[m * NB * 16];
-                hi[m] = row[m * NB * 16 + 8];
+                e[m] = row[m * NB * 8];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) acc[m][j] = 0.f;
             }
         }
+        auto scale = [&] {
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                y[m][0] = fmaf(__uint_as_float(e[m].x), acc[m][0], y[m][0]);
+                y[m][1] = fmaf(__uint_as_float(e[m].x), acc[m][1], y[m][1]);
+                y[m][2] = fmaf(__uint_as_float(e[m].z), acc[m][2], y[m][2]);
+                y[m][3] = fmaf(__uint_as_float(e[m].z), acc[m][3], y[m][3]);
+            }
+        };
 #pragma unroll 1
         for (int k0 = 0; k0 < KST; k0 += KG) {
-            uint32_t x[4];
-            uint4 w[2];
+            uint32_t x[KG / 2][4];
+            uint4 w[2][TPG];
+#pragma unroll
+            for (int t = 0; t < TPG; ++t) {
+                w[0][t] = lds16(mine + t * kTileBytes);
+                w[1][t] = lds16(mine + (TPI + t) * kTileBytes);
+            }
+#pragma unroll
+            for (int k = 0; k < KG; k += 2) ldmatrix4(x[k / 2], cols + k * 32);
+            if constexpr (LIFT) {
+#pragma unroll
+                for (int k = 0; k < KG / 2; ++k) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(x[k][j]) : "r"(0x5D805D80u));  // 2^60
+                }
+            }
 #pragma unroll
             for (int k = 0; k < KG; ++k) {
-                if (k % SPT == 0) {
-                    w[0] = lds16(mine + (k / SPT) * kTileBytes);
-                    w[1] = lds16(mine + (TPI + k / SPT) * kTileBytes);
-                }
                 if (SUB <= KG && k % SUB == 0) {
-#pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        lo[m] = row[(m * NB + k / SUB) * 16];
-                        hi[m] = row[(m * NB + k / SUB) * 16 + 8];
-                    }
+                    e[0] = row[k / SUB * 8];
+                    e[1] = row[(NB + k / SUB) * 8];
                 }
-                if ((k & 1) == 0) ldmatrix4(x, cols + (swz ^ (uint32_t)(k * 32)));
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
                     uint32_t a[4];
-                    U::kstep(w[m], k % SPT, lo[m].y, hi[m].y, a);
-                    const uint32_t b0 = x[2 * (k & 1)], b1 = x[2 * (k & 1) + 1];
+                    fragment(w[m][k / SPT], k % SPT, e[m].y, e[m].w, a);
+                    const uint32_t b0 = x[k / 2][2 * (k & 1)], b1 = x[k / 2][2 * (k & 1) + 1];
                     if (SUB <= KG && k % SUB == 0) mma16816<BF>(acc[m], a, b0, b1, zero4);
                     else mma16816<BF>(acc[m], a, b0, b1, acc[m]);
-                    if (SUB <= KG && k % SUB == SUB - 1) scale(acc[m], lo[m].x, hi[m].x, y[m]);
                 }
+                if (SUB <= KG && k % SUB == SUB - 1) scale();
             }
             mine += TPG * kTileBytes;
-            swz ^= KG * 32;  // the next KG / 2 groups of 4 pieces (KG = 4: the pieces' third bit)
-            if constexpr (SUB <= KG) row += KG / SUB * 16;
+            cols += KG * 32;
+            if constexpr (SUB <= KG) row += KG / SUB * 8;
         }
-        if constexpr (SUB > KG) {
-#pragma unroll
-            for (int m = 0; m < 2; ++m) scale(acc[m], lo[m].x, hi[m].x, y[m]);
-        }
+        if constexpr (SUB > KG) scale();
     }
 
-    static __device__ __forceinline__ void scale(const float (&acc)[4], uint32_t lo, uint32_t hi, float (&y)[4]) {
-        y[0] = fmaf(__uint_as_float(lo), acc[0], y[0]);
-        y[1] = fmaf(__uint_as_float(lo), acc[1], y[1]);
-        y[2] = fmaf(__uint_as_float(hi), acc[2], y[2]);
-        y[3] = fmaf(__uint_as_float(hi), acc[3], y[3]);
+    // The sums as they are.
+    static __device__ __forceinline__ void unscale(float (&y)[2][4]) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[m][j] *= j < 2 ? kUnscale : kUnscale / kLift8;
+        }
     }
 };
 
@@ -434,7 +481,7 @@ struct Cursor {
 
 template <int BITS, bool BF, int BSL>
 __global__ void __launch_bounds__(kThreads, 2) gate_up_kernel(const __grid_constant__ Params p) {
-    using It = Item<BITS, BF, BSL>;
+    using It = Item<BITS, BF, BSL, BF>;
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * kRingBytes);
@@ -535,6 +582,7 @@ __global__ void __launch_bounds__(kThreads, 2) gate_up_kernel(const __grid_const
     auto finish = [&](int u) {
         const int sg = u / NT, rt = u - sg * NT;
         const Seg s = L.seg[sg];
+        It::unscale(y);
 #pragma unroll 1
         for (int j = 0; j < 4; ++j) {  // (one at a time: four abreast need 30 registers more)
             const int col = 2 * (lane & 3) + (j & 1), row = rt * 16 + (lane >> 2) + 8 * (j >> 1);
@@ -542,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 2) gate_up_kernel(const __grid_const
             const float v0 = j == 0 ? y[1][0] : j == 1 ? y[1][1] : j == 2 ? y[1][2] : y[1][3];
             if (col < s.cnt) {
                 const int pair = L.sorted[s.first + col];
-                const float v = row < p.a.N ? activate(g, p.act) * v0 * L.w[pair] : 0.f;
+                const float v = row < p.a.N ? activate(g, p.act) * v0 * L.w[pair] * kColumnScale : 0.f;
                 const __nv_bfloat16 hi = __float2bfloat16_rn(v);
                 const float rest = v - __bfloat162float(hi);  // exact; NaN beside an infinity
                 uint16_t* dst = p.h + (int64_t)pair * 2 * p.inner + row;
@@ -614,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 2) gate_up_kernel(const __grid_const
 
 template <int BITS, int BSL>
 __global__ void __launch_bounds__(kThreads, 2) down_kernel(const __grid_constant__ Params p) {
-    using It = Item<BITS, true, BSL>;
+    using It = Item<BITS, true, BSL, false>;
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * kRingBytes);
@@ -732,6 +780,7 @@ __global__ void __launch_bounds__(kThreads, 2) down_kernel(const __grid_constant
         if (cur.c == 0 || cur.i == i1) {
             // the segment ends: its pairs' high and low parts are added and go to their tokens' sums
             const Seg s = L.seg[u];
+            It::unscale(y);
             if ((lane & 3) < s.cnt) {
                 float* dst = mine + L.token[s.first + (lane & 3)] * 32 + (lane >> 2);
 #pragma unroll
@@ -780,7 +829,7 @@ void set_vectors(Params& p, int bits) {
 
 template <int BITS, bool BF, int BSL>
 cudaError_t launch_gate_up(Params p, cudaStream_t s) {
-    using It = Item<BITS, BF, BSL>;
+    using It = Item<BITS, BF, BSL, BF>;
     set_vectors<It>(p, BITS);
     auto kern = gate_up_kernel<BITS, BF, BSL>;
     const int P = p.r.T * p.r.S;
@@ -795,7 +844,7 @@ cudaError_t launch_gate_up(Params p, cudaStream_t s) {
 
 template <int BITS, int BSL>
 cudaError_t launch_down(Params p, cudaStream_t s) {
-    using It = Item<BITS, true, BSL>;
+    using It = Item<BITS, true, BSL, false>;
     set_vectors<It>(p, BITS);
     auto kern = down_kernel<BITS, BSL>;
     const size_t smem = (size_t)kWarps * (kRingBytes + It::kTabBytes + p.r.T * 32 * 4) + Lists::bytes(p.r.T * p.r.S);
