@@ -8,8 +8,9 @@
 // row.  A cluster of CTAs takes a row, each CTA a range of its tokens:
 //
 //   1. the range goes to shared memory (one pass over memory) with its maximum;
-//   2. 2048 bins of equal width in max - x get the tokens' counts and the sums
-//      of their weights; the cluster adds them and each CTA forms the prefix;
+//   2. 2048 bins of equal width in max - x get the sums of their tokens' weights
+//      (under top-k first their counts, which need no weights); the cluster adds
+//      them and each CTA forms the prefix;
 //   3. a place in the order (the k-th token, the share p, the draw) lies in one
 //      bin: its tokens, or those of all bins up to it, if at most 1024, go to
 //      the first CTA, which sorts them and takes their sums in order;
@@ -23,9 +24,8 @@
 // of atomics changes them: results repeat, and agree with 64-bit floats but for
 // places that those do not settle either.
 //
-// Bound: the logits' bytes for many rows, in principle; the arithmetic of the
-// weights (35 instructions a token) is longer than those.  With top-k alone or
-// first, step 2 only counts.
+// Bound: the arithmetic of the weights (about 45 instructions a token) and one
+// returning shared-memory atomic, not the logits' bytes.
 #include <algorithm>
 #include <cmath>
 
@@ -34,9 +34,9 @@
 namespace mnb {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kBins = 2048, kPer = kBins / kThreads;  // bins of a thread in the prefix
+constexpr int kBins = 2048;
 constexpr int kList = 1024;                            // tokens that the first CTA sorts
+constexpr int kRankSort = 256;                         // up to so many by counting those before each
 constexpr int kUnit = 43;                              // a weight of 1 is 2^43 units
 constexpr int kMaxVocab = 1 << 24;
 constexpr float kCut = 46.f;                           // weights below 2^-46 are 0 units
@@ -118,16 +118,14 @@ struct Scale {
     float top, c_hi, c_lo, cut, per;  // maximum, log2 e / T in two floats, largest max - x of a weight above 0, bins per unit of max - x
 };
 
-// 2^-y of a token, y = (top - x) c, as `units` (43 bits) and a right shift.
+// 2^-y of a token, y = (top - x) c, as `units` (43 bits) and a right shift.  (top is finite.)
 __device__ __forceinline__ long long weight_parts(float x, const Scale& s, const unsigned long long* table, int& shift) {
     const float d = s.top - x;
     // d's own rounding error (exact: d + e = top - x)
     const float b = d - s.top;
-    const float e = x == s.top ? 0.f : (s.top - (d - b)) + (-x - b);
-    const float p = x == s.top ? 0.f : d * s.c_hi;
-    float rest = fmaf(d, s.c_hi, -p);
-    rest = fmaf(d, s.c_lo, rest);
-    rest = x == s.top ? 0.f : fmaf(e, s.c_hi, rest);
+    const float e = (s.top - (d - b)) + (-x - b);
+    const float p = d * s.c_hi;
+    const float rest = fmaf(e, s.c_hi, fmaf(d, s.c_lo, fmaf(d, s.c_hi, -p)));
     const float q = p + 12288.f;  // 1.5 * 2^13: p in units of 2^-10
     const int k = __float_as_int(q) - 0x46400000;
     const float z = (p - (q - 12288.f)) + rest;  // |z| <= 2^-11 and a little
@@ -140,40 +138,47 @@ __device__ __forceinline__ long long weight_parts(float x, const Scale& s, const
 }
 
 __device__ __forceinline__ unsigned long long weight_of(float x, const Scale& s, const unsigned long long* table, int extra) {
-    if (!(s.top - x <= s.cut) && x != s.top) return 0ull;  // also NaN and -inf
+    if (!(s.top - x <= s.cut)) return 0ull;  // also NaN and -inf
     int shift;
     const unsigned long long t = (unsigned long long)weight_parts(x, s, table, shift);
     shift += extra;
-    return shift > 0 ? (t + (1ull << (shift - 1))) >> shift : t;
+    return (t + ((1ull << shift) >> 1)) >> shift;
 }
 
+// Bin of a token of max - x = d: equal widths, -1 for a weight of 0 (NaN too).
 __device__ __forceinline__ int bin_of(float x, const Scale& s) {
-    const float d = x == s.top ? 0.f : s.top - x;
-    return d <= s.cut ? min((int)(d * s.per), kBins - 1) : -1;  // NaN: -1
+    const float d = s.top - x;
+    return d <= s.cut ? min(__float_as_int(fmaf(d, s.per, 8388608.f)) - 0x4B000000, kBins - 1) : -1;
 }
 
 // Shared memory of a CTA, before its tokens.
 struct Shared {
     unsigned long long table[1024];
-    unsigned long long mw[kBins];      // the cluster's sums, then their prefix
-    unsigned long long list[kList];    // (order, index) of gathered tokens
-    unsigned long long sums[kList];    // their weights' prefix
-    uint32_t mc[kBins];
-    uint32_t cnt[kBins], lo[kBins], hi[kBins];
-    unsigned long long scan_w[kWarps];
-    unsigned long long minp_w, total_w, res_w, found_w;
-    uint32_t scan_c[kWarps];
-    uint32_t top_key, listed, first_index, kmin, kmax, ties[8], found, found2, res_token;
-    uint32_t total_c;
+    unsigned long long mw[kBins];  // the cluster's sums, then their prefix
+    uint32_t mc[kBins];            // the cluster's counts, then their prefix
+    union {
+        struct {
+            uint32_t cnt[kBins], lo[kBins], hi[kBins];  // this CTA's, while they are gathered
+        };
+        struct {
+            unsigned long long list[kList];  // (order, index) of the cluster's gathered tokens (first CTA)
+            unsigned long long sums[kList];  // this CTA's gathered tokens, then the prefix of the list's weights
+        };
+    };
+    unsigned long long scan_w[32];
+    unsigned long long minp_w, res_w, found_w;
+    uint32_t scan_c[32];
+    uint32_t top_key, listed, mine, first_index, kmin, kmax, ties[8], found, found2, res_token;
     float res_x;
 };
 
-template <int DT>
+template <int DT, int THREADS>
 struct Row {
     static constexpr int E = DT == kF32 ? 4 : 8;  // tokens of a 16-byte window
     const uint8_t* base;                           // first window (16-byte aligned)
     int windows, skip, n, first;                   // windows; tokens before the range in the first; tokens; index of the first token
     bool edges;                                    // the first and last windows hold other memory
+    bool inf;                                      // the maximum is +inf: those tokens count as 0, all others as -inf
 
     __device__ __forceinline__ static void widen(const uint4& v, float (&x)[E]) {
         const uint32_t u[4] = {v.x, v.y, v.z, v.w};
@@ -208,11 +213,18 @@ struct Row {
         }
         return make_uint4(u[0], u[1], u[2], u[3]);
     }
+    __device__ __forceinline__ void values(int w, float (&x)[E]) const {
+        widen(raw(w), x);
+        if (inf) {
+#pragma unroll
+            for (int j = 0; j < E; ++j) x[j] = x[j] == INFINITY ? 0.f : -INFINITY;
+        }
+    }
     template <class F>
     __device__ __forceinline__ void each(F&& f) const {
-        for (int w = threadIdx.x; w < windows; w += kThreads) {
+        for (int w = threadIdx.x; w < windows; w += THREADS) {
             float x[E];
-            widen(raw(w), x);
+            values(w, x);
 #pragma unroll
             for (int j = 0; j < E; ++j) f(x[j], w * E + j);
         }
@@ -220,11 +232,12 @@ struct Row {
     __device__ __forceinline__ int index(int at) const { return first + at - skip; }
 };
 
-template <int DT>
+template <int DT, int THREADS>
 struct Sampler {
+    static constexpr int kWarps = THREADS / 32, kPer = kBins / THREADS;  // bins of a thread in the prefix
     Shared& S;
     const SampleParams& p;
-    Row<DT> row;
+    Row<DT, THREADS> row;
     Scale sc;
     int rank;
     int tid, lane, warp;
@@ -234,30 +247,32 @@ struct Sampler {
         else __syncthreads();
     }
 
-    // Bins' counts (and sums of weights) over the cluster, then their prefix in mc and mw.  bin(x) < 0: not counted.
-    template <bool WEIGHTS, class B>
+    // Bins' counts (CNT) and sums of weights (WGT) over the cluster, then their prefix in mc and mw.  bin(x) < 0: in none.
+    // MINP: minp_w gets the sum of the weights from `minp` on.
+    template <bool CNT, bool WGT, bool MINP, class B>
     __device__ __forceinline__ void histogram(B&& bin, unsigned long long minp) {
-        for (int i = tid; i < kBins; i += kThreads) {
-            S.cnt[i] = 0u;
-            if (WEIGHTS) S.lo[i] = S.hi[i] = 0u;
+        __syncthreads();
+        for (int i = tid; i < kBins; i += THREADS) {
+            if (CNT) S.cnt[i] = 0u;
+            if (WGT) S.lo[i] = S.hi[i] = 0u;
         }
-        if (tid == 0) S.minp_w = 0ull;
+        if (MINP && tid == 0) S.minp_w = 0ull;
         __syncthreads();
         unsigned long long keep = 0ull;
         row.each([&](float x, int) {
             const int b = bin(x);
             if (b < 0) return;
-            atomicAdd(&S.cnt[b], 1u);
-            if (WEIGHTS) {
+            if (CNT) atomicAdd(&S.cnt[b], 1u);
+            if (WGT) {
                 const unsigned long long w = weight_of(x, sc, S.table, p.extra);
-                if (w >= minp) keep += w;
+                if (MINP && w >= minp) keep += w;
                 const uint32_t lo = (uint32_t)w;
                 const uint32_t old = atomicAdd(&S.lo[b], lo);
                 const uint32_t hi = (uint32_t)(w >> 32) + (old + lo < old ? 1u : 0u);
                 if (hi) atomicAdd(&S.hi[b], hi);
             }
         });
-        if (WEIGHTS && minp != ~0ull) {
+        if (MINP) {
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) keep += __shfl_xor_sync(0xFFFFFFFFu, keep, o);
             if (lane == 0) atomicAdd(&S.minp_w, keep);
@@ -266,29 +281,29 @@ struct Sampler {
             cluster_sync();
             // each CTA adds a slice of the bins and hands it to all
             const int slice = kBins / p.C, b0 = rank * slice;
-            for (int i = tid; i < slice; i += kThreads) {
+            for (int i = tid; i < slice; i += THREADS) {
                 uint32_t c = 0;
                 unsigned long long w = 0;
                 for (int r = 0; r < p.C; ++r) {
-                    c += ld_u32(&S.cnt[b0 + i], r);
-                    if (WEIGHTS) w += ld_u32(&S.lo[b0 + i], r) + ((unsigned long long)ld_u32(&S.hi[b0 + i], r) << 32);
+                    if (CNT) c += ld_u32(&S.cnt[b0 + i], r);
+                    if (WGT) w += ld_u32(&S.lo[b0 + i], r) + ((unsigned long long)ld_u32(&S.hi[b0 + i], r) << 32);
                 }
                 for (int r = 0; r < p.C; ++r) {
-                    st_u32(&S.mc[b0 + i], r, c);
-                    if (WEIGHTS) st_u64(&S.mw[b0 + i], r, w);
+                    if (CNT) st_u32(&S.mc[b0 + i], r, c);
+                    if (WGT) st_u64(&S.mw[b0 + i], r, w);
                 }
             }
             unsigned long long all = 0;
-            if (WEIGHTS && minp != ~0ull && tid == 0) {
+            if (MINP && tid == 0) {
                 for (int r = 0; r < p.C; ++r) all += ld_u64(&S.minp_w, r);
             }
             cluster_sync();
-            if (WEIGHTS && minp != ~0ull && tid == 0) S.minp_w = all;  // (every CTA has read the others' parts)
+            if (MINP && tid == 0) S.minp_w = all;  // (every CTA has read the others' parts)
         } else {
             __syncthreads();
-            for (int i = tid; i < kBins; i += kThreads) {
-                S.mc[i] = S.cnt[i];
-                if (WEIGHTS) S.mw[i] = S.lo[i] + ((unsigned long long)S.hi[i] << 32);
+            for (int i = tid; i < kBins; i += THREADS) {
+                if (CNT) S.mc[i] = S.cnt[i];
+                if (WGT) S.mw[i] = S.lo[i] + ((unsigned long long)S.hi[i] << 32);
             }
             __syncthreads();
         }
@@ -297,17 +312,17 @@ struct Sampler {
         unsigned long long w[kPer], ws = 0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            cs += S.mc[tid * kPer + i];
+            if (CNT) cs += S.mc[tid * kPer + i];
             c[i] = cs;
-            if (WEIGHTS) ws += S.mw[tid * kPer + i];
+            if (WGT) ws += S.mw[tid * kPer + i];
             w[i] = ws;
         }
         uint32_t ci = cs;
         unsigned long long wi = ws;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t a = __shfl_up_sync(0xFFFFFFFFu, ci, o);
-            const unsigned long long b = __shfl_up_sync(0xFFFFFFFFu, wi, o);
+            const uint32_t a = CNT ? __shfl_up_sync(0xFFFFFFFFu, ci, o) : 0u;
+            const unsigned long long b = WGT ? __shfl_up_sync(0xFFFFFFFFu, wi, o) : 0ull;
             if (lane >= o) {
                 ci += a;
                 wi += b;
@@ -320,14 +335,15 @@ struct Sampler {
         __syncthreads();
         uint32_t cb = ci - cs;
         unsigned long long wb = wi - ws;
-        for (int k = 0; k < warp; ++k) {
-            cb += S.scan_c[k];
-            wb += S.scan_w[k];
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) {
+            if (CNT) cb += k < warp ? S.scan_c[k] : 0u;
+            if (WGT) wb += k < warp ? S.scan_w[k] : 0ull;
         }
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            S.mc[tid * kPer + i] = cb + c[i];
-            if (WEIGHTS) S.mw[tid * kPer + i] = wb + w[i];
+            if (CNT) S.mc[tid * kPer + i] = cb + c[i];
+            if (WGT) S.mw[tid * kPer + i] = wb + w[i];
         }
         __syncthreads();
     }
@@ -350,47 +366,80 @@ struct Sampler {
         return b;
     }
 
-    // Tokens with in(x) into the first CTA's list, sorted there, with the prefix of their weights; their number.
+    // The number of tokens with in(x); if it is at most kList, they are in the first CTA's list, sorted, with the prefix of
+    // their weights.
     template <class P>
     __device__ __forceinline__ int gather(P&& in) {
-        if (tid == 0) S.listed = 0u;
+        if (tid == 0) S.listed = S.mine = 0u;
         sync();
         row.each([&](float x, int at) {
             if (!in(x)) return;
-            const unsigned long long v = ((unsigned long long)(~key_of(x)) << 32) | (uint32_t)row.index(at);
-            if (p.C > 1) {
-                const uint32_t i = add_u32(&S.listed, 0, 1u);
-                if (i < kList) st_u64(&S.list[i], 0, v);
-            } else {
-                const uint32_t i = atomicAdd(&S.listed, 1u);
-                if (i < kList) S.list[i] = v;
-            }
+            // the lanes that found one take places together
+            const uint32_t mask = __activemask();
+            const int leader = __ffs(mask) - 1;
+            uint32_t i = 0;
+            if (lane == leader) i = atomicAdd(&S.mine, (uint32_t)__popc(mask));
+            i = __shfl_sync(mask, i, leader) + __popc(mask & ((1u << lane) - 1u));
+            if (i < kList) S.sums[i] = ((unsigned long long)(~key_of(x)) << 32) | (uint32_t)row.index(at);
         });
-        sync();
-        if (rank != 0) return 0;
-        const int n = min((int)S.listed, kList);
-        int size = 32;
-        while (size < n) size *= 2;
-        for (int i = n + tid; i < size; i += kThreads) S.list[i] = ~0ull;
         __syncthreads();
-        for (int k = 2; k <= size; k *= 2) {
-            for (int j = k / 2; j > 0; j /= 2) {
-                for (int t = tid; t < size / 2; t += kThreads) {
-                    const int a = 2 * t - (t & (j - 1)), b = a + j;
-                    const unsigned long long x = S.list[a], y = S.list[b];
-                    if ((x > y) == ((a & k) == 0)) {
-                        S.list[a] = y;
-                        S.list[b] = x;
+        const uint32_t mine = S.mine;
+        if (p.C > 1) {
+            if (tid == 0) S.found = mine ? add_u32(&S.listed, 0, mine) : 0u;
+            __syncthreads();
+            const uint32_t at = S.found;
+            for (uint32_t i = tid; i < mine && at + i < kList && i < kList; i += THREADS) st_u64(&S.list[at + i], 0, S.sums[i]);
+            cluster_sync();
+            if (tid == 0) S.found = ld_u32(&S.listed, 0);
+            __syncthreads();
+        } else {
+            for (uint32_t i = tid; i < mine && i < kList; i += THREADS) S.list[i] = S.sums[i];
+            if (tid == 0) S.found = mine;
+            __syncthreads();
+        }
+        const int n = (int)S.found;
+        __syncthreads();
+        if (n <= kList && rank == 0) sort(n);
+        return n;
+    }
+
+    __device__ __forceinline__ void sort(int n) {
+        unsigned long long w[kList / THREADS], s = 0;
+        if (n <= kRankSort) {
+            // the place of a token is the number of those before it
+            const unsigned long long v = tid < n ? S.list[tid] : ~0ull;
+            int place = 0;
+            if (tid < n) {
+#pragma unroll 4
+                for (int i = 0; i < n; ++i) place += S.list[i] < v ? 1 : 0;
+            }
+            __syncthreads();
+            if (tid < n) S.list[place] = v;
+            __syncthreads();
+        } else {
+            int size = 512;
+            while (size < n) size *= 2;
+            for (int i = n + tid; i < size; i += THREADS) S.list[i] = ~0ull;
+            __syncthreads();
+            for (int k = 2; k <= size; k *= 2) {
+                for (int j = k / 2; j > 0; j /= 2) {
+                    for (int t = tid; t < size / 2; t += THREADS) {
+                        const int a = 2 * t - (t & (j - 1)), b = a + j;
+                        const unsigned long long x = S.list[a], y = S.list[b];
+                        if ((x > y) == ((a & k) == 0)) {
+                            S.list[a] = y;
+                            S.list[b] = x;
+                        }
                     }
+                    __syncthreads();
                 }
-                __syncthreads();
             }
         }
-        // two tokens a thread
-        unsigned long long w[2], s = 0;
+        // the prefix of the weights: kList / THREADS tokens a thread
+        constexpr int per = kList / THREADS;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int at = 2 * tid + i;
+        for (int i = 0; i < per; ++i) {
+            const int at = per * tid + i;
             s += at < n ? weight_of(value_of(~(uint32_t)(S.list[at] >> 32)), sc, S.table, p.extra) : 0ull;
             w[i] = s;
         }
@@ -403,22 +452,19 @@ struct Sampler {
         if (lane == 31) S.scan_w[warp] = si;
         __syncthreads();
         unsigned long long before = si - s;
-        for (int k = 0; k < warp; ++k) before += S.scan_w[k];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) S.sums[2 * tid + i] = before + w[i];
+        for (int k = 0; k < kWarps; ++k) before += k < warp ? S.scan_w[k] : 0ull;
+#pragma unroll
+        for (int i = 0; i < per; ++i) S.sums[per * tid + i] = before + w[i];
         __syncthreads();
-        return n;
     }
 
     // (first CTA) First place of the sorted list whose prefix reaches `target`; n - 1 if none does.
     __device__ __forceinline__ int first_listed(unsigned long long target, int n) {
         if (tid == 0) S.found2 = (uint32_t)(n - 1);
         __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int at = 2 * tid + i;
-            if (at < n && S.sums[at] >= target && (at == 0 || S.sums[at - 1] < target)) S.found2 = (uint32_t)at;
-        }
+        for (int at = tid; at < n; at += THREADS)
+            if (S.sums[at] >= target && (at == 0 || S.sums[at - 1] < target)) S.found2 = (uint32_t)at;
         __syncthreads();
         const int at = (int)S.found2;
         __syncthreads();
@@ -431,19 +477,21 @@ struct Sampler {
         if (p.probs) {
             int shift;
             const double w = (double)weight_parts(x, sc, S.table, shift);
-            p.probs[r] = (float)(ldexp(w, -shift - p.extra) / (double)total);
+            p.probs[r] = (float)(w / (double)total * exp2i(-shift - p.extra));
         }
     }
+    static __device__ __forceinline__ double exp2i(int e) { return __longlong_as_double((long long)(1023 + e) << 52); }
 
     // The token at a place of the order: the first whose prefix of counts (COUNT) or weights reaches `target`, which the
-    // prefix in mc / mw of the bins by max - x does in bin `b`.  Every CTA gets its index, its logit and the sum of weights up to it.
+    // prefix in mc / mw of the bins by max - x does in bin `b`.  Every CTA gets the sum of weights up to it (found_w), the
+    // first its index and logit.  True if the bins' prefixes were overwritten.
     template <bool COUNT>
-    __device__ __forceinline__ void resolve(int b, unsigned long long target) {
+    __device__ __forceinline__ bool resolve(int b, unsigned long long target) {
+        b = max(b, 0);
         unsigned long long base_w = b ? S.mw[b - 1] : 0ull;
-        uint32_t base_c = b ? S.mc[b - 1] : 0u, n = S.mc[b] - base_c;
+        uint32_t base_c = COUNT && b ? S.mc[b - 1] : 0u, kmin = 0u, kmax = ~0u;
+        bool divided = false;
         __syncthreads();
-        const Scale s0 = sc;
-        uint32_t kmin = 0u, kmax = ~0u;
         auto extent = [&](auto&& in) {  // lowest and highest key of the tokens in(x)
             if (tid == 0) {
                 S.kmin = ~0u;
@@ -474,25 +522,26 @@ struct Sampler {
             kmax = S.kmax;
             __syncthreads();
         };
-        extent([&](float x) { return bin_of(x, s0) == b; });
-        while (n > kList && kmin < kmax) {
+        // (a NaN's key is above or below every number's, so x == x is asked)
+        auto in = [&](float x) { return divided ? x == x && key_of(x) >= kmin && key_of(x) <= kmax : bin_of(x, sc) == b; };
+        int m;
+        while ((m = gather(in)) > kList) {
+            if (!divided) extent(in);
+            divided = true;
+            if (kmin == kmax) break;
             const uint32_t k0 = kmin, k1 = kmax;
             const unsigned long long span = (unsigned long long)(k1 - k0) + 1ull;
-            // NaN is in no bin: its key is above or below every finite one's, and x == x is asked
             auto sub = [&](float x) {
                 const uint32_t k = key_of(x);
                 return x == x && k >= k0 && k <= k1 ? (int)((unsigned long long)(k1 - k) * kBins / span) : -1;
             };
-            histogram<true>(sub, ~0ull);
+            histogram<COUNT, true, false>(sub, 0ull);
             const int f = max(first_bin<COUNT>(target - (COUNT ? (unsigned long long)base_c : base_w)), 0);  // (one always does)
-            n = S.mc[f] - (f ? S.mc[f - 1] : 0u);
-            base_c += f ? S.mc[f - 1] : 0u;
+            if (COUNT) base_c += f ? S.mc[f - 1] : 0u;
             base_w += f ? S.mw[f - 1] : 0ull;
             extent([&](float x) { return sub(x) == f; });
         }
-        auto in = [&](float x) { return x == x && key_of(x) >= kmin && key_of(x) <= kmax; };
-        if (n <= kList) {
-            const int m = gather(in);
+        if (m <= kList) {
             if (rank == 0) {
                 const int at = COUNT ? min((int)(target - base_c), m) - 1 : first_listed(target - base_w, m);
                 if (tid == 0) {
@@ -507,14 +556,14 @@ struct Sampler {
             const unsigned long long w = weight_of(x0, sc, S.table, p.extra);
             const unsigned long long j = COUNT ? target - base_c : (target - base_w + w - 1) / w;  // from 1; w > 0, else no target is here
             // a thread counts windows that follow each other
-            const int per = (row.windows + kThreads - 1) / kThreads;
+            const int per = (row.windows + THREADS - 1) / THREADS;
             const int w0 = min(tid * per, row.windows), w1 = min(w0 + per, row.windows);
             uint32_t c = 0;
             for (int i = w0; i < w1; ++i) {
-                float x[Row<DT>::E];
-                Row<DT>::widen(row.raw(i), x);
+                float x[Row<DT, THREADS>::E];
+                row.values(i, x);
 #pragma unroll
-                for (int e = 0; e < Row<DT>::E; ++e) c += in(x[e]) ? 1u : 0u;
+                for (int e = 0; e < Row<DT, THREADS>::E; ++e) c += in(x[e]) ? 1u : 0u;
             }
             uint32_t ci = c;
 #pragma unroll
@@ -538,12 +587,12 @@ struct Sampler {
             if (j > before && j <= (unsigned long long)before + c) {
                 uint32_t left = (uint32_t)(j - before);
                 for (int i = w0; i < w1; ++i) {
-                    float x[Row<DT>::E];
-                    Row<DT>::widen(row.raw(i), x);
+                    float x[Row<DT, THREADS>::E];
+                    row.values(i, x);
 #pragma unroll
-                    for (int e = 0; e < Row<DT>::E; ++e)
+                    for (int e = 0; e < Row<DT, THREADS>::E; ++e)
                         if (in(x[e]) && --left == 0u) {
-                            const uint32_t token = (uint32_t)row.index(i * Row<DT>::E + e);
+                            const uint32_t token = (uint32_t)row.index(i * Row<DT, THREADS>::E + e);
                             if (p.C > 1) st_u32(&S.res_token, 0, token);
                             else S.res_token = token;
                         }
@@ -555,22 +604,22 @@ struct Sampler {
             }
         }
         sync();
-        if (p.C > 1 && rank != 0 && tid == 0) S.found_w = ld_u64(&S.res_w, 0);
-        else if (tid == 0) S.found_w = S.res_w;
+        if (tid == 0) S.found_w = p.C > 1 ? ld_u64(&S.res_w, 0) : S.res_w;
         sync();  // (the next resolve writes the first CTA's result)
+        return divided;
     }
 };
 
-template <int DT>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) {
+template <int DT, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const SampleParams p) {
     extern __shared__ __align__(16) uint8_t smem[];
     Shared& S = *reinterpret_cast<Shared*>(smem);
     uint8_t* data = smem + (sizeof(Shared) + 15) / 16 * 16;
-    constexpr int E = Row<DT>::E, esize = 16 / E;
+    constexpr int E = Row<DT, THREADS>::E, esize = 16 / E;
     const int tid = threadIdx.x;
     const int rank = p.C > 1 ? (int)cluster_ctarank() : 0;
     const int64_t r = blockIdx.x / p.C;
-    for (int i = tid; i < 1024; i += kThreads) S.table[i] = g_table.v[i];
+    for (int i = tid; i < 1024; i += THREADS) S.table[i] = g_table.v[i];
     if (tid == 0) {
         S.top_key = 0u;
         S.first_index = ~0u;
@@ -593,7 +642,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
     }
 
     // ---- 1. the range, and the row's maximum ----
-    Row<DT> row;
+    Row<DT, THREADS> row;
     row.first = min(rank * p.seg, p.V);
     row.n = min(p.seg, p.V - row.first);
     const uint8_t* src = static_cast<const uint8_t*>(p.logits) + (size_t)(r * p.stride + row.first) * esize;
@@ -601,12 +650,13 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
     row.skip = (int)(src - row.base) / esize;
     row.windows = row.n > 0 ? (row.skip + row.n + E - 1) / E : 0;
     row.edges = true;
+    row.inf = false;
     float top = -INFINITY;
-    for (int w = tid; w < row.windows; w += kThreads) {
+    for (int w = tid; w < row.windows; w += THREADS) {
         const uint4 v = row.raw(w);
         if (p.staged) *reinterpret_cast<uint4*>(data + (size_t)w * 16) = v;
         float x[E];
-        Row<DT>::widen(v, x);
+        Row<DT, THREADS>::widen(v, x);
 #pragma unroll
         for (int j = 0; j < E; ++j) top = fmaxf(top, x[j]);  // passes over NaN
     }
@@ -622,7 +672,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
             for (int c = 0; c < p.C; ++c) max_u32(&S.top_key, c, k);
         else atomicMax(&S.top_key, k);
     }
-    Sampler<DT> q{S, p, row, {}, rank, tid, tid & 31, tid >> 5};
+    Sampler<DT, THREADS> q{S, p, row, {}, rank, tid, tid & 31, tid >> 5};
     q.sync();
     top = value_of(S.top_key);
     if (top == -INFINITY) {  // nothing can be drawn
@@ -632,7 +682,6 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
         }
         return;
     }
-    q.sc.top = top;
     if (temperature == 0.f) {
         // the first token with the maximum
         uint32_t at = ~0u;
@@ -651,6 +700,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
         }
         return;
     }
+    q.row.inf = top == INFINITY;
+    q.sc.top = q.row.inf ? 0.f : top;
     const double c = fmin(1.4426950408889634 / (double)temperature, 1e38);
     q.sc.c_hi = (float)c;
     q.sc.c_lo = (float)(c - (double)q.sc.c_hi);
@@ -661,48 +712,56 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
     const unsigned long long one = 1ull << (kUnit - p.extra);
     const unsigned long long minp = min_p > 0.f ? (unsigned long long)ceil((double)fminf(min_p, 1.f) * (double)one) : 0ull;
     auto bin = [&](float x) { return bin_of(x, q.sc); };
+    auto weigh = [&] {
+        if (minp) q.template histogram<false, true, true>(bin, minp);
+        else q.template histogram<false, true, false>(bin, 0ull);
+    };
+    auto upto = [&](int last) {
+        return [&, last](float x) { const int b = bin_of(x, q.sc); return b >= 0 && b <= last; };
+    };
     bool by_k = top_k > 0 && top_k < p.V;
-    int last = -1;  // the list takes the bins up to this one
+    int n = kList + 1;  // tokens of the list that holds all that can be kept
+    unsigned long long total = 0ull, kept = 0ull, least = ~0ull;  // sums: of the top k, of what is kept; of what min-p keeps
     if (by_k) {
-        q.template histogram<false>(bin, 0ull);
+        q.template histogram<true, false, false>(bin, 0ull);
         const int b = q.template first_bin<true>((unsigned long long)top_k);
         if (b < 0) by_k = false;  // every token of a weight above 0 is among the k
-        else if (S.mc[b] <= (uint32_t)kList) last = b;
+        else if (S.mc[b] <= (uint32_t)kList) n = q.gather(upto(b));
     }
-    unsigned long long total = 0ull, kept = 0ull, least = 0ull;  // sums: of the top k, of what is kept; of what min-p keeps
-    if (last < 0) {
-        q.template histogram<true>(bin, minp);
+    if (n > kList) {
+        weigh();
+        if (minp) least = S.minp_w;
         total = S.mw[kBins - 1];
-        least = minp ? S.minp_w : ~0ull;
+        bool whole = true;  // mw is that of the bins
         if (by_k) {
-            q.template resolve<true>(q.template first_bin<true>((unsigned long long)top_k), (unsigned long long)top_k);
+            whole = !q.template resolve<true>(q.template first_bin<true>((unsigned long long)top_k), (unsigned long long)top_k);
             total = S.found_w;
-            q.template histogram<true>(bin, minp);  // (a divided bin took its place)
         }
         kept = total;
         if (top_p < 1.f) {
             unsigned long long target = (unsigned long long)ceil((double)fmaxf(top_p, 0.f) * (double)total);
             target = min(max(target, 1ull), total);
+            if (!whole) weigh();
+            whole = true;
             const int b = q.template first_bin<false>(target);
-            if (S.mc[b] <= (uint32_t)kList) {
-                last = b;
-            } else {
-                q.template resolve<false>(b, target);
+            // a nucleus of a few bins of the largest weights: all of it, and the draw from it
+            if (b < kBins / 4) n = q.gather(upto(b));
+            if (n > kList) {
+                whole = !q.template resolve<false>(b, target);
                 kept = S.found_w;
-                q.template histogram<true>(bin, minp);
             }
         }
-        if (last < 0) {
+        if (n > kList) {
             kept = min(kept, least);
             const unsigned long long target = min((unsigned long long)((double)u * (double)kept) + 1ull, kept);
+            if (!whole) weigh();
             q.template resolve<false>(q.template first_bin<false>(target), target);
             if (rank == 0) q.write(r, (int)S.res_token, S.res_x, kept);
             return;
         }
     }
 
-    // ---- 3. all that can be kept fits the list ----
-    const int n = q.gather([&](float x) { return bin_of(x, q.sc) >= 0 && bin_of(x, q.sc) <= last; });
+    // ---- 3. all that can be kept is in the list ----
     if (rank == 0) {
         if (by_k && total == 0ull) total = S.sums[min(top_k, n) - 1];
         kept = total;
@@ -714,13 +773,9 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
         if (minp) {  // weights descend along the list: the sum of those from minp on
             if (tid == 0) S.minp_w = 0ull;
             __syncthreads();
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int at = 2 * tid + i;
-                if (at < n) {
-                    const unsigned long long w = S.sums[at] - (at ? S.sums[at - 1] : 0ull);
-                    if (w >= minp) atomicAdd(&S.minp_w, w);
-                }
+            for (int at = tid; at < n; at += THREADS) {
+                const unsigned long long w = S.sums[at] - (at ? S.sums[at - 1] : 0ull);
+                if (w >= minp) atomicAdd(&S.minp_w, w);
             }
             __syncthreads();
             kept = min(kept, S.minp_w);
@@ -731,23 +786,28 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p) 
     }
 }
 
-template <int DT>
-cudaError_t launch_sample(SampleParams p, int64_t rows, cudaStream_t s) {
+template <int DT, int THREADS>
+cudaError_t launch_threads(SampleParams p, int64_t rows, cudaStream_t s) {
     constexpr int esize = DT == kF32 ? 4 : 2;
     const size_t fixed = (sizeof(Shared) + 15) / 16 * 16;
-    const size_t limit = device_info().smem_optin;
-    // CTAs a row: until the row's ranges fit a third of an SM's shared memory each, or all SMs have one
-    p.C = 1;
-    auto seg_of = [&](int c) { return ((p.V + c - 1) / c + 7) / 8 * 8; };
-    while (p.C < 8 && ((size_t)seg_of(p.C) * esize > 40 * 1024 || rows * p.C * 2 <= dec::kSms) && p.V > p.C * 2048) p.C *= 2;
-    p.seg = seg_of(p.C);
     size_t bytes = ((size_t)p.seg * esize + 15) / 16 * 16 + 16;
-    p.staged = fixed + bytes <= limit;  // else the passes read memory (L2)
+    // a range in shared memory where two CTAs of 512 threads (one of 1024) still fit an SM; else the passes read L2
+    p.staged = fixed + bytes <= (THREADS == 512 ? device_info().smem_optin / 2 - 1024 : device_info().smem_optin);
     if (!p.staged) bytes = 0;
-    auto kern = sample_kernel<DT>;
+    auto kern = sample_kernel<DT, THREADS>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(fixed + bytes));
     if (e != cudaSuccess) return e;
-    return dec::launch_pdl(kern, dim3((unsigned)(rows * p.C)), dim3(kThreads), fixed + bytes, s, p.C, p);
+    return dec::launch_pdl(kern, dim3((unsigned)(rows * p.C)), dim3(THREADS), fixed + bytes, s, p.C, p);
+}
+
+template <int DT>
+cudaError_t launch_sample(SampleParams p, int64_t rows, cudaStream_t s) {
+    // CTAs a row: as many as the SMs hold at two an SM, up to a portable cluster, none with fewer than 2048 tokens
+    p.C = 1;
+    while (p.C < 8 && rows * p.C * 2 <= 2 * dec::kSms && p.V > p.C * 2048) p.C *= 2;
+    p.seg = ((p.V + p.C - 1) / p.C + 7) / 8 * 8;
+    // few rows: one CTA an SM, of 1024 threads
+    return rows * p.C <= dec::kSms / 2 ? launch_threads<DT, 1024>(p, rows, s) : launch_threads<DT, 512>(p, rows, s);
 }
 
 }  // namespace
