@@ -24,8 +24,8 @@
 // of atomics changes them: results repeat, and agree with 64-bit floats but for
 // places that those do not settle either.
 //
-// Bound: the arithmetic of the weights (about 45 instructions a token) and one
-// returning shared-memory atomic, not the logits' bytes.
+// Bound: the arithmetic of the weights (about 45 instructions a token), not the
+// logits' bytes; few rows: the barriers of a cluster, about 0.7 us each.
 #include <algorithm>
 #include <cmath>
 
@@ -39,7 +39,8 @@ constexpr int kList = 1024;                            // tokens that the first 
 constexpr int kRankSort = 256;                         // up to so many by counting those before each
 constexpr int kUnit = 43;                              // a weight of 1 is 2^43 units
 constexpr int kMaxVocab = 1 << 24;
-constexpr float kCut = 46.f;                           // weights below 2^-46 are 0 units
+constexpr int kGathers = 32;                           // of a row: 2 of nuclei, 3 of places with at most 4 divisions each
+constexpr float kCut = kUnit + 0.99f;                  // weights below 2^-kCut (2^extra times that) are 0 units
 
 // 2^43 * 2^(-j / 1024), from the exponential series in double at compile time (good to 2^-50).
 struct Table {
@@ -89,6 +90,8 @@ __device__ __forceinline__ unsigned long long ld_u64(const unsigned long long* p
     asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(map_to(p, rank)) : "memory");
     return v;
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void st_u32(uint32_t* p, int rank, uint32_t v) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_to(p, rank)), "r"(v) : "memory");
 }
@@ -115,7 +118,8 @@ __device__ __forceinline__ uint32_t key_of(float f) {
 __device__ __forceinline__ float value_of(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k); }
 
 struct Scale {
-    float top, c_hi, c_lo, cut, per;  // maximum, log2 e / T in two floats, largest max - x of a weight above 0, bins per unit of max - x
+    float top, c_hi, c_lo;  // maximum, log2 e / T in two floats
+    float cut, per;         // largest max - x of a weight above 0, bins per unit of max - x
 };
 
 // 2^-y of a token, y = (top - x) c, as `units` (43 bits) and a right shift.  (top is finite.)
@@ -137,12 +141,13 @@ __device__ __forceinline__ long long weight_parts(float x, const Scale& s, const
     return t + (((long long)(int)(t >> 13) * f) >> 29);  // (t / 2^43 in units of 2^-30) * f
 }
 
+// The weight in units of 2^-(43 - extra), rounded.
 __device__ __forceinline__ unsigned long long weight_of(float x, const Scale& s, const unsigned long long* table, int extra) {
-    if (!(s.top - x <= s.cut)) return 0ull;  // also NaN and -inf
     int shift;
     const unsigned long long t = (unsigned long long)weight_parts(x, s, table, shift);
-    shift += extra;
-    return (t + ((1ull << shift) >> 1)) >> shift;
+    shift = (shift + extra) & 63;  // at most 43 up to the cut
+    const unsigned long long w = (t + ((1ull << shift) >> 1)) >> shift;
+    return s.top - x <= s.cut ? w : 0ull;  // also NaN and -inf: 0
 }
 
 // Bin of a token of max - x = d: equal widths, -1 for a weight of 0 (NaN too).
@@ -158,7 +163,7 @@ struct Shared {
     uint32_t mc[kBins];            // the cluster's counts, then their prefix
     union {
         struct {
-            uint32_t cnt[kBins], lo[kBins], hi[kBins];  // this CTA's, while they are gathered
+            uint32_t cnt[kBins], lo[kBins], hi[kBins];  // this CTA's, while they are summed
         };
         struct {
             unsigned long long list[kList];  // (order, index) of the cluster's gathered tokens (first CTA)
@@ -168,7 +173,9 @@ struct Shared {
     unsigned long long scan_w[32];
     unsigned long long minp_w, res_w, found_w;
     uint32_t scan_c[32];
-    uint32_t top_key, listed, mine, first_index, kmin, kmax, ties[8], found, found2, res_token;
+    uint32_t listed[kGathers];  // (first CTA) tokens of each gather
+    uint32_t tops[8], ties[8];  // of each CTA: its largest key; its tokens of a value
+    uint32_t mine, first_index, kmin, kmax, found, found2, res_token;
     float res_x;
 };
 
@@ -221,6 +228,15 @@ struct Row {
         }
     }
     template <class F>
+    __device__ __forceinline__ void each_four(F&& f) const {
+        for (int w = threadIdx.x; w < windows; w += THREADS) {
+            float x[E];
+            values(w, x);
+            f(x);
+            if constexpr (E == 8) f(x + 4);
+        }
+    }
+    template <class F>
     __device__ __forceinline__ void each(F&& f) const {
         for (int w = threadIdx.x; w < windows; w += THREADS) {
             float x[E];
@@ -241,6 +257,7 @@ struct Sampler {
     Scale sc;
     int rank;
     int tid, lane, warp;
+    int gathers = 0;
 
     __device__ __forceinline__ void sync() const {
         if (p.C > 1) cluster_sync();
@@ -253,23 +270,42 @@ struct Sampler {
     __device__ __forceinline__ void histogram(B&& bin, unsigned long long minp) {
         __syncthreads();
         for (int i = tid; i < kBins; i += THREADS) {
-            if (CNT) S.cnt[i] = 0u;
+            S.cnt[i] = 0u;
             if (WGT) S.lo[i] = S.hi[i] = 0u;
         }
         if (MINP && tid == 0) S.minp_w = 0ull;
         __syncthreads();
         unsigned long long keep = 0ull;
-        row.each([&](float x, int) {
-            const int b = bin(x);
-            if (b < 0) return;
-            if (CNT) atomicAdd(&S.cnt[b], 1u);
-            if (WGT) {
-                const unsigned long long w = weight_of(x, sc, S.table, p.extra);
-                if (MINP && w >= minp) keep += w;
-                const uint32_t lo = (uint32_t)w;
-                const uint32_t old = atomicAdd(&S.lo[b], lo);
-                const uint32_t hi = (uint32_t)(w >> 32) + (old + lo < old ? 1u : 0u);
-                if (hi) atomicAdd(&S.hi[b], hi);
+        // Sums of weights: without counts and up to 65536 tokens a CTA as three sums of 16, 16 and the upper bits, which
+        // nobody has to wait for; else of 32 bits with a carry.
+        const bool three = !CNT && p.seg <= 65536;
+        row.each_four([&](const float* x) {
+            int b[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                b[j] = bin(x[j]);
+                if (CNT && b[j] >= 0) atomicAdd(&S.cnt[b[j]], 1u);
+            }
+            // four weights abreast, without a branch: token by token would leave one chain of them at a time
+            if constexpr (WGT) {
+                unsigned long long w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[j] = weight_of(x[j], sc, S.table, p.extra);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (b[j] < 0) continue;
+                    if (MINP && w[j] >= minp) keep += w[j];
+                    const uint32_t lo = (uint32_t)w[j];
+                    uint32_t hi = (uint32_t)(w[j] >> 32);
+                    if (three) {
+                        atomicAdd(&S.lo[b[j]], lo & 0xFFFFu);
+                        atomicAdd(&S.cnt[b[j]], lo >> 16);
+                    } else {
+                        const uint32_t old = atomicAdd(&S.lo[b[j]], lo);
+                        hi += old + lo < old ? 1u : 0u;
+                    }
+                    if (hi) atomicAdd(&S.hi[b[j]], hi);
+                }
             }
         });
         if (MINP) {
@@ -282,15 +318,23 @@ struct Sampler {
             // each CTA adds a slice of the bins and hands it to all
             const int slice = kBins / p.C, b0 = rank * slice;
             for (int i = tid; i < slice; i += THREADS) {
-                uint32_t c = 0;
-                unsigned long long w = 0;
-                for (int r = 0; r < p.C; ++r) {
-                    if (CNT) c += ld_u32(&S.cnt[b0 + i], r);
-                    if (WGT) w += ld_u32(&S.lo[b0 + i], r) + ((unsigned long long)ld_u32(&S.hi[b0 + i], r) << 32);
+                uint32_t c[8], lo[8], hi[8];  // (their loads are independent: a distributed one takes 0.3 us)
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    c[r] = (CNT || three) && r < p.C ? ld_u32(&S.cnt[b0 + i], r) : 0u;
+                    lo[r] = WGT && r < p.C ? ld_u32(&S.lo[b0 + i], r) : 0u;
+                    hi[r] = WGT && r < p.C ? ld_u32(&S.hi[b0 + i], r) : 0u;
+                }
+                uint32_t cs = 0;
+                unsigned long long ws = 0;
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    if (CNT) cs += c[r];
+                    ws += lo[r] + ((unsigned long long)(WGT && three ? c[r] : 0u) << 16) + ((unsigned long long)hi[r] << 32);
                 }
                 for (int r = 0; r < p.C; ++r) {
-                    if (CNT) st_u32(&S.mc[b0 + i], r, c);
-                    if (WGT) st_u64(&S.mw[b0 + i], r, w);
+                    if (CNT) st_u32(&S.mc[b0 + i], r, cs);
+                    if (WGT) st_u64(&S.mw[b0 + i], r, ws);
                 }
             }
             unsigned long long all = 0;
@@ -303,7 +347,7 @@ struct Sampler {
             __syncthreads();
             for (int i = tid; i < kBins; i += THREADS) {
                 if (CNT) S.mc[i] = S.cnt[i];
-                if (WGT) S.mw[i] = S.lo[i] + ((unsigned long long)S.hi[i] << 32);
+                if (WGT) S.mw[i] = S.lo[i] + ((unsigned long long)(three ? S.cnt[i] : 0u) << 16) + ((unsigned long long)S.hi[i] << 32);
             }
             __syncthreads();
         }
@@ -366,12 +410,34 @@ struct Sampler {
         return b;
     }
 
+    // An upper bound of the tokens in the bins up to b: each bin's sum over its least weight.
+    __device__ __forceinline__ float most_tokens(int b) {
+        float n = 0.f;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int j = tid * kPer + i;
+            // (a weight at the far edge, half a bin past its middle, and a unit for the rounding)
+            const float w = (float)(S.mw[j] - (j ? S.mw[j - 1] : 0ull));
+            if (j <= b) n += w * exp2f(((float)j + 1.f) * ((kCut - p.extra) / kBins) - (float)(kUnit - p.extra)) * 1.001f;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
+        if (lane == 0) S.scan_w[warp] = __float_as_uint(n);
+        __syncthreads();
+        n = 0.f;
+        for (int k = 0; k < kWarps; ++k) n += __uint_as_float((uint32_t)S.scan_w[k]);
+        __syncthreads();
+        return n;
+    }
+
     // The number of tokens with in(x); if it is at most kList, they are in the first CTA's list, sorted, with the prefix of
     // their weights.
     template <class P>
     __device__ __forceinline__ int gather(P&& in) {
-        if (tid == 0) S.listed = S.mine = 0u;
-        sync();
+        __syncthreads();
+        if (tid == 0) S.mine = 0u;
+        __syncthreads();
+        uint32_t* const listed = &S.listed[min(gathers++, kGathers - 1)];
         row.each([&](float x, int at) {
             if (!in(x)) return;
             // the lanes that found one take places together
@@ -385,12 +451,12 @@ struct Sampler {
         __syncthreads();
         const uint32_t mine = S.mine;
         if (p.C > 1) {
-            if (tid == 0) S.found = mine ? add_u32(&S.listed, 0, mine) : 0u;
+            if (tid == 0) S.found = mine ? add_u32(listed, 0, mine) : 0u;
             __syncthreads();
             const uint32_t at = S.found;
             for (uint32_t i = tid; i < mine && at + i < kList && i < kList; i += THREADS) st_u64(&S.list[at + i], 0, S.sums[i]);
             cluster_sync();
-            if (tid == 0) S.found = ld_u32(&S.listed, 0);
+            if (tid == 0) S.found = ld_u32(listed, 0);
             __syncthreads();
         } else {
             for (uint32_t i = tid; i < mine && i < kList; i += THREADS) S.list[i] = S.sums[i];
@@ -484,8 +550,8 @@ struct Sampler {
 
     // The token at a place of the order: the first whose prefix of counts (COUNT) or weights reaches `target`, which the
     // prefix in mc / mw of the bins by max - x does in bin `b`.  Every CTA gets the sum of weights up to it (found_w), the
-    // first its index and logit.  True if the bins' prefixes were overwritten.
-    template <bool COUNT>
+    // first its index and logit.  True if the bins' prefixes were overwritten.  LAST: only the first CTA gets anything.
+    template <bool COUNT, bool LAST>
     __device__ __forceinline__ bool resolve(int b, unsigned long long target) {
         b = max(b, 0);
         unsigned long long base_w = b ? S.mw[b - 1] : 0ull;
@@ -603,7 +669,12 @@ struct Sampler {
                 S.res_x = x0;
             }
         }
+        if (LAST && m <= kList) {
+            __syncthreads();
+            return divided;
+        }
         sync();
+        if (LAST) return divided;
         if (tid == 0) S.found_w = p.C > 1 ? ld_u64(&S.res_w, 0) : S.res_w;
         sync();  // (the next resolve writes the first CTA's result)
         return divided;
@@ -620,10 +691,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
     const int rank = p.C > 1 ? (int)cluster_ctarank() : 0;
     const int64_t r = blockIdx.x / p.C;
     for (int i = tid; i < 1024; i += THREADS) S.table[i] = g_table.v[i];
-    if (tid == 0) {
-        S.top_key = 0u;
-        S.first_index = ~0u;
-    }
+    if (tid < kGathers) S.listed[tid] = 0u;
+    if (tid == 0) S.first_index = ~0u;
+    if (p.C > 1) cluster_arrive();  // waited for before the first access to another CTA
     griddep_wait();
     griddep_launch_dependents();
 
@@ -638,6 +708,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
             if (p.probs) p.probs[r] = 0.f;
             set_status(p.status, 1 /* MNB_ERR_INVALID_ARG */);
         }
+        if (p.C > 1) cluster_wait();
         return;  // the whole cluster does
     }
 
@@ -664,17 +735,25 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
         row.base = data;
         row.edges = false;  // the ends hold -inf there
     }
-    if (p.C > 1) cluster_sync();  // every CTA's shared memory is set up
-    else __syncthreads();
     const uint32_t k = __reduce_max_sync(0xFFFFFFFFu, key_of(top));
-    if ((tid & 31) == 0) {
-        if (p.C > 1)
-            for (int c = 0; c < p.C; ++c) max_u32(&S.top_key, c, k);
-        else atomicMax(&S.top_key, k);
+    if ((tid & 31) == 0) S.scan_c[tid >> 5] = k;
+    __syncthreads();
+    if (tid < 32) {
+        const uint32_t mine = __reduce_max_sync(0xFFFFFFFFu, tid < THREADS / 32 ? S.scan_c[tid] : 0u);
+        if (p.C > 1) {
+            cluster_wait();
+            if (tid < p.C) st_u32(&S.tops[rank], tid, mine);
+        } else if (tid == 0) {
+            S.tops[0] = mine;
+        }
+    } else if (p.C > 1) {
+        cluster_wait();
     }
     Sampler<DT, THREADS> q{S, p, row, {}, rank, tid, tid & 31, tid >> 5};
     q.sync();
-    top = value_of(S.top_key);
+    uint32_t best = S.tops[0];
+    for (int c = 1; c < p.C; ++c) best = max(best, S.tops[c]);
+    top = value_of(best);
     if (top == -INFINITY) {  // nothing can be drawn
         if (rank == 0 && tid == 0) {
             p.tokens[r] = -1;
@@ -705,7 +784,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
     const double c = fmin(1.4426950408889634 / (double)temperature, 1e38);
     q.sc.c_hi = (float)c;
     q.sc.c_lo = (float)(c - (double)q.sc.c_hi);
-    q.sc.cut = fminf(__fdiv_rn(kCut, q.sc.c_hi), 3.4e38f);
+    q.sc.cut = fminf(__fdiv_rn(kCut - p.extra, q.sc.c_hi), 3.4e38f);
     q.sc.per = (float)kBins / q.sc.cut;
 
     // ---- 2. bins ----
@@ -734,7 +813,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
         total = S.mw[kBins - 1];
         bool whole = true;  // mw is that of the bins
         if (by_k) {
-            whole = !q.template resolve<true>(q.template first_bin<true>((unsigned long long)top_k), (unsigned long long)top_k);
+            whole = !q.template resolve<true, false>(q.template first_bin<true>((unsigned long long)top_k), (unsigned long long)top_k);
             total = S.found_w;
         }
         kept = total;
@@ -744,10 +823,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
             if (!whole) weigh();
             whole = true;
             const int b = q.template first_bin<false>(target);
-            // a nucleus of a few bins of the largest weights: all of it, and the draw from it
-            if (b < kBins / 4) n = q.gather(upto(b));
+            // a nucleus that fits the list: all of it, and the draw from it
+            if (q.most_tokens(b) <= (float)kList) n = q.gather(upto(b));
             if (n > kList) {
-                whole = !q.template resolve<false>(b, target);
+                whole = !q.template resolve<false, false>(b, target);
                 kept = S.found_w;
             }
         }
@@ -755,7 +834,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
             kept = min(kept, least);
             const unsigned long long target = min((unsigned long long)((double)u * (double)kept) + 1ull, kept);
             if (!whole) weigh();
-            q.template resolve<false>(q.template first_bin<false>(target), target);
+            q.template resolve<false, true>(q.template first_bin<false>(target), target);
             if (rank == 0) q.write(r, (int)S.res_token, S.res_x, kept);
             return;
         }

@@ -776,8 +776,8 @@ MNB_API size_t mnb_moe_workspace_size(int64_t T, int64_t S, int64_t E, int64_t h
  *   min-p   of these, those with w_i >= min_p (0: all; above 1 acts as 1)
  * and the token is the first in that order whose sum of kept weights, its own
  * included, exceeds u times the sum of all kept ones.  T == 0 takes the first
- * token of the order.  Weights below 2^-46 of the largest are never drawn; a
- * NaN counts as -inf.  A row without a logit above -inf gets token -1,
+ * token of the order.  Weights below 2^-44 of the largest (2^-39 for the largest
+ * V) are never drawn; a NaN counts as -inf.  A row without a logit above -inf gets token -1,
  * probability 0.  Sums are exact integers (units of 2^-43 of the largest
  * weight for V below 2^19): results repeat, and agree with 64-bit arithmetic.
  *   logits       device [B, V] of dtype, row stride in elements, aligned to the
