@@ -156,6 +156,25 @@ __device__ __forceinline__ int bin_of(float x, const Scale& s) {
     return d <= s.cut ? min(__float_as_int(fmaf(d, s.per, 8388608.f)) - 0x4B000000, kBins - 1) : -1;
 }
 
+// f * n for 0 <= f <= 1, exactly, rounded down (UP: up).  (Every thread forms it: in integers, as a few 64-bit floating
+// point operations by all of them take microseconds on this part.)
+template <bool UP>
+__device__ __forceinline__ unsigned long long share_of(float f, unsigned long long n) {
+    const uint32_t u = __float_as_uint(f), e = u >> 23;
+    const unsigned long long m = e ? (u & 0x7FFFFFu) | 0x800000u : u & 0x7FFFFFu;
+    const int s = 150 - (int)(e ? e : 1u);  // f = m / 2^s, s from 23 to 149
+    const unsigned long long hi = __umul64hi(m, n), lo = m * n;
+    unsigned long long q, rest;
+    if (s < 64) {
+        q = (hi << (64 - s)) | (lo >> s);
+        rest = lo << (64 - s);
+    } else {
+        q = s < 128 ? hi >> (s - 64) : 0ull;
+        rest = lo | (s < 128 ? hi & ((1ull << (s - 64)) - 1ull) : hi);
+    }
+    return UP && rest ? q + 1ull : q;
+}
+
 // Shared memory of a CTA, before its tokens.
 struct Shared {
     unsigned long long table[1024];
@@ -177,6 +196,7 @@ struct Shared {
     uint32_t tops[8], ties[8];  // of each CTA: its largest key; its tokens of a value
     uint32_t mine, first_index, kmin, kmax, found, found2, res_token;
     float res_x;
+    Scale scale;
 };
 
 template <int DT, int THREADS>
@@ -712,6 +732,14 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
         return;  // the whole cluster does
     }
 
+    if (tid == 0) {  // (64-bit floating point: by one thread, beside the loads)
+        const double c = fmin(1.4426950408889634 / (double)temperature, 1e38);
+        S.scale.c_hi = (float)c;
+        S.scale.c_lo = (float)(c - (double)S.scale.c_hi);
+        S.scale.cut = fminf(__fdiv_rn(kCut - p.extra, S.scale.c_hi), 3.4e38f);
+        S.scale.per = (float)kBins / S.scale.cut;
+    }
+
     // ---- 1. the range, and the row's maximum ----
     Row<DT, THREADS> row;
     row.first = min(rank * p.seg, p.V);
@@ -780,16 +808,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
         return;
     }
     q.row.inf = top == INFINITY;
+    q.sc = S.scale;
     q.sc.top = q.row.inf ? 0.f : top;
-    const double c = fmin(1.4426950408889634 / (double)temperature, 1e38);
-    q.sc.c_hi = (float)c;
-    q.sc.c_lo = (float)(c - (double)q.sc.c_hi);
-    q.sc.cut = fminf(__fdiv_rn(kCut - p.extra, q.sc.c_hi), 3.4e38f);
-    q.sc.per = (float)kBins / q.sc.cut;
 
     // ---- 2. bins ----
     const unsigned long long one = 1ull << (kUnit - p.extra);
-    const unsigned long long minp = min_p > 0.f ? (unsigned long long)ceil((double)fminf(min_p, 1.f) * (double)one) : 0ull;
+    const unsigned long long minp = min_p > 0.f ? share_of<true>(fminf(min_p, 1.f), one) : 0ull;
     auto bin = [&](float x) { return bin_of(x, q.sc); };
     auto weigh = [&] {
         if (minp) q.template histogram<false, true, true>(bin, minp);
@@ -818,8 +842,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
         }
         kept = total;
         if (top_p < 1.f) {
-            unsigned long long target = (unsigned long long)ceil((double)fmaxf(top_p, 0.f) * (double)total);
-            target = min(max(target, 1ull), total);
+            const unsigned long long target = max(share_of<true>(fmaxf(top_p, 0.f), total), 1ull);
             if (!whole) weigh();
             whole = true;
             const int b = q.template first_bin<false>(target);
@@ -832,7 +855,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
         }
         if (n > kList) {
             kept = min(kept, least);
-            const unsigned long long target = min((unsigned long long)((double)u * (double)kept) + 1ull, kept);
+            const unsigned long long target = share_of<false>(u, kept) + 1ull;
             if (!whole) weigh();
             q.template resolve<false, true>(q.template first_bin<false>(target), target);
             if (rank == 0) q.write(r, (int)S.res_token, S.res_x, kept);
@@ -845,21 +868,18 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
         if (by_k && total == 0ull) total = S.sums[min(top_k, n) - 1];
         kept = total;
         if (top_p < 1.f) {
-            unsigned long long target = (unsigned long long)ceil((double)fmaxf(top_p, 0.f) * (double)total);
-            target = min(max(target, 1ull), total);
+            const unsigned long long target = max(share_of<true>(fmaxf(top_p, 0.f), total), 1ull);
             kept = S.sums[q.first_listed(target, n)];
         }
-        if (minp) {  // weights descend along the list: the sum of those from minp on
-            if (tid == 0) S.minp_w = 0ull;
+        if (minp) {  // weights descend along the list: the sum before the first below minp
+            if (tid == 0) S.mine = (uint32_t)n;
             __syncthreads();
-            for (int at = tid; at < n; at += THREADS) {
-                const unsigned long long w = S.sums[at] - (at ? S.sums[at - 1] : 0ull);
-                if (w >= minp) atomicAdd(&S.minp_w, w);
-            }
+            for (int at = tid; at < n; at += THREADS)
+                if (S.sums[at] - (at ? S.sums[at - 1] : 0ull) < minp) atomicMin(&S.mine, (uint32_t)at);
             __syncthreads();
-            kept = min(kept, S.minp_w);
+            kept = min(kept, S.sums[max((int)S.mine, 1) - 1]);
         }
-        const unsigned long long target = min((unsigned long long)((double)u * (double)kept) + 1ull, kept);
+        const unsigned long long target = share_of<false>(u, kept) + 1ull;
         const int at = q.first_listed(target, n);
         q.write(r, (int)(uint32_t)S.list[at], value_of(~(uint32_t)(S.list[at] >> 32)), kept);
     }
