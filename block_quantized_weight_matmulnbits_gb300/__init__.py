@@ -634,20 +634,32 @@ def mnb_cache_compact(state, planes, refs_out, tables_out, counts, workspace=Non
 
 # ---- around the attention: norm, experts, the next token ----------------------------------------
 
-def _here(what, t):
-    """The tensor's address; it has to live on the current device, whose stream the call goes to."""
+# Tensors have to live on the current device, whose stream the call goes to (`dev`, asked once a call).
+
+def _current_device():
+    return -2 if _device is None else _device()
+
+
+def _away(what):
+    _fail(f"{what}: a tensor on the current CUDA device is wanted")
+
+
+def _here(what, t, dev):
     d = t.get_device()
-    if d < 0 or (_device is not None and d != _device()):
-        _fail(f"{what}: a tensor on the current CUDA device is wanted")
+    if d < 0 or (d != dev and dev != -2):
+        _away(what)
     return t.data_ptr()
 
 
-def _row_matrix(what, t, shape, dtype=None):
+def _row_matrix(what, t, shape, dev, dtype=None):
     """(pointer, row stride) of a [rows, columns] tensor with unit stride in a row."""
     st = t.stride()
-    if t.shape != shape or len(shape) != 2 or (st[1] != 1 and shape[1] > 1 and shape[0]) or (dtype is not None and t.dtype is not dtype):
+    if len(st) != 2 or t.shape != shape or (st[1] != 1 and shape[1] > 1 and shape[0]) or (dtype is not None and t.dtype is not dtype):
         _fail(f"{what}: a [rows, columns] tensor of the call's shape and dtype with unit stride in a row is wanted")
-    return _here(what, t), st[0]
+    d = t.get_device()
+    if d < 0 or (d != dev and dev != -2):
+        _away(what)
+    return t.data_ptr(), st[0]
 
 
 def mnb_rms_norm(x, weight, eps, residual=None, residual_out=None, y=None, codes=None, scales=None, block_size=0, flags=0,
@@ -656,24 +668,25 @@ def mnb_rms_norm(x, weight, eps, residual=None, residual_out=None, y=None, codes
     to codes [T, KB * block_size] and scales [T, KB].  x [T, width]; weight [width] or None."""
     if not _codes:
         _setup()
-    shape, dt = x.shape, x.dtype
+    shape, dt, dev = x.shape, x.dtype, _current_device() if x.is_cuda else -2
     code = _codes.get(dt)
     if code is None:
         _fail("x: a float32, float16 or bfloat16 tensor is wanted")
-    xp, xs = _row_matrix("x", x, shape)
-    rp, rs = (None, 0) if residual is None else _row_matrix("residual", residual, shape, dt)
-    sp, ss = (None, 0) if residual_out is None else _row_matrix("residual_out", residual_out, shape, dt)
-    yp, ys, yd = None, 0, 0
+    xp, xs = _row_matrix("x", x, shape, dev)
+    rp = sp = yp = wp = cp = ap = None
+    rs = ss = ys = yd = wd = 0
+    if residual is not None:
+        rp, rs = _row_matrix("residual", residual, shape, dev, dt)
+    if residual_out is not None:
+        sp, ss = _row_matrix("residual_out", residual_out, shape, dev, dt)
     if y is not None:
-        yp, ys = _row_matrix("y", y, shape)
+        yp, ys = _row_matrix("y", y, shape, dev)
         yd = _codes.get(y.dtype, -1)
-    wp, wd = None, 0
     if weight is not None:
         wd = _codes.get(weight.dtype, -1)
         if weight.numel() != shape[1] or not weight.is_contiguous():
             _fail("weight: a contiguous [width] tensor is wanted")
-        wp = _here("weight", weight)
-    cp = ap = None
+        wp = _here("weight", weight, dev)
     if codes is not None or scales is not None:
         if codes is None or scales is None or block_size < 1:
             _fail("codes, scales: both, with a block_size, are wanted")
@@ -681,7 +694,7 @@ def mnb_rms_norm(x, weight, eps, residual=None, residual_out=None, y=None, codes
         if codes.dtype is not _int8 or codes.shape != (shape[0], kb * block_size) or not codes.is_contiguous() or \
                 scales.dtype is not _float32 or scales.shape != (shape[0], kb) or not scales.is_contiguous():
             _fail("codes, scales: contiguous int8 [T, KB * block_size] and f32 [T, KB] tensors are wanted")
-        cp, ap = _here("codes", codes), _here("scales", scales)
+        cp, ap = _here("codes", codes, dev), _here("scales", scales, dev)
     a = RmsNormArgs(xp, rp, sp, wp, yp, cp, ap, shape[0], shape[1], block_size, xs, rs, ss, ys, code, wd, yd, eps, flags, _current(stream))
     st = (_lib or load()).mnb_rms_norm(a)
     if st:
@@ -702,32 +715,33 @@ def expert_weights(packed, scales, zero_points, E, N, K, bits, block_size) -> Ex
     if zero_points is not None and (zero_points.element_size() != 1 or zero_points.numel() != E * N * -(-kb * bits // 8) or
                                     not zero_points.is_contiguous()):
         _fail("zero_points: a contiguous uint8 [E, N, ceil(KB * bits / 8)] tensor is wanted")
-    w = ExpertWeights(_here("packed", packed), _here("scales", scales), None if zero_points is None else _here("zero_points", zero_points),
-                      E, N, K, bits, block_size, _codes[scales.dtype])
+    dev = _current_device() if packed.is_cuda else -2
+    w = ExpertWeights(_here("packed", packed, dev), _here("scales", scales, dev),
+                      None if zero_points is None else _here("zero_points", zero_points, dev), E, N, K, bits, block_size, _codes[scales.dtype])
     w.tensors = (packed, scales, zero_points)
     w.ref = ctypes.pointer(w)
     return w
 
 
-def _route(logits, top_k, ids, weights, bias, scoring, renormalize, scale, stream):
+def _route(logits, top_k, ids, weights, bias, scoring, renormalize, scale, stream, dev):
     shape, code = logits.shape, _codes.get(logits.dtype)
     if code is None:
         _fail("logits: a float32, float16 or bfloat16 tensor is wanted")
-    lp, ls = _row_matrix("logits", logits, shape)
+    lp, ls = _row_matrix("logits", logits, shape, dev)
     bp = ip = wp = None
     if bias is not None:
         if bias.dtype is not _float32 or bias.numel() != shape[1] or not bias.is_contiguous():
             _fail("bias: a contiguous f32 [E] tensor is wanted")
-        bp = _here("bias", bias)
+        bp = _here("bias", bias, dev)
     if ids is not None:
         ip = _i32("ids", ids)
         if ids.shape != (shape[0], top_k):
             _fail("ids: an int32 [T, top_k] tensor is wanted")
-        _here("ids", ids)
+        _here("ids", ids, dev)
     if weights is not None:
         if weights.dtype is not _float32 or weights.shape != (shape[0], top_k) or not weights.is_contiguous():
             _fail("weights: a contiguous f32 [T, top_k] tensor is wanted")
-        wp = _here("weights", weights)
+        wp = _here("weights", weights, dev)
     return MoeRouteArgs(lp, bp, ip, wp, shape[0], shape[1], top_k, ls, code, scoring, 1 if renormalize else 0, scale, stream)
 
 
@@ -735,7 +749,8 @@ def mnb_moe_route(logits, ids, weights, bias=None, scoring=MNB_MOE_SOFTMAX, reno
     """The experts (int32 [T, S]) of each token's logits [T, E] and their weights (f32 [T, S])."""
     if not _codes:
         _setup()
-    a = _route(logits, ids.shape[-1], ids, weights, bias, scoring, renormalize, scale, _current(stream))
+    dev = _current_device() if logits.is_cuda else -2
+    a = _route(logits, ids.shape[-1], ids, weights, bias, scoring, renormalize, scale, _current(stream), dev)
     st = (_lib or load()).mnb_moe_route(a)
     if st:
         _check(st, "mnb_moe_route")
@@ -751,14 +766,14 @@ def mnb_moe(x, logits, gate, up, down, y, top_k, ids=None, weights=None, bias=No
     ids and weights [T, top_k], where given, get the selection."""
     if not _codes:
         _setup()
-    s = _current(stream)
-    r = _route(logits, top_k, ids, weights, bias, scoring, renormalize, scale, s)
+    s, dev = _current(stream), _current_device()
+    r = _route(logits, top_k, ids, weights, bias, scoring, renormalize, scale, s, dev)
     shape = x.shape
     code, out = _codes.get(x.dtype, -1), _codes.get(y.dtype, -1)
     if len(shape) != 2 or shape[0] != r.T or shape[1] != gate.K:
         _fail("x: [T, hidden] rows, one for each row of logits, are wanted")
-    xp, xs = _row_matrix("x", x, shape)
-    yp, ys = _row_matrix("y", y, shape)
+    xp, xs = _row_matrix("x", x, shape, dev)
+    yp, ys = _row_matrix("y", y, shape, dev)
     ws_ptr, ws_bytes = _space(workspace)
     a = MoeArgs(xp, yp, gate.ref, up.ref, down.ref, xs, ys, code, out, activation, ws_ptr, ws_bytes, s)
     st = (_lib or load()).mnb_moe(a, r)
@@ -766,12 +781,15 @@ def mnb_moe(x, logits, gate, up, down, y, top_k, ids=None, weights=None, bias=No
         _check(st, "mnb_moe")
 
 
-def _per_row(what, t, dtype, n):
+def _per_row(what, t, dtype, n, dev):
     if t is None:
         return None
+    d = t.get_device()
     if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
         _fail(f"{what}: a contiguous {dtype} tensor with a value for each row is wanted")
-    return _here(what, t)
+    if d < 0 or (d != dev and dev != -2):
+        _away(what)
+    return t.data_ptr()
 
 
 def mnb_sample(logits, u, tokens, temperature=None, top_k=None, top_p=None, min_p=None, probs=None, stream=None):
@@ -779,16 +797,16 @@ def mnb_sample(logits, u, tokens, temperature=None, top_k=None, top_p=None, min_
     value for each row, or None; probs (f32 [B]) gets the tokens' probabilities after the cuts."""
     if not _codes:
         _setup()
-    shape, code = logits.shape, _codes.get(logits.dtype)
+    shape, code, dev = logits.shape, _codes.get(logits.dtype), _current_device() if logits.is_cuda else -2
     if code is None:
         _fail("logits: a float32, float16 or bfloat16 tensor is wanted")
-    lp, ls = _row_matrix("logits", logits, shape)
+    lp, ls = _row_matrix("logits", logits, shape, dev)
     if u is None or tokens is None:
         _fail("u, tokens: a tensor with a value for each row is wanted")
-    n = shape[0]
-    a = SampleArgs(lp, _per_row("u", u, _float32, n), _per_row("temperature", temperature, _float32, n), _per_row("top_k", top_k, _int32, n),
-                   _per_row("top_p", top_p, _float32, n), _per_row("min_p", min_p, _float32, n), _per_row("tokens", tokens, _int32, n),
-                   _per_row("probs", probs, _float32, n), n, shape[1], ls, code, _current(stream))
+    n, f = shape[0], _float32
+    a = SampleArgs(lp, _per_row("u", u, f, n, dev), _per_row("temperature", temperature, f, n, dev), _per_row("top_k", top_k, _int32, n, dev),
+                   _per_row("top_p", top_p, f, n, dev), _per_row("min_p", min_p, f, n, dev), _per_row("tokens", tokens, _int32, n, dev),
+                   _per_row("probs", probs, f, n, dev), n, shape[1], ls, code, _current(stream))
     st = (_lib or load()).mnb_sample(a)
     if st:
         _check(st, "mnb_sample")
