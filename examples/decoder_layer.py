@@ -1,5 +1,5 @@
-"""A decoder layer's attention block on the library, as a server runs it: int4 projections, rotary positions, a paged
-cache and attention over it.
+"""A decoder layer on the library, as a server runs it: int4 projections, rotary positions, a paged cache and attention
+over it; around them the norms, a mixture of experts and the draw of the next tokens.
 
     python examples/decoder_layer.py            # prefill two prompts, fork samples of one, decode, free and compact
 
@@ -10,6 +10,12 @@ Each step is a handful of calls on the current stream:
     mnb_rotary_append     queries and keys turned, keys and values written to the pages
     mnb_paged_attention   the new tokens over everything cached
     mnb_matmul            output product
+
+and, where the layer's experts and a vocabulary follow (Decoder),
+
+    mnb_rms_norm          before the QKV product; the attention's residual added and normed; the experts' likewise
+    mnb_matmul, mnb_moe   the router's logits; the experts they select, with their weighted sum
+    mnb_matmul, mnb_sample  the vocabulary's logits and a token of each row
 """
 import math
 import os
@@ -37,9 +43,10 @@ class Linear:
         self.packed = aligned(mnb.mnb_packed_size(n, k, 4, 32))
         mnb.mnb_pack_weights(codes, self.packed, n, k, 4, 32)
 
-    def __call__(self, x):
-        y = torch.empty((x.shape[0], self.n), dtype=torch.bfloat16, device="cuda")
-        mnb.mnb_matmul(x, self.packed, self.scales, None, y, x.shape[0], self.n, self.k, 4, 32, mnb.MNB_BF16, mnb.MNB_BF16, mnb.MNB_F16)
+    def __call__(self, x, dtype=torch.bfloat16):
+        y = torch.empty((x.shape[0], self.n), dtype=dtype, device="cuda")
+        out = mnb.MNB_F32 if dtype == torch.float32 else mnb.MNB_BF16
+        mnb.mnb_matmul(x, self.packed, self.scales, None, y, x.shape[0], self.n, self.k, 4, 32, mnb.MNB_BF16, out, mnb.MNB_F16)
         return y
 
     def dense(self):
@@ -98,6 +105,53 @@ class Layer:
         return self.out(o.view(-1, h * d))
 
 
+def experts(count, n, k, gen, deviation):
+    """Random int4 weights [n, k] of `count` experts."""
+    size = mnb.mnb_packed_size(n, k, 4, 32)
+    packed = aligned(count * size)
+    for e in range(count):
+        codes = torch.randint(0, 256, (n, k // 32, 16), generator=gen, device="cuda", dtype=torch.uint8)
+        mnb.mnb_pack_weights(codes, packed[e * size:(e + 1) * size], n, k, 4, 32)
+    scales = torch.full((count, n, k // 32), deviation / 4.6, device="cuda", dtype=torch.float16)
+    return mnb.expert_weights(packed, scales, None, count, n, k, 4, 32)
+
+
+class Decoder:
+    """A layer with its norms and experts between an embedding and a vocabulary: rows of tokens in, a token a row out."""
+
+    def __init__(self, layer, hidden=512, count=8, top_k=2, inner=256, vocab=2000, max_rows=64, seed=0):
+        gen = torch.Generator(device="cuda").manual_seed(seed + 100)
+        self.layer, self.top_k, self.eps = layer, top_k, 1e-5
+        self.embedding = torch.randn((vocab, hidden), generator=gen, device="cuda").to(torch.bfloat16)
+        self.gains = [(1 + 0.1 * torch.randn(hidden, generator=gen, device="cuda")).to(torch.bfloat16) for _ in range(3)]
+        self.router, self.head = Linear(count, hidden, gen, hidden ** -0.5), Linear(vocab, hidden, gen, 2 * hidden ** -0.5)
+        self.gate, self.up = (experts(count, inner, hidden, gen, hidden ** -0.5) for _ in range(2))
+        self.down = experts(count, hidden, inner, gen, inner ** -0.5)
+        self.ws = aligned(mnb.mnb_moe_workspace_size(max_rows, top_k, count, hidden, inner))
+
+    def before(self, x):
+        y = torch.empty_like(x)
+        mnb.mnb_rms_norm(x, self.gains[0], self.eps, y=y)
+        return y
+
+    def after(self, x, attended, u, temperature=None, top_k=None, top_p=None, min_p=None):
+        """The tokens that follow rows x, whose attention block gave `attended` (x becomes the layer's sums)."""
+        y, mixed = torch.empty_like(x), torch.empty_like(x)
+        mnb.mnb_rms_norm(attended, self.gains[1], self.eps, residual=x, residual_out=x, y=y)
+        mnb.mnb_moe(y, self.router(y, torch.float32), self.gate, self.up, self.down, mixed, self.top_k, workspace=self.ws)
+        mnb.mnb_rms_norm(mixed, self.gains[2], self.eps, residual=x, residual_out=x, y=y)
+        tokens = torch.empty(x.shape[0], dtype=torch.int32, device="cuda")
+        mnb.mnb_sample(self.head(y, torch.float32), u, tokens, temperature=temperature, top_k=top_k, top_p=top_p, min_p=min_p)
+        return tokens
+
+    def step(self, tokens, seqs, new, lens, u, **cuts):
+        """The token that follows each sequence's last of `tokens` (new[i] of sequence seqs[i])."""
+        x = self.embedding[tokens.long()]
+        attended = self.layer.step(self.before(x), seqs, new, lens)
+        last = self.layer.ints(new).cumsum(0) - 1
+        return self.after(x[last], attended[last], u, **cuts)
+
+
 def main():
     layer = Layer()
     gen = torch.Generator(device="cuda").manual_seed(1)
@@ -113,6 +167,18 @@ def main():
     counts = layer.compact()
     print("pages held:", int(counts[0]), "moved:", int(counts[1]), "lengths:", layer.lens.tolist())
     assert mnb.mnb_get_device_error() == 0 and torch.isfinite(y).all()
+
+    model, lens = Decoder(Layer(seed=1)), [5, 3]                   # tokens in, tokens out: a greedy row and a drawn one
+    cuts = dict(temperature=torch.tensor([0.0, 0.8], device="cuda"), top_p=torch.tensor([1.0, 0.95], device="cuda"))
+    draw = lambda: torch.rand(2, generator=gen, device="cuda")  # noqa: E731
+    tokens = model.step(layer.ints([11, 7, 300, 5, 42, 8, 9, 10]), [0, 1], [5, 3], lens, draw(), **cuts)
+    said = [tokens.tolist()]
+    for _ in range(6):
+        lens = [n + 1 for n in lens]
+        tokens = model.step(tokens, [0, 1], [1, 1], lens, draw(), **cuts)
+        said.append(tokens.tolist())
+    print("tokens of the two sequences:", [list(t) for t in zip(*said)])
+    assert mnb.mnb_get_device_error() == 0 and all(0 <= t < 2000 for row in said for t in row)
 
 
 if __name__ == "__main__":
