@@ -284,6 +284,12 @@ struct Sampler {
         else __syncthreads();
     }
 
+    // After the last gather: the others read the first CTA's counter, so its shared memory stays until they have.
+    __device__ __forceinline__ void leave() const {
+        __syncthreads();
+        if (p.C > 1) cluster_sync();
+    }
+
     // Bins' counts (CNT) and sums of weights (WGT) over the cluster, then their prefix in mc and mw.  bin(x) < 0: in none.
     // MINP: minp_w gets the sum of the weights from `minp` on.
     template <bool CNT, bool WGT, bool MINP, class B>
@@ -859,6 +865,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
             if (!whole) weigh();
             q.template resolve<false, true>(q.template first_bin<false>(target), target);
             if (rank == 0) q.write(r, (int)S.res_token, S.res_x, kept);
+            q.leave();
             return;
         }
     }
@@ -883,6 +890,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
         const int at = q.first_listed(target, n);
         q.write(r, (int)(uint32_t)S.list[at], value_of(~(uint32_t)(S.list[at] >> 32)), kept);
     }
+    q.leave();
 }
 
 template <int DT, int THREADS>
