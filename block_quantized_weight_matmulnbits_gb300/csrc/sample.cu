@@ -160,7 +160,7 @@ __device__ __forceinline__ int bin_of(float x, const Scale& s) {
 // point operations by all of them take microseconds on this part.)
 template <bool UP>
 __device__ __forceinline__ unsigned long long share_of(float f, unsigned long long n) {
-    const uint32_t u = __float_as_uint(f), e = u >> 23;
+    const uint32_t u = __float_as_uint(f) & 0x7FFFFFFFu, e = u >> 23;  // (-0 is 0)
     const unsigned long long m = e ? (u & 0x7FFFFFu) | 0x800000u : u & 0x7FFFFFu;
     const int s = 150 - (int)(e ? e : 1u);  // f = m / 2^s, s from 23 to 149
     const unsigned long long hi = __umul64hi(m, n), lo = m * n;

@@ -139,6 +139,21 @@ def test_wrong_parameters_are_reported(mnb):
     assert (tokens >= 0).all() and mnb.mnb_get_device_error() == 0
 
 
+@pytest.mark.parametrize("v", [600, 30000])
+def test_edges_of_the_parameters(mnb, v):
+    """-0 is 0; the largest u below 1; a share of 0 keeps one token; the smallest and largest temperatures."""
+    x = logits_of(6, v, "f32", 7)
+    zero, one = [-0.0] * 6, [1 - 2.0 ** -24] * 6
+    first = torch.argmax(x, 1).int()
+    for p in ([-0.0] * 6, None, [2.0 ** -149] * 6, [1.0 - 2.0 ** -24] * 6):
+        tokens, _ = run(mnb, x, u=zero, p=p, m=zero)
+        assert torch.equal(tokens, first)
+        run(mnb, x, u=one, p=p)
+    tokens, _ = run(mnb, x, u=one, p=[-1.0] * 6, m=[-1.0] * 6, k=-5)
+    assert torch.equal(tokens, first)
+    run(mnb, x, t=[2.0 ** -149, 1e-30, 1e-3, 1e30, 3e38, float("inf")])
+
+
 def test_streams_and_graphs(mnb):
     x = logits_of(9, 30001, "bf16", 5)
     u, t = torch.rand(9, device="cuda"), torch.empty(9, dtype=torch.int32, device="cuda")
