@@ -305,6 +305,12 @@ mnb_status mnb_rms_norm(const mnb_rms_norm_args* a) {
         (a->y && !dec::aligned_to(a->y, dec::dt_bytes(a->out_dtype))) || !dec::aligned_to(a->codes, 16) ||
         !dec::aligned_to(a->scales, 4))
         return MNB_ERR_INVALID_ARG;
+    // an output in an input's place has its values where the input's are
+    if (a->y && ((a->y == a->x && (a->out_dtype != a->dtype || st[3] != st[0])) ||
+                 (a->y == a->residual && (a->out_dtype != a->dtype || st[3] != st[1]))))
+        return MNB_ERR_INVALID_ARG;
+    if (a->residual_out && ((a->residual_out == a->x && st[2] != st[0]) || (a->residual_out == a->residual && st[2] != st[1])))
+        return MNB_ERR_INVALID_ARG;
     if (a->T >= (int64_t(1) << 38)) return MNB_ERR_UNSUPPORTED;
 
     NormParams p{};

@@ -662,8 +662,10 @@ MNB_API mnb_status mnb_cache_compact(const mnb_cache_state* state, const mnb_pag
  *                 but from the unrounded Y, and a block with an infinity or a
  *                 NaN has scale NaN and codes 0.  block_size: a power of two,
  *                 at least 16; a block as wide as the row gives one scale a row.
- * residual_out and y may be x or residual (same pointer and strides); any
- * other overlap is undefined.  width (with codes KB * block_size) is at most
+ * residual_out and y may each be x or residual (same pointer, strides and
+ * type, else MNB_ERR_INVALID_ARG); any other overlap is undefined.  The sum of
+ * squares is f32: a row whose sum is past its range gives zeros, one whose
+ * squares all underflow counts as zeros beside eps.  width (with codes KB * block_size) is at most
  * 32768, else MNB_ERR_UNSUPPORTED.  16-byte accesses where every base and
  * stride allows them, narrower ones otherwise.  T == 0 is a no-op. */
 typedef struct mnb_rms_norm_args {

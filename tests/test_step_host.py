@@ -38,6 +38,13 @@ def test_norm_limits():
     assert lib.mnb_rms_norm(ctypes.byref(_norm(**none))) == mnb.MNB_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("bad", [{"y": 4096, "out_dtype": mnb.MNB_F32}, {"y": 4096, "y_stride": 128},
+                                 {"residual_out": 4096, "residual_out_stride": 128}, {"y": 12288, "out_dtype": mnb.MNB_F32}])
+def test_norm_output_over_an_input_of_another_layout(bad):
+    a = _norm(**{**dict(x=4096, residual=12288, residual_out=16384, y=20480, dtype=mnb.MNB_BF16, out_dtype=mnb.MNB_BF16), **bad})
+    assert mnb.load().mnb_rms_norm(ctypes.byref(a)) == mnb.MNB_ERR_INVALID_ARG
+
+
 def test_norm_binding_checks():
     x = torch.ones((2, 64))
     for kw in (dict(y=torch.ones((2, 63))), dict(residual=torch.ones((2, 64), dtype=torch.float16), y=x), dict(codes=x, y=x),
