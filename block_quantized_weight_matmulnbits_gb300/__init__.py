@@ -719,6 +719,7 @@ def expert_weights(packed, scales, zero_points, E, N, K, bits, block_size) -> Ex
     w = ExpertWeights(_here("packed", packed, dev), _here("scales", scales, dev),
                       None if zero_points is None else _here("zero_points", zero_points, dev), E, N, K, bits, block_size, _codes[scales.dtype])
     w.tensors = (packed, scales, zero_points)
+    w.dev = dev
     w.ref = ctypes.pointer(w)
     return w
 
@@ -772,6 +773,8 @@ def mnb_moe(x, logits, gate, up, down, y, top_k, ids=None, weights=None, bias=No
     code, out = _codes.get(x.dtype, -1), _codes.get(y.dtype, -1)
     if len(shape) != 2 or shape[0] != r.T or shape[1] != gate.K:
         _fail("x: [T, hidden] rows, one for each row of logits, are wanted")
+    if dev != -2 and not (gate.dev == up.dev == down.dev == dev):
+        _away("gate, up, down")
     xp, xs = _row_matrix("x", x, shape, dev)
     yp, ys = _row_matrix("y", y, shape, dev)
     ws_ptr, ws_bytes = _space(workspace)

@@ -185,6 +185,9 @@ size_t mnb_moe_workspace_size(int64_t T, int64_t S, int64_t E, int64_t hidden, i
         hidden < 1 || hidden >= (int64_t(1) << 30) || inner < 1 || inner >= (int64_t(1) << 30))
         return 0;
     const size_t pairs = (size_t)(T * S);
+    // (the kernels count row tiles of segments, and their depths' chunks, in 32 bits)
+    const int64_t longest = hidden > inner ? hidden : inner;
+    if ((longest / 16 + 1) * T * S >= (int64_t(1) << 31)) return 0;
     return moe::round256(sizeof(moe::Plan)) + moe::round256(pairs * 4 * (((size_t)inner + 15) / 16 * 16));
 }
 

@@ -736,6 +736,8 @@ typedef enum mnb_activation { MNB_ACT_SILU = 0, MNB_ACT_GELU_TANH = 1 } mnb_acti
  *     Y[t] = sum_s w[t, s] * down_e ( act(gate_e X[t]) * (up_e X[t]) ),   e = ids[t, s].
  * Products accumulate in f32; what lies between the products keeps 16 bits
  * (two bf16 parts), whatever act_dtype is; Y is rounded once to out_dtype.
+ * bf16 values of X, and w * act() * up between the products, are held in a
+ * range of 2^-60 to 2^67: larger ones are infinite, smaller ones lose bits.
  * Results repeat.  The weights of experts that no token selects are not read.
  *   x, y         device [T, hidden] of act_dtype (bf16 or f16) and out_dtype
  *                with the given row strides (elements, at least hidden),
@@ -748,7 +750,8 @@ typedef enum mnb_activation { MNB_ACT_SILU = 0, MNB_ACT_GELU_TANH = 1 } mnb_acti
  *                graphs in flight together) need workspaces of their own.
  * T <= 64 and T * S <= 1024, one bits, block_size and scale_dtype, and act_dtype
  * not f32, else MNB_ERR_UNSUPPORTED (mnb_moe_route and mnb_matmul_grouped serve
- * more tokens).  A weight whose header does not match sets
+ * more tokens), nor sizes whose workspace size is 0.  Y may be X; no other
+ * overlap is allowed.  A weight whose header does not match sets
  * MNB_ERR_LAYOUT_MISMATCH in the device status word.  T == 0 is a no-op. */
 typedef struct mnb_moe_args {
     const void* x;

@@ -226,6 +226,29 @@ def test_large_intermediate_values_fit(mnb, small):
     assert (np.abs(R.f64(y) - ref) <= tol + np.abs(ref) * 2.0 ** -16).all()
 
 
+@pytest.mark.parametrize("size", [2.0 ** -28, 2.0 ** 30])
+@pytest.mark.parametrize("t", [2, 20])
+def test_range_of_bf16(mnb, small, size, t):
+    """Values near both ends of the documented range: h is of the order of size^2."""
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    x = (torch.randn((t, 256), generator=gen, device="cuda") * size).to(torch.bfloat16)
+    logits = torch.randn((t, 6), generator=gen, device="cuda")
+    y = torch.empty((t, 256), device="cuda")
+    layer(mnb, small, x, logits, y, scratch(mnb, t, 2, 6, 256, 192))
+    ids, w = R.route(R.f64(logits), 2, None, False, True, 1.0)
+    ref, tol = R.moe(R.f64(x), ids, w, small[0].w, small[1].w, small[2].w, False)
+    # (and 2^-17 of each expert's share, the weights' own bound, which test_layer counts from the kernel's weights)
+    share = sum(R.moe(R.f64(x), ids[:, s:s + 1], w[:, s:s + 1], small[0].w, small[1].w, small[2].w, False)[0].__abs__() for s in range(2))
+    assert (np.abs(R.f64(y) - ref) <= tol + share * 2.0 ** -16).all()
+
+
+def test_weights_of_another_device_are_refused(mnb, small, monkeypatch):
+    x, logits = torch.ones((1, 256), dtype=torch.bfloat16, device="cuda"), torch.zeros((1, 6), device="cuda")
+    monkeypatch.setattr(small[1].handle, "dev", 1)  # as expert_weights() on that device would note it
+    with pytest.raises(ValueError):
+        layer(mnb, small, x, logits, torch.empty((1, 256), device="cuda"), scratch(mnb, 1, 2, 6, 256, 192))
+
+
 def test_wrong_headers_are_reported(mnb, small):
     x, logits = torch.ones((1, 256), dtype=torch.bfloat16, device="cuda"), torch.zeros((1, 6), device="cuda")
     y, ws = torch.empty((1, 256), device="cuda"), scratch(mnb, 1, 2, 6, 256, 192)

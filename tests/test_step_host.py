@@ -127,6 +127,12 @@ def test_moe_limits():
         assert mnb.mnb_moe_workspace_size(*bad) == 0
 
 
+def test_moe_counts_fit_32_bits():
+    assert mnb.mnb_moe_workspace_size(64, 16, 64, 64, 1 << 24) > 0
+    for hidden, inner in ((64, 1 << 25), (1 << 25, 64)):
+        assert mnb.mnb_moe_workspace_size(64, 16, 64, hidden, inner) == 0
+
+
 def _sample(**kw):
     a = mnb.SampleArgs()
     a.logits = a.u = a.tokens = a.temperature = a.top_k = a.top_p = a.min_p = a.probs = 4096
