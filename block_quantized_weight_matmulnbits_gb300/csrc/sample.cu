@@ -24,8 +24,10 @@
 // of atomics changes them: results repeat, and agree with 64-bit floats but for
 // places that those do not settle either.
 //
-// Bound: the arithmetic of the weights (about 45 instructions a token), not the
-// logits' bytes; few rows: the barriers of a cluster, about 0.7 us each.
+// Bound: the arithmetic of the weights and their bins (about 75 instructions a
+// token of the 90 to 110 in all), not the logits' bytes: 64 rows of 128000 f32 in
+// 70 us (0.5 TB/s), 256 of 50257 f16 in 81, 16 of 200003 f32 in 41.  Few rows: the
+// barriers of a cluster, about 0.7 us each; one row of 128000 bf16 takes 15.4 us.
 #include <algorithm>
 #include <cmath>
 
@@ -38,6 +40,7 @@ constexpr int kBins = 2048;
 constexpr int kList = 1024;                            // tokens that the first CTA sorts
 constexpr int kRankSort = 256;                         // up to so many by counting those before each
 constexpr int kUnit = 43;                              // a weight of 1 is 2^43 units
+constexpr int kAbreast = 4;                            // weights that a thread forms at a time
 constexpr int kMaxVocab = 1 << 24;
 constexpr int kGathers = 32;                           // of a row: 2 of nuclei, 3 of places with at most 4 divisions each
 constexpr float kCut = kUnit + 0.99f;                  // weights below 2^-kCut (2^extra times that) are 0 units
@@ -247,23 +250,40 @@ struct Row {
             for (int j = 0; j < E; ++j) x[j] = x[j] == INFINITY ? 0.f : -INFINITY;
         }
     }
+    // Every window of the thread, the next one loaded ahead (from L2 where the range is not in shared memory).
     template <class F>
-    __device__ __forceinline__ void each_four(F&& f) const {
-        for (int w = threadIdx.x; w < windows; w += THREADS) {
+    __device__ __forceinline__ void each_window(F&& f) const {
+        int w = threadIdx.x;
+        uint4 next = make_uint4(0, 0, 0, 0);
+        if (w < windows) next = raw(w);
+#pragma unroll 1
+        while (w < windows) {
+            const uint4 v = next;
+            const int at = w;
+            w += THREADS;
+            if (w < windows) next = raw(w);
             float x[E];
-            values(w, x);
-            f(x);
-            if constexpr (E == 8) f(x + 4);
+            widen(v, x);
+            if (inf) {
+#pragma unroll
+                for (int j = 0; j < E; ++j) x[j] = x[j] == INFINITY ? 0.f : -INFINITY;
+            }
+            f(x, at * E);
         }
     }
     template <class F>
-    __device__ __forceinline__ void each(F&& f) const {
-        for (int w = threadIdx.x; w < windows; w += THREADS) {
-            float x[E];
-            values(w, x);
+    __device__ __forceinline__ void each_few(F&& f) const {
+        each_window([&](const float (&x)[E], int) {
 #pragma unroll
-            for (int j = 0; j < E; ++j) f(x[j], w * E + j);
-        }
+            for (int j = 0; j < E; j += kAbreast) f(x + j);
+        });
+    }
+    template <class F>
+    __device__ __forceinline__ void each(F&& f) const {
+        each_window([&](const float (&x)[E], int at) {
+#pragma unroll
+            for (int j = 0; j < E; ++j) f(x[j], at + j);
+        });
     }
     __device__ __forceinline__ int index(int at) const { return first + at - skip; }
 };
@@ -305,20 +325,20 @@ struct Sampler {
         // Sums of weights: without counts and up to 65536 tokens a CTA as three sums of 16, 16 and the upper bits, which
         // nobody has to wait for; else of 32 bits with a carry.
         const bool three = !CNT && p.seg <= 65536;
-        row.each_four([&](const float* x) {
-            int b[4];
+        row.each_few([&](const float* x) {
+            int b[kAbreast];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < kAbreast; ++j) {
                 b[j] = bin(x[j]);
                 if (CNT && b[j] >= 0) atomicAdd(&S.cnt[b[j]], 1u);
             }
-            // four weights abreast, without a branch: token by token would leave one chain of them at a time
+            // weights abreast, without a branch: token by token would leave one chain of them at a time
             if constexpr (WGT) {
-                unsigned long long w[4];
+                unsigned long long w[kAbreast];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) w[j] = weight_of(x[j], sc, S.table, p.extra);
+                for (int j = 0; j < kAbreast; ++j) w[j] = weight_of(x[j], sc, S.table, p.extra);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < kAbreast; ++j) {
                     if (b[j] < 0) continue;
                     if (MINP && w[j] >= minp) keep += w[j];
                     const uint32_t lo = (uint32_t)w[j];
@@ -456,23 +476,35 @@ struct Sampler {
         return n;
     }
 
+    // So many bins as a difference of max - x, and a little (bin b's values lie within half a bin of b / per; the last bin's
+    // anywhere above).
+    __device__ __forceinline__ float radius_of(int b, float bins) const { return b < kBins - 1 ? (bins + 0x1p-8f) / sc.per : INFINITY; }
+
     // The number of tokens with in(x); if it is at most kList, they are in the first CTA's list, sorted, with the prefix of
     // their weights.
+    // Few windows have any: those without a token within `radius` of max - x = mid are passed over (in(x) implies that).
     template <class P>
-    __device__ __forceinline__ int gather(P&& in) {
+    __device__ __forceinline__ int gather(P&& in, float mid, float radius) {
         __syncthreads();
         if (tid == 0) S.mine = 0u;
         __syncthreads();
         uint32_t* const listed = &S.listed[min(gathers++, kGathers - 1)];
-        row.each([&](float x, int at) {
-            if (!in(x)) return;
-            // the lanes that found one take places together
-            const uint32_t mask = __activemask();
-            const int leader = __ffs(mask) - 1;
-            uint32_t i = 0;
-            if (lane == leader) i = atomicAdd(&S.mine, (uint32_t)__popc(mask));
-            i = __shfl_sync(mask, i, leader) + __popc(mask & ((1u << lane) - 1u));
-            if (i < kList) S.sums[i] = ((unsigned long long)(~key_of(x)) << 32) | (uint32_t)row.index(at);
+        row.each_window([&](const float (&x)[Row<DT, THREADS>::E], int at) {
+            float near = INFINITY;
+#pragma unroll
+            for (int j = 0; j < Row<DT, THREADS>::E; ++j) near = fminf(near, fabsf((sc.top - x[j]) - mid));  // passes over NaN
+            if (!(near <= radius)) return;
+#pragma unroll
+            for (int j = 0; j < Row<DT, THREADS>::E; ++j) {
+                if (!in(x[j])) continue;
+                // the lanes that found one take places together
+                const uint32_t mask = __activemask();
+                const int leader = __ffs(mask) - 1;
+                uint32_t i = 0;
+                if (lane == leader) i = atomicAdd(&S.mine, (uint32_t)__popc(mask));
+                i = __shfl_sync(mask, i, leader) + __popc(mask & ((1u << lane) - 1u));
+                if (i < kList) S.sums[i] = ((unsigned long long)(~key_of(x[j])) << 32) | (uint32_t)row.index(at + j);
+            }
         });
         __syncthreads();
         const uint32_t mine = S.mine;
@@ -617,7 +649,7 @@ struct Sampler {
         // (a NaN's key is above or below every number's, so x == x is asked)
         auto in = [&](float x) { return divided ? x == x && key_of(x) >= kmin && key_of(x) <= kmax : bin_of(x, sc) == b; };
         int m;
-        while ((m = gather(in)) > kList) {
+        while ((m = gather(in, divided ? 0.f : b / sc.per, divided ? INFINITY : radius_of(b, 0.5f))) > kList) {
             if (!divided) extent(in);
             divided = true;
             if (kmin == kmax) break;
@@ -835,7 +867,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
         q.template histogram<true, false, false>(bin, 0ull);
         const int b = q.template first_bin<true>((unsigned long long)top_k);
         if (b < 0) by_k = false;  // every token of a weight above 0 is among the k
-        else if (S.mc[b] <= (uint32_t)kList) n = q.gather(upto(b));
+        else if (S.mc[b] <= (uint32_t)kList) n = q.gather(upto(b), 0.f, q.radius_of(b, b + 0.5f));
     }
     if (n > kList) {
         weigh();
@@ -853,7 +885,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
             whole = true;
             const int b = q.template first_bin<false>(target);
             // a nucleus that fits the list: all of it, and the draw from it
-            if (q.most_tokens(b) <= (float)kList) n = q.gather(upto(b));
+            if (q.most_tokens(b) <= (float)kList) n = q.gather(upto(b), 0.f, q.radius_of(b, b + 0.5f));
             if (n > kList) {
                 whole = !q.template resolve<false, false>(b, target);
                 kept = S.found_w;
