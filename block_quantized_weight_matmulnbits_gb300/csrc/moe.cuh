@@ -15,7 +15,7 @@
 // the sums are scaled at the end.  Columns of bf16 are scaled by 2^60 (h where
 // it is written, x in the loop), so that the products are normal numbers.
 //
-// The warp-level MMA of this part is slow (one m16n8k16 in 7 cycles an SM): 16
+// The warp-level MMA of this part is slow (one m16n8k16 in 8 cycles an SM): 16
 // of them for the 2 KB of an item take about as long as its bytes from memory,
 // so none is spent on anything else (sums of x for the zero points by an MMA
 // with ones: half as long again).

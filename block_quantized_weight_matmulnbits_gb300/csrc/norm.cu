@@ -13,8 +13,9 @@
 // largest of all and reaches the block's scale.
 //
 // Measured: 4999 rows of 5120 f16 with a residual 38.6 us (5300 GB/s, 0.78 of a
-// copy); 16384 rows of 4096 bf16 to codes of blocks of 32 in 106 us (4500 GB/s),
-// bound there by the instructions of the codes (issue slots 68% full); 64 rows
+// copy); 16384 rows of 4096 bf16 to codes of blocks of 32 in 98 us (4880 GB/s),
+// bound there by instructions and by 32 warps an SM (with 80 and 128 registers a
+// thread instead of 64, so 24 and 16 warps: 108 and 127 us); 64 rows
 // of 8192 2.7 us, a launch and one chain of load, reduction and store.
 #include <algorithm>
 #include <cmath>
@@ -274,8 +275,8 @@ cudaError_t launch_norm(const NormParams& p, bool wide, cudaStream_t s) {
     constexpr int V = DT == kF32 ? 4 : 8;
     const int vecs = ((p.codes ? p.padded : p.width) + V - 1) / V;
     // few rows: as many threads as a row has vectors, up to 1024 (one round trip of loads); many: up to 4 vectors a thread,
-    // so that fewer threads wait at the barrier of a row (16384 rows of 4096 to codes: 106 us with 128 threads, 118 with
-    // 256, 156 with 512; 4999 rows of 5120: 38.6, 38.6, 42.2)
+    // so that fewer threads wait at the barrier of a row (16384 rows of 4096 to codes: 98 us with 128 threads, 111 with
+    // 256, 148 with 512; 4999 rows of 5120: 38.5, 38.5, 41.5)
     const int want = p.rows <= 2 * dec::kSms ? 1024 : 128;
     int vpt = 1;
     while (vpt < (DT == kF32 ? 8 : 4) && vecs > vpt * want) vpt *= 2;
