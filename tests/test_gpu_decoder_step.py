@@ -137,3 +137,30 @@ def test_prompt_and_single_tokens(mnb, example):
         last = model.step(tokens[i:i + 1], [1], [1], [i + 1], u, **cuts)
     assert 0 <= int(whole) < 2000 and 0 <= int(last) < 2000
     assert mnb.mnb_get_device_error() == 0
+
+
+def test_rows_that_lie_far_apart(mnb):
+    """Row strides past 2^31 elements: the same results as from rows side by side."""
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    far = torch.empty(2 ** 31 + 4096, dtype=torch.bfloat16, device="cuda")
+    apart = lambda: far.as_strided((2, 256), (2 ** 31, 1), 0)  # noqa: E731
+    x = torch.randn((2, 256), generator=gen, device="cuda").to(torch.bfloat16)
+    apart().copy_(x)
+    y, z = torch.empty_like(x), far.as_strided((2, 256), (2 ** 31, 1), 1024)
+    mnb.mnb_rms_norm(x, None, 1e-5, y=y)
+    mnb.mnb_rms_norm(apart(), None, 1e-5, y=z)
+    assert torch.equal(y, z)
+    u = torch.rand(2, generator=gen, device="cuda")
+    a, b = (torch.empty(2, dtype=torch.int32, device="cuda") for _ in range(2))
+    mnb.mnb_sample(x, u, a)
+    mnb.mnb_sample(apart(), u, b)
+    assert torch.equal(a, b)
+    gate, up, down = (R.Experts(mnb, 4, n, k, 4, 32, "f16", True, gen).handle for n, k in ((64, 256), (64, 256), (256, 64)))
+    logits = torch.randn((2, 4), generator=gen, device="cuda").to(torch.bfloat16)
+    spread = far.as_strided((2, 4), (2 ** 31, 1), 2048)
+    spread.copy_(logits)
+    from tests import _gpu as G
+    ws = G.aligned_empty(mnb.mnb_moe_workspace_size(2, 2, 4, 256, 64))
+    mnb.mnb_moe(x, logits, gate, up, down, y, 2, workspace=ws)
+    mnb.mnb_moe(apart(), spread, gate, up, down, z, 2, workspace=ws)
+    assert torch.equal(y, z) and mnb.mnb_get_device_error() == 0
