@@ -24,9 +24,9 @@
 // of atomics changes them: results repeat, and agree with 64-bit floats but for
 // places that those do not settle either.
 //
-// Bound: the arithmetic of the weights and their bins (about 75 instructions a
-// token of the 90 to 110 in all), not the logits' bytes: 64 rows of 128000 f32 in
-// 70 us (0.5 TB/s), 256 of 50257 f16 in 81, 16 of 200003 f32 in 41.  Few rows: the
+// Bound: the arithmetic of the weights and their bins (about 70 instructions a
+// token of the 80 to 100 in all), not the logits' bytes: 64 rows of 128000 f32 in
+// 70 us (0.5 TB/s), 256 of 50257 f16 in 80, 16 of 200003 f32 in 40.  Few rows: the
 // barriers of a cluster, about 0.7 us each; one row of 128000 bf16 takes 15.4 us.
 #include <algorithm>
 #include <cmath>
@@ -45,7 +45,7 @@ constexpr int kMaxVocab = 1 << 24;
 constexpr int kGathers = 32;                           // of a row: 2 of nuclei, 3 of places with at most 4 divisions each
 constexpr float kCut = kUnit + 0.99f;                  // weights below 2^-kCut (2^extra times that) are 0 units
 
-// 2^43 * 2^(-j / 1024), from the exponential series in double at compile time (good to 2^-50).
+// 2^44 * 2^(-j / 1024), from the exponential series in double at compile time (good to 2^-50).
 struct Table {
     unsigned long long v[1024];
     constexpr Table() : v() {
@@ -56,7 +56,7 @@ struct Table {
                 term = term * a / n;
                 sum += term;
             }
-            v[j] = (unsigned long long)(sum * 8796093022208.0 + 0.5);
+            v[j] = (unsigned long long)(sum * 17592186044416.0 + 0.5);
         }
     }
 };
@@ -125,12 +125,11 @@ struct Scale {
     float cut, per;         // largest max - x of a weight above 0, bins per unit of max - x
 };
 
-// 2^-y of a token, y = (top - x) c, as `units` (43 bits) and a right shift.  (top is finite.)
+// 2^-y of a token, y = (top - x) c, as `units` (of 2^-44) and a right shift.  (top is finite.)
 __device__ __forceinline__ long long weight_parts(float x, const Scale& s, const unsigned long long* table, int& shift) {
+    // d and its own rounding error (exact: d + e = top - x; top - x >= 0, so the larger of top and -x is so in magnitude)
     const float d = s.top - x;
-    // d's own rounding error (exact: d + e = top - x)
-    const float b = d - s.top;
-    const float e = (s.top - (d - b)) + (-x - b);
+    const float e = fminf(s.top, -x) - (d - fmaxf(s.top, -x));
     const float p = d * s.c_hi;
     const float rest = fmaf(e, s.c_hi, fmaf(d, s.c_lo, fmaf(d, s.c_hi, -p)));
     const float q = p + 12288.f;  // 1.5 * 2^13: p in units of 2^-10
@@ -141,7 +140,7 @@ __device__ __forceinline__ long long weight_parts(float x, const Scale& s, const
     const int f = __float2int_rn(fmaf(a * a, fmaf(a, 0.16666667f, 0.5f), a) * 4398046511104.f);
     const long long t = (long long)table[k & 1023];
     shift = k >> 10;
-    return t + (((long long)(int)(t >> 13) * f) >> 29);  // (t / 2^43 in units of 2^-30) * f
+    return t + (((long long)(int)(t >> 14) * f) >> 28);  // (t / 2^44 in units of 2^-30) * f
 }
 
 // The weight in units of 2^-(43 - extra), rounded.
@@ -149,7 +148,7 @@ __device__ __forceinline__ unsigned long long weight_of(float x, const Scale& s,
     int shift;
     const unsigned long long t = (unsigned long long)weight_parts(x, s, table, shift);
     shift = (shift + extra) & 63;  // at most 43 up to the cut
-    const unsigned long long w = (t + ((1ull << shift) >> 1)) >> shift;
+    const unsigned long long w = ((t >> shift) + 1ull) >> 1;
     return s.top - x <= s.cut ? w : 0ull;  // also NaN and -inf: 0
 }
 
@@ -601,7 +600,7 @@ struct Sampler {
         if (p.probs) {
             int shift;
             const double w = (double)weight_parts(x, sc, S.table, shift);
-            p.probs[r] = (float)(w / (double)total * exp2i(-shift - p.extra));
+            p.probs[r] = (float)(w / (double)total * exp2i(-1 - shift - p.extra));
         }
     }
     static __device__ __forceinline__ double exp2i(int e) { return __longlong_as_double((long long)(1023 + e) << 52); }
