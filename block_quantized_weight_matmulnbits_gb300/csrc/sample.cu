@@ -207,7 +207,7 @@ struct Row {
     const uint8_t* base;                           // first window (16-byte aligned)
     int windows, skip, n, first;                   // windows; tokens before the range in the first; tokens; index of the first token
     bool edges;                                    // the first and last windows hold other memory
-    bool inf;                                      // the maximum is +inf: those tokens count as 0, all others as -inf
+    float mul, only;                               // what logits are multiplied by; 0: those equal to `only` count as 0, others as -inf
 
     __device__ __forceinline__ static void widen(const uint4& v, float (&x)[E]) {
         const uint32_t u[4] = {v.x, v.y, v.z, v.w};
@@ -242,12 +242,15 @@ struct Row {
         }
         return make_uint4(u[0], u[1], u[2], u[3]);
     }
+    __device__ __forceinline__ void scale(float (&x)[E]) const {
+        if (mul != 1.f) {
+#pragma unroll
+            for (int j = 0; j < E; ++j) x[j] = mul > 0.f ? x[j] * mul : x[j] == only ? 0.f : -INFINITY;
+        }
+    }
     __device__ __forceinline__ void values(int w, float (&x)[E]) const {
         widen(raw(w), x);
-        if (inf) {
-#pragma unroll
-            for (int j = 0; j < E; ++j) x[j] = x[j] == INFINITY ? 0.f : -INFINITY;
-        }
+        scale(x);
     }
     // Every window of the thread, the next one loaded ahead (from L2 where the range is not in shared memory).
     template <class F>
@@ -263,10 +266,7 @@ struct Row {
             if (w < windows) next = raw(w);
             float x[E];
             widen(v, x);
-            if (inf) {
-#pragma unroll
-                for (int j = 0; j < E; ++j) x[j] = x[j] == INFINITY ? 0.f : -INFINITY;
-            }
+            scale(x);
             f(x, at * E);
         }
     }
@@ -769,8 +769,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
         return;  // the whole cluster does
     }
 
+    // Under a temperature near the ends of f32, differences of logits or log2 e / T would pass its range or be subnormal: both
+    // are taken with a power of two.
+    const float lift = temperature >= 0x1p64f ? 0x1p-64f : temperature < 0x1p-100f ? 0x1p64f : 1.f;
     if (tid == 0) {  // (64-bit floating point: by one thread, beside the loads)
-        const double c = fmin(1.4426950408889634 / (double)temperature, 1e38);
+        const double c = 1.4426950408889634 / ((double)temperature * (double)lift);
         S.scale.c_hi = (float)c;
         S.scale.c_lo = (float)(c - (double)S.scale.c_hi);
         S.scale.cut = fminf(__fdiv_rn(kCut - p.extra, S.scale.c_hi), 3.4e38f);
@@ -786,7 +789,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
     row.skip = (int)(src - row.base) / esize;
     row.windows = row.n > 0 ? (row.skip + row.n + E - 1) / E : 0;
     row.edges = true;
-    row.inf = false;
+    row.mul = 1.f;
+    row.only = 0.f;
     float top = -INFINITY;
     for (int w = tid; w < row.windows; w += THREADS) {
         const uint4 v = row.raw(w);
@@ -844,9 +848,13 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
         }
         return;
     }
-    q.row.inf = top == INFINITY;
     q.sc = S.scale;
-    q.sc.top = q.row.inf ? 0.f : top;
+    q.sc.top = top * lift;
+    q.row.mul = lift;
+    if (isinf(q.sc.top)) {  // (of a finite maximum: nothing but its equals is near enough to weigh anything)
+        q.row.mul = q.sc.top = 0.f;
+        q.row.only = top;
+    }
 
     // ---- 2. bins ----
     const unsigned long long one = 1ull << (kUnit - p.extra);
