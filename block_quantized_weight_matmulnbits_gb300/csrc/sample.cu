@@ -17,17 +17,22 @@
 //   4. a bin with more of them is divided again, over the range of its values,
 //      until it has few or one value, whose j-th token is counted out.
 //
-// A draw depends on sums of up to a million weights next to a border, so the
-// weights are integers: 2^-y in units of 2^-43, y = (max - x) / T * log2 e in two
-// floats, from a table of 2^(-j / 1024) and a cubic of the rest (relative error
-// below 2^-34, one rounding of half a unit).  Their sums are exact and no order
-// of atomics changes them: results repeat, and agree with 64-bit floats but for
-// places that those do not settle either.
+// A draw depends on sums of up to millions of weights next to a border, so the
+// weights are integers: 2^-y, y = (max - x) / T * log2 e in two floats, from a
+// table of 2^(-j / 1024) and a cubic of the rest (relative error below 2^-34).
+// The unit goes by the bin: 2^-43 of the bin's octave (2^-(43 - extra) from 2^19
+// tokens on), so a weight keeps its bits however small it is, and many equal ones
+// do not lose them in one direction.  Sums inside a bin are exact, their prefix
+// over the bins is kept in units of 2^-43 and a fraction of 32 bits and floored
+// once; no order of atomics changes them.  So results repeat, and a sum up to a
+// place is within 2^-33 of what is kept of its value: two roundings down of 2^-37
+// at most, the weights' 2^-34, and 2^-36 for all weights past the last bin.
 //
-// Bound: the arithmetic of the weights and their bins (about 70 instructions a
-// token of the 80 to 100 in all), not the logits' bytes: 64 rows of 128000 f32 in
-// 70 us (0.5 TB/s), 256 of 50257 f16 in 80, 16 of 200003 f32 in 40.  Few rows: the
-// barriers of a cluster, about 0.7 us each; one row of 128000 bf16 takes 15.4 us.
+// Bound: the arithmetic of the weights and their bins, not the logits' bytes: 64
+// rows of 128000 f32 in 75 us (0.44 TB/s), 256 of 50257 f16 in 83, 16 of 200003 f32
+// in 41 (with one unit for all bins 70, 80 and 40: a third atomic addition for small
+// weights).  Few rows: the barriers of a cluster, about 0.7 us each; one row of
+// 128000 bf16 takes 15.9 us.
 #include <algorithm>
 #include <cmath>
 
@@ -39,13 +44,14 @@ namespace {
 constexpr int kBins = 2048;
 constexpr int kList = 1024;                            // tokens that the first CTA sorts
 constexpr int kRankSort = 256;                         // up to so many by counting those before each
-constexpr int kUnit = 43;                              // a weight of 1 is 2^43 units
+constexpr int kUnit = 43;                              // sums are in units of 2^-43 (2^extra times that) of the largest weight
+constexpr int kTableUnit = 53;                         // the table's numbers in units of 2^-53
+constexpr int kListUnit = 52;                          // weights of a list that spans bins: 1024 of them fit
 constexpr int kAbreast = 4;                            // weights that a thread forms at a time
 constexpr int kMaxVocab = 1 << 24;
 constexpr int kGathers = 32;                           // of a row: 2 of nuclei, 3 of places with at most 4 divisions each
-constexpr float kCut = kUnit + 0.99f;                  // weights below 2^-kCut (2^extra times that) are 0 units
 
-// 2^44 * 2^(-j / 1024), from the exponential series in double at compile time (good to 2^-50).
+// 2^53 * 2^(-j / 1024), from the exponential series in double at compile time (good to 2^-50).
 struct Table {
     unsigned long long v[1024];
     constexpr Table() : v() {
@@ -56,7 +62,7 @@ struct Table {
                 term = term * a / n;
                 sum += term;
             }
-            v[j] = (unsigned long long)(sum * 17592186044416.0 + 0.5);
+            v[j] = (unsigned long long)(sum * 9007199254740992.0 + 0.5);
         }
     }
 };
@@ -73,7 +79,8 @@ struct SampleParams {
     float* probs;
     int64_t stride;
     int V, C, seg, staged;
-    int extra;  // weights lose this many bits more, so that V of them fit 63
+    int extra;  // sums lose this many bits, so that V weights fit 63
+    int cut;    // octaves of the bins: weights below 2^-cut of the largest are left out
     int* status;
 };
 
@@ -122,10 +129,10 @@ __device__ __forceinline__ float value_of(uint32_t k) { return __uint_as_float((
 
 struct Scale {
     float top, c_hi, c_lo;  // maximum, log2 e / T in two floats
-    float cut, per;         // largest max - x of a weight above 0, bins per unit of max - x
+    float cut, per;         // largest max - x of a weight that counts, bins per unit of max - x
 };
 
-// 2^-y of a token, y = (top - x) c, as `units` (of 2^-44) and a right shift.  (top is finite.)
+// 2^-y of a token, y = (top - x) c, in units of 2^-53 before a right shift.  (top is finite.)
 __device__ __forceinline__ long long weight_parts(float x, const Scale& s, const unsigned long long* table, int& shift) {
     // d and its own rounding error (exact: d + e = top - x; top - x >= 0, so the larger of top and -x is so in magnitude)
     const float d = s.top - x;
@@ -140,19 +147,27 @@ __device__ __forceinline__ long long weight_parts(float x, const Scale& s, const
     const int f = __float2int_rn(fmaf(a * a, fmaf(a, 0.16666667f, 0.5f), a) * 4398046511104.f);
     const long long t = (long long)table[k & 1023];
     shift = k >> 10;
-    return t + (((long long)(int)(t >> 14) * f) >> 28);  // (t / 2^44 in units of 2^-30) * f
+    return t + (((long long)(int)(t >> 23) * f) >> 19);  // (t / 2^53 in units of 2^-30) * f
 }
 
-// The weight in units of 2^-(43 - extra), rounded.
-__device__ __forceinline__ unsigned long long weight_of(float x, const Scale& s, const unsigned long long* table, int extra) {
+// The weight of a token in a bin, in units of 2^-(52 - coarser), rounded.  (coarser may be negative where the shift makes up
+// for it; a token in no bin gets anything.)
+__device__ __forceinline__ unsigned long long weight_of(float x, const Scale& s, const unsigned long long* table, int coarser) {
     int shift;
     const unsigned long long t = (unsigned long long)weight_parts(x, s, table, shift);
-    shift = (shift + extra) & 63;  // at most 43 up to the cut
-    const unsigned long long w = ((t >> shift) + 1ull) >> 1;
-    return s.top - x <= s.cut ? w : 0ull;  // also NaN and -inf: 0
+    return ((t >> ((shift + coarser) & 63)) + 1ull) >> 1;
 }
 
-// Bin of a token of max - x = d: equal widths, -1 for a weight of 0 (NaN too).
+// v * 2^o, at most 2^63 - 1.
+__device__ __forceinline__ unsigned long long shift_up(unsigned long long v, int o) {
+    constexpr unsigned long long most = ~0ull >> 1;
+    return v > most >> o ? most : v << o;
+}
+
+// 2^e for e from -126 to 127.
+__device__ __forceinline__ float pow2f(int e) { return __int_as_float((127 + e) << 23); }
+
+// Bin of a token of max - x = d: equal widths, -1 for one that does not count (NaN too).
 __device__ __forceinline__ int bin_of(float x, const Scale& s) {
     const float d = s.top - x;
     return d <= s.cut ? min(__float_as_int(fmaf(d, s.per, 8388608.f)) - 0x4B000000, kBins - 1) : -1;
@@ -184,14 +199,14 @@ struct Shared {
     uint32_t mc[kBins];            // the cluster's counts, then their prefix
     union {
         struct {
-            uint32_t cnt[kBins], lo[kBins], hi[kBins];  // this CTA's, while they are summed
+            uint32_t cnt[kBins], lo[kBins], hi[kBins];  // this CTA's, while they are summed; lo: then the fractions of the cluster's
         };
         struct {
             unsigned long long list[kList];  // (order, index) of the cluster's gathered tokens (first CTA)
             unsigned long long sums[kList];  // this CTA's gathered tokens, then the prefix of the list's weights
         };
     };
-    unsigned long long scan_w[32];
+    unsigned long long scan_w[32], scan_f[32];
     unsigned long long minp_w, res_w, found_w;
     uint32_t scan_c[32];
     uint32_t listed[kGathers];  // (first CTA) tokens of each gather
@@ -199,6 +214,16 @@ struct Shared {
     uint32_t mine, first_index, kmin, kmax, found, found2, res_token;
     float res_x;
     Scale scale;
+};
+// Other CTAs write the first one's list while it may still read the fractions in lo.
+static_assert(sizeof(Shared::cnt) == sizeof(Shared::list), "the list must not reach lo");
+static_assert(kBins == 2048, "octave() divides by it");
+
+// The place of min-p among the bins: those before `lo` hold only weights above it, those after `hi` none.
+struct MinP {
+    float p;  // 0: none
+    int lo, hi, oct;               // oct: octave of lo
+    unsigned long long least;      // the smallest weight that is kept, in units of that octave
 };
 
 template <int DT, int THREADS>
@@ -296,7 +321,33 @@ struct Sampler {
     Scale sc;
     int rank;
     int tid, lane, warp;
+    MinP mp{};
     int gathers = 0;
+
+    // The octave that the unit of a bin's weights goes by: no weight of the bin is below 2 octaves under it, none above it.
+    __device__ __forceinline__ int octave(int b) const { return (max(b - 1, 0) * p.cut) >> 11; }
+    __device__ __forceinline__ int coarser(int oct) const { return kListUnit - kUnit + p.extra - oct; }
+
+    __device__ __forceinline__ void set_min_p(float min_p) {
+        mp.p = 0.f;
+        if (!(min_p > 0.f)) return;
+        const float q = fminf(min_p, 1.f);
+        // the bin of its place, or two where it is nearer to their border than the bins are exact (0.001)
+        const float at = -log2f(q) * ((float)kBins / (float)p.cut);
+        if (at > (float)kBins - 0.4f) return;  // all that counts is kept
+        mp.p = q;
+        mp.lo = max(__float2int_rn(at - 0.01f), 0);
+        mp.hi = min(__float2int_rn(at + 0.01f), kBins - 1);
+        mp.oct = octave(mp.lo);
+        mp.least = share_of<true>(fminf(q * pow2f(mp.oct), 1.f), 1ull << (kUnit - p.extra));
+    }
+    // Whether min-p keeps a token in a bin.
+    __device__ __forceinline__ bool keeps(float x) const {
+        int shift;
+        const unsigned long long t = (unsigned long long)weight_parts(x, sc, S.table, shift);
+        const float least = mp.p * pow2f(shift);  // of t in units of 2^-53
+        return least <= 2.f && t >= share_of<true>(0.5f * least, 2ull << kTableUnit);
+    }
 
     __device__ __forceinline__ void sync() const {
         if (p.C > 1) cluster_sync();
@@ -310,9 +361,10 @@ struct Sampler {
     }
 
     // Bins' counts (CNT) and sums of weights (WGT) over the cluster, then their prefix in mc and mw.  bin(x) < 0: in none.
-    // MINP: minp_w gets the sum of the weights from `minp` on.
-    template <bool CNT, bool WGT, bool MINP, class B>
-    __device__ __forceinline__ void histogram(B&& bin, unsigned long long minp) {
+    // ALL: the bins by max - x, each summed in units of its octave, the prefix in those of octave 0; else bins of one
+    // octave `oct`, whose units the prefix keeps.  MINP: minp_w gets the sum of what min-p keeps of the bins lo and hi.
+    template <bool CNT, bool WGT, bool MINP, bool ALL, class B>
+    __device__ __forceinline__ void histogram(B&& bin, int oct) {
         __syncthreads();
         for (int i = tid; i < kBins; i += THREADS) {
             S.cnt[i] = 0u;
@@ -335,11 +387,14 @@ struct Sampler {
             if constexpr (WGT) {
                 unsigned long long w[kAbreast];
 #pragma unroll
-                for (int j = 0; j < kAbreast; ++j) w[j] = weight_of(x[j], sc, S.table, p.extra);
+                for (int j = 0; j < kAbreast; ++j) w[j] = weight_of(x[j], sc, S.table, coarser(ALL ? octave(b[j]) : oct));
 #pragma unroll
                 for (int j = 0; j < kAbreast; ++j) {
                     if (b[j] < 0) continue;
-                    if (MINP && w[j] >= minp) keep += w[j];
+                    if (MINP && b[j] >= mp.lo && b[j] <= mp.hi) {
+                        const int finer = octave(b[j]) - mp.oct;
+                        if (w[j] >= mp.least << finer) keep += w[j] >> finer;
+                    }
                     const uint32_t lo = (uint32_t)w[j];
                     uint32_t hi = (uint32_t)(w[j] >> 32);
                     if (three) {
@@ -377,9 +432,11 @@ struct Sampler {
                     if (CNT) cs += c[r];
                     ws += lo[r] + ((unsigned long long)(WGT && three ? c[r] : 0u) << 16) + ((unsigned long long)hi[r] << 32);
                 }
+                const int o = ALL ? octave(b0 + i) : 0;
                 for (int r = 0; r < p.C; ++r) {
                     if (CNT) st_u32(&S.mc[b0 + i], r, cs);
-                    if (WGT) st_u64(&S.mw[b0 + i], r, ws);
+                    if (WGT) st_u64(&S.mw[b0 + i], r, ws >> o);
+                    if (WGT && ALL) st_u32(&S.lo[b0 + i], r, fraction(ws, o));  // (nobody else reads that bin's lo)
                 }
             }
             unsigned long long all = 0;
@@ -392,49 +449,65 @@ struct Sampler {
             __syncthreads();
             for (int i = tid; i < kBins; i += THREADS) {
                 if (CNT) S.mc[i] = S.cnt[i];
-                if (WGT) S.mw[i] = S.lo[i] + ((unsigned long long)(three ? S.cnt[i] : 0u) << 16) + ((unsigned long long)S.hi[i] << 32);
+                if (WGT) {
+                    const unsigned long long ws = S.lo[i] + ((unsigned long long)(three ? S.cnt[i] : 0u) << 16) + ((unsigned long long)S.hi[i] << 32);
+                    const int o = ALL ? octave(i) : 0;
+                    S.mw[i] = ws >> o;
+                    if (ALL) S.lo[i] = fraction(ws, o);
+                }
             }
             __syncthreads();
         }
         // inclusive prefix: kPer bins a thread
+        constexpr bool FRAC = WGT && ALL;
         uint32_t c[kPer], cs = 0;
-        unsigned long long w[kPer], ws = 0;
+        unsigned long long w[kPer], ws = 0, f[kPer], fs = 0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             if (CNT) cs += S.mc[tid * kPer + i];
             c[i] = cs;
             if (WGT) ws += S.mw[tid * kPer + i];
             w[i] = ws;
+            if (FRAC) fs += S.lo[tid * kPer + i];
+            f[i] = fs;
         }
         uint32_t ci = cs;
-        unsigned long long wi = ws;
+        unsigned long long wi = ws, fi = fs;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t a = CNT ? __shfl_up_sync(0xFFFFFFFFu, ci, o) : 0u;
             const unsigned long long b = WGT ? __shfl_up_sync(0xFFFFFFFFu, wi, o) : 0ull;
+            const unsigned long long d = FRAC ? __shfl_up_sync(0xFFFFFFFFu, fi, o) : 0ull;
             if (lane >= o) {
                 ci += a;
                 wi += b;
+                fi += d;
             }
         }
         if (lane == 31) {
             S.scan_c[warp] = ci;
             S.scan_w[warp] = wi;
+            S.scan_f[warp] = fi;
         }
         __syncthreads();
         uint32_t cb = ci - cs;
-        unsigned long long wb = wi - ws;
+        unsigned long long wb = wi - ws, fb = fi - fs;
 #pragma unroll
         for (int k = 0; k < kWarps; ++k) {
             if (CNT) cb += k < warp ? S.scan_c[k] : 0u;
             if (WGT) wb += k < warp ? S.scan_w[k] : 0ull;
+            if (FRAC) fb += k < warp ? S.scan_f[k] : 0ull;
         }
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             if (CNT) S.mc[tid * kPer + i] = cb + c[i];
-            if (WGT) S.mw[tid * kPer + i] = wb + w[i];
+            if (WGT) S.mw[tid * kPer + i] = wb + w[i] + (FRAC ? (fb + f[i]) >> 32 : 0ull);
         }
         __syncthreads();
+    }
+    // What a sum in units of an octave has below the units of octave 0, in 32 bits.
+    static __device__ __forceinline__ uint32_t fraction(unsigned long long w, int o) {
+        return o ? (uint32_t)((w << (64 - o)) >> 32) : 0u;
     }
 
     // First bin whose prefix reaches `target` (-1: none does).
@@ -455,15 +528,15 @@ struct Sampler {
         return b;
     }
 
-    // An upper bound of the tokens in the bins up to b: each bin's sum over its least weight.
+    // About the most tokens that the bins up to b hold: each bin's sum over its least weight.  (gather() counts them.)
     __device__ __forceinline__ float most_tokens(int b) {
         float n = 0.f;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int j = tid * kPer + i;
-            // (a weight at the far edge, half a bin past its middle, and a unit for the rounding)
+            // (a weight at the far edge, half a bin past its middle)
             const float w = (float)(S.mw[j] - (j ? S.mw[j - 1] : 0ull));
-            if (j <= b) n += w * exp2f(((float)j + 1.f) * ((kCut - p.extra) / kBins) - (float)(kUnit - p.extra)) * 1.001f;
+            if (j <= b) n += w * exp2f(((float)j + 0.5f) * ((float)p.cut / kBins) - (float)(kUnit - p.extra)) * 1.001f;
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
@@ -480,10 +553,10 @@ struct Sampler {
     __device__ __forceinline__ float radius_of(int b, float bins) const { return b < kBins - 1 ? (bins + 0x1p-8f) / sc.per : INFINITY; }
 
     // The number of tokens with in(x); if it is at most kList, they are in the first CTA's list, sorted, with the prefix of
-    // their weights.
+    // their weights (in units of 2^-(52 - coarser)).
     // Few windows have any: those without a token within `radius` of max - x = mid are passed over (in(x) implies that).
     template <class P>
-    __device__ __forceinline__ int gather(P&& in, float mid, float radius) {
+    __device__ __forceinline__ int gather(P&& in, float mid, float radius, int coarser) {
         __syncthreads();
         if (tid == 0) S.mine = 0u;
         __syncthreads();
@@ -522,11 +595,11 @@ struct Sampler {
         }
         const int n = (int)S.found;
         __syncthreads();
-        if (n <= kList && rank == 0) sort(n);
+        if (n <= kList && rank == 0) sort(n, coarser);
         return n;
     }
 
-    __device__ __forceinline__ void sort(int n) {
+    __device__ __forceinline__ void sort(int n, int coarser) {
         unsigned long long w[kList / THREADS], s = 0;
         if (n <= kRankSort) {
             // the place of a token is the number of those before it
@@ -563,7 +636,7 @@ struct Sampler {
 #pragma unroll
         for (int i = 0; i < per; ++i) {
             const int at = per * tid + i;
-            s += at < n ? weight_of(value_of(~(uint32_t)(S.list[at] >> 32)), sc, S.table, p.extra) : 0ull;
+            s += at < n ? weight_of(value_of(~(uint32_t)(S.list[at] >> 32)), sc, S.table, coarser) : 0ull;
             w[i] = s;
         }
         unsigned long long si = s;
@@ -594,13 +667,14 @@ struct Sampler {
         return at;
     }
 
-    __device__ __forceinline__ void write(int64_t r, int token, float x, unsigned long long total) {
+    // (total: in units of 2^-unit)
+    __device__ __forceinline__ void write(int64_t r, int token, float x, unsigned long long total, int unit) {
         if (tid != 0) return;
         p.tokens[r] = token;
         if (p.probs) {
             int shift;
             const double w = (double)weight_parts(x, sc, S.table, shift);
-            p.probs[r] = (float)(w / (double)total * exp2i(-1 - shift - p.extra));
+            p.probs[r] = (float)(w / (double)total * exp2i(unit - kTableUnit - shift));
         }
     }
     static __device__ __forceinline__ double exp2i(int e) { return __longlong_as_double((long long)(1023 + e) << 52); }
@@ -611,8 +685,11 @@ struct Sampler {
     template <bool COUNT, bool LAST>
     __device__ __forceinline__ bool resolve(int b, unsigned long long target) {
         b = max(b, 0);
-        unsigned long long base_w = b ? S.mw[b - 1] : 0ull;
-        uint32_t base_c = COUNT && b ? S.mc[b - 1] : 0u, kmin = 0u, kmax = ~0u;
+        const int oct = octave(b);
+        const unsigned long long base_w = b ? S.mw[b - 1] : 0ull;
+        // what is left of the target inside the bin (weights in units of its octave), and the weights before what is looked into
+        unsigned long long left = COUNT ? target - (b ? S.mc[b - 1] : 0u) : shift_up(target - base_w, oct), passed = 0ull;
+        uint32_t kmin = 0u, kmax = ~0u;
         bool divided = false;
         __syncthreads();
         auto extent = [&](auto&& in) {  // lowest and highest key of the tokens in(x)
@@ -648,7 +725,7 @@ struct Sampler {
         // (a NaN's key is above or below every number's, so x == x is asked)
         auto in = [&](float x) { return divided ? x == x && key_of(x) >= kmin && key_of(x) <= kmax : bin_of(x, sc) == b; };
         int m;
-        while ((m = gather(in, divided ? 0.f : b / sc.per, divided ? INFINITY : radius_of(b, 0.5f))) > kList) {
+        while ((m = gather(in, divided ? 0.f : b / sc.per, divided ? INFINITY : radius_of(b, 0.5f), coarser(oct))) > kList) {
             if (!divided) extent(in);
             divided = true;
             if (kmin == kmax) break;
@@ -658,17 +735,21 @@ struct Sampler {
                 const uint32_t k = key_of(x);
                 return x == x && k >= k0 && k <= k1 ? (int)((unsigned long long)(k1 - k) * kBins / span) : -1;
             };
-            histogram<COUNT, true, false>(sub, 0ull);
-            const int f = max(first_bin<COUNT>(target - (COUNT ? (unsigned long long)base_c : base_w)), 0);  // (one always does)
-            if (COUNT) base_c += f ? S.mc[f - 1] : 0u;
-            base_w += f ? S.mw[f - 1] : 0ull;
+            histogram<COUNT, true, false, false>(sub, oct);
+            // (the prefix over the bins is floored, so what is left may be up to a unit more than the bin has: its last token)
+            if (!COUNT) left = min(left, S.mw[kBins - 1]);
+            const int f = max(first_bin<COUNT>(left), 0);  // (one always does)
+            if (f) {
+                left -= COUNT ? (unsigned long long)S.mc[f - 1] : S.mw[f - 1];
+                passed += S.mw[f - 1];
+            }
             extent([&](float x) { return sub(x) == f; });
         }
         if (m <= kList) {
             if (rank == 0) {
-                const int at = COUNT ? min((int)(target - base_c), m) - 1 : first_listed(target - base_w, m);
+                const int at = COUNT ? min((int)left, m) - 1 : first_listed(left, m);
                 if (tid == 0) {
-                    S.res_w = base_w + S.sums[at];
+                    S.res_w = base_w + ((passed + S.sums[at]) >> oct);
                     S.res_token = (uint32_t)S.list[at];
                     S.res_x = value_of(~(uint32_t)(S.list[at] >> 32));
                 }
@@ -676,8 +757,8 @@ struct Sampler {
         } else {
             // one value, more than fits the list: the j-th of its tokens
             const float x0 = value_of(kmin);
-            const unsigned long long w = weight_of(x0, sc, S.table, p.extra);
-            const unsigned long long j = COUNT ? target - base_c : (target - base_w + w - 1) / w;  // from 1; w > 0, else no target is here
+            const unsigned long long w = weight_of(x0, sc, S.table, coarser(oct));
+            const unsigned long long j = COUNT ? left : min((left + w - 1) / w, (unsigned long long)m);  // from 1
             // a thread counts windows that follow each other
             const int per = (row.windows + THREADS - 1) / THREADS;
             const int w0 = min(tid * per, row.windows), w1 = min(w0 + per, row.windows);
@@ -722,7 +803,7 @@ struct Sampler {
                 }
             }
             if (rank == 0 && tid == 0) {
-                S.res_w = base_w + j * w;
+                S.res_w = base_w + ((passed + j * w) >> oct);
                 S.res_x = x0;
             }
         }
@@ -776,7 +857,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
         const double c = 1.4426950408889634 / ((double)temperature * (double)lift);
         S.scale.c_hi = (float)c;
         S.scale.c_lo = (float)(c - (double)S.scale.c_hi);
-        S.scale.cut = fminf(__fdiv_rn(kCut - p.extra, S.scale.c_hi), 3.4e38f);
+        S.scale.cut = fminf(__fdiv_rn((float)p.cut, S.scale.c_hi), 3.4e38f);
         S.scale.per = (float)kBins / S.scale.cut;
     }
 
@@ -857,12 +938,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
     }
 
     // ---- 2. bins ----
-    const unsigned long long one = 1ull << (kUnit - p.extra);
-    const unsigned long long minp = min_p > 0.f ? share_of<true>(fminf(min_p, 1.f), one) : 0ull;
+    q.set_min_p(min_p);
     auto bin = [&](float x) { return bin_of(x, q.sc); };
     auto weigh = [&] {
-        if (minp) q.template histogram<false, true, true>(bin, minp);
-        else q.template histogram<false, true, false>(bin, 0ull);
+        if (q.mp.p > 0.f) q.template histogram<false, true, true, true>(bin, 0);
+        else q.template histogram<false, true, false, true>(bin, 0);
     };
     auto upto = [&](int last) {
         return [&, last](float x) { const int b = bin_of(x, q.sc); return b >= 0 && b <= last; };
@@ -871,14 +951,14 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
     int n = kList + 1;  // tokens of the list that holds all that can be kept
     unsigned long long total = 0ull, kept = 0ull, least = ~0ull;  // sums: of the top k, of what is kept; of what min-p keeps
     if (by_k) {
-        q.template histogram<true, false, false>(bin, 0ull);
+        q.template histogram<true, false, false, true>(bin, 0);
         const int b = q.template first_bin<true>((unsigned long long)top_k);
-        if (b < 0) by_k = false;  // every token of a weight above 0 is among the k
-        else if (S.mc[b] <= (uint32_t)kList) n = q.gather(upto(b), 0.f, q.radius_of(b, b + 0.5f));
+        if (b < 0) by_k = false;  // every token that counts is among the k
+        else if (S.mc[b] <= (uint32_t)kList) n = q.gather(upto(b), 0.f, q.radius_of(b, b + 0.5f), 0);
     }
     if (n > kList) {
         weigh();
-        if (minp) least = S.minp_w;
+        if (q.mp.p > 0.f) least = (q.mp.lo ? S.mw[q.mp.lo - 1] : 0ull) + (S.minp_w >> q.mp.oct);
         total = S.mw[kBins - 1];
         bool whole = true;  // mw is that of the bins
         if (by_k) {
@@ -892,7 +972,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
             whole = true;
             const int b = q.template first_bin<false>(target);
             // a nucleus that fits the list: all of it, and the draw from it
-            if (q.most_tokens(b) <= (float)kList) n = q.gather(upto(b), 0.f, q.radius_of(b, b + 0.5f));
+            if (q.most_tokens(b) <= (float)kList) n = q.gather(upto(b), 0.f, q.radius_of(b, b + 0.5f), 0);
             if (n > kList) {
                 whole = !q.template resolve<false, false>(b, target);
                 kept = S.found_w;
@@ -903,7 +983,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
             const unsigned long long target = share_of<false>(u, kept) + 1ull;
             if (!whole) weigh();
             q.template resolve<false, true>(q.template first_bin<false>(target), target);
-            if (rank == 0) q.write(r, (int)S.res_token, S.res_x, kept);
+            if (rank == 0) q.write(r, (int)S.res_token, S.res_x, kept, kUnit - p.extra);
             q.leave();
             return;
         }
@@ -911,23 +991,25 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
 
     // ---- 3. all that can be kept is in the list ----
     if (rank == 0) {
-        if (by_k && total == 0ull) total = S.sums[min(top_k, n) - 1];
-        kept = total;
+        // (its weights are finer than the sums of the bins, which a nucleus that was found among those goes by)
+        const bool all = total == 0ull;
+        kept = S.sums[min(all ? top_k : n, n) - 1];
         if (top_p < 1.f) {
-            const unsigned long long target = max(share_of<true>(fmaxf(top_p, 0.f), total), 1ull);
-            kept = S.sums[q.first_listed(target, n)];
+            const unsigned long long target = max(share_of<true>(fmaxf(top_p, 0.f), all ? kept : total), 1ull);
+            kept = S.sums[q.first_listed(all ? target : shift_up(target, kListUnit - kUnit + p.extra), n)];
         }
-        if (minp) {  // weights descend along the list: the sum before the first below minp
+        if (min_p > 0.f) {  // weights descend along the list: the sum before the first that is not kept
+            q.mp.p = fminf(min_p, 1.f);
             if (tid == 0) S.mine = (uint32_t)n;
             __syncthreads();
             for (int at = tid; at < n; at += THREADS)
-                if (S.sums[at] - (at ? S.sums[at - 1] : 0ull) < minp) atomicMin(&S.mine, (uint32_t)at);
+                if (!q.keeps(value_of(~(uint32_t)(S.list[at] >> 32)))) atomicMin(&S.mine, (uint32_t)at);
             __syncthreads();
             kept = min(kept, S.sums[max((int)S.mine, 1) - 1]);
         }
         const unsigned long long target = share_of<false>(u, kept) + 1ull;
         const int at = q.first_listed(target, n);
-        q.write(r, (int)(uint32_t)S.list[at], value_of(~(uint32_t)(S.list[at] >> 32)), kept);
+        q.write(r, (int)(uint32_t)S.list[at], value_of(~(uint32_t)(S.list[at] >> 32)), kept, kListUnit);
     }
     q.leave();
 }
@@ -986,6 +1068,9 @@ mnb_status mnb_sample(const mnb_sample_args* a) {
     p.V = (int)a->V;
     p.stride = a->B > 1 ? a->row_stride : a->V;
     while (((int64_t)p.V >> p.extra) >= (1 << 19)) ++p.extra;  // V * 2^(43 - extra) below 2^63
+    p.cut = 36;  // V weights of 2^-cut are below 2^-36
+    while ((int64_t(1) << (p.cut - 36)) < p.V) ++p.cut;
+    p.cut = std::max(p.cut, 44);
     if (inject_launch_failure()) return MNB_ERR_CUDA;
     const cudaStream_t s = (cudaStream_t)a->stream;
     ProfileScope prof("mnb_sample", s);

@@ -781,10 +781,13 @@ MNB_API size_t mnb_moe_workspace_size(int64_t T, int64_t S, int64_t E, int64_t h
  *   min-p   of these, those with w_i >= min_p (0: all; above 1 acts as 1)
  * and the token is the first in that order whose sum of kept weights, its own
  * included, exceeds u times the sum of all kept ones.  T == 0 takes the first
- * token of the order.  Weights below 2^-44 of the largest (2^-39 for the largest
- * V) are never drawn; a NaN counts as -inf.  A row without a logit above -inf gets token -1,
- * probability 0.  Sums are exact integers (units of 2^-43 of the largest
- * weight for V below 2^19): results repeat, and agree with 64-bit arithmetic.
+ * token of the order.  A NaN counts as -inf.  A row without a logit above -inf gets
+ * token -1, probability 0.  Every sum of weights is within 2^-33 of the kept
+ * sum of its value in exact arithmetic, for any V: a token drawn is that of the
+ * definition unless u is nearer than that to a border, and so is what the cuts
+ * keep (a weight within 2^-33 of itself of min_p may be kept or not).  Weights
+ * below 2^-44 of the largest, for V above 256 below 2^-36 / V of it, are left out
+ * (2^-36 of a row in all).  Sums are exact integers: results repeat.
  *   logits       device [B, V] of dtype, row stride in elements, aligned to the
  *                element
  *   u            device f32 [B], in [0, 1)
