@@ -5,7 +5,11 @@
 // after everything else.  A token's weights are exp(l - max) of its experts,
 // divided by the sum over its experts (renormalised) or over all of them, or
 // the sigmoids, divided by their sum or not, times a scale.  An expert of logit
-// -inf weighs 0; where all do, every weight is 0.
+// -inf weighs 0; where all do, every weight is 0.  Sigmoids that are divided by
+// their sum and all below exp(-60) are exp(l) to 2^-86 of themselves, and are taken
+// relative to the largest, as their sum would be subnormal or 0 in 32 bits.  Where
+// it is 0 in 64 bits too (logits below -745, the lowest value of a mask), so are
+// the weights.
 #pragma once
 
 #include "moe.h"
@@ -20,7 +24,9 @@ __device__ __forceinline__ uint32_t order_key(float f) {
     return isnan(f) ? 1u : (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-__device__ __forceinline__ float sigmoid(float v) { return 1.f / (1.f + expf(-v)); }
+// (below -80 1 + exp(v) is 1, and exp(-v) soon past the range)
+__device__ __forceinline__ float sigmoid(float v) { return v > -80.f ? 1.f / (1.f + expf(-v)) : expf(v); }
+constexpr float kTail = -60.f, kNone = -745.f;
 
 // Key of expert e of logit l: what is ordered.
 __device__ __forceinline__ uint32_t route_key(const Route& r, float l, int e) {
@@ -30,8 +36,12 @@ __device__ __forceinline__ uint32_t route_key(const Route& r, float l, int e) {
 
 // Weight of place s of a token with the given logits, whose experts are ids[0 .. S - 1].
 __device__ __forceinline__ float route_weight(const Route& r, const float* logit, const int* ids, int s) {
-    const float top = logit[ids[0]];
-    auto score = [&](float l) { return r.sigmoid ? sigmoid(l) : l != -INFINITY ? expf(l - top) : 0.f; };
+    float top = logit[ids[0]];
+    if (r.sigmoid && r.renorm)  // (a bias may have put another one first)
+        for (int j = 1; j < r.S; ++j) top = fmaxf(top, logit[ids[j]]);
+    const bool plain = r.sigmoid && !(r.renorm && top < kTail);
+    const float least = r.sigmoid ? kNone : -INFINITY;
+    auto score = [&](float l) { return plain ? sigmoid(l) : l <= least ? 0.f : expf(l - top); };
     float w = score(logit[ids[s]]), sum = 0.f;
     if (r.renorm) {
         for (int j = 0; j < r.S; ++j) sum += score(logit[ids[j]]);
@@ -87,10 +97,17 @@ __device__ __forceinline__ void route_token(const Route& r, int64_t t, int& expe
         }
     }
     float w;
-    if (r.sigmoid) {
+    bool plain = r.sigmoid;
+    if (r.sigmoid && r.renorm) {  // (a bias may have put another one first)
+        top = lane < r.S ? logit : -INFINITY;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        plain = !(top < kTail);
+    }
+    if (plain) {
         w = lane < r.S ? sigmoid(logit) : 0.f;
     } else {
-        w = lane < r.S && logit != -INFINITY ? expf(logit - top) : 0.f;
+        w = lane >= r.S || logit <= (r.sigmoid ? kNone : -INFINITY) ? 0.f : expf(logit - top);
         if (!r.renorm) {
 #pragma unroll
             for (int j = 0; j < VPL; ++j)

@@ -695,7 +695,8 @@ MNB_API mnb_status mnb_rms_norm(const mnb_rms_norm_args* args);
  *   renormalize  1: a token's weights are its S scores (exp(logit) or the
  *                sigmoids) divided by their sum; 0: the softmax over all E, or
  *                the sigmoids as they are.  An expert of logit -inf weighs 0,
- *                and where every selected one does, so do all.
+ *                and where every selected one does, so do all (as where every
+ *                selected sigmoid is 0 in 64 bits: logits below -745).
  *   scale        multiplies the weights
  *   ids, weights device int32 and f32 [T, S]: the result.  NULL: not wanted
  * S <= 32 and E <= 1024, else MNB_ERR_UNSUPPORTED.  ids is what
