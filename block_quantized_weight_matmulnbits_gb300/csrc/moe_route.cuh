@@ -25,7 +25,11 @@ __device__ __forceinline__ uint32_t order_key(float f) {
 }
 
 // (below -80 1 + exp(v) is 1, and exp(-v) soon past the range)
-__device__ __forceinline__ float sigmoid(float v) { return v > -80.f ? 1.f / (1.f + expf(-v)) : expf(v); }
+__device__ __forceinline__ float sigmoid(float v) {
+    const bool far = v <= -80.f;
+    const float e = expf(far ? v : -v);
+    return far ? e : 1.f / (1.f + e);
+}
 constexpr float kTail = -60.f, kNone = -745.f;
 
 // Key of expert e of logit l: what is ordered.
@@ -38,10 +42,15 @@ __device__ __forceinline__ uint32_t route_key(const Route& r, float l, int e) {
 __device__ __forceinline__ float route_weight(const Route& r, const float* logit, const int* ids, int s) {
     float top = logit[ids[0]];
     if (r.sigmoid && r.renorm)  // (a bias may have put another one first)
+#pragma unroll 1
         for (int j = 1; j < r.S; ++j) top = fmaxf(top, logit[ids[j]]);
     const bool plain = r.sigmoid && !(r.renorm && top < kTail);
     const float least = r.sigmoid ? kNone : -INFINITY;
-    auto score = [&](float l) { return plain ? sigmoid(l) : l <= least ? 0.f : expf(l - top); };
+    auto score = [&](float l) {
+        const bool far = !plain || l <= -80.f;
+        const float e = expf(!plain ? l - top : far ? l : -l);
+        return !far ? 1.f / (1.f + e) : !plain && l <= least ? 0.f : e;
+    };
     float w = score(logit[ids[s]]), sum = 0.f;
     if (r.renorm) {
         for (int j = 0; j < r.S; ++j) sum += score(logit[ids[j]]);
