@@ -10,6 +10,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
+#include <unordered_map>
 #include <vector>
 
 #include "mnb.h"
@@ -98,6 +99,29 @@ mnb_status from_cuda(cudaError_t e) {
 }
 
 }  // namespace
+
+cudaError_t allow_shared(const void* kern) {
+    static std::mutex mu;
+    static std::unordered_map<const void*, int> limits;
+    int limit = 0;
+    {
+        std::lock_guard<std::mutex> lk(mu);
+        const auto at = limits.find(kern);
+        if (at != limits.end()) limit = at->second;
+    }
+    if (limit == 0) {
+        cudaFuncAttributes a;
+        const cudaError_t e = cudaFuncGetAttributes(&a, kern);
+        if (e != cudaSuccess) return e;
+        const size_t optin = device_info().smem_optin;
+        if (optin <= a.sharedSizeBytes) return cudaErrorUnknown;  // (no device)
+        limit = (int)(optin - a.sharedSizeBytes);
+        std::lock_guard<std::mutex> lk(mu);
+        limits[kern] = limit;
+    }
+    // (set in every call: a reset of the device takes it back)
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, limit);
+}
 
 bool current_context_id(unsigned long long* id) {
     // cuCtxGetCurrent / cuCtxGetId through the runtime's driver entry points,

@@ -128,6 +128,14 @@ struct DeviceInfo {
 };
 const DeviceInfo& device_info();
 
+// Lets a kernel have as much dynamic shared memory as a block can beside its static part.  The limit belongs to the
+// function, not to a call: with the call's own size another thread's smaller call could lower it before the launch.
+cudaError_t allow_shared(const void* kern);
+template <typename... P>
+cudaError_t allow_shared(void (*kern)(P...)) {
+    return allow_shared(reinterpret_cast<const void*>(kern));
+}
+
 // Device address of the current device's status word (see mnb_get_device_error).
 int* device_status_word();
 

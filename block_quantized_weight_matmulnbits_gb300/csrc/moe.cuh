@@ -840,7 +840,7 @@ cudaError_t launch_gate_up(Params p, cudaStream_t s) {
     auto kern = gate_up_kernel<BITS, BF, BSL>;
     const int P = p.r.T * p.r.S;
     const size_t smem = (size_t)kWarps * (kRingBytes + It::kTabBytes + 2 * 32 * 16) + Lists::bytes(P);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = allow_shared(kern);
     if (e != cudaSuccess) return e;
     // two CTAs an SM; no more than the row tiles of the most experts that can be active
     const int64_t most = (int64_t)(P < p.r.E ? P : p.r.E) * p.a.row_tiles;
@@ -854,7 +854,7 @@ cudaError_t launch_down(Params p, cudaStream_t s) {
     set_vectors<It>(p, BITS);
     auto kern = down_kernel<BITS, BSL>;
     const size_t smem = (size_t)kWarps * (kRingBytes + It::kTabBytes + p.r.T * 32 * 4) + Lists::bytes(p.r.T * p.r.S);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = allow_shared(kern);
     if (e != cudaSuccess) return e;
     const int64_t groups = (p.a.row_tiles + 1) / 2;
     // as many CTAs a group of 32 rows as two an SM hold, up to a portable cluster

@@ -1023,7 +1023,7 @@ cudaError_t launch_threads(SampleParams p, int64_t rows, cudaStream_t s) {
     p.staged = fixed + bytes <= (THREADS == 512 ? device_info().smem_optin / 2 - 1024 : device_info().smem_optin);
     if (!p.staged) bytes = 0;
     auto kern = sample_kernel<DT, THREADS>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(fixed + bytes));
+    const cudaError_t e = allow_shared(kern);
     if (e != cudaSuccess) return e;
     return dec::launch_pdl(kern, dim3((unsigned)(rows * p.C)), dim3(THREADS), fixed + bytes, s, p.C, p);
 }
