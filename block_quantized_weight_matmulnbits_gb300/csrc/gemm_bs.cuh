@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_bs_kernel(MatmulParams p, Ge
 template <int BITS, bool BF16X>
 cudaError_t launch(const MatmulParams& p, const Geom& geo, const Maps& m, cudaStream_t s) {
     auto go = [&](auto kern) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)geo.total_bytes);
+        cudaError_t e = allow_shared(kern);
         if (e != cudaSuccess) return e;
         kern<<<(unsigned)(geo.n_tiles * geo.m_tiles), kThreads, geo.total_bytes, s>>>(p, geo, m.x, m.w);
         return cudaGetLastError();

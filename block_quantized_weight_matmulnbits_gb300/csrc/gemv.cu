@@ -510,8 +510,7 @@ bool gemv_supported(const MatmulParams& p) {
 
 template <int BITS, int SPB_LOG>
 static cudaError_t launch_one(const MatmulParams& p, const GemvGeom& geo, int64_t grid, cudaStream_t s) {
-    cudaError_t e = cudaFuncSetAttribute(gemv_kernel<BITS, SPB_LOG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)geo.total_bytes);
+    cudaError_t e = allow_shared(gemv_kernel<BITS, SPB_LOG>);
     if (e != cudaSuccess) return e;
     gemv_kernel<BITS, SPB_LOG><<<(unsigned)grid, kThreads, geo.total_bytes, s>>>(p, geo);
     return cudaGetLastError();

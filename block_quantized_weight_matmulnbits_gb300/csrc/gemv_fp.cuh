@@ -315,7 +315,7 @@ cudaError_t launch_fmt(const FpParams& p, const FGeom& geo, cudaStream_t s) {
     const bool bf = p.act_dtype == kBF16;
     const int pdl = (p.flags & kFlagPDL) ? 1 : 0;
     auto go = [&](auto kern) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)geo.total_bytes);
+        cudaError_t e = allow_shared(kern);
         if (e != cudaSuccess) return e;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)geo.G);

@@ -432,7 +432,7 @@ cudaError_t launch_variant(const MatmulParams& p, const Geom& geo, const int8_t*
                            cudaStream_t s) {
     const int pdl = (p.flags & kFlagPDL) ? 1 : 0;
     auto kern = gemv_i8_kernel<BITS, MT, SPB_LOG>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)geo.total_bytes);
+    cudaError_t e = allow_shared(kern);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.L.NT * geo.C));

@@ -784,7 +784,7 @@ cudaError_t launch_k(const MatmulParams& p, const KGeom& geo, cudaStream_t s, co
         gk.total_bytes = geo.x_bytes + geo.red_bytes + kperm_x_bytes(p.L, p.M);  // X as given, for the gather
     }
     const MoeKs none{};
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)gk.total_bytes);
+    cudaError_t e = allow_shared(kern);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)gk.G);

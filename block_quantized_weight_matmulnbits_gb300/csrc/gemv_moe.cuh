@@ -171,7 +171,7 @@ template <int BITS, bool BF16X, int MT, int SPB_LOG>
 cudaError_t launch_variant(const MatmulParams& p, const gmma::Geom& geo, const MoeArgs& g, unsigned groups,
                            size_t smem_bytes, cudaStream_t s) {
     auto kern = gemv_moe_kernel<BITS, BF16X, MT, SPB_LOG>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes);
+    cudaError_t e = allow_shared(kern);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.L.NT * geo.C), groups);

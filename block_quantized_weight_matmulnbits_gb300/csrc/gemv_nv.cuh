@@ -336,7 +336,7 @@ inline cudaError_t launch(const FpParams& p, const NGeom& geo, cudaStream_t s) {
     const bool bf = p.act_dtype == kBF16;
     const int pdl = (p.flags & kFlagPDL) ? 1 : 0;
     auto go = [&](auto kern) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)geo.total_bytes);
+        cudaError_t e = allow_shared(kern);
         if (e != cudaSuccess) return e;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)geo.G);

@@ -316,7 +316,7 @@ template <int BITS, bool BF16X, int MT, int SPB_LOG, int TPW>
 cudaError_t launch_p(const MatmulParams& p, const PGeom& geo, int grid, cudaStream_t s) {
     const int pdl = (p.flags & kFlagPDL) ? 1 : 0;
     auto kern = gemv_pers_kernel<BITS, BF16X, MT, SPB_LOG, TPW>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)geo.total_bytes);
+    cudaError_t e = allow_shared(kern);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);

@@ -372,7 +372,7 @@ template <int BITS, bool BF16X, int MT, int SPB_LOG>
 cudaError_t launch_s(const MatmulParams& p, const SGeom& geo, cudaStream_t s) {
     const int pdl = (p.flags & kFlagPDL) ? 1 : 0;
     auto kern = gemv_stream_kernel<BITS, BF16X, MT, SPB_LOG>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)geo.total_bytes);
+    cudaError_t e = allow_shared(kern);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)geo.G);

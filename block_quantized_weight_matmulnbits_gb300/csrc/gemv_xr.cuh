@@ -340,7 +340,7 @@ template <int BITS, bool BF16X, int TPW, int SPB_LOG>
 cudaError_t launch_x(const MatmulParams& p, const XGeom& geo, cudaStream_t s) {
     const int pdl = (p.flags & kFlagPDL) ? 1 : 0;
     auto kern = gemv_xr_kernel<BITS, BF16X, TPW, SPB_LOG>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)geo.total_bytes);
+    cudaError_t e = allow_shared(kern);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)geo.G);

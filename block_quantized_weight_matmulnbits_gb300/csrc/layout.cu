@@ -215,7 +215,7 @@ cudaError_t launch_gather_kperm(const void* x, const int32_t* perm, void* xp, in
     if (M <= 0 || L.K <= 0) return cudaSuccess;
     const size_t smem = (size_t)L.K * 2;
     if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(gather_kperm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaError_t e = allow_shared(gather_kperm_kernel);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};

@@ -74,3 +74,30 @@ def test_experts(mnb):
         done.append((got, want))
     assert together(calls) == set()
     assert all(torch.equal(a, b) for a, b in done) and mnb.mnb_get_device_error() == 0
+
+
+@pytest.mark.parametrize("m", [1, 2, 8, 64])
+@pytest.mark.parametrize("acc", [0, 4])
+def test_products(mnb, m, acc):
+    """Products of few and many rows whose shared memory goes by K."""
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    calls, done = [], []
+    for n, k in ((256, 256), (256, 8192)):
+        codes = torch.randint(0, 256, (n, k // 32, 16), generator=gen, device="cuda", dtype=torch.uint8)
+        scales = (torch.rand((n, k // 32), generator=gen, device="cuda") * 0.01).half()
+        packed = G.aligned_empty(mnb.mnb_packed_size(n, k, 4, 32))
+        mnb.mnb_pack_weights(codes, packed, n, k, 4, 32)
+        x = torch.randn((m, k), generator=gen, device="cuda").half()
+        want, got = torch.empty((m, n), dtype=torch.float16, device="cuda"), torch.empty((m, n), dtype=torch.float16, device="cuda")
+        ws = G.aligned_empty(max(256, mnb.mnb_workspace_size(m, n, k, 4, 32, acc)))
+
+        def make(stream, x=x, packed=packed, scales=scales, n=n, k=k, ws=ws, y=got):
+            a = mnb._matmul_args(x, packed, scales, None, y, m, n, k, 4, 32, mnb.MNB_F16, mnb.MNB_F16, mnb.MNB_F16, None, None, mnb.MNB_F32,
+                                 acc, ws, "auto", stream, 0)
+            return lambda: mnb.load().mnb_matmul_ex(a)
+
+        mnb.mnb_matmul_ex(x, packed, scales, None, want, m, n, k, 4, 32, mnb.MNB_F16, mnb.MNB_F16, mnb.MNB_F16, accuracy_level=acc, workspace=ws)
+        calls.append(make)
+        done.append((got, want))
+    assert together(calls) == set()
+    assert all(torch.equal(a, b) for a, b in done) and mnb.mnb_get_device_error() == 0
