@@ -720,7 +720,8 @@ def expert_weights(packed, scales, zero_points, E, N, K, bits, block_size) -> Ex
                       None if zero_points is None else _here("zero_points", zero_points, dev), E, N, K, bits, block_size, _codes[scales.dtype])
     w.tensors = (packed, scales, zero_points)
     w.dev = dev
-    w.ref = ctypes.pointer(w)
+    # (ctypes.pointer(w) would hold w: a cycle that keeps the weights on the GPU until the collector runs)
+    w.ref = ctypes.POINTER(ExpertWeights).from_buffer(ctypes.c_void_p(ctypes.addressof(w)))
     return w
 
 
