@@ -768,7 +768,12 @@ def mnb_moe(x, logits, gate, up, down, y, top_k, ids=None, weights=None, bias=No
     ids and weights [T, top_k], where given, get the selection."""
     if not _codes:
         _setup()
-    s, dev = _current(stream), _current_device()
+    s, dev = _current(stream), _current_device() if logits.is_cuda else -2
+    ws_ptr, ws_bytes = _space(workspace)
+    if workspace is not None:
+        if not workspace.is_contiguous():
+            _fail("workspace: a contiguous buffer is wanted")
+        _here("workspace", workspace, dev)
     r = _route(logits, top_k, ids, weights, bias, scoring, renormalize, scale, s, dev)
     shape = x.shape
     code, out = _codes.get(x.dtype, -1), _codes.get(y.dtype, -1)
@@ -778,7 +783,6 @@ def mnb_moe(x, logits, gate, up, down, y, top_k, ids=None, weights=None, bias=No
         _away("gate, up, down")
     xp, xs = _row_matrix("x", x, shape, dev)
     yp, ys = _row_matrix("y", y, shape, dev)
-    ws_ptr, ws_bytes = _space(workspace)
     a = MoeArgs(xp, yp, gate.ref, up.ref, down.ref, xs, ys, code, out, activation, ws_ptr, ws_bytes, s)
     st = (_lib or load()).mnb_moe(a, r)
     if st:

@@ -34,3 +34,11 @@ def test_weights_go_with_their_descriptor(monkeypatch):
 def test_descriptor_points_to_itself(monkeypatch):
     w, _ = _weights(monkeypatch)
     assert (w.ref.contents.E, w.ref.contents.N, w.ref.contents.K) == (2, 16, 32) and w.ref.contents.packed_b == w.packed_b
+
+
+def test_workspace_is_checked():
+    x, logits, y = torch.ones((1, 32), dtype=torch.bfloat16), torch.ones((1, 2)), torch.ones((1, 32))
+    w = mnb.ExpertWeights()
+    for workspace in (torch.empty(1 << 20, dtype=torch.uint8), torch.empty((1 << 12, 512), dtype=torch.uint8)[:, :256], torch.empty(0)):
+        with pytest.raises(ValueError, match="workspace"):
+            mnb.mnb_moe(x, logits, w, w, w, y, 1, workspace=workspace, stream=0)
