@@ -15,10 +15,9 @@
 // the sums are scaled at the end.  Columns of bf16 are scaled by 2^60 (h where
 // it is written, x in the loop), so that the products are normal numbers.
 //
-// The warp-level MMA of this part is slow (one m16n8k16 in 8 cycles an SM): 16
-// of them for the 2 KB of an item take about as long as its bytes from memory,
-// so none is spent on anything else (sums of x for the zero points by an MMA
-// with ones: half as long again).
+// A warp-level m16n8k16 takes 8 cycles of a quarter of an SM, 2 of the SM: the 16
+// of an item's 2 KB take 32 cycles, its bytes from memory about 90.  So the MMAs
+// are not the bound, but the instructions around them come close to it.
 //
 // The work of a warp comes in items: two row tiles that multiply the same
 // columns (gate and up of one row tile; two neighbouring row tiles of down), 128
@@ -51,10 +50,11 @@
 // flight when gate_up ends.
 //
 // Measured (int4, f16 or bf16 scales, both kernels): 4 tokens x 2 of 8 experts of
-// 4096 x 14336 in 146 us (3480 GB/s, half a copy's rate; 101 us of it are MMAs,
-// issue slots 62% full in gate_up), 16 tokens x 8 of 64 experts of 2048 x 1408 in 78, one token
-// x 8 of 64 of 2048 x 1024 in 20.5, of which about 8 stream weights and the rest
-// is the start, routing and the joins of two kernels.
+// 4096 x 14336 in 147 us (3470 GB/s, half a copy's rate; 24 us of it are MMAs,
+// issue slots 61% full in gate_up and 51% in down, by 16 warps an SM), 16 tokens x
+// 8 of 64 experts of 2048 x 1408 in 78, one token x 8 of 64 of 2048 x 1024 in 20.9,
+// of which about 8 stream weights and the rest is the start, routing and the joins
+// of two kernels.
 #pragma once
 
 #include "decoder.h"

@@ -14,7 +14,7 @@
 //
 // Measured: 4999 rows of 5120 f16 with a residual 38.6 us (5300 GB/s, 0.78 of a
 // copy); 16384 rows of 4096 bf16 to codes of blocks of 32 in 98 us (4880 GB/s),
-// bound there by instructions and by 32 warps an SM (with 80 and 128 registers a
+// bound there by instructions (36 a value) and by 32 warps an SM (with 80 and 128 registers a
 // thread instead of 64, so 24 and 16 warps: 108 and 127 us); 64 rows
 // of 8192 2.7 us, a launch and one chain of load, reduction and store.
 #include <algorithm>
@@ -262,7 +262,8 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(NormParams p) {
 
 template <int DT, int VPT>
 cudaError_t launch_vpt(const NormParams& p, int threads, bool wide, cudaStream_t s) {
-    const int64_t fit = std::max(1, 2048 / threads) * (int64_t)dec::kSms;  // CTAs that the SMs hold
+    // CTAs of 2048 threads an SM; half of them are resident at 64 registers (1024 to 16384 threads an SM take the same time)
+    const int64_t fit = std::max(1, 2048 / threads) * (int64_t)dec::kSms;
     const unsigned grid = (unsigned)std::min<int64_t>(p.rows, fit);
     constexpr int V = DT == kF32 ? 4 : 8;
     const size_t smem = p.codes && (1 << p.bs_shift) > 32 * V ? (size_t)p.blocks * 8 : 0;

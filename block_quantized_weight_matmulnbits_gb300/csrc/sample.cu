@@ -28,11 +28,11 @@
 // place is within 2^-33 of what is kept of its value: two roundings down of 2^-37
 // at most, the weights' 2^-34, and 2^-36 for all weights past the last bin.
 //
-// Bound: the arithmetic of the weights and their bins, not the logits' bytes: 64
-// rows of 128000 f32 in 75 us (0.44 TB/s), 256 of 50257 f16 in 83, 16 of 200003 f32
-// in 41 (with one unit for all bins 70, 80 and 40: a third atomic addition for small
-// weights).  Few rows: the barriers of a cluster, about 0.7 us each; one row of
-// 128000 bf16 takes 15.9 us.
+// Bound: the arithmetic of the weights and their bins (95 to 120 instructions a
+// token), not the logits' bytes: 64 rows of 128000 f32 in 75 us (0.44 TB/s), 256 of
+// 50257 f16 in 83, 16 of 200003 f32 in 41 (with one unit for all bins 70, 80 and
+// 40: a third atomic addition for small weights).  Few rows: the barriers of a
+// cluster, about 0.7 us each; one row of 128000 bf16 takes 15.9 us.
 #include <algorithm>
 #include <cmath>
 
@@ -1034,7 +1034,8 @@ cudaError_t launch_sample(SampleParams p, int64_t rows, cudaStream_t s) {
     p.C = 1;
     while (p.C < 8 && rows * p.C * 2 <= 2 * dec::kSms && p.V > p.C * 2048) p.C *= 2;
     p.seg = ((p.V + p.C - 1) / p.C + 7) / 8 * 8;
-    // few rows: one CTA an SM, of 1024 threads
+    // CTAs for at most half the SMs: 1024 threads each; more: 512, of which an SM holds two (both within 64 registers, with
+    // about 270 bytes of spills).  Between a half and all of the SMs each has one CTA of 512.
     return rows * p.C <= dec::kSms / 2 ? launch_threads<DT, 1024>(p, rows, s) : launch_threads<DT, 512>(p, rows, s);
 }
 

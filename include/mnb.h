@@ -662,6 +662,8 @@ MNB_API mnb_status mnb_cache_compact(const mnb_cache_state* state, const mnb_pag
  *                 but from the unrounded Y, and a block with an infinity or a
  *                 NaN has scale NaN and codes 0.  block_size: a power of two,
  *                 at least 16; a block as wide as the row gives one scale a row.
+ *                 For a caller's own int8 product: the library's products take
+ *                 X and, at accuracy level 4, quantise it themselves.
  * residual_out and y may each be x or residual (same pointer, strides and
  * type, else MNB_ERR_INVALID_ARG); any other overlap is undefined.  The sum of
  * squares is f32: a row whose sum is past its range gives zeros, one whose
@@ -739,7 +741,9 @@ typedef enum mnb_activation { MNB_ACT_SILU = 0, MNB_ACT_GELU_TANH = 1 } mnb_acti
  * (two bf16 parts), whatever act_dtype is; Y is rounded once to out_dtype.
  * bf16 values of X, and w * act() * up between the products, are held in a
  * range of 2^-60 to 2^67: larger ones are infinite, smaller ones lose bits.
- * Results repeat.  The weights of experts that no token selects are not read.
+ * Results repeat; a token's w are those of mnb_moe_route but for their last
+ * bits (other orders of the same sums).  The weights of experts that no token
+ * selects are not read.
  *   x, y         device [T, hidden] of act_dtype (bf16 or f16) and out_dtype
  *                with the given row strides (elements, at least hidden),
  *                aligned to the element; 16-byte rows (base, stride and
