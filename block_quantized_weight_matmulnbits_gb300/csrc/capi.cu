@@ -10,7 +10,6 @@
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
-#include <unordered_map>
 #include <vector>
 
 #include "mnb.h"
@@ -101,13 +100,26 @@ mnb_status from_cuda(cudaError_t e) {
 }  // namespace
 
 cudaError_t allow_shared(const void* kern) {
+    // Limits by kernel.  (A table that neither allocates nor ends before other threads do; a kernel that finds it full is asked
+    // every time.)
+    struct Slot {
+        const void* kern;
+        int limit;
+    };
+    constexpr uint32_t kSlots = 2048;
     static std::mutex mu;
-    static std::unordered_map<const void*, int> limits;
+    static Slot slots[kSlots];
+    const auto slot = [&]() -> Slot* {
+        uint32_t at = (uint32_t)((reinterpret_cast<uintptr_t>(kern) * 0x9E3779B97F4A7C15ull) >> 53);
+        for (uint32_t i = 0; i < kSlots; ++i, at = (at + 1) % kSlots)
+            if (slots[at].kern == kern || !slots[at].kern) return &slots[at];
+        return nullptr;
+    };
     int limit = 0;
     {
         std::lock_guard<std::mutex> lk(mu);
-        const auto at = limits.find(kern);
-        if (at != limits.end()) limit = at->second;
+        const Slot* s = slot();
+        if (s && s->kern) limit = s->limit;
     }
     if (limit == 0) {
         cudaFuncAttributes a;
@@ -117,7 +129,7 @@ cudaError_t allow_shared(const void* kern) {
         if (optin <= a.sharedSizeBytes) return cudaErrorUnknown;  // (no device)
         limit = (int)(optin - a.sharedSizeBytes);
         std::lock_guard<std::mutex> lk(mu);
-        limits[kern] = limit;
+        if (Slot* s = slot()) *s = Slot{kern, limit};
     }
     // (set in every call: a reset of the device takes it back)
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, limit);

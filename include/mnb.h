@@ -791,7 +791,7 @@ MNB_API size_t mnb_moe_workspace_size(int64_t T, int64_t S, int64_t E, int64_t h
  * sum of its value in exact arithmetic, for any V: a token drawn is that of the
  * definition unless u is nearer than that to a border, and so is what the cuts
  * keep (a weight within 2^-33 of itself of min_p may be kept or not).  Weights
- * below 2^-44 of the largest, for V above 256 below 2^-36 / V of it, are left out
+ * below 2^-44 of the largest, for V above 256 below 2^-36 / V of it, may be left out
  * (2^-36 of a row in all).  Sums are exact integers: results repeat.
  *   logits       device [B, V] of dtype, row stride in elements, aligned to the
  *                element
